@@ -43,6 +43,12 @@ SIGNATURES = [
     ("dg_m_grouped_fp8_fp4_gemm_nt_contiguous", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     ("dg_m_grouped_fp8_fp4_gemm_nt_masked", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     ("dg_pack_sf_ue8m0", _I, [_P, _P, _I, _I, _I, _P]),
+    ("dg_add_rms_norm", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    ("dg_add_rms_norm_backward", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    ("dg_moe_route", _I, [_P, _P, _P, _P, _P]),
+    ("dg_moe_route_backward", _I, [_P, _P, _P, _P, _P, _P]),
+    ("dg_moe_fp8_few_tokens", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    ("dg_moe_fp8_fp4_few_tokens", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     ("dg_get_mk_alignment_for_contiguous_layout", _I, []),
     ("dg_set_mk_alignment_for_contiguous_layout", _I, [_I]),
     ("dg_get_theoretical_mk_alignment_for_contiguous_layout", _I, []),
@@ -388,6 +394,174 @@ def dg_pack_sf_ue8m0(sf: torch.Tensor, out: Optional[torch.Tensor] = None, strea
     _need(tuple(out.shape) == shape, "out shape mismatch")
     _check("dg_pack_sf_ue8m0", lib.dg_pack_sf_ue8m0(_ptr(sf), _ptr(out), mn, kg, int(mn_major), _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------------------------
+# Around the GEMMs: norm, router, and the mixture-of-experts layer for a few tokens
+# --------------------------------------------------------------------------------------
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}      # dg_type
+_SCORING = {"softmax": 0, "sigmoid": 1}             # dg_route_scoring
+
+
+class _NormDesc(ctypes.Structure):
+    _fields_ = [("T", _I), ("H", _I), ("ldx", ctypes.c_size_t), ("ldr", ctypes.c_size_t), ("ldo", ctypes.c_size_t),
+                ("residual_type", _I), ("weight_type", _I), ("eps", ctypes.c_float)]
+
+
+class _RouteDesc(ctypes.Structure):
+    _fields_ = [("T", _I), ("E", _I), ("topk", _I), ("ld", ctypes.c_size_t), ("logits_type", _I), ("scoring", _I),
+                ("renormalize", _I), ("scale", ctypes.c_float)]
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    _here(t, name)
+    _need(t.dtype in _TYPES, f"{name} must be bf16 or float32")
+    return _TYPES[t.dtype]
+
+
+def _rows(t: torch.Tensor, name: str, shape) -> int:
+    """Row stride of a 2-D tensor whose columns are contiguous."""
+    _need(tuple(t.shape) == shape, f"{name} shape mismatch")
+    _need(t.stride(1) == 1 or shape[1] == 1, f"{name} must have contiguous columns")
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def dg_add_rms_norm(x, residual, weight, eps, residual_out=None, y=None, q=None, sf=None, rstd=None, stream=None) -> None:
+    """s = x + residual, y = s * rsqrt(mean(s^2) + eps) * weight, and y in E4M3 with a scale per 128
+    columns. x [T, H] bf16, residual [T, H] bf16 or float32 (or None), weight [H] bf16 or float32.
+    Written where given: residual_out [T, H] = s in residual's type (x's without residual), y [T, H]
+    bf16, q [T, H] e4m3 with sf [ceil(H/512), ceil4(T)] int32 (a and sfa of the GEMMs), rstd [T]
+    float32. x, residual and residual_out may have strided rows; residual_out may be residual."""
+    lib = load_library()
+    _need(_type(x, "x") == 0 and x.dim() == 2, "x must be a 2-D bf16 tensor")
+    T, H = x.shape
+    ldx = _rows(x, "x", (T, H))
+    wt = _type(weight, "weight")
+    _need(tuple(weight.shape) == (H,) and weight.is_contiguous(), "weight must be a contiguous [H] tensor")
+    rt, ldr, ldo = 0, H, H
+    if residual is not None:
+        rt, ldr = _type(residual, "residual"), _rows(residual, "residual", (T, H))
+    if residual_out is not None:
+        ot, ldo = _type(residual_out, "residual_out"), _rows(residual_out, "residual_out", (T, H))
+        _need(residual is None or ot == rt, "residual_out must have residual's type")
+        rt = ot
+    if y is not None:
+        _bf16(y, "y")
+        _need(tuple(y.shape) == (T, H), "y shape mismatch")
+    if q is not None:
+        _fp8(q, "q")
+        _need(tuple(q.shape) == (T, H), "q shape mismatch")
+    if sf is not None:
+        _i32(sf, "sf")
+        _need(tuple(sf.shape) == sf_shape(T, -(-H // 128) * 128), "sf shape mismatch")
+    if rstd is not None:
+        _f32(rstd, "rstd")
+        _need(tuple(rstd.shape) == (T,), "rstd shape mismatch")
+    _check("dg_add_rms_norm",
+           lib.dg_add_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(q), _ptr(sf),
+                               _ptr(rstd), ctypes.byref(_NormDesc(T, H, ldx, ldr, ldo, rt, wt, eps)), _stream(stream)))
+
+
+def dg_add_rms_norm_backward(dy, s, weight, rstd, ds, dx, dresidual, dw, stream=None) -> None:
+    """Gradient of dg_add_rms_norm from dy [T, H] bf16 (gradient of y), s [T, H] (its residual_out),
+    weight [H], rstd [T] float32 and ds [T, H] of s's type (gradient of residual_out, or None). Writes
+    the gradient of s to dx [T, H] bf16 and to dresidual [T, H] of s's type (either may be None), and
+    dw [H] float32."""
+    lib = load_library()
+    _bf16(dy, "dy")
+    _need(dy.dim() == 2, "dy must be 2-D")
+    T, H = dy.shape
+    rt, wt = _type(s, "s"), _type(weight, "weight")
+    _need(tuple(s.shape) == (T, H) and s.is_contiguous(), "s must be a contiguous [T, H] tensor")
+    _need(tuple(weight.shape) == (H,) and weight.is_contiguous(), "weight must be a contiguous [H] tensor")
+    _f32(rstd, "rstd"); _f32(dw, "dw")
+    _need(tuple(rstd.shape) == (T,) and tuple(dw.shape) == (H,), "shape mismatch")
+    for t, name in ((ds, "ds"), (dresidual, "dresidual")):
+        if t is not None:
+            _here(t, name)
+            _need(tuple(t.shape) == (T, H) and t.is_contiguous() and t.dtype == s.dtype,
+                  f"{name} must be a contiguous [T, H] tensor of s's type")
+    if dx is not None:
+        _bf16(dx, "dx")
+        _need(tuple(dx.shape) == (T, H), "dx shape mismatch")
+    _check("dg_add_rms_norm_backward",
+           lib.dg_add_rms_norm_backward(_ptr(dy), _ptr(s), _ptr(weight), _ptr(rstd), _ptr(ds), _ptr(dx), _ptr(dresidual),
+                                        _ptr(dw), T, H, rt, wt, _stream(stream)))
+
+
+def dg_moe_route(logits, topk_ids, topk_weights, scoring="softmax", renormalize=True, scale=1.0, stream=None):
+    """Top-k router: topk_ids [T, k] int32 (largest logit first, ties by lowest index, -1 where no
+    unmasked expert is left) and topk_weights [T, k] float32 from logits [T, E] bf16 or float32 (rows may
+    be strided; -inf and NaN mask an expert). scoring: "softmax" or "sigmoid"."""
+    lib = load_library()
+    lt = _type(logits, "logits")
+    _need(logits.dim() == 2, "logits must be 2-D")
+    T, E = logits.shape
+    ld = _rows(logits, "logits", (T, E))
+    _i32(topk_ids, "topk_ids"); _f32(topk_weights, "topk_weights")
+    _need(topk_ids.dim() == 2 and topk_ids.shape[0] == T and topk_weights.shape == topk_ids.shape, "shape mismatch")
+    _need(scoring in _SCORING, "scoring must be softmax or sigmoid")
+    desc = _RouteDesc(T, E, topk_ids.shape[1], ld, lt, _SCORING[scoring], bool(renormalize), scale)
+    _check("dg_moe_route", lib.dg_moe_route(_ptr(logits), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(desc), _stream(stream)))
+    return topk_ids, topk_weights
+
+
+def dg_moe_route_backward(logits, topk_ids, dweights, dlogits, scoring="softmax", renormalize=True, scale=1.0,
+                          stream=None) -> torch.Tensor:
+    """Gradient of dg_moe_route: dlogits [T, E] (contiguous, logits' type) from dweights [T, k] float32."""
+    lib = load_library()
+    lt = _type(logits, "logits")
+    _need(logits.dim() == 2, "logits must be 2-D")
+    T, E = logits.shape
+    ld = _rows(logits, "logits", (T, E))
+    _i32(topk_ids, "topk_ids"); _f32(dweights, "dweights"); _here(dlogits, "dlogits")
+    _need(topk_ids.dim() == 2 and topk_ids.shape[0] == T and dweights.shape == topk_ids.shape, "shape mismatch")
+    _need(tuple(dlogits.shape) == (T, E) and dlogits.is_contiguous() and dlogits.dtype == logits.dtype,
+          "dlogits must be a contiguous [T, E] tensor of logits' type")
+    _need(scoring in _SCORING, "scoring must be softmax or sigmoid")
+    desc = _RouteDesc(T, E, topk_ids.shape[1], ld, lt, _SCORING[scoring], bool(renormalize), scale)
+    _check("dg_moe_route_backward",
+           lib.dg_moe_route_backward(_ptr(logits), _ptr(topk_ids), _ptr(dweights), _ptr(dlogits), ctypes.byref(desc),
+                                     _stream(stream)))
+    return dlogits
+
+
+def _few_tokens(name, per_byte, weight, scales, x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream):
+    lib = load_library()
+    _fp8(x, "x"); _i32(sfx, "sfx"); weight(w13, "w13"); _i32(sf13, "sf13"); weight(w2, "w2"); _i32(sf2, "sf2")
+    _i32(topk_ids, "topk_ids"); _f32(topk_weights, "topk_weights"); _bf16(y, "y")
+    _need(x.dim() == 2 and w13.dim() == 3 and w2.dim() == 3 and topk_ids.dim() == 2, "wrong number of dimensions")
+    T, H = x.shape
+    E, N, _ = w13.shape
+    I, k = N // 2, topk_ids.shape[1]
+    _need(tuple(w13.shape) == (E, 2 * I, H // per_byte) and tuple(w2.shape) == (E, H, I // per_byte)
+          and H % per_byte == 0 and I % per_byte == 0, "weight shape mismatch")
+    _need(tuple(topk_ids.shape) == (T, k) and topk_weights.shape == topk_ids.shape and tuple(y.shape) == (T, H), "shape mismatch")
+    _need(tuple(sfx.shape) == sf_shape(T, H) and tuple(sf13.shape) == scales(2 * I, H, E)
+          and tuple(sf2.shape) == scales(H, I, E), "scale shape mismatch")
+    if c is not None:
+        _bf16(c, "c")
+        _need(tuple(c.shape) == (T, H), "c shape mismatch")
+    _check(name, getattr(lib, name)(_ptr(x), _ptr(sfx), _ptr(w13), _ptr(sf13), _ptr(w2), _ptr(sf2), _ptr(topk_ids),
+                                    _ptr(topk_weights), _ptr(c), _ptr(y), T, k, E, H, I, _stream(stream)))
+    return y
+
+
+def dg_moe_fp8_few_tokens(x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream=None) -> torch.Tensor:
+    """Mixture-of-experts layer for at most 32 tokens: y = c + sum over the slots of weight *
+    w2[e] @ (silu(gate) * up), (gate; up) = w13[e] @ x. x [T, H] e4m3 with sfx, w13 [E, 2I, H] e4m3 (gate
+    rows first) and w2 [E, H, I] e4m3 with their block scales as for the M-grouped GEMMs, topk_ids [T, k]
+    int32 (-1: empty slot), topk_weights [T, k] float32, c [T, H] bf16 or None (may be y), y [T, H] bf16."""
+    return _few_tokens("dg_moe_fp8_few_tokens", 1, _fp8, lambda n, k, g: sf_shape(-(-n // 128), k, g), x, sfx, w13, sf13,
+                       w2, sf2, topk_ids, topk_weights, c, y, stream)
+
+
+def dg_moe_fp8_fp4_few_tokens(x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream=None) -> torch.Tensor:
+    """dg_moe_fp8_few_tokens with the weights in packed E2M1: w13 [E, 2I, H/2] with sf13 [E, H/128, ceil4(2I)],
+    w2 [E, H, I/2] with sf2 [E, I/128, ceil4(H)]."""
+    return _few_tokens("dg_moe_fp8_fp4_few_tokens", 2, _fp4, sf_fp4_shape, x, sfx, w13, sf13, w2, sf2, topk_ids,
+                       topk_weights, c, y, stream)
 
 
 def dg_get_mk_alignment_for_contiguous_layout() -> int:

@@ -17,7 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdg.so")
-SOURCES = [os.path.join(CSRC, "dg_api.cu"), os.path.join(CSRC, "dg_no_alloc.cu"), os.path.join(CSRC, "dg_diag.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("dg_api.cu", "dg_no_alloc.cu", "dg_diag.cu", "dg_norm.cu", "dg_route.cu", "dg_moe.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,7 +32,7 @@ def build(verbose: bool = False, out: str = LIB) -> str:
     deps = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "dg.h")]
     if os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(d) for d in deps):
         return out
-    cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-t", "0", "-shared", "-Xcompiler", "-fPIC",
            "-Xptxas", "-v", "-diag-suppress", "177", "-I", INCLUDE, "-I", CSRC, "-o", out + ".tmp", *SOURCES]
     res = subprocess.run(cmd, capture_output=True, text=True)
     log = res.stdout + res.stderr

@@ -11,12 +11,14 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "debug_state.h"
 #include "dg.h"
 #include "fp8_gemm.cuh"
 #include "fp8_gemm_pair.cuh"
+#include "runtime.h"
 #include "workspace_cache.h"
 
 namespace {
@@ -971,6 +973,35 @@ dg_status run_dense_single(DeviceState& dsr, const void* a, const int32_t* sfa, 
 namespace dg {
 int debug_fault_mode() { return g_fault.load(); }
 unsigned long long pipeline_wait_timeout_ns() { return wait_timeout_ns(); }
+
+// runtime.h: what the other translation units take from this one
+dg_status launch_context(LaunchContext* out) {
+  DeviceState* ds = nullptr;
+  if (dg_status s = device_state(&ds); s != DG_OK) return s;
+  out->sms = sms_to_use(*ds);
+  out->status = ds->status;
+  out->pdl = pdl_enabled();
+  return DG_OK;
+}
+
+dg_status record_cuda_error(cudaError_t e) { return cuda_fail(e); }
+
+dg_status StreamWorkspace::acquire(cudaStream_t stream, size_t bytes, void** out) {
+  DeviceState* ds = nullptr;
+  if (dg_status s = device_state(&ds); s != DG_OK) return s;
+  constexpr size_t kCounters = kSkCounterInts * sizeof(int);
+  auto* lease = new (std::nothrow) WorkspaceLease;
+  if (!lease) return cuda_fail(cudaErrorMemoryAllocation);
+  if (dg_status s = stream_workspace(*ds, stream, kCounters + bytes, lease); s != DG_OK) {
+    delete lease;
+    return s;
+  }
+  lease_ = lease;
+  *out = static_cast<char*>(lease->ptr) + kCounters;
+  return DG_OK;
+}
+
+StreamWorkspace::~StreamWorkspace() { delete static_cast<WorkspaceLease*>(lease_); }
 }  // namespace dg
 
 // ======================================================================================

@@ -258,6 +258,128 @@ dg_status dg_m_grouped_fp8_fp4_gemm_nt_masked(const void* a, const int32_t* sfa,
 dg_status dg_pack_sf_ue8m0(const float* sf_fp32, int32_t* out, int mn, int kgroups, int mn_major_in,
                            cudaStream_t stream);
 
+/* Element types of the operators below, where an argument may have either. */
+typedef enum { DG_BF16 = 0, DG_F32 = 1 } dg_type;
+
+/* Sizes, strides (in elements) and options of dg_add_rms_norm. */
+typedef struct {
+  int T, H;
+  size_t ldx, ldr, ldo;               /* row strides of x, residual, residual_out */
+  int residual_type, weight_type;     /* dg_type */
+  float eps;
+} dg_norm_desc;
+
+/*
+ * Residual addition and RMS norm, with the E4M3 rows and scales the GEMMs take as A (an extra entry
+ * point of this library: the pages leave the activations' FP8 casting to the caller). For every row t < T:
+ *     s = x + residual;   rstd = (mean over the H columns of s^2 + eps)^(-1/2);   y = s * rstd * weight
+ *     q = E4M3(y * 2^-n_g), n_g the least integer with max|y_g| * 2^-n_g <= 448 in each group g of 128
+ *     columns, sf the codes n_g + 127 (clamped to [1, 254]; 127 for a group of zeros)
+ * computed in FP32; each output is rounded once, where it is stored, to nearest even.
+ *   x            : BF16 [T, H], rows desc->ldx elements apart.
+ *   residual     : [T, H] of residual_type, rows ldr elements apart; NULL for none (s = x).
+ *   weight       : [H] of weight_type.
+ *   residual_out : s, [T, H] of residual_type, rows ldo elements apart; may be `residual` (in place)
+ *                  or NULL.
+ *   y            : BF16 [T, H] or NULL; may be x if ldx == H.
+ *   q, sf        : E4M3 [T, H] and packed scales int32 [ceil(H/512), ceil4(T)], exactly the operands a
+ *                  and sfa of the GEMMs with K = H (padding rows and bytes 0); both or neither.
+ *   rstd         : float32 [T], for the gradient, or NULL.
+ * An element of y that is not finite becomes the NaN code of q and does not count for its group's scale.
+ * Limits: H > 0, H % 8 == 0 (H % 128 == 0 with q), H <= 16384 (DG_ERR_UNSUPPORTED above), T >= 0;
+ * at least one of residual_out, y and q; eps >= 0 and finite. Base pointers and row strides are multiples
+ * of 16 bytes (rstd: 4).
+ */
+dg_status dg_add_rms_norm(const void* x, const void* residual, const void* weight, void* residual_out, void* y, void* q,
+                          int32_t* sf, float* rstd, const dg_norm_desc* desc, cudaStream_t stream);
+
+/*
+ * Gradient of dg_add_rms_norm (E4M3 rounding passes it through). With s and rstd as the forward call
+ * wrote them, xhat = s * rstd, g = dy * weight, per row:
+ *     d  = rstd * (g - xhat * mean(g * xhat)) + ds        (the gradient of s, hence of x and of residual)
+ *     dw = sum over the rows of dy * xhat
+ *   dy        : BF16 [T, H] gradient of y.      s : [T, H] of residual_type.      weight : [H] of weight_type.
+ *   rstd      : float32 [T].                    ds : [T, H] of residual_type, the gradient that reaches
+ *               residual_out by other paths, or NULL.
+ *   dx        : d in BF16 [T, H], or NULL.      dresidual : d in residual_type [T, H], or NULL; may be ds.
+ *               At least one of the two (dx may be dy).
+ *   dw        : float32 [H], written (zeros for T = 0). Summed in a fixed order: the same inputs give
+ *               the same bits on the same number of SMs.
+ * All contiguous. Limits as dg_add_rms_norm. Uses the stream's workspace.
+ */
+dg_status dg_add_rms_norm_backward(const void* dy, const void* s, const void* weight, const float* rstd, const void* ds,
+                                   void* dx, void* dresidual, float* dw, int T, int H, int residual_type,
+                                   int weight_type, cudaStream_t stream);
+
+/* Score of an expert in the router. */
+typedef enum { DG_ROUTE_SOFTMAX = 0, DG_ROUTE_SIGMOID = 1 } dg_route_scoring;
+
+/* Sizes and options of the router. */
+typedef struct {
+  int T, E, topk;
+  size_t ld;                          /* row stride of logits, in elements */
+  int logits_type;                    /* dg_type */
+  int scoring;                        /* dg_route_scoring */
+  int renormalize;                    /* 0 or 1 */
+  float scale;
+} dg_route_desc;
+
+/*
+ * Top-k router of a mixture of experts (an extra entry point of this library).
+ *   logits       : [T, E] of desc->logits_type, rows desc->ld elements apart.
+ *   topk_ids     : int32 [T, topk]: the experts of the row's largest logits, largest first, equal logits
+ *                  by lowest index. An expert whose logit is -infinity or NaN is masked: it is never chosen
+ *                  and has no part in the softmax; a slot for which none is left gets -1.
+ *   topk_weights : float32 [T, topk]: scale * p, p the softmax of the row's logits or the sigmoid of the
+ *                  expert's own; with renormalize = 1 divided by its sum over the row's chosen experts
+ *                  (0 where that sum is 0). 0 in slots with id -1.
+ * Limits: 0 < topk <= E; E <= 1024 and topk <= 32 (DG_ERR_UNSUPPORTED above); scale finite. Pointers are
+ * aligned to their element.
+ */
+dg_status dg_moe_route(const void* logits, int32_t* topk_ids, float* topk_weights, const dg_route_desc* desc,
+                       cudaStream_t stream);
+
+/*
+ * Gradient of dg_moe_route's weights with respect to its logits.
+ *   logits, topk_ids, desc : as the forward call had and wrote them (a row's ids are distinct
+ *              or -1). An id outside [-1, E) is taken as -1 and sets DG_ERR_BAD_INDEX on the device.
+ *   dweights : float32 [T, topk]; entries of slots with id -1 are not read as values.
+ *   dlogits  : [T, E] of logits_type, contiguous, fully written.
+ */
+dg_status dg_moe_route_backward(const void* logits, const int32_t* topk_ids, const float* dweights, void* dlogits,
+                                const dg_route_desc* desc, cudaStream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (an extra entry point of this library; the grouped
+ * GEMMs above are the form for many). With (G_e; U_e) the rows of w13[e]:
+ *     y[t] = c[t] + sum over slots j with e = topk_ids[t, j] >= 0 of
+ *                   topk_weights[t, j] * w2[e] @ (silu(G_e x_t) * (U_e x_t)),     silu(v) = v / (1 + exp(-v))
+ *   x, sfx   : E4M3 [T, H] and its packed scales [ceil(H/512), ceil4(T)] (a and sfa of the GEMMs).
+ *   w13, sf13: E4M3 [E, 2 I, H], the I gate rows before the I up rows, and the packed scales of its
+ *              128 x 128 blocks: b and sfb of the M-grouped NT GEMMs with N = 2 I, K = H.
+ *   w2, sf2  : E4M3 [E, H, I]: the same with N = H, K = I.
+ *   topk_ids, topk_weights : int32 and float32 [T, topk]; -1 is an empty slot, and a token without any
+ *              gets c[t] (or 0). An id outside [-1, E) is taken as -1 and sets DG_ERR_BAD_INDEX on the device.
+ *   c        : BF16 [T, H] addend (a shared expert's output, the residual) or NULL; may be y.
+ *   y        : BF16 [T, H].
+ * FP32 accumulation; the experts' inner values are held in FP16 with a power-of-two scale per 64 columns,
+ * y is rounded once. The values of experts that a token does not name never reach it.
+ * Limits: T <= 32, topk <= 16, E <= 1024, H and I <= 16384 (DG_ERR_UNSUPPORTED above); H and I positive
+ * multiples of 128. Pointers 16-byte aligned (topk_ids, topk_weights: 4). Uses the stream's workspace.
+ */
+dg_status dg_moe_fp8_few_tokens(const void* x, const int32_t* sfx, const void* w13, const int32_t* sf13, const void* w2,
+                                const int32_t* sf2, const int32_t* topk_ids, const float* topk_weights, const void* c,
+                                void* y, int T, int topk, int E, int H, int I, cudaStream_t stream);
+
+/*
+ * The same layer with the experts' weights in E2M1: w13 uint8 [E, 2 I, H/2] with sf13 int32 [E, H/128,
+ * ceil4(2 I)], w2 uint8 [E, H, I/2] with sf2 int32 [E, I/128, ceil4(H)], as b and sfb of the FP8 x FP4
+ * GEMMs (16-byte alignment is enough here).
+ */
+dg_status dg_moe_fp8_fp4_few_tokens(const void* x, const int32_t* sfx, const void* w13, const int32_t* sf13, const void* w2,
+                                    const int32_t* sf2, const int32_t* topk_ids, const float* topk_weights, const void* c,
+                                    void* y, int T, int topk, int E, int H, int I, cudaStream_t stream);
+
 /*
  * Dense GEMM that allocates no device memory (the pages have no counterpart: this is an
  * extra entry point of this library).
