@@ -95,8 +95,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # the raw handle: torch.cuda.current_stream() would build a Stream object for every call (3 us)
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -116,9 +116,10 @@ def _need(cond: bool, msg: str) -> None:
 def _here(t: torch.Tensor, name: str) -> None:
     # the library works on the current device (and its stream): memory of another GPU would be
     # read through the wrong device's mappings
-    _need(t.is_cuda, f"{name} must be a CUDA tensor")
-    _need(t.device.index == torch.cuda.current_device(),
-          f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _fp8(t: torch.Tensor, name: str) -> None:
@@ -402,6 +403,9 @@ def dg_pack_sf_ue8m0(sf: torch.Tensor, out: Optional[torch.Tensor] = None, strea
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}      # dg_type
 _SCORING = {"softmax": 0, "sigmoid": 1}             # dg_route_scoring
+_STREAM_DTYPES = (torch.bfloat16, torch.float32)
+_BF16_ONLY, _F32_ONLY, _I32_ONLY = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_FP8_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
 class _NormDesc(ctypes.Structure):
@@ -414,53 +418,75 @@ class _RouteDesc(ctypes.Structure):
                 ("renormalize", _I), ("scale", ctypes.c_float)]
 
 
-def _type(t: torch.Tensor, name: str) -> int:
+# These calls are short (a few microseconds on the device), so their checks read each property of a
+# tensor once and build a message only where one fails.
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The device of a call's first tensor, which has to be the current one."""
     _here(t, name)
-    _need(t.dtype in _TYPES, f"{name} must be bf16 or float32")
-    return _TYPES[t.dtype]
+    return t.get_device()
 
 
-def _rows(t: torch.Tensor, name: str, shape) -> int:
-    """Row stride of a 2-D tensor whose columns are contiguous."""
-    _need(tuple(t.shape) == shape, f"{name} shape mismatch")
-    _need(t.stride(1) == 1 or shape[1] == 1, f"{name} must have contiguous columns")
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+def _refuse(t: torch.Tensor, name: str, dtypes, shape, dev: int):
+    _here(t, name)
+    _need(t.get_device() == dev, f"{name} is on another device")
+    _need(t.dtype in dtypes, f"{name} must have type {' or '.join(str(d).replace('torch.', '').replace('bfloat16', 'bf16') for d in dtypes)}")
+    _need(t.shape == shape, f"{name} shape mismatch: {tuple(t.shape)}, expected {shape}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t: torch.Tensor, name: str, dtypes, shape, dev: int) -> int:
+    """Pointer of a contiguous tensor of one of the types and of the shape."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _refuse(t, name, dtypes, shape, dev)
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, shape, dev: int):
+    """Pointer and row stride of a 2-D tensor whose columns are contiguous."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
+        ld, step = t.stride()
+        _need(step == 1 or shape[1] <= 1, f"{name} must have contiguous columns")
+        return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
+    _refuse(t, name, dtypes, shape, dev)
+
+
+def _two_d(t: torch.Tensor, name: str):
+    _need(t.dim() == 2, f"{name} must be 2-D")
+    return t.shape
 
 
 def dg_add_rms_norm(x, residual, weight, eps, residual_out=None, y=None, q=None, sf=None, rstd=None, stream=None) -> None:
     """s = x + residual, y = s * rsqrt(mean(s^2) + eps) * weight, and y in E4M3 with a scale per 128
     columns. x [T, H] bf16, residual [T, H] bf16 or float32 (or None), weight [H] bf16 or float32.
-    Written where given: residual_out [T, H] = s in residual's type (x's without residual), y [T, H]
-    bf16, q [T, H] e4m3 with sf [ceil(H/512), ceil4(T)] int32 (a and sfa of the GEMMs), rstd [T]
+    Written where given: residual_out [T, H] = s in residual's type (bf16 or float32 without residual),
+    y [T, H] bf16, q [T, H] e4m3 with sf [ceil(H/512), ceil4(T)] int32 (a and sfa of the GEMMs), rstd [T]
     float32. x, residual and residual_out may have strided rows; residual_out may be residual."""
-    lib = load_library()
-    _need(_type(x, "x") == 0 and x.dim() == 2, "x must be a 2-D bf16 tensor")
-    T, H = x.shape
-    ldx = _rows(x, "x", (T, H))
-    wt = _type(weight, "weight")
-    _need(tuple(weight.shape) == (H,) and weight.is_contiguous(), "weight must be a contiguous [H] tensor")
-    rt, ldr, ldo = 0, H, H
+    dev = _device(x, "x")
+    T, H = shape = _two_d(x, "x")
+    px, ldx = _rows(x, "x", _BF16_ONLY, shape, dev)
+    pw = _arg(weight, "weight", _STREAM_DTYPES, (H,), dev)
+    pr = po = py = pq = ps = pd = None
+    ldr = ldo = H
+    rt = torch.bfloat16
     if residual is not None:
-        rt, ldr = _type(residual, "residual"), _rows(residual, "residual", (T, H))
+        pr, ldr = _rows(residual, "residual", _STREAM_DTYPES, shape, dev)
+        rt = residual.dtype
     if residual_out is not None:
-        ot, ldo = _type(residual_out, "residual_out"), _rows(residual_out, "residual_out", (T, H))
-        _need(residual is None or ot == rt, "residual_out must have residual's type")
-        rt = ot
+        po, ldo = _rows(residual_out, "residual_out", _STREAM_DTYPES, shape, dev)
+        _need(residual is None or residual_out.dtype == rt, "residual_out must have residual's type")
+        rt = residual_out.dtype
     if y is not None:
-        _bf16(y, "y")
-        _need(tuple(y.shape) == (T, H), "y shape mismatch")
+        py = _arg(y, "y", _BF16_ONLY, shape, dev)
     if q is not None:
-        _fp8(q, "q")
-        _need(tuple(q.shape) == (T, H), "q shape mismatch")
+        pq = _arg(q, "q", _FP8_DTYPES, shape, dev)
     if sf is not None:
-        _i32(sf, "sf")
-        _need(tuple(sf.shape) == sf_shape(T, -(-H // 128) * 128), "sf shape mismatch")
+        ps = _arg(sf, "sf", _I32_ONLY, (-(-H // 512), 4 * (-(-T // 4))), dev)
     if rstd is not None:
-        _f32(rstd, "rstd")
-        _need(tuple(rstd.shape) == (T,), "rstd shape mismatch")
-    _check("dg_add_rms_norm",
-           lib.dg_add_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(q), _ptr(sf),
-                               _ptr(rstd), ctypes.byref(_NormDesc(T, H, ldx, ldr, ldo, rt, wt, eps)), _stream(stream)))
+        pd = _arg(rstd, "rstd", _F32_ONLY, (T,), dev)
+    desc = _NormDesc(T, H, ldx, ldr, ldo, _TYPES[rt], _TYPES[weight.dtype], eps)
+    _check("dg_add_rms_norm", (_lib or load_library()).dg_add_rms_norm(px, pr, pw, po, py, pq, ps, pd, ctypes.byref(desc),
+                                                                      _stream(stream)))
 
 
 def dg_add_rms_norm_backward(dy, s, weight, rstd, ds, dx, dresidual, dw, stream=None) -> None:
@@ -468,83 +494,77 @@ def dg_add_rms_norm_backward(dy, s, weight, rstd, ds, dx, dresidual, dw, stream=
     weight [H], rstd [T] float32 and ds [T, H] of s's type (gradient of residual_out, or None). Writes
     the gradient of s to dx [T, H] bf16 and to dresidual [T, H] of s's type (either may be None), and
     dw [H] float32."""
-    lib = load_library()
-    _bf16(dy, "dy")
-    _need(dy.dim() == 2, "dy must be 2-D")
-    T, H = dy.shape
-    rt, wt = _type(s, "s"), _type(weight, "weight")
-    _need(tuple(s.shape) == (T, H) and s.is_contiguous(), "s must be a contiguous [T, H] tensor")
-    _need(tuple(weight.shape) == (H,) and weight.is_contiguous(), "weight must be a contiguous [H] tensor")
-    _f32(rstd, "rstd"); _f32(dw, "dw")
-    _need(tuple(rstd.shape) == (T,) and tuple(dw.shape) == (H,), "shape mismatch")
-    for t, name in ((ds, "ds"), (dresidual, "dresidual")):
-        if t is not None:
-            _here(t, name)
-            _need(tuple(t.shape) == (T, H) and t.is_contiguous() and t.dtype == s.dtype,
-                  f"{name} must be a contiguous [T, H] tensor of s's type")
-    if dx is not None:
-        _bf16(dx, "dx")
-        _need(tuple(dx.shape) == (T, H), "dx shape mismatch")
+    dev = _device(dy, "dy")
+    T, H = shape = _two_d(dy, "dy")
+    pdy = _arg(dy, "dy", _BF16_ONLY, shape, dev)
+    ps = _arg(s, "s", _STREAM_DTYPES, shape, dev)
+    same = (s.dtype,)
+    pw = _arg(weight, "weight", _STREAM_DTYPES, (H,), dev)
+    pr = _arg(rstd, "rstd", _F32_ONLY, (T,), dev)
+    pds = None if ds is None else _arg(ds, "ds", same, shape, dev)
+    pdx = None if dx is None else _arg(dx, "dx", _BF16_ONLY, shape, dev)
+    pdr = None if dresidual is None else _arg(dresidual, "dresidual", same, shape, dev)
+    pdw = _arg(dw, "dw", _F32_ONLY, (H,), dev)
     _check("dg_add_rms_norm_backward",
-           lib.dg_add_rms_norm_backward(_ptr(dy), _ptr(s), _ptr(weight), _ptr(rstd), _ptr(ds), _ptr(dx), _ptr(dresidual),
-                                        _ptr(dw), T, H, rt, wt, _stream(stream)))
+           (_lib or load_library()).dg_add_rms_norm_backward(pdy, ps, pw, pr, pds, pdx, pdr, pdw, T, H, _TYPES[s.dtype],
+                                                             _TYPES[weight.dtype], _stream(stream)))
+
+
+def _route_args(logits, topk_ids, scoring, renormalize, scale):
+    dev = _device(logits, "logits")
+    T, E = shape = _two_d(logits, "logits")
+    p, ld = _rows(logits, "logits", _STREAM_DTYPES, shape, dev)
+    k = _two_d(topk_ids, "topk_ids")[1]
+    _need(scoring in _SCORING, "scoring must be softmax or sigmoid")
+    desc = _RouteDesc(T, E, k, ld, _TYPES[logits.dtype], _SCORING[scoring], bool(renormalize), scale)
+    return dev, shape, (T, k), p, ctypes.byref(desc)
 
 
 def dg_moe_route(logits, topk_ids, topk_weights, scoring="softmax", renormalize=True, scale=1.0, stream=None):
     """Top-k router: topk_ids [T, k] int32 (largest logit first, ties by lowest index, -1 where no
     unmasked expert is left) and topk_weights [T, k] float32 from logits [T, E] bf16 or float32 (rows may
     be strided; -inf and NaN mask an expert). scoring: "softmax" or "sigmoid"."""
-    lib = load_library()
-    lt = _type(logits, "logits")
-    _need(logits.dim() == 2, "logits must be 2-D")
-    T, E = logits.shape
-    ld = _rows(logits, "logits", (T, E))
-    _i32(topk_ids, "topk_ids"); _f32(topk_weights, "topk_weights")
-    _need(topk_ids.dim() == 2 and topk_ids.shape[0] == T and topk_weights.shape == topk_ids.shape, "shape mismatch")
-    _need(scoring in _SCORING, "scoring must be softmax or sigmoid")
-    desc = _RouteDesc(T, E, topk_ids.shape[1], ld, lt, _SCORING[scoring], bool(renormalize), scale)
-    _check("dg_moe_route", lib.dg_moe_route(_ptr(logits), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(desc), _stream(stream)))
+    dev, _, slots, p, desc = _route_args(logits, topk_ids, scoring, renormalize, scale)
+    pi = _arg(topk_ids, "topk_ids", _I32_ONLY, slots, dev)
+    pw = _arg(topk_weights, "topk_weights", _F32_ONLY, slots, dev)
+    _check("dg_moe_route", (_lib or load_library()).dg_moe_route(p, pi, pw, desc, _stream(stream)))
     return topk_ids, topk_weights
 
 
 def dg_moe_route_backward(logits, topk_ids, dweights, dlogits, scoring="softmax", renormalize=True, scale=1.0,
                           stream=None) -> torch.Tensor:
     """Gradient of dg_moe_route: dlogits [T, E] (contiguous, logits' type) from dweights [T, k] float32."""
-    lib = load_library()
-    lt = _type(logits, "logits")
-    _need(logits.dim() == 2, "logits must be 2-D")
-    T, E = logits.shape
-    ld = _rows(logits, "logits", (T, E))
-    _i32(topk_ids, "topk_ids"); _f32(dweights, "dweights"); _here(dlogits, "dlogits")
-    _need(topk_ids.dim() == 2 and topk_ids.shape[0] == T and dweights.shape == topk_ids.shape, "shape mismatch")
-    _need(tuple(dlogits.shape) == (T, E) and dlogits.is_contiguous() and dlogits.dtype == logits.dtype,
-          "dlogits must be a contiguous [T, E] tensor of logits' type")
-    _need(scoring in _SCORING, "scoring must be softmax or sigmoid")
-    desc = _RouteDesc(T, E, topk_ids.shape[1], ld, lt, _SCORING[scoring], bool(renormalize), scale)
-    _check("dg_moe_route_backward",
-           lib.dg_moe_route_backward(_ptr(logits), _ptr(topk_ids), _ptr(dweights), _ptr(dlogits), ctypes.byref(desc),
-                                     _stream(stream)))
+    dev, shape, slots, p, desc = _route_args(logits, topk_ids, scoring, renormalize, scale)
+    pi = _arg(topk_ids, "topk_ids", _I32_ONLY, slots, dev)
+    pw = _arg(dweights, "dweights", _F32_ONLY, slots, dev)
+    po = _arg(dlogits, "dlogits", (logits.dtype,), shape, dev)
+    _check("dg_moe_route_backward", (_lib or load_library()).dg_moe_route_backward(p, pi, pw, po, desc, _stream(stream)))
     return dlogits
 
 
-def _few_tokens(name, per_byte, weight, scales, x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream):
-    lib = load_library()
-    _fp8(x, "x"); _i32(sfx, "sfx"); weight(w13, "w13"); _i32(sf13, "sf13"); weight(w2, "w2"); _i32(sf2, "sf2")
-    _i32(topk_ids, "topk_ids"); _f32(topk_weights, "topk_weights"); _bf16(y, "y")
-    _need(x.dim() == 2 and w13.dim() == 3 and w2.dim() == 3 and topk_ids.dim() == 2, "wrong number of dimensions")
-    T, H = x.shape
-    E, N, _ = w13.shape
-    I, k = N // 2, topk_ids.shape[1]
-    _need(tuple(w13.shape) == (E, 2 * I, H // per_byte) and tuple(w2.shape) == (E, H, I // per_byte)
-          and H % per_byte == 0 and I % per_byte == 0, "weight shape mismatch")
-    _need(tuple(topk_ids.shape) == (T, k) and topk_weights.shape == topk_ids.shape and tuple(y.shape) == (T, H), "shape mismatch")
-    _need(tuple(sfx.shape) == sf_shape(T, H) and tuple(sf13.shape) == scales(2 * I, H, E)
-          and tuple(sf2.shape) == scales(H, I, E), "scale shape mismatch")
-    if c is not None:
-        _bf16(c, "c")
-        _need(tuple(c.shape) == (T, H), "c shape mismatch")
-    _check(name, getattr(lib, name)(_ptr(x), _ptr(sfx), _ptr(w13), _ptr(sf13), _ptr(w2), _ptr(sf2), _ptr(topk_ids),
-                                    _ptr(topk_weights), _ptr(c), _ptr(y), T, k, E, H, I, _stream(stream)))
+def _few_tokens(name, fp4, x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream):
+    dev = _device(x, "x")
+    T, H = shape = _two_d(x, "x")
+    _need(w13.dim() == 3, "w13 must be 3-D")
+    E, N = w13.shape[:2]
+    I, k = N // 2, _two_d(topk_ids, "topk_ids")[1]
+    per, dtypes = (2, _FP4_DTYPES) if fp4 else (1, _FP8_DTYPES)
+    _need(N % 2 == 0 and H % 128 == 0 and I % 128 == 0, "H and I (w13 has 2 I rows) must be multiples of 128")
+    if fp4:
+        s13, s2 = (E, H // 128, N), (E, I // 128, H)
+    else:
+        s13, s2 = (E, -(-H // 512), 4 * (-(-N // 512))), (E, -(-I // 512), 4 * (-(-H // 512)))
+    px = _arg(x, "x", _FP8_DTYPES, shape, dev)
+    psx = _arg(sfx, "sfx", _I32_ONLY, (-(-H // 512), 4 * (-(-T // 4))), dev)
+    p13 = _arg(w13, "w13", dtypes, (E, N, H // per), dev)
+    ps13 = _arg(sf13, "sf13", _I32_ONLY, s13, dev)
+    p2 = _arg(w2, "w2", dtypes, (E, H, I // per), dev)
+    ps2 = _arg(sf2, "sf2", _I32_ONLY, s2, dev)
+    pi = _arg(topk_ids, "topk_ids", _I32_ONLY, (T, k), dev)
+    pw = _arg(topk_weights, "topk_weights", _F32_ONLY, (T, k), dev)
+    pc = None if c is None else _arg(c, "c", _BF16_ONLY, shape, dev)
+    py = _arg(y, "y", _BF16_ONLY, shape, dev)
+    _check(name, getattr(_lib or load_library(), name)(px, psx, p13, ps13, p2, ps2, pi, pw, pc, py, T, k, E, H, I, _stream(stream)))
     return y
 
 
@@ -553,15 +573,13 @@ def dg_moe_fp8_few_tokens(x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c,
     w2[e] @ (silu(gate) * up), (gate; up) = w13[e] @ x. x [T, H] e4m3 with sfx, w13 [E, 2I, H] e4m3 (gate
     rows first) and w2 [E, H, I] e4m3 with their block scales as for the M-grouped GEMMs, topk_ids [T, k]
     int32 (-1: empty slot), topk_weights [T, k] float32, c [T, H] bf16 or None (may be y), y [T, H] bf16."""
-    return _few_tokens("dg_moe_fp8_few_tokens", 1, _fp8, lambda n, k, g: sf_shape(-(-n // 128), k, g), x, sfx, w13, sf13,
-                       w2, sf2, topk_ids, topk_weights, c, y, stream)
+    return _few_tokens("dg_moe_fp8_few_tokens", False, x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream)
 
 
 def dg_moe_fp8_fp4_few_tokens(x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream=None) -> torch.Tensor:
     """dg_moe_fp8_few_tokens with the weights in packed E2M1: w13 [E, 2I, H/2] with sf13 [E, H/128, ceil4(2I)],
     w2 [E, H, I/2] with sf2 [E, I/128, ceil4(H)]."""
-    return _few_tokens("dg_moe_fp8_fp4_few_tokens", 2, _fp4, sf_fp4_shape, x, sfx, w13, sf13, w2, sf2, topk_ids,
-                       topk_weights, c, y, stream)
+    return _few_tokens("dg_moe_fp8_fp4_few_tokens", True, x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream)
 
 
 def dg_get_mk_alignment_for_contiguous_layout() -> int:
