@@ -98,6 +98,15 @@ def test_layer(lib, T, E, k, H, I, fmt):
     assert lib.dg_get_device_status() == 0
 
 
+@pytest.mark.parametrize("T, E, k, H, I", [(32, 40, 8, 128, 640), (32, 64, 8, 256, 384), (8, 64, 8, 128, 640), (20, 50, 6, 384, 896), (7, 100, 9, 512, 640)])
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_short_rows_many_units(lib, T, E, k, H, I, fmt):
+    # a row is one to four pieces and a block has several units: the copies run past unit boundaries.
+    # No addend, so that the experts' part alone is judged.
+    p = Layer(T, E, k, H, I, fmt, seed=T + H + I, c=False)
+    check(p.run(lib), *p.oracle())
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_empty_slots_duplicates_and_bad_ids(lib, fmt):
     p = Layer(12, 5, 4, 256, 128, fmt, seed=7)
