@@ -7,6 +7,11 @@
 //
 // Every sum and statistic is FP32; s, y and dx are rounded once, where they are stored, and q is
 // rounded from the FP32 y.
+//
+// Both are bound by memory: a row is read once and written once. A team of warps owns a row; a thread
+// copies its own columns of the row after it asynchronously to shared memory while it works on one, so
+// that loads stay in flight through the row's reduction and stores, and no thread waits for another's
+// copies. Blocks are persistent: weight (and the gradient's share of dw) stay in registers over the rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,42 +30,117 @@ using dg::LaunchContext;
 
 constexpr int kVec = 8;                 // elements a thread takes at once
 constexpr int kMaxH = 16384;
-constexpr int kThreads = 256;           // threads of a forward block, at most (8 vectors each at kMaxH)
-constexpr int kGradThreads = 512;       // and of a gradient block, whose threads hold four arrays (4 vectors each)
+constexpr int kMaxV = 4;                // vectors of a row per thread
+constexpr int kMaxTeam = 512;           // threads of a row
+constexpr int kMaxSmem = 200 * 1024;    // of a block's rows in shared memory
 
-// Eight consecutive elements, BF16 or FP32, to and from FP32 (loads at L2: the row may have been
-// written by the kernel before this one in the stream, whose end this one overlaps).
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = dg::ld_cg_v4(p);
-  dg::unpack_bf16(u.x, v[0], v[1]);
-  dg::unpack_bf16(u.y, v[2], v[3]);
-  dg::unpack_bf16(u.z, v[4], v[5]);
-  dg::unpack_bf16(u.w, v[6], v[7]);
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const uint4 a = dg::ld_cg_v4(p), b = dg::ld_cg_v4(p + 4);
-  v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-  v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Two FP32 values in a register pair, and the two-lane instructions on them.
+struct Two {
+  float x, y;
+};
+__device__ __forceinline__ unsigned long long bits(Two a) {
+  unsigned long long v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a.x), "f"(a.y));
+  return v;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(dg::pack_bf16(v[0], v[1]), dg::pack_bf16(v[2], v[3]),
-                                            dg::pack_bf16(v[4], v[5]), dg::pack_bf16(v[6], v[7]));
+__device__ __forceinline__ Two two(unsigned long long v) {
+  Two a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(v));
+  return a;
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return two(d);
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return two(d);
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return two(d);
+}
+__device__ __forceinline__ Two both(float v) { return {v, v}; }
+
+// Eight consecutive elements as they are stored, and their FP32 values.
+template <class T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  static constexpr int kChunks = 1;     // of 16 bytes
+  uint4 u[1];
+  __device__ __forceinline__ Two pair(int i) const {
+    Two t;
+    dg::unpack_bf16(i == 0 ? u[0].x : i == 1 ? u[0].y : i == 2 ? u[0].z : u[0].w, t.x, t.y);
+    return t;
+  }
+};
+template <>
+struct Raw<float> {
+  static constexpr int kChunks = 2;
+  uint4 u[2];
+  __device__ __forceinline__ Two pair(int i) const {
+    const uint4& v = u[i / 2];
+    return i % 2 ? Two{__uint_as_float(v.z), __uint_as_float(v.w)} : Two{__uint_as_float(v.x), __uint_as_float(v.y)};
+  }
+};
+
+// Loads at L2: what a kernel reads may have been written by the one before it in the stream, whose end
+// this one overlaps.
+template <class T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < Raw<T>::kChunks; ++i) r.u[i] = dg::ld_cg_v4(reinterpret_cast<const uint4*>(p) + i);
+  return r;
 }
 
-// Sum over the block's threads, the same value in each. `part`: one float per warp.
-__device__ __forceinline__ float block_sum(float v, float* part) {
+// Columns: a warp owns V * 256 consecutive ones of its row (whole words of packed scales for V >= 2), of
+// which vector j of a lane is columns 256 j + 8 lane .. + 7. In shared memory chunk i of that vector lies at
+// [(j * kChunks + i) * 32 + lane] of the warp's region.
+template <class T>
+__device__ __forceinline__ void copy_piece(uint4* to, const T* from, int j, int lane) {
+#pragma unroll
+  for (int i = 0; i < Raw<T>::kChunks; ++i)
+    dg::cp_async_16(dg::smem_addr(to + (j * Raw<T>::kChunks + i) * 32 + lane), reinterpret_cast<const uint4*>(from) + i);
+}
+template <class T>
+__device__ __forceinline__ Raw<T> piece(const uint4* at, int j, int lane) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < Raw<T>::kChunks; ++i) r.u[i] = at[(j * Raw<T>::kChunks + i) * 32 + lane];
+  return r;
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const Two (&v)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(dg::pack_bf16(v[0].x, v[0].y), dg::pack_bf16(v[1].x, v[1].y),
+                                            dg::pack_bf16(v[2].x, v[2].y), dg::pack_bf16(v[3].x, v[3].y));
+}
+__device__ __forceinline__ void store8(float* p, const Two (&v)[4]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+
+// Sum over a team's threads, the same value in each; `part`: one float per warp of the block. Teams of
+// several warps meet at the barrier of their own number.
+__device__ __forceinline__ float team_sum(float v, float* part, int team, int team_index) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  const int warps = blockDim.x / 32;
-  if (warps == 1) return v;
+  if (team == 32) return v;
   if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(team_index + 1), "r"(team) : "memory");
+  const float* mine = part + team_index * (team / 32);
   float s = 0;
-  for (int i = 0; i < warps; ++i) s += part[i];
+  for (int i = 0; i < team / 32; ++i) s += mine[i];
   return s;
 }
 
@@ -74,86 +154,159 @@ struct NormArgs {
   int32_t* sf;
   R* residual_out;         // or null
   float* rstd;             // or null
-  int T, H;
+  int T, H, team, depth;   // threads and rows of shared memory of a team: the row worked on and, if they fit, the next
   size_t ldx, ldr, ldo;
   float eps, inv_h;
 };
 
-// One row per block; a thread holds V vectors of 8 columns, V * 8 FP32 values in registers.
+template <class R>
+__host__ __device__ constexpr int norm_row_chunks(int V) { return V * (1 + Raw<R>::kChunks); }
+
 template <class R, class W, int V>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs<R, W> a) {
-  __shared__ float part[kThreads / 32];
-  __shared__ uint8_t codes[kMaxH / 128];
+__global__ void __launch_bounds__(kMaxTeam) norm_kernel(const NormArgs<R, W> a) {
+  extern __shared__ uint4 ring[];
+  __shared__ float part[2][kMaxTeam / 32];
+  const int team_index = threadIdx.x / a.team, tid = threadIdx.x % a.team, teams = blockDim.x / a.team;
+  const int lane = threadIdx.x & 31, column = (tid / 32 * V * 32 + lane) * kVec;     // of vector 0; vector j is 256 j further
+  constexpr int kApart = 32 * kVec, kRow = norm_row_chunks<R>(V) * 32;
+  uint4* mine = ring + threadIdx.x / 32 * a.depth * kRow;                            // the warp's region
+  const long long t0 = static_cast<long long>(blockIdx.x) * teams + team_index, step = static_cast<long long>(gridDim.x) * teams;
+  const long long t4 = (static_cast<long long>(a.T) + 3) / 4 * 4;
+  bool in[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) in[j] = column + j * kApart < a.H;
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
-  const int t = blockIdx.x;
-  const int nvec = a.H / kVec;
-  float v[V][8];
-  float sum = 0;
+  // this thread's first column in the row to copy, then in the row worked on: advanced row by row
+  const __nv_bfloat16* xf = a.x + t0 * a.ldx + column;
+  const R* rf = a.residual ? a.residual + t0 * a.ldr + column : nullptr;
+  long long tf = t0;
+  auto fetch = [&](int stage) {
+    if (tf < a.T) {
+      uint4* xs = mine + stage * kRow;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = j * blockDim.x + threadIdx.x;
-    if (c < nvec) {
-      load8(a.x + t * a.ldx + c * kVec, v[j]);
-      if (a.residual) {
-        float r[8];
-        load8(a.residual + t * a.ldr + c * kVec, r);
+      for (int j = 0; j < V; ++j)
+        if (in[j]) {
+          copy_piece(xs, xf + j * kApart, j, lane);
+          if (rf) copy_piece(xs + V * 32, rf + j * kApart, j, lane);
+        }
+    }
+    tf += step;
+    xf += step * a.ldx;
+    if (rf) rf += step * a.ldr;
+    cp_async_commit();
+  };
+  fetch(0);
+  Raw<W> w[V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] += r[i];
+  for (int j = 0; j < V; ++j)
+    if (in[j]) w[j] = load_raw(a.weight + column + j * kApart);
+  R* so = a.residual_out ? a.residual_out + t0 * a.ldo + column : nullptr;
+  const long long first = t0 * a.H + column;
+  __nv_bfloat16* yo = a.y ? a.y + first : nullptr;
+  uint8_t* qo = a.q ? a.q + first : nullptr;
+  // a group is 16 neighbouring lanes' vector (H % 128 == 0: all 16 have one, or none has), so a warp's 2 V
+  // codes fill V / 2 words, which lane 0 writes; V = 1 is a row of at most two groups
+  const int groups = a.H / 128, word = column / 512, words = (groups + 3) / 4;
+  int32_t* sfo = a.sf + word * t4 + t0;
+  int flip = 0;
+  for (long long t = t0; t < a.T; t += step, flip ^= 1) {
+    if (a.depth == 2) {
+      fetch(flip ^ 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    const uint4* xs = mine + (a.depth == 2 ? flip * kRow : 0);
+    Two v[V][4];
+    Two sum = both(0);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (in[j]) {
+        const Raw<__nv_bfloat16> x = piece<__nv_bfloat16>(xs, j, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = x.pair(i);
+        if (a.residual) {
+          const Raw<R> r = piece<R>(xs + V * 32, j, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j][i] = v[j][i] + r.pair(i);
+        }
+        if (so) store8(so + j * kApart, v[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = fma2(v[j][i], v[j][i], sum);
       }
-      if (a.residual_out) store8(a.residual_out + t * a.ldo + c * kVec, v[j]);
+    // each thread's share of the mean: a sum over the whole row could leave FP32's range before its mean does
+    const float rstd = 1.0f / sqrtf(team_sum((sum.x + sum.y) * a.inv_h, part[flip], a.team, team_index) + a.eps);
+    if (a.rstd && tid == 0) a.rstd[t] = rstd;
+    float m[V];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(v[j][i], v[j][i], sum);
+    for (int j = 0; j < V; ++j) {
+      m[j] = 0;
+      if (in[j]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[j][i] = v[j][i] * both(rstd) * w[j].pair(i);
+          m[j] = fmaxf(m[j], fmaxf(fabsf(v[j][i].x), fabsf(v[j][i].y)));   // passes NaN over
+        }
+        if (yo) store8(yo + j * kApart, v[j]);
+      }
     }
-  }
-  // each thread's share of the mean: a sum over the whole row could leave FP32's range before its mean does
-  const float rstd = 1.0f / sqrtf(block_sum(sum * a.inv_h, part) + a.eps);
-  if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
+    if (qo) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = j * blockDim.x + threadIdx.x;
-    if (c < nvec) {
-      float w[8];
-      load8(a.weight + c * kVec, w);
+      for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * rstd * w[i];
-      if (a.y) store8(a.y + static_cast<long long>(t) * a.H + c * kVec, v[j]);
-    }
-    if (a.q) {
-      // a group is 16 neighbouring threads (H % 128 == 0: all 16 have a vector, or none has); an
-      // element that is not finite becomes the NaN code and does not count for the scale
-      float m = 0;
-      if (c < nvec) {
+        for (int j = 0; j < V; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
+      float top = m[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float f = fabsf(v[j][i]);
-          if (!(f < INFINITY)) v[j][i] = NAN;
-          m = fmaxf(m, f < INFINITY ? f : 0.0f);
+      for (int j = 1; j < V; ++j) top = fmaxf(top, m[j]);
+      if (__any_sync(0xFFFFFFFFu, top == INFINITY)) {
+        // an infinity becomes the NaN code (as a NaN does by itself) and does not count for the scale
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          m[j] = 0;
+          if (in[j])
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (!(fabsf(v[j][i].x) < INFINITY)) v[j][i].x = NAN;
+              if (!(fabsf(v[j][i].y) < INFINITY)) v[j][i].y = NAN;
+              m[j] = fmaxf(m[j], fmaxf(fabsf(v[j][i].x), fabsf(v[j][i].y)));
+            }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
         }
       }
+      uint32_t codes = 0;      // of this half of the warp: vector j's in byte j
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      if (c < nvec) {
-        const int e = dg::ue8m0_for_amax(m);
-        const float k = dg::ue8m0_inverse(e);
-        const uint32_t lo = dg::pack_e4m3(v[j][0] * k, v[j][1] * k, v[j][2] * k, v[j][3] * k);
-        const uint32_t hi = dg::pack_e4m3(v[j][4] * k, v[j][5] * k, v[j][6] * k, v[j][7] * k);
-        *reinterpret_cast<uint2*>(a.q + static_cast<long long>(t) * a.H + c * kVec) = make_uint2(lo, hi);
-        if ((c & 15) == 0) codes[c / 16] = static_cast<uint8_t>(e);
+      for (int j = 0; j < V; ++j)
+        if (in[j]) {
+          const int e = dg::ue8m0_for_amax(m[j]);
+          const Two k = both(dg::ue8m0_inverse(e));
+          Two z[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = v[j][i] * k;
+          *reinterpret_cast<uint2*>(qo + j * kApart) =
+              make_uint2(dg::pack_e4m3(z[0].x, z[0].y, z[1].x, z[1].y), dg::pack_e4m3(z[2].x, z[2].y, z[3].x, z[3].y));
+          codes |= static_cast<uint32_t>(m[j] == 0 ? 127 : e) << (8 * j);
+        }
+      const uint32_t upper = __shfl_down_sync(0xFFFFFFFFu, codes, 16);
+      if (lane == 0) {
+        // bytes of the groups that are there, and 0 after them
+        if (word < words) sfo[0] = static_cast<int32_t>(__byte_perm(codes, upper, 0x5140));
+        if (V > 2 && word + 1 < words) sfo[t4] = static_cast<int32_t>(__byte_perm(codes, upper, 0x7362));
       }
+      if (t == a.T - 1) {
+        // and the words of the padding rows
+        const int pad = static_cast<int>(t4 - a.T);
+        for (int i = tid; i < words * pad; i += a.team) a.sf[i / pad * t4 + a.T + i % pad] = 0;
+      }
+      qo += step * a.H;
+      sfo += step;
     }
+    if (so) so += step * a.ldo;
+    if (yo) yo += step * a.H;
+    if (a.depth == 1) fetch(0);
   }
-  if (!a.q) return;
-  __syncthreads();
-  const int groups = a.H / 128, words = (groups + 3) / 4;
-  const long long t4 = (static_cast<long long>(a.T) + 3) / 4 * 4;
-  for (int i = threadIdx.x; i < words; i += blockDim.x) {
-    uint32_t word = 0;
-    for (int b = 0; b < 4 && 4 * i + b < groups; ++b) word |= static_cast<uint32_t>(codes[4 * i + b]) << (8 * b);
-    a.sf[i * t4 + t] = static_cast<int32_t>(word);
-    if (t == a.T - 1)
-      for (long long p = a.T; p < t4; ++p) a.sf[i * t4 + p] = 0;
-  }
+  cp_async_wait<0>();
 }
 
 template <class R, class W>
@@ -166,116 +319,193 @@ struct NormGradArgs {
   __nv_bfloat16* dx;       // or null
   R* dresidual;            // or null
   float* partial;          // [gridDim.x, H]
-  int T, H;
+  int T, H, team, depth;
+  float inv_h;
 };
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ...: a thread keeps its columns' share of dw in registers
-// over all of them, so dw costs one row of partial sums per block.
+template <class R>
+__host__ __device__ constexpr int grad_row_chunks(int V) { return V * (1 + 2 * Raw<R>::kChunks); }
+
+// A thread keeps its columns' share of dw in registers over all of its team's rows, so dw costs one row
+// of partial sums per block. The row's values are read from shared memory twice, before and after the
+// reduction, rather than held.
 template <class R, class W, int V>
-__global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const NormGradArgs<R, W> a) {
-  __shared__ float part[2][kGradThreads / 32];
+__global__ void __launch_bounds__(kMaxTeam) norm_grad_kernel(const NormGradArgs<R, W> a) {
+  extern __shared__ uint4 ring[];
+  __shared__ float part[2][kMaxTeam / 32];
+  const int team_index = threadIdx.x / a.team, tid = threadIdx.x % a.team, teams = blockDim.x / a.team;
+  const int lane = threadIdx.x & 31, column = (tid / 32 * V * 32 + lane) * kVec;     // as in the forward kernel
+  constexpr int kApart = 32 * kVec, kRow = grad_row_chunks<R>(V) * 32;
+  uint4* mine = ring + threadIdx.x / 32 * a.depth * kRow;
+  const long long t0 = static_cast<long long>(blockIdx.x) * teams + team_index, step = static_cast<long long>(gridDim.x) * teams;
+  bool in[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) in[j] = column + j * kApart < a.H;
+  constexpr int kS = V * 32, kDs = V * (1 + Raw<R>::kChunks) * 32;                   // where s and ds begin in a row's region
   dg::grid_dependency_wait();
-  const int nvec = a.H / kVec;
-  constexpr bool kKeep = V <= 2;   // four vectors do not fit the registers: weight and s are then read again, from L2
-  float w[kKeep ? V : 1][8], dw[V][8];
+  long long tf = t0, at_f = t0 * a.H + column;      // the row to copy, and this thread's first element of it
+  auto fetch = [&](int stage) {
+    if (tf < a.T) {
+      uint4* to = mine + stage * kRow;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (in[j]) {
+          copy_piece(to, a.dy + at_f + j * kApart, j, lane);
+          copy_piece(to + kS, a.s + at_f + j * kApart, j, lane);
+          if (a.ds) copy_piece(to + kDs, a.ds + at_f + j * kApart, j, lane);
+        }
+    }
+    tf += step;
+    at_f += step * a.H;
+    cp_async_commit();
+  };
+  fetch(0);
+  Raw<W> w[V];
+  Two dw[V][4];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int c = j * blockDim.x + threadIdx.x;
+    if (in[j]) w[j] = load_raw(a.weight + column + j * kApart);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[j][i] = 0;
-    if (kKeep && c < nvec) load8(a.weight + c * kVec, w[kKeep ? j : 0]);
+    for (int i = 0; i < 4; ++i) dw[j][i] = both(0);
   }
+  long long at_o = t0 * a.H + column;
   int flip = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, flip ^= 1) {
-    const long long row = static_cast<long long>(t) * a.H;
+  for (long long t = t0; t < a.T; t += step, flip ^= 1) {
     const float rstd = __ldcg(a.rstd + t);
-    float dy[V][8], xhat[kKeep ? V : 1][8];
-    float sum = 0;
+    if (a.depth == 2) {
+      fetch(flip ^ 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    const uint4* at = mine + (a.depth == 2 ? flip * kRow : 0);
+    Two sum = both(0);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = j * blockDim.x + threadIdx.x;
-      if (c < nvec) {
-        load8(a.dy + row + c * kVec, dy[j]);
-        float (&xh)[8] = xhat[kKeep ? j : 0];
-        load8(a.s + row + c * kVec, xh);
-        if (!kKeep) load8(a.weight + c * kVec, w[0]);
+    for (int j = 0; j < V; ++j)
+      if (in[j]) {
+        const Raw<__nv_bfloat16> dy = piece<__nv_bfloat16>(at, j, lane);
+        const Raw<R> s = piece<R>(at + kS, j, lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xh[i] *= rstd;
-          dw[j][i] = fmaf(dy[j][i], xh[i], dw[j][i]);
-          dy[j][i] *= w[kKeep ? j : 0][i];
-          sum = fmaf(dy[j][i], xh[i], sum);
+        for (int i = 0; i < 4; ++i) {
+          const Two p = dy.pair(i) * (s.pair(i) * both(rstd));
+          dw[j][i] = dw[j][i] + p;
+          sum = fma2(p, w[j].pair(i), sum);
         }
       }
-    }
-    const float mean = block_sum(sum, part[flip]) / static_cast<float>(a.H);
+    const float mean = team_sum((sum.x + sum.y) * a.inv_h, part[flip], a.team, team_index);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int c = j * blockDim.x + threadIdx.x;
-      if (c < nvec) {
-        float d[8];
+      if (in[j]) {
+        const Raw<__nv_bfloat16> dy = piece<__nv_bfloat16>(at, j, lane);
+        const Raw<R> s = piece<R>(at + kS, j, lane);
+        Two d[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = 0;
-        if (a.ds) load8(a.ds + row + c * kVec, d);
-        float (&xh)[8] = xhat[kKeep ? j : 0];
-        if (!kKeep) load8(a.s + row + c * kVec, xh);
+        for (int i = 0; i < 4; ++i) d[i] = both(0);
+        if (a.ds) {
+          const Raw<R> ds = piece<R>(at + kDs, j, lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = fmaf(rstd, fmaf(-(kKeep ? xh[i] : xh[i] * rstd), mean, dy[j][i]), d[i]);
-        if (a.dx) store8(a.dx + row + c * kVec, d);
-        if (a.dresidual) store8(a.dresidual + row + c * kVec, d);
+          for (int i = 0; i < 4; ++i) d[i] = ds.pair(i);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          d[i] = fma2(both(rstd), fma2(s.pair(i) * both(rstd), both(-mean), dy.pair(i) * w[j].pair(i)), d[i]);
+        if (a.dx) store8(a.dx + at_o + j * kApart, d);
+        if (a.dresidual) store8(a.dresidual + at_o + j * kApart, d);
       }
     }
+    at_o += step * a.H;
+    if (a.depth == 1) fetch(0);
   }
+  cp_async_wait<0>();
   dg::grid_launch_dependents();
+  // the teams' shares, one after another, through shared memory
+  float* total = reinterpret_cast<float*>(ring);
+  for (int k = 0; k < teams; ++k) {
+    if (teams > 1) __syncthreads();
+    if (team_index != k) continue;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = j * blockDim.x + threadIdx.x;
-    if (c < nvec) store8(a.partial + static_cast<long long>(blockIdx.x) * a.H + c * kVec, dw[j]);
+    for (int j = 0; j < V; ++j) {
+      if (!in[j]) continue;
+      const int c = column + j * kApart;
+      if (k > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[j][i] = dw[j][i] + Two{total[c + 2 * i], total[c + 2 * i + 1]};
+      }
+      store8(k == teams - 1 ? a.partial + static_cast<long long>(blockIdx.x) * a.H + c : total + c, dw[j]);
+    }
   }
 }
 
-// dw[c] = sum over the blocks' partial sums, in their order: 32 columns per block of 8 warps, each
-// warp every eighth row of them.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, float* dw, int rows, int H) {
-  __shared__ float part[8][33];
+// dw[c] = sum over the blocks' partial sums, in a fixed order: 32 columns per block, each of its 32 warps
+// every 32nd row of them.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* partial, float* dw, int rows, int H) {
+  __shared__ float part[32][33];
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int c = blockIdx.x * 32 + lane;
   float sum = 0;
   if (c < H)
-    for (int r = warp; r < rows; r += 8) sum += __ldcg(partial + static_cast<long long>(r) * H + c);
+#pragma unroll 4
+    for (int r = warp; r < rows; r += 32) sum += __ldcg(partial + static_cast<long long>(r) * H + c);
   part[warp][lane] = sum;
   __syncthreads();
-  if (warp == 0 && c < H) {
-    float v = 0;
+  sum = part[lane][warp];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += part[i][lane];
-    dw[c] = v;
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < static_cast<unsigned>(H)) dw[blockIdx.x * 32 + warp] = sum;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Threads of a row and vectors per thread: the fewest vectors that fit a block, then the warps that they take.
+// Vectors per thread, threads of a row, and rows that a block works on at a time. Up to 32 threads'
+// vectors a row is one warp's; longer ones are spread over as few warps as four vectors each allow, and
+// blocks of short rows hold several teams to have 256 threads.
 struct Shape {
-  int v, threads;
+  int v, team, teams;
+  int threads() const { return team * teams; }
 };
-Shape row_shape(int H, int max_threads) {
+Shape row_shape(int H) {
   const int nvec = H / kVec;
-  int v = 1;
-  while (v * max_threads < nvec) v *= 2;
-  return {v, ((nvec + v - 1) / v + 31) / 32 * 32};
+  const int v = nvec <= 32 ? 1 : nvec <= 64 ? 2 : kMaxV;
+  const int team = (nvec + 32 * v - 1) / (32 * v) * 32;
+  return {v, team, std::max(1, 256 / team)};
 }
 
-template <int kMaxV, class F>
+template <class F>
 dg_status with_v(int v, F f) {
   switch (v) {
     case 1: return f(std::integral_constant<int, 1>());
     case 2: return f(std::integral_constant<int, 2>());
-    case 4: return f(std::integral_constant<int, 4>());
     default: return f(std::integral_constant<int, kMaxV>());
   }
+}
+
+// Blocks for T rows: those that are resident together, at most one per team of rows. `row`: bytes of a
+// block's rows in shared memory, two of which per team are taken if they fit.
+struct Resident {
+  unsigned blocks = 0;
+  size_t smem = 0;
+  int depth = 0;
+};
+template <auto kKernel>
+dg_status resident_blocks(const Shape& shape, size_t row, int T, int sms, Resident* out) {
+  static thread_local struct { int dev = -1, threads = 0; size_t smem = 0; int per_sm = 0; } last;
+  out->depth = 2 * row <= kMaxSmem ? 2 : 1;
+  out->smem = out->depth * row;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && last.dev != dev) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess && (last.dev != dev || last.threads != shape.threads() || last.smem != out->smem)) {
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, shape.threads(), out->smem);
+    if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess) last = {dev, shape.threads(), out->smem, n};
+  }
+  if (e != cudaSuccess) return dg::record_cuda_error(e);
+  const long long wanted = (static_cast<long long>(T) + shape.teams - 1) / shape.teams;
+  out->blocks = static_cast<unsigned>(std::min(wanted, static_cast<long long>(last.per_sm) * sms));
+  return DG_OK;
 }
 
 // Calls f with null pointers of the residual stream's type and the weight's.
@@ -313,15 +543,18 @@ dg_status dg_add_rms_norm(const void* x, const void* residual, const void* weigh
     return DG_ERR_MISALIGNED;
   LaunchContext ctx;
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
-  const Shape shape = row_shape(H, kThreads);
+  const Shape shape = row_shape(H);
   return with_types(residual_type, weight_type, [&](auto* r, auto* w) {
     using R = std::remove_const_t<std::remove_pointer_t<decltype(r)>>;
     using W = std::remove_const_t<std::remove_pointer_t<decltype(w)>>;
-    const NormArgs<R, W> a{static_cast<const __nv_bfloat16*>(x), static_cast<const R*>(residual),
-                           static_cast<const W*>(weight), static_cast<__nv_bfloat16*>(y), static_cast<uint8_t*>(q), sf,
-                           static_cast<R*>(residual_out), rstd, T, H, ldx, ldr, ldo, eps, 1.0f / static_cast<float>(H)};
-    return with_v<8>(shape.v, [&](auto v) {
-      return dg::launch(norm_kernel<R, W, decltype(v)::value>, static_cast<unsigned>(T), static_cast<unsigned>(shape.threads), 0, stream, ctx.pdl, a);
+    return with_v(shape.v, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      Resident at;
+      if (dg_status s = resident_blocks<norm_kernel<R, W, V>>(shape, sizeof(uint4) * norm_row_chunks<R>(V) * shape.threads(), T, ctx.sms, &at); s != DG_OK) return s;
+      const NormArgs<R, W> a{static_cast<const __nv_bfloat16*>(x), static_cast<const R*>(residual), static_cast<const W*>(weight),
+                             static_cast<__nv_bfloat16*>(y), static_cast<uint8_t*>(q), sf,
+                             static_cast<R*>(residual_out), rstd, T, H, shape.team, at.depth, ldx, ldr, ldo, eps, 1.0f / static_cast<float>(H)};
+      return dg::launch(norm_kernel<R, W, V>, at.blocks, static_cast<unsigned>(shape.threads()), at.smem, stream, ctx.pdl, a);
     });
   });
 }
@@ -339,24 +572,25 @@ dg_status dg_add_rms_norm_backward(const void* dy, const void* s, const void* we
   if (dg_status e = dg::launch_context(&ctx); e != DG_OK) return e;
   const unsigned dw_blocks = static_cast<unsigned>((H + 31) / 32);
   if (T == 0)   // the sum over no rows
-    return dg::launch(norm_dw_kernel, dw_blocks, 256, 0, stream, ctx.pdl, static_cast<const float*>(nullptr), dw, 0, H);
-  const int blocks = std::min(T, 2 * ctx.sms);
-  dg::StreamWorkspace ws;
-  void* partial = nullptr;
-  if (dg_status e = ws.acquire(stream, static_cast<size_t>(blocks) * H * sizeof(float), &partial); e != DG_OK) return e;
-  const Shape shape = row_shape(H, kGradThreads);
-  const dg_status e = with_types(residual_type, weight_type, [&](auto* r, auto* w) {
+    return dg::launch(norm_dw_kernel, dw_blocks, 1024, 0, stream, ctx.pdl, static_cast<const float*>(nullptr), dw, 0, H);
+  const Shape shape = row_shape(H);
+  return with_types(residual_type, weight_type, [&](auto* r, auto* w) {
     using R = std::remove_const_t<std::remove_pointer_t<decltype(r)>>;
     using W = std::remove_const_t<std::remove_pointer_t<decltype(w)>>;
-    const NormGradArgs<R, W> a{static_cast<const __nv_bfloat16*>(dy), static_cast<const R*>(s), static_cast<const W*>(weight),
-                               rstd, static_cast<const R*>(ds), static_cast<__nv_bfloat16*>(dx), static_cast<R*>(dresidual),
-                               static_cast<float*>(partial), T, H};
-    return with_v<4>(shape.v, [&](auto v) {
-      return dg::launch(norm_grad_kernel<R, W, decltype(v)::value>, static_cast<unsigned>(blocks), static_cast<unsigned>(shape.threads), 0, stream, ctx.pdl, a);
+    return with_v(shape.v, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      Resident at;
+      if (dg_status e = resident_blocks<norm_grad_kernel<R, W, V>>(shape, sizeof(uint4) * grad_row_chunks<R>(V) * shape.threads(), T, ctx.sms, &at); e != DG_OK) return e;
+      dg::StreamWorkspace ws;
+      void* partial = nullptr;
+      if (dg_status e = ws.acquire(stream, static_cast<size_t>(at.blocks) * H * sizeof(float), &partial); e != DG_OK) return e;
+      const NormGradArgs<R, W> a{static_cast<const __nv_bfloat16*>(dy), static_cast<const R*>(s), static_cast<const W*>(weight), rstd,
+                                 static_cast<const R*>(ds), static_cast<__nv_bfloat16*>(dx), static_cast<R*>(dresidual),
+                                 static_cast<float*>(partial), T, H, shape.team, at.depth, 1.0f / static_cast<float>(H)};
+      if (dg_status e = dg::launch(norm_grad_kernel<R, W, V>, at.blocks, static_cast<unsigned>(shape.threads()), at.smem, stream, ctx.pdl, a); e != DG_OK) return e;
+      return dg::launch(norm_dw_kernel, dw_blocks, 1024, 0, stream, ctx.pdl, static_cast<const float*>(partial), dw, static_cast<int>(at.blocks), H);
     });
   });
-  if (e != DG_OK) return e;
-  return dg::launch(norm_dw_kernel, dw_blocks, 256, 0, stream, ctx.pdl, static_cast<const float*>(partial), dw, blocks, H);
 }
 
 }  // extern "C"

@@ -16,18 +16,17 @@ __device__ __forceinline__ float ue8m0_value(uint32_t e) {
   return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
 }
 
-// Least code e in [1, 254] with amax <= 448 * 2^(e - 127); 127 (scale 1) for a group of zeros.
-// 448 = 1.75 * 2^8: the mantissa of amax decides whether its own exponent less 8 is enough.
+// Least code e in [1, 254] with amax <= 448 * 2^(e - 127); for 0 the least of all, 1.
+// 448 = 1.75 * 2^8: the exponent of amax less 8, one more if the mantissa is above 0.75 = 0x600000 / 2^23,
+// which is when adding 0x1FFFFF carries into the exponent.
 __device__ __forceinline__ int ue8m0_for_amax(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  if (b == 0) return 127;
-  const int e = static_cast<int>(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return e < 1 ? 1 : e > 254 ? 254 : e;
+  const int e = static_cast<int>((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 8;
+  return min(max(e, 1), 254);
 }
 
-// 2^(127 - e) for a code e in [1, 254]: what brings a group to E4M3's range.
+// 2^(127 - e) for a code e in [1, 254]: what brings a group to E4M3's range (2^-127 is subnormal).
 __device__ __forceinline__ float ue8m0_inverse(int e) {
-  return __uint_as_float(e == 254 ? 0x00400000u : static_cast<uint32_t>(254 - e) << 23);
+  return __uint_as_float(max(static_cast<uint32_t>(254 - e) << 23, 0x00400000u));
 }
 
 // Four floats -> four E4M3 bytes, round to nearest even; |v| <= 448 or NaN.
