@@ -7,8 +7,14 @@
 // An expert whose logit is -inf or NaN is masked: never chosen, and no part of the softmax. Slots for
 // which no expert is left get id -1 and weight 0.
 //
-// One warp per row. The experts' values stay in registers, expert 32 j + lane in register j of a
-// lane; a choice is two warp-wide reductions, the largest key and the lowest index that has it.
+// One warp per row, its logits in registers. A choice of k among all E by
+// k rounds over every register costs about 50 instructions a round, more than reading the row allows; so
+// most of the row is sorted out first. The k-th largest of the 32 lanes' own maxima is a lower bound of
+// the k-th largest logit; what reaches it (k and a few) is gathered, one per lane, and each candidate
+// counts those before it. Rows with more than 32 candidates (large k, many equal logits) take the rounds
+// over all. 65536 rows of 256 FP32 logits, k = 8: 30 us, 2.3 TB/s, bound by issued instructions (500 a row,
+// 85 % of the issue slots); the rounds alone took 70 us. Blocks that loop over rows with the next row's
+// loads in flight were slower (34 us: the registers cost more warps than the loads cost time).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,14 +42,61 @@ __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) {
 __device__ __forceinline__ void store_grad(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_grad(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Unsigned keys in the order of the values (-0 as +0); 0 for a masked expert (-inf, NaN).
-__device__ __forceinline__ uint32_t order_key(float x) {
-  if (!(x > -INFINITY)) return 0;
-  const uint32_t b = __float_as_uint(x + 0.0f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+// A lane's logits of a row: kVec consecutive ones (1, or 16 bytes where rows are aligned to that) of every
+// 32 * kVec; -infinity, as a masked expert's, past the row's end.
+template <class L, int J, int kVec>
+struct Lane {
+  static constexpr int kCount = J * kVec;
+  static __device__ __forceinline__ int index(int lane, int i) { return (i / kVec * 32 + lane) * kVec + i % kVec; }
+  static __device__ __forceinline__ void load(const L* row, int lane, int E, float (&v)[kCount]) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int at = index(lane, j * kVec);
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) v[j * kVec + c] = -INFINITY;
+      if (at >= E) continue;
+      if constexpr (kVec == 1) {
+        v[j] = load_logit(row + at);
+      } else {
+        const uint4 u = __ldcg(reinterpret_cast<const uint4*>(row + at));
+        if constexpr (kVec == 4) {
+          v[j * 4] = __uint_as_float(u.x), v[j * 4 + 1] = __uint_as_float(u.y), v[j * 4 + 2] = __uint_as_float(u.z), v[j * 4 + 3] = __uint_as_float(u.w);
+        } else {
+          dg::unpack_bf16(u.x, v[j * 8], v[j * 8 + 1]);
+          dg::unpack_bf16(u.y, v[j * 8 + 2], v[j * 8 + 3]);
+          dg::unpack_bf16(u.z, v[j * 8 + 4], v[j * 8 + 5]);
+          dg::unpack_bf16(u.w, v[j * 8 + 6], v[j * 8 + 7]);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(L* row, int lane, int E, const float (&v)[kCount]) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int at = index(lane, j * kVec);
+      if (at >= E) continue;
+      if constexpr (kVec == 1)
+        store_grad(row + at, v[j]);
+      else if constexpr (kVec == 4)
+        *reinterpret_cast<float4*>(row + at) = make_float4(v[j * 4], v[j * 4 + 1], v[j * 4 + 2], v[j * 4 + 3]);
+      else
+        *reinterpret_cast<uint4*>(row + at) = make_uint4(dg::pack_bf16(v[j * 8], v[j * 8 + 1]), dg::pack_bf16(v[j * 8 + 2], v[j * 8 + 3]),
+                                                         dg::pack_bf16(v[j * 8 + 4], v[j * 8 + 5]), dg::pack_bf16(v[j * 8 + 6], v[j * 8 + 7]));
+    }
+  }
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+template <int N>
+__device__ __forceinline__ float max_of(const float (&v)[N]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+  return m;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -65,56 +118,99 @@ struct RouteArgs {
   float scale;
 };
 
-template <class L, int P>
+template <class L, int J, int kVec>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs<L> a) {
+  using At = Lane<L, J, kVec>;
+  constexpr int P = At::kCount;
+  __shared__ float2 gathered[kWarps][32], chosen[kWarps][32];
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
   const int lane = threadIdx.x & 31;
+  // (logit, expert) of the candidates, and of the chosen by slot
+  float2* const candidates = gathered[threadIdx.x / 32];
+  float2* const slots = chosen[threadIdx.x / 32];
   const long long t = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
   if (t >= a.T) return;
-  const L* row = a.logits + t * a.ld;
-  uint32_t key[P];
+  float v[P];
+  At::load(a.logits + t * a.ld, lane, a.E, v);
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
-    const int e = 32 * j + lane;
-    key[j] = e < a.E ? order_key(load_logit(row + e)) : 0;
-  }
+  for (int i = 0; i < P; ++i) v[i] = fmaxf(v[i], -INFINITY);        // NaN is masked as -inf is
+  const float mine = max_of(v), top = warp_max(mine);
   float total = 0;   // of the softmax over every expert, relative to the largest
-  uint32_t top = 0;
-  if (!a.sigmoid && !a.renorm) {
+  if (!a.sigmoid && !a.renorm && top > -INFINITY) {
 #pragma unroll
-    for (int j = 0; j < P; ++j) top = max(top, key[j]);
-    top = __reduce_max_sync(kAll, top);
-    const float largest = key_value(top);
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-      if (key[j]) total += expf(key_value(key[j]) - largest);
+    for (int i = 0; i < P; ++i) total += expf(v[i] - top);
     total = warp_sum(total);
   }
-  int my_id = -1;
-  uint32_t my_key = 0;
-  for (int i = 0; i < a.k; ++i) {
-    uint32_t best = 0;
-    int at = 0;
+  int found = 0, n = 32;
+  float2 cand = make_float2(v[0], __int_as_float(lane));
+  if (P == 1) {
+    candidates[lane] = cand;
+    __syncwarp();
+  } else {
+    float left = mine, bound = top;
+    for (int i = 1; i < a.k; ++i) {
+      left = left == bound ? -INFINITY : left;
+      bound = warp_max(left);
+    }
+    bound = fmaxf(bound, -3.402823466e38f);                       // any logit that is not masked
+    int count = 0;
 #pragma unroll
-    for (int j = P - 1; j >= 0; --j)
-      if (key[j] >= best) best = key[j], at = j;      // the lowest of equal ones
-    const uint32_t m = __reduce_max_sync(kAll, best);
-    if (m == 0) break;
-    const int e = static_cast<int>(__reduce_min_sync(kAll, best == m ? static_cast<uint32_t>(32 * at + lane) : kAll));
-    if (lane == i) my_id = e, my_key = m;
+    for (int i = 0; i < P; ++i) count += v[i] >= bound;
+    int at = count;
 #pragma unroll
-    for (int j = 0; j < P; ++j)
-      if (32 * j + lane == e) key[j] = 0;
-    if (i == 0) top = m;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kAll, at, o);
+      if (lane >= o) at += x;
+    }
+    n = __shfl_sync(kAll, at, 31);
+    if (n <= 32) {
+      at -= count;
+      if (count > 0) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (v[i] >= bound) candidates[at++] = make_float2(v[i], __int_as_float(At::index(lane, i)));
+      }
+      __syncwarp();
+      if (lane < n) cand = candidates[lane];
+    }
   }
+  if (n <= 32) {
+    // how many candidates come before this lane's: larger ones, and equal ones of a lower index
+    const int id = __float_as_int(cand.y);
+    const bool live = lane < n && cand.x > -INFINITY;
+    int before = 0;
+    for (int i = 0; i < n; ++i) {
+      const float2 c = candidates[i];
+      before += c.x > cand.x || (c.x == cand.x && __float_as_int(c.y) < id);
+    }
+    found = min(a.k, __popc(__ballot_sync(kAll, live)));
+    if (live && before < a.k) slots[before] = cand;
+  } else {
+    for (; found < a.k; ++found) {
+      const float m = warp_max(max_of(v));
+      if (!(m > -INFINITY)) break;
+      uint32_t id = kAll;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (v[i] == m) id = min(id, static_cast<uint32_t>(At::index(lane, i)));
+      id = __reduce_min_sync(kAll, id);
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (At::index(lane, i) == static_cast<int>(id)) v[i] = -INFINITY;
+      if (lane == 0) slots[found] = make_float2(m, __int_as_float(static_cast<int>(id)));
+    }
+  }
+  __syncwarp();
+  const bool have = lane < found;
+  const float2 slot = slots[lane];
   float w = 0;
-  if (my_id >= 0) w = a.sigmoid ? sigmoid(key_value(my_key)) : expf(key_value(my_key) - key_value(top));
+  if (have) w = a.sigmoid ? sigmoid(slot.x) : expf(slot.x - top);
   if (a.renorm) total = warp_sum(w);
   if (a.renorm || !a.sigmoid) w = total > 0 ? w / total : total == 0 ? 0.0f : NAN;
   if (lane < a.k) {
-    a.ids[t * a.k + lane] = my_id;
-    a.weights[t * a.k + lane] = my_id >= 0 ? a.scale * w : 0.0f;
+    a.ids[t * a.k + lane] = have ? __float_as_int(slot.y) : -1;
+    a.weights[t * a.k + lane] = have ? a.scale * w : 0.0f;
   }
 }
 
@@ -136,86 +232,92 @@ struct RouteGradArgs {
 //   softmax               : dl_i = p_i ([i chosen] d_i - sum p d)  for every expert i
 //   sigmoid, renormalised : dl_j = q_j (d_j - sum q d) (1 - p_j)
 //   sigmoid               : dl_j = d_j p_j (1 - p_j)
-template <class L, int P>
+//
+// Every lane writes its share of the row; the lanes that have a chosen slot then write over it.
+template <class L, int J, int kVec>
 __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const RouteGradArgs<L> a) {
-  __shared__ float row_out[kWarps][32 * P];
+  using At = Lane<L, J, kVec>;
+  constexpr int P = At::kCount;
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const long long t = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
   if (t >= a.T) return;
   const L* row = a.logits + t * a.ld;
-  float* out = row_out[threadIdx.x / 32];
+  float all[P];
+  const bool dense = !a.sigmoid && !a.renorm;
+  if (dense) At::load(row, lane, a.E, all);           // in flight while the ids are followed
   int id = lane < a.k ? __ldcg(a.ids + t * a.k + lane) : -1;
   if (id < -1 || id >= a.E) {
     atomicOr(a.status, dg::kBadIndexBit);
     id = -1;
   }
+  const float g = id >= 0 ? __ldcg(a.dweights + t * a.k + lane) : 0.0f;
   const float x = id >= 0 ? load_logit(row + id) : -INFINITY;
-  const bool chosen = id >= 0 && x > -INFINITY;
-  const float d = chosen ? a.scale * __ldcg(a.dweights + t * a.k + lane) : 0.0f;
+  const bool chosen = x > -INFINITY;
+  const float d = chosen ? a.scale * g : 0.0f;
   float dl;
-  float all[P];
+  if (dense) {
 #pragma unroll
-  for (int j = 0; j < P; ++j) all[j] = 0;
-  if (a.sigmoid) {
-    const float p = chosen ? sigmoid(x) : 0.0f;
-    float q = p, lean = d;
-    if (a.renorm) {
-      const float total = warp_sum(p);
-      q = total > 0 ? p / total : 0.0f;
-      lean = d - warp_sum(q * d);
-    }
-    dl = q * lean * (1.0f / (1.0f + expf(x)));      // 1 - p, without the cancellation
-  } else if (a.renorm) {
-    const uint32_t top = __reduce_max_sync(kAll, chosen ? order_key(x) : 0);
-    const float p = chosen ? expf(x - key_value(top)) : 0.0f;
-    const float total = warp_sum(p);
-    const float q = total > 0 ? p / total : 0.0f;
-    dl = q * (d - warp_sum(q * d));
-  } else {
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const int e = 32 * j + lane;
-      all[j] = e < a.E ? load_logit(row + e) : -INFINITY;
-      top = max(top, order_key(all[j]));
-    }
-    top = __reduce_max_sync(kAll, top);
-    const float largest = key_value(top);
+    for (int i = 0; i < P; ++i) all[i] = fmaxf(all[i], -INFINITY);
+    const float top = warp_max(max_of(all)), base = top > -INFINITY ? top : 0.0f;
     float total = 0;
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      all[j] = order_key(all[j]) ? expf(all[j] - largest) : 0.0f;
-      total += all[j];
+    for (int i = 0; i < P; ++i) {
+      all[i] = expf(all[i] - base);
+      total += all[i];
     }
     total = warp_sum(total);
-    const float inv = total > 0 ? 1.0f / total : 0.0f;
-    const float p = chosen ? expf(x - largest) * inv : 0.0f;
+    const float inv = total > 0 ? 1.0f / total : total == 0 ? 0.0f : NAN;
+    const float p = chosen ? expf(x - base) * inv : 0.0f;
     const float inner = warp_sum(p * d);
     dl = p * (d - inner);
 #pragma unroll
-    for (int j = 0; j < P; ++j) all[j] *= -inv * inner;
+    for (int i = 0; i < P; ++i) all[i] *= -inv * inner;
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) all[i] = 0;
+    const float top = warp_max(chosen ? x : -INFINITY);
+    const float p = !chosen ? 0.0f : a.sigmoid ? sigmoid(x) : expf(x - top);
+    float q = p, lean = d;
+    if (a.renorm) {
+      const float total = warp_sum(p);
+      q = total > 0 ? p / total : total == 0 ? 0.0f : NAN;
+      lean = d - warp_sum(q * d);
+    }
+    dl = q * lean;
+    if (a.sigmoid) dl *= 1.0f / (1.0f + expf(x));      // 1 - p, without the cancellation
   }
-#pragma unroll
-  for (int j = 0; j < P; ++j) out[32 * j + lane] = all[j];
-  __syncwarp();
-  if (chosen) out[id] = dl;
-  __syncwarp();
   L* to = a.dlogits + t * a.E;
-#pragma unroll
-  for (int j = 0; j < P; ++j)
-    if (32 * j + lane < a.E) store_grad(to + 32 * j + lane, out[32 * j + lane]);
+  At::store(to, lane, a.E, all);
+  __syncwarp();
+  if (chosen) store_grad(to + id, dl);
 }
 
-template <class F>
-dg_status with_p(int E, F f) {
-  if (E <= 32) return f(std::integral_constant<int, 1>());
-  if (E <= 64) return f(std::integral_constant<int, 2>());
-  if (E <= 128) return f(std::integral_constant<int, 4>());
-  if (E <= 256) return f(std::integral_constant<int, 8>());
-  if (E <= 512) return f(std::integral_constant<int, 16>());
-  return f(std::integral_constant<int, 32>());
+// Calls f with a lane's vectors and their length. `aligned`: every row is a whole number of 16-byte pieces.
+template <class L, class F>
+dg_status with_shape(int E, bool aligned, F f) {
+  constexpr int kWide = 16 / sizeof(L);
+  using std::integral_constant;
+  if (aligned) {
+    const integral_constant<int, kWide> vec;
+    if (E <= 32 * kWide) return f(integral_constant<int, 1>(), vec);
+    if (E <= 64 * kWide) return f(integral_constant<int, 2>(), vec);
+    if (E <= 128 * kWide) return f(integral_constant<int, 4>(), vec);
+    if constexpr (kWide == 4) return f(integral_constant<int, 8>(), vec);
+  }
+  const integral_constant<int, 1> one;
+  if (E <= 32) return f(integral_constant<int, 1>(), one);
+  if (E <= 64) return f(integral_constant<int, 2>(), one);
+  if (E <= 128) return f(integral_constant<int, 4>(), one);
+  if (E <= 256) return f(integral_constant<int, 8>(), one);
+  if (E <= 512) return f(integral_constant<int, 16>(), one);
+  return f(integral_constant<int, 32>(), one);
+}
+template <class L>
+bool whole_pieces(const void* p, size_t ld, int E) {
+  constexpr size_t kWide = 16 / sizeof(L);
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % kWide == 0 && E % kWide == 0;
 }
 
 dg_status check(const void* logits, const void* ids, const void* weights, const dg_route_desc* desc) {
@@ -250,8 +352,8 @@ dg_status dg_moe_route(const void* logits, int32_t* topk_ids, float* topk_weight
     using L = std::remove_pointer_t<decltype(type)>;
     const RouteArgs<L> a{static_cast<const L*>(logits), topk_ids, topk_weights, desc->T, desc->E, desc->topk, desc->ld,
                          desc->scoring == DG_ROUTE_SIGMOID, desc->renormalize, desc->scale};
-    return with_p(desc->E, [&](auto p) {
-      return dg::launch(route_kernel<L, decltype(p)::value>, row_blocks(desc->T), kWarps * 32, 0, stream, ctx.pdl, a);
+    return with_shape<L>(desc->E, whole_pieces<L>(logits, desc->ld, desc->E), [&](auto j, auto vec) {
+      return dg::launch(route_kernel<L, decltype(j)::value, decltype(vec)::value>, row_blocks(desc->T), kWarps * 32, 0, stream, ctx.pdl, a);
     });
   };
   return desc->logits_type == DG_BF16 ? run(static_cast<__nv_bfloat16*>(nullptr)) : run(static_cast<float*>(nullptr));
@@ -269,8 +371,9 @@ dg_status dg_moe_route_backward(const void* logits, const int32_t* topk_ids, con
     using L = std::remove_pointer_t<decltype(type)>;
     const RouteGradArgs<L> a{static_cast<const L*>(logits), topk_ids, dweights, static_cast<L*>(dlogits), ctx.status,
                              desc->T, desc->E, desc->topk, desc->ld, desc->scoring == DG_ROUTE_SIGMOID, desc->renormalize, desc->scale};
-    return with_p(desc->E, [&](auto p) {
-      return dg::launch(route_grad_kernel<L, decltype(p)::value>, row_blocks(desc->T), kWarps * 32, 0, stream, ctx.pdl, a);
+    const bool aligned = whole_pieces<L>(logits, desc->ld, desc->E) && whole_pieces<L>(dlogits, desc->E, desc->E);
+    return with_shape<L>(desc->E, aligned, [&](auto j, auto vec) {
+      return dg::launch(route_grad_kernel<L, decltype(j)::value, decltype(vec)::value>, row_blocks(desc->T), kWarps * 32, 0, stream, ctx.pdl, a);
     });
   };
   return desc->logits_type == DG_BF16 ? run(static_cast<__nv_bfloat16*>(nullptr)) : run(static_cast<float*>(nullptr));
