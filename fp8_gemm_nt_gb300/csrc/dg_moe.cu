@@ -9,17 +9,17 @@
 // At a few tokens an expert has one to a handful of rows, so the time is that of reading the weights
 // of the experts in use, once. Both kernels stream them: every warp has a ring of its own in shared
 // memory that it fills with asynchronous copies, so that no warp waits for another between copies.
-// The tokens' side is small, shared by all blocks and stays in L2: a warp reads its fragments of it
-// straight into registers, one piece ahead. A warp multiplies 16 weight rows by up to 8 * NT tokens with
-// m16n8k16 MMAs: the weights are the M operand, an expert's tokens the N columns. Operands are FP16,
-// which holds E4M3 and E2M1 exactly; accumulation is FP32, and the scales are applied to FP32 partial sums.
+// A warp multiplies 16 weight rows (or 32) by up to 8 tokens (or 16) with m16n8 MMAs: the weights are
+// the M operand, an expert's tokens the N columns. The first product's operands are both E4M3 (E2M1 is
+// one with two exponent bits, moved into place), the second's FP16, which holds E4M3 and E2M1 exactly.
+// Accumulation is FP32, and the scales are applied to FP32 partial sums.
 //
-// An expert's tokens are compacted into jobs of at most 8 * NT columns; each distinct (expert, token)
+// An expert's tokens are compacted into jobs of at most 8 (16) columns; each distinct (expert, token)
 // pair is a slot. The first kernel writes h = weight * silu(g) * u of every slot to the workspace, in
-// FP16 with one power-of-two scale per 64 columns (11 bits of every value within 2^-29 of the
-// largest of its 64; the plain FP32 would double what the second kernel reads). The second kernel
-// owns output rows: a block sums all experts for its 16 rows of W2 and every token, in an order
-// that depends on the sizes alone, and writes each output once. No atomics on values.
+// FP16 with one power-of-two scale per 64 or 128 columns (11 bits of every value within 2^-29 of the
+// largest; plain FP32 would double what the second kernel reads). The second kernel owns output rows: a
+// block sums all experts for its 16 (32) rows of W2 and every token, in an order that depends on the
+// sizes alone, and writes each output once. No atomics on values.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -43,13 +43,9 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxH = 16384;
 constexpr int kMaxSlots = kMaxTokens * kMaxTopk;
 constexpr int kUpWarps = 8;
-constexpr int kDownWarps = 16;
-constexpr int kUpStages = 4;            // of a warp's ring
-constexpr int kDownStages = 4;
-constexpr int kHBlock = 8 * kUpWarps;   // columns of h that share a scale: one block's rows in the first kernel
-static_assert(kHBlock == 64, "h's layout has two scales per 128 columns");
-constexpr int kHBytes = 272;            // 128 columns of h of a slot: 256 bytes of FP16, two FP32 scales, padding
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kHBytes = 272;            // 128 columns of h of a slot: 256 bytes of FP16, FP32 scales of both halves, padding
+constexpr int kMaxSmem = 216 * 1024;
 
 struct MoeArgs {
   const uint8_t* x;        // [T, H] E4M3
@@ -164,7 +160,7 @@ __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, Rout
 }
 
 // -------------------------------------------------------------------------------------------
-// A warp's 16 x 128 piece of the weights
+// A warp's piece of the weights: 16 kM rows x 128 columns
 // -------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {
@@ -179,9 +175,19 @@ __device__ __forceinline__ uint32_t half2_of_e2m1(uint32_t two) {
   return d;
 }
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
+// Four E2M1 codes as E4M3 of 2^-6 of their values: the sign to bit 7, the two exponent bits and the
+// mantissa bit to the lowest exponent bits and the highest mantissa bit (E2M1's subnormal 0.5 becomes
+// the subnormal 2^-7). Even elements of eight are the low nibbles, odd ones the high nibbles.
+__device__ __forceinline__ uint32_t e4m3_of_even(uint32_t w) { return (w << 4 & 0x80808080u) | (w << 2 & 0x1C1C1C1Cu); }
+__device__ __forceinline__ uint32_t e4m3_of_odd(uint32_t w) { return (w & 0x80808080u) | (w >> 2 & 0x1C1C1C1Cu); }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -189,6 +195,11 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 __device__ __forceinline__ uint4 lds128(uint32_t p) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
   return v;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t p) {
@@ -202,6 +213,7 @@ __device__ __forceinline__ uint2 ld_cg_v2(const void* p) {
   return v;
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ float float_of(const uint4& v, int i) { return __uint_as_float(word_of(v, i)); }
 
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -210,55 +222,97 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // The K order of a product is free. Within 128 columns, lane 4 g + q (g the row or column of the MMA
-// fragment) takes, in the E4M3 form, columns 64 p + 16 q .. + 15 of half p: one 128-bit load of E4M3
-// holds four MMAs' fragments of a row. In the E2M1 form it takes columns 32 b + 8 q .. + 7 of block b:
-// the columns of an MMA then share a scale.
+// fragment) takes, in the E4M3 form, columns 64 p + 16 q .. + 15 of half p: one 128-bit load of a row holds
+// its fragments of two (four) MMAs. In the E2M1 form it takes columns 32 b + 8 q .. + 7 of block b: the
+// columns of an MMA then share a scale.
 //
-// A ring stage: the weights' 16 rows, then their scales. Chunk c (16 bytes) of a 128-byte row has the
-// halves of odd rows exchanged, so that the eight lanes of a 128-bit shared load (two rows, four chunks)
-// cover every bank once; 64-byte rows of E2M1, read 4 bytes per lane (eight rows, one chunk), are
-// permuted over four rows pairs for the same reason.
-template <bool kFp4>
+// Rings hold 128-byte rows of E4M3 and 64-byte rows of E2M1, in 16-byte chunks that are permuted so that
+// the lanes of one shared load cover every bank once: two rows of four chunks (128-bit loads of E4M3),
+// eight rows of one (32-bit loads of E2M1), four rows of two (64-bit loads of the E2M1 form's tokens).
+__device__ __forceinline__ int chunk_e4m3(int row, int c) { return row * 128 + ((c ^ ((row & 1) << 2)) << 4); }
+__device__ __forceinline__ int chunk_e2m1(int row, int c) { return row * 64 + ((c ^ ((row >> 1) & 3)) << 4); }
+__device__ __forceinline__ int chunk_pair(int row, int c) { return row * 128 + ((c ^ ((row & 3) << 1)) << 4); }
+
+template <bool kFp4, int kM>
 struct Piece {
   static constexpr int kRowBytes = kFp4 ? 64 : 128;
-  static constexpr int kBytes = 16 * kRowBytes;
-  static constexpr int kCopies = kBytes / 512;              // 16 bytes per lane each
-  static constexpr int kCopyRows = 16 / kCopies;
-  // E4M3: the four packed words of neighbouring 128-row blocks that hold the rows'; E2M1: a word per row
-  static constexpr int kScaleBytes = kFp4 ? 64 : 32;
-  static constexpr int kStage = kBytes + kScaleBytes;
+  static constexpr int kBytes = 16 * kM * kRowBytes;
+  static constexpr int kCopyRows = 512 / kRowBytes;         // rows of one copy by a whole warp, 16 bytes a lane
+  static constexpr int kCopies = 16 * kM / kCopyRows;
+  // E4M3: a packed word of one 128-row block (with its neighbours); E2M1: one per row
+  static constexpr int kScaleBytes = kFp4 ? 64 * kM : 16;
 
-  static __device__ __forceinline__ int chunk(int row, int c) {
-    return kFp4 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : row * 128 + ((c ^ ((row & 1) << 2)) << 4);
-  }
-  // this lane's row (of the first copy), chunk and place in a stage; copy i is kCopyRows rows further
+  static __device__ __forceinline__ int chunk(int row, int c) { return kFp4 ? chunk_e2m1(row, c) : chunk_e4m3(row, c); }
+  // this lane's row (of the first copy), first byte of it and place in a stage; copy i is kCopyRows rows further
   static __device__ __forceinline__ int row(int lane) { return lane / (kRowBytes / 16); }
   static __device__ __forceinline__ int column(int lane) { return lane % (kRowBytes / 16) * 16; }
   static __device__ __forceinline__ int place(int lane) { return chunk(row(lane), lane % (kRowBytes / 16)); }
+
+  // E2M1: the stage's scales (4 of every row) as FP32, times `by`, at `to` [16 kM][4]. Ends with the warp's
+  // writes visible.
+  static __device__ __forceinline__ void expand_scales(uint32_t scales, float* to, int lane, float by) {
+    if constexpr (kM == 1) {
+      const uint32_t w = lds32(scales + lane / 2 * 4) >> (lane & 1) * 16;
+      reinterpret_cast<float2*>(to)[lane] = make_float2(dg::ue8m0_value(w & 255) * by, dg::ue8m0_value(w >> 8 & 255) * by);
+    } else {
+      const uint32_t w = lds32(scales + lane * 4);
+      reinterpret_cast<float4*>(to)[lane] = make_float4(dg::ue8m0_value(w & 255) * by, dg::ue8m0_value(w >> 8 & 255) * by,
+                                                        dg::ue8m0_value(w >> 16 & 255) * by, dg::ue8m0_value(w >> 24) * by);
+    }
+    __syncwarp();
+  }
 };
-static_assert(Piece<true>::kCopyRows == 8 && Piece<false>::kCopyRows == 4, "the swizzles repeat every 2 and 8 rows");
+static_assert(Piece<true, 1>::kCopyRows == 8 && Piece<false, 1>::kCopyRows == 4, "the permutations repeat every 2 and 8 rows");
+
+// Shapes. kBig (more than 8 tokens): experts then have several tokens, and reading the tokens' side again
+// for every 16 weight rows would cost as much as the weights; a warp's pieces have 32 rows and 16 columns.
+template <bool kFp4, bool kBig>
+struct Up {
+  static constexpr int kM = kBig ? 2 : 1, kCols = kBig ? 16 : 8;
+  static constexpr int kBlock = 8 * kM * kUpWarps;          // columns of h of a block
+  static constexpr int kStages = kBig ? (kFp4 ? 5 : 4) : (kFp4 ? 5 : 4);
+  static constexpr int kBlocksPerSm = kBig ? 1 : 2;
+  using P = Piece<kFp4, kM>;
+  static constexpr int kStage = P::kBytes + (kFp4 ? P::kScaleBytes : 0) + kCols * 128;
+  static constexpr int kRing = kUpWarps * kStages * kStage;
+  static constexpr int kExpanded = kFp4 ? kUpWarps * 256 * kM : 0;   // E2M1: the piece's scales as FP32, per warp
+  // then the tokens' scales [groups, T], and for E4M3 each warp's two scales of every group
+  static int smem(int groups, int T) { return kRing + kExpanded + (groups * T + 1) / 2 * 8 + (kFp4 ? 0 : kUpWarps * groups * 8); }
+};
+template <bool kFp4, bool kBig>
+struct Down {
+  static constexpr int kM = kBig ? 2 : 1, kCols = kBig ? 16 : 8;
+  static constexpr int kRows = 16 * kM;
+  static constexpr int kWarps = kBig ? 8 : 16;
+  static constexpr int kStages = kFp4 ? 5 : 4;
+  using P = Piece<kFp4, kM>;
+  static constexpr int kStage = P::kBytes + P::kScaleBytes;
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kExpanded = kFp4 ? kWarps * 256 * kM : 0;
+  // then every warp's sums of a tile, twice: [2][warps][T][kRows]
+  static int smem(int T) { return kRing + kExpanded + 2 * kWarps * T * kRows * 4; }
+};
 
 // -------------------------------------------------------------------------------------------
 // First kernel: h = weight * silu(G x) * (U x)
 // -------------------------------------------------------------------------------------------
 
-template <bool kFp4>
-__host__ __device__ constexpr int up_ring_bytes() { return kUpWarps * kUpStages * Piece<kFp4>::kStage; }
-
-template <bool kFp4, int NT>
-__global__ void __launch_bounds__(32 * kUpWarps, 2) moe_up_kernel(const MoeArgs a) {
+template <bool kFp4, bool kBig>
+__global__ void __launch_bounds__(32 * kUpWarps, Up<kFp4, kBig>::kBlocksPerSm) moe_up_kernel(const MoeArgs a) {
+  using C = Up<kFp4, kBig>;
+  using P = typename C::P;
+  constexpr int kM = C::kM, NT = C::kCols / 8, kStages = C::kStages;
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ Routing r;
-  __shared__ float block_max[2][kUpWarps][NT * 8];
-  using P = Piece<kFp4>;
+  __shared__ float block_max[2][kUpWarps][C::kCols];
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g8 = lane / 4, q4 = lane & 3;
   const int t4 = (a.T + 3) / 4 * 4;
-  const int groups = a.H / 128, blocks = a.I / kHBlock;
-  build_routing<NT * 8, 32 * kUpWarps>(a, r, *reinterpret_cast<RoutingScratch*>(dyn), blockIdx.x == 0);
-  // after the rings: the tokens' scales [groups, T], and per warp the weights' two scales of every group
-  float* sx = reinterpret_cast<float*>(dyn + up_ring_bytes<kFp4>());
+  const int groups = a.H / 128, blocks = a.I / C::kBlock;
+  build_routing<C::kCols, 32 * kUpWarps>(a, r, *reinterpret_cast<RoutingScratch*>(dyn), blockIdx.x == 0);
+  float* expanded = reinterpret_cast<float*>(dyn + C::kRing) + warp * 64 * kM;
+  float* sx = reinterpret_cast<float*>(dyn + C::kRing + C::kExpanded);
   float2* sw = reinterpret_cast<float2*>(sx + (groups * a.T + 1) / 2 * 2) + warp * groups;
   for (int i = threadIdx.x; i < (groups + 3) / 4 * a.T; i += 32 * kUpWarps) {
     const int w = i / a.T, t = i % a.T;
@@ -268,18 +322,20 @@ __global__ void __launch_bounds__(32 * kUpWarps, 2) moe_up_kernel(const MoeArgs 
   __syncthreads();
 
   const int units = r.jobs * blocks;
-  const uint32_t ring = dg::smem_addr(dyn) + warp * kUpStages * P::kStage;
+  const uint32_t ring = dg::smem_addr(dyn) + warp * kStages * C::kStage;
+  constexpr int kTokens = P::kBytes + (kFp4 ? P::kScaleBytes : 0);  // where a stage's tokens begin
   const long long row_bytes = kFp4 ? a.H / 2 : a.H;
   const int n4 = kFp4 ? 2 * a.I : (a.I / 64 + 3) / 4 * 4;           // words of a scale row (2 I is a multiple of 4)
-  // the copies run kUpStages - 1 pieces ahead of the products, over the block's units one after another
-  int fu = blockIdx.x, fg = 0;
+  // the copies run kStages - 1 pieces ahead of the products, over the block's units one after another
+  int fu = blockIdx.x, fg = 0, fcount = 0;
   uint32_t fto = ring;
   const uint8_t* gate_from = nullptr;
   const uint8_t* up_from = nullptr;
   const int32_t* scale_from = nullptr;
+  const uint8_t* x_from[2 * NT];                                    // columns lane / 8 + 4 i of the job
   uint32_t next_gate = 0, next_up = 0;                              // E4M3: packed scale word `lane` of the unit
   auto load_scales = [&](int u) {
-    const int e = r.job_expert[u / blocks], i0 = u % blocks * kHBlock;
+    const int e = r.job_expert[u / blocks], i0 = u % blocks * C::kBlock;
     if (lane < (groups + 3) / 4) {
       const int32_t* sf = a.sf13 + (static_cast<long long>(e) * ((groups + 3) / 4) + lane) * n4;
       next_gate = dg::ld_cg_s32(sf + i0 / 128);
@@ -289,119 +345,102 @@ __global__ void __launch_bounds__(32 * kUpWarps, 2) moe_up_kernel(const MoeArgs 
   auto fetch = [&] {
     if (fu < units) {
       if (fg == 0) {
-        const int e = r.job_expert[fu / blocks], i0 = fu % blocks * kHBlock + warp * 8;
-        const uint8_t* w = a.w13 + static_cast<long long>(e) * 2 * a.I * row_bytes;
-        const int row = P::row(lane);
-        gate_from = w + (i0 + row) * row_bytes + P::column(lane);
+        const int job = fu / blocks, e = r.job_expert[job], i0 = fu % blocks * C::kBlock + warp * 8 * kM;
+        gate_from = a.w13 + (static_cast<long long>(e) * 2 * a.I + i0 + P::row(lane)) * row_bytes + P::column(lane);
         up_from = gate_from + a.I * row_bytes;
+        fcount = r.job_count[job];
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+          const int col = lane / 8 + 4 * i;
+          x_from[i] = col < fcount ? a.x + static_cast<long long>(r.token[r.job_slot[job] + col]) * a.H + (lane & 7) * 16 : nullptr;
+        }
         if (kFp4) {
-          scale_from = a.sf13 + static_cast<long long>(e) * groups * n4 + (lane < 2 ? i0 : a.I + i0 - 8) + 4 * lane;
-        } else if (groups >= kUpStages - 1) {
+          const int part = lane & 3;
+          scale_from = a.sf13 + static_cast<long long>(e) * groups * n4 + i0 + lane / 4 * 8 + (part < 2 ? 4 * part : a.I + 4 * part - 8);
+        } else if (groups >= kStages - 1) {
           load_scales(fu);
         }
       }
       const uint32_t to = fto + P::place(lane);
+      constexpr int kHalf = 8 / P::kCopyRows;                       // copies of a tile's 8 gate rows, then as many of its up rows
 #pragma unroll
       for (int i = 0; i < P::kCopies; ++i) {
-        const uint8_t* from = i < P::kCopies / 2 ? gate_from + i * P::kCopyRows * row_bytes
-                                                 : up_from + (i - P::kCopies / 2) * P::kCopyRows * row_bytes;
-        dg::cp_async_16(to + i * 512, from);
+        const int rows = i / (2 * kHalf) * 8 + i % kHalf * P::kCopyRows;
+        dg::cp_async_16(to + i * 512, (i / kHalf % 2 ? up_from : gate_from) + rows * row_bytes);
       }
       gate_from += P::kRowBytes;
       up_from += P::kRowBytes;
       if (kFp4) {
-        if (lane < 4) dg::cp_async_16(fto + P::kBytes + 16 * lane, scale_from);
+        if (lane < 4 * kM) dg::cp_async_16(fto + P::kBytes + 16 * lane, scale_from);
         scale_from += n4;
       }
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i)
+        if (x_from[i]) {
+          const int col = lane / 8 + 4 * i, c = lane & 7;
+          dg::cp_async_16(fto + kTokens + (kFp4 ? chunk_pair(col, c) : chunk_e4m3(col, c)), x_from[i]);
+          x_from[i] += 128;
+        }
       if (++fg == groups) fg = 0, fu += gridDim.x;
     }
-    fto = fto + P::kStage == ring + kUpStages * P::kStage ? ring : fto + P::kStage;
+    fto = fto + C::kStage == ring + kStages * C::kStage ? ring : fto + C::kStage;
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kUpStages - 1; ++i) fetch();
+  for (int i = 0; i < kStages - 1; ++i) fetch();
 
   int flip = 0;
   uint32_t at = ring;
   for (int u = blockIdx.x; u < units; u += gridDim.x, flip ^= 1) {
     const int job = u / blocks, blk = u % blocks, slot = r.job_slot[job], count = r.job_count[job];
-    float sum[NT][4];
+    float sum[kM][NT][4];
     const float* sxt[NT][2];
-    const uint8_t* xt[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[n][i] = 0;
+      for (int m = 0; m < kM; ++m) sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = n * 8 + 2 * q4 + i;
         sxt[n][i] = sx + (col < count ? r.token[slot + col] : 0);
       }
-      const int col = n * 8 + g8;                                   // its fragments: null past the job's tokens
-      xt[n] = col < count ? a.x + static_cast<long long>(r.token[slot + col]) * a.H + (kFp4 ? 8 * q4 : 16 * q4) : nullptr;
     }
     if constexpr (!kFp4) {
-      // the unit's scales as FP32, read while the unit before was computed (unless the copies, kUpStages - 1
+      // the unit's scales as FP32, read while the unit before was computed (unless the copies, kStages - 1
       // pieces ahead, are then past the next unit's start)
-      if (groups < kUpStages - 1) load_scales(u);
+      if (groups < kStages - 1) load_scales(u);
       __syncwarp();
       if (lane < (groups + 3) / 4)
         for (int b = 0; b < 4 && 4 * lane + b < groups; ++b)
           sw[4 * lane + b] = make_float2(dg::ue8m0_value(next_gate >> (8 * b) & 255), dg::ue8m0_value(next_up >> (8 * b) & 255));
       __syncwarp();
     }
-    // E4M3: two 16-byte loads per eight tokens and 128 columns; E2M1: four of 8 bytes
-    uint32_t xr[NT][8];
-    auto load_x = [&](int g) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (xt[n]) {
-          if constexpr (kFp4) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint2 v = ld_cg_v2(xt[n] + g * 128 + b * 32);
-              xr[n][2 * b] = v.x, xr[n][2 * b + 1] = v.y;
-            }
-          } else {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const uint4 v = dg::ld_cg_v4(xt[n] + g * 128 + p * 64);
-              xr[n][4 * p] = v.x, xr[n][4 * p + 1] = v.y, xr[n][4 * p + 2] = v.z, xr[n][4 * p + 3] = v.w;
-            }
-          }
-        }
-    };
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xr[n][i] = 0;
-    load_x(0);
     for (int g = 0; g < groups; ++g) {
-      uint32_t xn[NT][8];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) xn[n][i] = xr[n][i];
-      if (g + 1 < groups) load_x(g + 1);
-      cp_async_wait<kUpStages - 2>();
+      cp_async_wait<kStages - 2>();
       __syncwarp();
       fetch();
-      float acc[NT][4];
+      const uint32_t tokens = at + kTokens;
+      float acc[kM][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0;
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0;
       if constexpr (!kFp4) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const uint4 w0 = lds128(at + P::chunk(g8, 4 * p + q4)), w1 = lds128(at + P::chunk(g8 + 8, 4 * p + q4));
+          uint4 x[NT];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t u0 = word_of(w0, i), u1 = word_of(w1, i);
-            const uint32_t a0 = half2_of_e4m3(u0), a2 = half2_of_e4m3(u0 >> 16), a1 = half2_of_e4m3(u1), a3 = half2_of_e4m3(u1 >> 16);
+          for (int n = 0; n < NT; ++n)
+            if (n == 0 || n * 8 < count) x[n] = lds128(tokens + chunk_e4m3(8 * n + g8, 4 * p + q4));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint32_t x = xn[n][4 * p + i];
-              mma_16816(acc[n], a0, a1, a2, a3, half2_of_e4m3(x), half2_of_e4m3(x >> 16));
-            }
+          for (int m = 0; m < kM; ++m) {
+            const uint4 w0 = lds128(at + P::chunk(16 * m + g8, 4 * p + q4)), w1 = lds128(at + P::chunk(16 * m + 8 + g8, 4 * p + q4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              if (n == 0 || n * 8 < count) {
+                mma_e4m3(acc[m][n], w0.x, w1.x, w0.y, w1.y, x[n].x, x[n].y);
+                mma_e4m3(acc[m][n], w0.z, w1.z, w0.w, w1.w, x[n].z, x[n].w);
+              }
           }
         }
         const float2 s = sw[g];
@@ -409,35 +448,44 @@ __global__ void __launch_bounds__(32 * kUpWarps, 2) moe_up_kernel(const MoeArgs 
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float t = sxt[n][i][g * a.T];
-            sum[n][i] = fmaf(t * s.x, acc[n][i], sum[n][i]);
-            sum[n][2 + i] = fmaf(t * s.y, acc[n][2 + i], sum[n][2 + i]);
-          }
-      } else {
-        const uint32_t z0 = lds32(at + P::kBytes + 4 * g8), z1 = lds32(at + P::kBytes + 32 + 4 * g8);
+            const float t = sxt[n][i][g * a.T], tx = t * s.x, ty = t * s.y;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t u0 = lds32(at + P::chunk(g8, b) + 4 * q4), u1 = lds32(at + P::chunk(g8 + 8, b) + 4 * q4);
-          const float e0 = dg::ue8m0_value(z0 >> (8 * b) & 255), e1 = dg::ue8m0_value(z1 >> (8 * b) & 255);
-          float part[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t v0 = u0 >> (16 * i), v1 = u1 >> (16 * i);
-            const uint32_t a0 = half2_of_e2m1(v0 & 255), a1 = half2_of_e2m1(v1 & 255), a2 = half2_of_e2m1(v0 >> 8 & 255), a3 = half2_of_e2m1(v1 >> 8 & 255);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint32_t x = xn[n][2 * b + i];
-              mma_16816(part[n], a0, a1, a2, a3, half2_of_e4m3(x), half2_of_e4m3(x >> 16));
+            for (int m = 0; m < kM; ++m) {
+              sum[m][n][i] = fmaf(tx, acc[m][n][i], sum[m][n][i]);
+              sum[m][n][2 + i] = fmaf(ty, acc[m][n][2 + i], sum[m][n][2 + i]);
             }
           }
+      } else {
+        P::expand_scales(at + P::kBytes, expanded, lane, 64.0f);    // E2M1 enters the MMAs as 2^-6 of itself
+        uint4 scale[kM][2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc[n][0] = fmaf(e0, part[n][0], acc[n][0]);
-            acc[n][1] = fmaf(e0, part[n][1], acc[n][1]);
-            acc[n][2] = fmaf(e1, part[n][2], acc[n][2]);
-            acc[n][3] = fmaf(e1, part[n][3], acc[n][3]);
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) scale[m][i] = reinterpret_cast<const uint4*>(expanded)[16 * m + 8 * i + g8];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t even[NT], odd[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (n == 0 || n * 8 < count) {
+              const uint2 x = lds64(tokens + chunk_pair(8 * n + g8, 2 * b + q4 / 2) + 8 * (q4 & 1));
+              even[n] = __byte_perm(x.x, x.y, 0x6420), odd[n] = __byte_perm(x.x, x.y, 0x7531);
+            }
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            const uint32_t u0 = lds32(at + P::chunk(16 * m + g8, b) + 4 * q4), u1 = lds32(at + P::chunk(16 * m + 8 + g8, b) + 4 * q4);
+            const uint32_t a0 = e4m3_of_even(u0), a1 = e4m3_of_even(u1), a2 = e4m3_of_odd(u0), a3 = e4m3_of_odd(u1);
+            const float e0 = float_of(scale[m][0], b), e1 = float_of(scale[m][1], b);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              if (n == 0 || n * 8 < count) {
+                float part[4] = {0, 0, 0, 0};
+                mma_e4m3(part, a0, a1, a2, a3, even[n], odd[n]);
+                acc[m][n][0] = fmaf(e0, part[0], acc[m][n][0]);
+                acc[m][n][1] = fmaf(e0, part[1], acc[m][n][1]);
+                acc[m][n][2] = fmaf(e1, part[2], acc[m][n][2]);
+                acc[m][n][3] = fmaf(e1, part[3], acc[m][n][3]);
+              }
           }
         }
 #pragma unroll
@@ -445,48 +493,63 @@ __global__ void __launch_bounds__(32 * kUpWarps, 2) moe_up_kernel(const MoeArgs 
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float t = sxt[n][i][g * a.T];
-            sum[n][i] = fmaf(t, acc[n][i], sum[n][i]);
-            sum[n][2 + i] = fmaf(t, acc[n][2 + i], sum[n][2 + i]);
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+              sum[m][n][i] = fmaf(t, acc[m][n][i], sum[m][n][i]);
+              sum[m][n][2 + i] = fmaf(t, acc[m][n][2 + i], sum[m][n][2 + i]);
+            }
           }
       }
-      at = at + P::kStage == ring + kUpStages * P::kStage ? ring : at + P::kStage;
+      at = at + C::kStage == ring + kStages * C::kStage ? ring : at + C::kStage;
     }
-    // column blk * 64 + warp * 8 + g8 of h for tokens 2 q4, 2 q4 + 1 of each eight: gate in sum[0..1], up in sum[2..3]
-    float hv[NT][2];
+    // column blk * kBlock + (warp * kM + m) * 8 + g8 of h for tokens 2 q4, 2 q4 + 1 of each eight: gate in
+    // sum[0..1], up in sum[2..3]
+    float hv[kM][NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = n * 8 + 2 * q4 + i;
-        const float gate = sum[n][i];
-        hv[n][i] = col < count ? r.coef[slot + col] * (gate / (1.0f + expf(-gate)) * sum[n][2 + i]) : 0.0f;
-        float m = fabsf(hv[n][i]);
-        m = m < INFINITY ? m : 0.0f;
+        const float w = col < count ? r.coef[slot + col] : 0.0f;
+        float top = 0;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-        if (g8 == 0) block_max[flip][warp][col] = m;
+        for (int m = 0; m < kM; ++m) {
+          const float gate = sum[m][n][i];
+          hv[m][n][i] = col < count ? w * (gate / (1.0f + expf(-gate)) * sum[m][n][2 + i]) : 0.0f;
+          const float v = fabsf(hv[m][n][i]);
+          top = fmaxf(top, v < INFINITY ? v : 0.0f);
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        if (g8 == 0) block_max[flip][warp][col] = top;
       }
     __syncthreads();
-    // where the second kernel's lanes find this column in the 64: E4M3 as 16-byte pieces of two loads, each
-    // of 64 bytes over four lanes; E2M1 in order
-    const int cc = warp * 8 + g8;
-    const int place = kFp4 ? cc * 2 : (cc % 16) / 8 * 64 + cc / 16 * 16 + cc % 8 * 2;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = n * 8 + 2 * q4 + i;
         if (col >= count) continue;
-        float m = 0;
+        float top = 0;
 #pragma unroll
-        for (int w = 0; w < kUpWarps; ++w) m = fmaxf(m, block_max[flip][w][col]);
+        for (int w = 0; w < kUpWarps; ++w) top = fmaxf(top, block_max[flip][w][col]);
         // the largest to [2^14, 2^15); both powers stay normal
-        const int ex = min(max(static_cast<int>(__float_as_uint(m) >> 23), 27), 254) - 127 - 14;
-        const float up = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        uint8_t* row = a.h + (static_cast<long long>(slot + col) * (a.I / 128) + blk / 2) * kHBytes;
-        *reinterpret_cast<__half*>(row + (blk & 1) * 128 + place) = __float2half_rn(hv[n][i] * up);
-        if (warp == 0 && g8 == 0)
-          reinterpret_cast<float*>(row + 256)[blk & 1] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 254) - 127 - 14;
+        const float up = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23), down = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        uint8_t* row = a.h + (static_cast<long long>(slot + col) * (a.I / 128) + blk * C::kBlock / 128) * kHBytes;
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+          // where the second kernel's lanes find this column of the 128: E4M3 as 16-byte pieces of two loads,
+          // each of 64 bytes over four lanes; E2M1 in order
+          const int cc = blk * C::kBlock % 128 + (warp * kM + m) * 8 + g8;
+          const int place = kFp4 ? cc * 2 : cc / 64 * 128 + cc % 16 / 8 * 64 + cc % 64 / 16 * 16 + cc % 8 * 2;
+          *reinterpret_cast<__half*>(row + place) = __float2half_rn(hv[m][n][i] * up);
+        }
+        if (warp == 0 && g8 == 0) {
+          float* to = reinterpret_cast<float*>(row + 256);
+          if (kM == 2) to[0] = to[1] = down;
+          else to[blk & 1] = down;
+        }
       }
   }
   cp_async_wait<0>();
@@ -496,198 +559,217 @@ __global__ void __launch_bounds__(32 * kUpWarps, 2) moe_up_kernel(const MoeArgs 
 // Second kernel: y = c + W2 h
 // -------------------------------------------------------------------------------------------
 
-template <bool kFp4>
-__host__ __device__ constexpr int down_ring_bytes() { return kDownWarps * kDownStages * Piece<kFp4>::kStage; }
-
-template <bool kFp4, int NT>
-__global__ void __launch_bounds__(32 * kDownWarps, 1) moe_down_kernel(const MoeArgs a) {
+template <bool kFp4, bool kBig>
+__global__ void __launch_bounds__(32 * Down<kFp4, kBig>::kWarps, 1) moe_down_kernel(const MoeArgs a) {
+  using C = Down<kFp4, kBig>;
+  using P = typename C::P;
+  constexpr int kM = C::kM, NT = C::kCols / 8, kStages = C::kStages, kWarps = C::kWarps;
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ Routing r;
-  using P = Piece<kFp4>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g8 = lane / 4, q4 = lane & 3;
   // The first kernel let this one start only after its own wait: ids and weights are there, h is not yet.
-  build_routing<NT * 8, 32 * kDownWarps>(a, r, *reinterpret_cast<RoutingScratch*>(dyn), false);
+  build_routing<C::kCols, 32 * kWarps>(a, r, *reinterpret_cast<RoutingScratch*>(dyn), false);
 
-  const int groups = a.I / 128, items = r.jobs * groups, tiles = a.H / 16;
-  const long long row_bytes = kFp4 ? a.I / 2 : a.I;
+  const int groups = a.I / 128, items = r.jobs * groups, tiles = a.H / C::kRows;
+  const uint32_t row_bytes = kFp4 ? a.I / 2 : a.I;
   const int n4 = kFp4 ? a.H : (a.H / 128 + 3) / 4 * 4;
-  const uint32_t ring = dg::smem_addr(dyn) + warp * kDownStages * P::kStage;
-  // every warp's sums of a tile, [2][warps][T][16]: the tile before is being added up meanwhile
-  float* sums = reinterpret_cast<float*>(dyn + down_ring_bytes<kFp4>());
-  const int tile_sums = kDownWarps * a.T * 16;
-  for (int i = threadIdx.x; i < 2 * tile_sums; i += 32 * kDownWarps) sums[i] = 0;
+  const uint32_t ring = dg::smem_addr(dyn) + warp * kStages * C::kStage;
+  float* expanded = reinterpret_cast<float*>(dyn + C::kRing) + warp * 64 * kM;
+  // every warp's sums of a tile, [2][warps][T][kRows]: the tile before is being added up meanwhile
+  float* sums = reinterpret_cast<float*>(dyn + C::kRing + C::kExpanded);
+  const int tile_sums = kWarps * a.T * C::kRows;
+  for (int i = threadIdx.x; i < 2 * tile_sums; i += 32 * kWarps) sums[i] = 0;
 
-  // a warp takes every sixteenth of the tile's (job, K-group) items
-  const bool busy = warp < items;
-  int ft = busy ? blockIdx.x : tiles, fjob = warp / groups, fg = warp % groups;
+  // a warp takes a run of the tile's (job, K-group) items
+  const int begin = warp * items / kWarps, end = (warp + 1) * items / kWarps, begin_job = begin / groups, begin_g = begin % groups;
+  int ft = begin < end ? blockIdx.x : tiles, fi = begin, fjob = begin_job, fg = begin_g;
   uint32_t fto = ring;
+  const uint8_t* w_from = nullptr;
+  const int32_t* scale_from = nullptr;
+  const int scale_row = kFp4 ? n4 : 0;
+  auto aim = [&] {
+    const int e = r.job_expert[fjob];
+    w_from = a.w2 + (static_cast<long long>(e) * a.H + ft * C::kRows + P::row(lane)) * row_bytes + fg * P::kRowBytes + P::column(lane);
+    scale_from = kFp4 ? a.sf2 + (static_cast<long long>(e) * groups + fg) * n4 + ft * C::kRows + 4 * lane
+                      : a.sf2 + static_cast<long long>(e) * ((groups + 3) / 4) * n4 + (ft * C::kRows / 128 & ~3);
+  };
+  if (ft < tiles) aim();
   auto fetch = [&] {
     if (ft < tiles) {
-      const int e = r.job_expert[fjob], row = P::row(lane);
-      const uint8_t* from = a.w2 + (static_cast<long long>(e) * a.H + ft * 16 + row) * row_bytes + fg * P::kRowBytes + P::column(lane);
       const uint32_t to = fto + P::place(lane);
 #pragma unroll
-      for (int i = 0; i < P::kCopies; ++i) dg::cp_async_16(to + i * 512, from + i * P::kCopyRows * row_bytes);
-      if (kFp4) {
-        if (lane < 4) dg::cp_async_16(fto + P::kBytes + 16 * lane, a.sf2 + (static_cast<long long>(e) * groups + fg) * n4 + ft * 16 + 4 * lane);
-      } else if (lane == 0) {
-        dg::cp_async_16(fto + P::kBytes, a.sf2 + (static_cast<long long>(e) * ((groups + 3) / 4) + fg / 4) * n4 + (ft / 8 & ~3));
+      for (int i = 0; i < P::kCopies; ++i) dg::cp_async_16(to + i * 512, w_from + i * P::kCopyRows * row_bytes);
+      if (lane < P::kScaleBytes / 16) dg::cp_async_16(fto + P::kBytes + 16 * lane, kFp4 ? scale_from : scale_from + fg / 4 * n4);
+      w_from += P::kRowBytes;
+      scale_from += scale_row;
+      ++fg;
+      if (++fi == end) {
+        fi = begin, fjob = begin_job, fg = begin_g, ft += gridDim.x;
+        if (ft < tiles) aim();
+      } else if (fg == groups) {
+        fg = 0, ++fjob;
+        aim();
       }
-      for (fg += kDownWarps; fg >= groups; fg -= groups) ++fjob;
-      if (fjob >= r.jobs) fjob = warp / groups, fg = warp % groups, ft += gridDim.x;
     }
-    fto = fto + P::kStage == ring + kDownStages * P::kStage ? ring : fto + P::kStage;
+    fto = fto + C::kStage == ring + kStages * C::kStage ? ring : fto + C::kStage;
     cp_async_commit();
   };
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kDownStages - 1; ++i) fetch();
+  for (int i = 0; i < kStages - 1; ++i) fetch();
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
 
-  // this lane's fragments of an item's tokens (as FP16 pairs) and the scales of its two columns
-  uint32_t hr[NT][16];
+  // this lane's fragments of an item's tokens (as FP16 pairs) and the scales of its two columns, one item ahead
+  uint4 hr[NT][4];
   uint2 hs[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     hs[n][0] = hs[n][1] = make_uint2(0, 0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) hr[n][i] = 0;
+    for (int i = 0; i < 4; ++i) hr[n][i] = make_uint4(0, 0, 0, 0);
   }
+  const uint32_t slot_bytes = groups * kHBytes;                     // at most 512 slots of 128 groups: 32 bits are enough
   auto load_h = [&](int job, int g) {
     const int slot = r.job_slot[job], count = r.job_count[job];
+    const uint8_t* base = a.h + (slot * slot_bytes + g * kHBytes);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const uint8_t* base = a.h + (static_cast<long long>(slot + n * 8) * groups + g) * kHBytes;
       if (n * 8 + g8 < count) {
-        const uint8_t* from = base + static_cast<long long>(g8) * groups * kHBytes + q4 * 16;
+        const uint8_t* from = base + (n * 8 + g8) * slot_bytes + q4 * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 v = dg::ld_cg_v4(from + i * 64);
-          hr[n][4 * i] = v.x, hr[n][4 * i + 1] = v.y, hr[n][4 * i + 2] = v.z, hr[n][4 * i + 3] = v.w;
-        }
+        for (int i = 0; i < 4; ++i) hr[n][i] = dg::ld_cg_v4(from + i * 64);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (n * 8 + 2 * q4 + i < count) hs[n][i] = ld_cg_v2(base + static_cast<long long>(2 * q4 + i) * groups * kHBytes + 256);
+        if (n * 8 + 2 * q4 + i < count) hs[n][i] = ld_cg_v2(base + (n * 8 + 2 * q4 + i) * slot_bytes + 256);
     }
   };
-  if (busy && static_cast<int>(blockIdx.x) < tiles) load_h(warp / groups, warp % groups);
+  if (begin < end && static_cast<int>(blockIdx.x) < tiles) load_h(begin_job, begin_g);
 
   uint32_t at = ring;
   int flip = 0;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, flip ^= 1) {
-    float* mine = sums + flip * tile_sums + warp * a.T * 16;
-    float sum[NT][4];
+    float* mine = sums + flip * tile_sums + warp * a.T * C::kRows;
+    float sum[kM][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0;
-    int job = warp / groups, g = warp % groups;
-    while (job < r.jobs) {
-      int next_job = job, next_g = g + kDownWarps;
-      for (; next_g >= groups; next_g -= groups) ++next_job;
-      auto load_next = [&] {
-        if (next_job < r.jobs) load_h(next_job, next_g);
-        else if (tile + static_cast<int>(gridDim.x) < tiles) load_h(warp / groups, warp % groups);
-      };
-      // sixteen tokens' fragments take the registers that a second set would need: they are loaded after use
-      constexpr bool kAhead = NT == 1;
-      uint32_t hc[NT][16];
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0;
+    int job = begin_job, g = begin_g;
+    for (int it = begin; it < end; ++it) {
+      const int slot = r.job_slot[job], count = r.job_count[job];
+      uint4 hc[NT][4];
       float sc[NT][2][2];
-      if constexpr (kAhead) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) hc[n][i] = hr[n][i];
+        for (int i = 0; i < 4; ++i) hc[n][i] = hr[n][i];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) sc[n][i][0] = __uint_as_float(hs[n][i].x), sc[n][i][1] = __uint_as_float(hs[n][i].y);
-        }
-        load_next();
+        for (int i = 0; i < 2; ++i) sc[n][i][0] = __uint_as_float(hs[n][i].x), sc[n][i][1] = __uint_as_float(hs[n][i].y);
       }
-      auto frag = [&](int n, int i) { return kAhead ? hc[n][i] : hr[n][i]; };
-      auto col_scale = [&](int n, int i, int p) { return kAhead ? sc[n][i][p] : __uint_as_float(p ? hs[n][i].y : hs[n][i].x); };
-      cp_async_wait<kDownStages - 2>();
+      const bool last = it + 1 == end, turn = g + 1 == groups;
+      if (!last) load_h(turn ? job + 1 : job, turn ? 0 : g + 1);
+      else if (tile + static_cast<int>(gridDim.x) < tiles) load_h(begin_job, begin_g);
+      cp_async_wait<kStages - 2>();
       __syncwarp();
       fetch();
       if constexpr (!kFp4) {
-        const float s = dg::ue8m0_value(lds32(at + P::kBytes + (tile / 8 & 3) * 4) >> (8 * (g & 3)) & 255);
+        const float s = dg::ue8m0_value(lds32(at + P::kBytes + (tile * C::kRows / 128 & 3) * 4) >> (8 * (g & 3)) & 255);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const uint4 w0 = lds128(at + P::chunk(g8, 4 * p + q4)), w1 = lds128(at + P::chunk(g8 + 8, 4 * p + q4));
-          float acc[NT][4];
+          float t[NT][2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0;
+          for (int n = 0; n < NT; ++n) t[n][0] = s * sc[n][0][p], t[n][1] = s * sc[n][1][p];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t u0 = word_of(w0, i), u1 = word_of(w1, i);
-            const uint32_t a0 = half2_of_e4m3(u0), a2 = half2_of_e4m3(u0 >> 16), a1 = half2_of_e4m3(u1), a3 = half2_of_e4m3(u1 >> 16);
+          for (int m = 0; m < kM; ++m) {
+            const uint4 w0 = lds128(at + P::chunk(16 * m + g8, 4 * p + q4)), w1 = lds128(at + P::chunk(16 * m + 8 + g8, 4 * p + q4));
+            float acc[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816(acc[n], a0, a1, a2, a3, frag(n, 8 * p + 2 * i), frag(n, 8 * p + 2 * i + 1));
-          }
+            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t u0 = word_of(w0, i), u1 = word_of(w1, i);
+              const uint32_t a0 = half2_of_e4m3(u0), a2 = half2_of_e4m3(u0 >> 16), a1 = half2_of_e4m3(u1), a3 = half2_of_e4m3(u1 >> 16);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float t = s * col_scale(n, i, p);
-              sum[n][i] = fmaf(t, acc[n][i], sum[n][i]);
-              sum[n][2 + i] = fmaf(t, acc[n][2 + i], sum[n][2 + i]);
+              for (int n = 0; n < NT; ++n)
+                if (n == 0 || n * 8 < count)
+                  mma_f16(acc[n], a0, a1, a2, a3, word_of(hc[n][2 * p + i / 2], i % 2 * 2), word_of(hc[n][2 * p + i / 2], i % 2 * 2 + 1));
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                sum[m][n][i] = fmaf(t[n][i], acc[n][i], sum[m][n][i]);
+                sum[m][n][2 + i] = fmaf(t[n][i], acc[n][2 + i], sum[m][n][2 + i]);
+              }
+          }
         }
       } else {
-        const uint32_t z0 = lds32(at + P::kBytes + 4 * g8), z1 = lds32(at + P::kBytes + 32 + 4 * g8);
+        P::expand_scales(at + P::kBytes, expanded, lane, 1.0f);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t u0 = lds32(at + P::chunk(g8, b) + 4 * q4), u1 = lds32(at + P::chunk(g8 + 8, b) + 4 * q4);
-          const float e0 = dg::ue8m0_value(z0 >> (8 * b) & 255), e1 = dg::ue8m0_value(z1 >> (8 * b) & 255);
-          float part[NT][4];
+        for (int m = 0; m < kM; ++m) {
+          const uint4 s0 = reinterpret_cast<const uint4*>(expanded)[16 * m + g8], s1 = reinterpret_cast<const uint4*>(expanded)[16 * m + 8 + g8];
+          float half[NT][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0;
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t u0 = lds32(at + P::chunk(16 * m + g8, b) + 4 * q4), u1 = lds32(at + P::chunk(16 * m + 8 + g8, b) + 4 * q4);
+            const float e0 = float_of(s0, b), e1 = float_of(s1, b);
+            float part[NT][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t v0 = u0 >> (16 * i), v1 = u1 >> (16 * i);
-            const uint32_t a0 = half2_of_e2m1(v0 & 255), a1 = half2_of_e2m1(v1 & 255), a2 = half2_of_e2m1(v0 >> 8 & 255), a3 = half2_of_e2m1(v1 >> 8 & 255);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816(part[n], a0, a1, a2, a3, frag(n, 4 * b + 2 * i), frag(n, 4 * b + 2 * i + 1));
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float t = col_scale(n, i, b / 2);
-              sum[n][i] = fmaf(t * e0, part[n][i], sum[n][i]);
-              sum[n][2 + i] = fmaf(t * e1, part[n][2 + i], sum[n][2 + i]);
+              const uint32_t v0 = u0 >> (16 * i), v1 = u1 >> (16 * i);
+              const uint32_t a0 = half2_of_e2m1(v0 & 255), a1 = half2_of_e2m1(v1 & 255), a2 = half2_of_e2m1(v0 >> 8 & 255), a3 = half2_of_e2m1(v1 >> 8 & 255);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                if (n == 0 || n * 8 < count) mma_f16(part[n], a0, a1, a2, a3, word_of(hc[n][b], 2 * i), word_of(hc[n][b], 2 * i + 1));
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float e = i < 2 ? e0 : e1;
+                half[n][i] = b % 2 == 0 ? e * part[n][i] : fmaf(e, part[n][i], half[n][i]);
+                if (b % 2 == 1) sum[m][n][i] = fmaf(sc[n][i % 2][b / 2], half[n][i], sum[m][n][i]);
+              }
+          }
         }
       }
-      if constexpr (!kAhead) load_next();
-      at = at + P::kStage == ring + kDownStages * P::kStage ? ring : at + P::kStage;
-      if (next_job != job) {
-        // rows g8 and g8 + 8 of the job's tokens, into the warp's sums
-        const int slot = r.job_slot[job], count = r.job_count[job];
+      at = at + C::kStage == ring + kStages * C::kStage ? ring : at + C::kStage;
+      if (last || turn) {
+        // rows g8 and g8 + 8 of each 16 for the job's tokens, into the warp's sums
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int col = n * 8 + 2 * q4 + i;
             if (col < count) {
-              float* to = mine + r.token[slot + col] * 16;
-              to[g8] += sum[n][i];
-              to[g8 + 8] += sum[n][2 + i];
+              float* to = mine + r.token[slot + col] * C::kRows + g8;
+#pragma unroll
+              for (int m = 0; m < kM; ++m) {
+                to[16 * m] += sum[m][n][i];
+                to[16 * m + 8] += sum[m][n][2 + i];
+              }
             }
-            sum[n][i] = sum[n][2 + i] = 0;
+#pragma unroll
+            for (int m = 0; m < kM; ++m) sum[m][n][i] = sum[m][n][2 + i] = 0;
           }
         __syncwarp();
       }
-      job = next_job, g = next_g;
+      g = turn ? 0 : g + 1;
+      job += turn;
     }
     __syncthreads();
     float* all = sums + flip * tile_sums;
-    for (int i = threadIdx.x; i < a.T * 16; i += 32 * kDownWarps) {
-      const long long to = static_cast<long long>(i / 16) * a.H + tile * 16 + i % 16;
+    for (int i = threadIdx.x; i < a.T * C::kRows; i += 32 * kWarps) {
+      const long long to = static_cast<long long>(i / C::kRows) * a.H + tile * C::kRows + i % C::kRows;
       float v = a.c ? __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(a.c) + to))) : 0.0f;
 #pragma unroll
-      for (int w = 0; w < kDownWarps; ++w) {
-        v += all[w * a.T * 16 + i];
-        all[w * a.T * 16 + i] = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        v += all[w * a.T * C::kRows + i];
+        all[w * a.T * C::kRows + i] = 0;
       }
       a.y[to] = __float2bfloat16_rn(v);
     }
@@ -697,28 +779,26 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) moe_down_kernel(const MoeA
 
 // -------------------------------------------------------------------------------------------
 
-template <bool kFp4, int NT>
+template <bool kFp4, bool kBig>
 dg_status run_layer(const MoeArgs& a, const LaunchContext& ctx, cudaStream_t stream) {
-  constexpr int kMaxSmem = 200 * 1024;
+  using U = Up<kFp4, kBig>;
+  using D = Down<kFp4, kBig>;
+  static_assert(sizeof(RoutingScratch) <= U::kRing && sizeof(RoutingScratch) <= D::kRing, "scratch in the rings");
+  const int up_smem = U::smem(a.H / 128, a.T), down_smem = D::smem(a.T);
+  if (up_smem > kMaxSmem || down_smem > kMaxSmem) return DG_ERR_UNSUPPORTED;
   // once per thread and device: the limit, above what any shape needs
   static thread_local int ready = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && ready != dev) {
-    e = cudaFuncSetAttribute(moe_up_kernel<kFp4, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<kFp4, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    e = cudaFuncSetAttribute(moe_up_kernel<kFp4, kBig>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<kFp4, kBig>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return dg::record_cuda_error(e);
-  const int groups = a.H / 128;
-  const int up_smem = up_ring_bytes<kFp4>() + (groups * a.T + 1) / 2 * 8 + (kFp4 ? 0 : kUpWarps * groups * 8);
-  const int down_smem = down_ring_bytes<kFp4>() + 2 * kDownWarps * a.T * 16 * 4;
-  static_assert(up_ring_bytes<kFp4>() + (kMaxH / 128) * (kMaxTokens * 4 + kUpWarps * 8) <= kMaxSmem &&
-                down_ring_bytes<kFp4>() + 2 * kDownWarps * kMaxTokens * 16 * 4 <= kMaxSmem, "shared memory");
-  static_assert(sizeof(RoutingScratch) <= up_ring_bytes<kFp4>() && sizeof(RoutingScratch) <= down_ring_bytes<kFp4>(), "scratch in the rings");
-  const unsigned up_grid = static_cast<unsigned>(2 * ctx.sms), down_grid = static_cast<unsigned>(std::min(ctx.sms, a.H / 16));
-  if (dg_status s = dg::launch(moe_up_kernel<kFp4, NT>, up_grid, 32 * kUpWarps, static_cast<size_t>(up_smem), stream, ctx.pdl, a); s != DG_OK) return s;
-  return dg::launch(moe_down_kernel<kFp4, NT>, down_grid, 32 * kDownWarps, static_cast<size_t>(down_smem), stream, ctx.pdl, a);
+  const unsigned up_grid = static_cast<unsigned>(U::kBlocksPerSm * ctx.sms), down_grid = static_cast<unsigned>(std::min(ctx.sms, a.H / D::kRows));
+  if (dg_status s = dg::launch(moe_up_kernel<kFp4, kBig>, up_grid, 32 * kUpWarps, static_cast<size_t>(up_smem), stream, ctx.pdl, a); s != DG_OK) return s;
+  return dg::launch(moe_down_kernel<kFp4, kBig>, down_grid, 32 * D::kWarps, static_cast<size_t>(down_smem), stream, ctx.pdl, a);
 }
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -742,7 +822,7 @@ dg_status few_tokens(const void* x, const int32_t* sfx, const void* w13, const i
   const MoeArgs a{static_cast<const uint8_t*>(x), sfx, static_cast<const uint8_t*>(w13), sf13, static_cast<const uint8_t*>(w2), sf2,
                   ids, weights, static_cast<const __nv_bfloat16*>(c), static_cast<__nv_bfloat16*>(y), static_cast<uint8_t*>(h),
                   ctx.status, T, topk, E, H, I};
-  return T <= 8 ? run_layer<kFp4, 1>(a, ctx, stream) : run_layer<kFp4, 2>(a, ctx, stream);
+  return T <= 8 ? run_layer<kFp4, false>(a, ctx, stream) : run_layer<kFp4, true>(a, ctx, stream);
 }
 
 }  // namespace
