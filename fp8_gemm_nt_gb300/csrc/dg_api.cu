@@ -986,6 +986,13 @@ dg_status launch_context(LaunchContext* out) {
 
 dg_status record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
+bool byte_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows, uint32_t box_bytes) {
+  const uint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
+  const uint32_t box[2] = {box_bytes, box_rows};
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                  box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 dg_status StreamWorkspace::acquire(cudaStream_t stream, size_t bytes, void** out) {
   DeviceState* ds = nullptr;
   if (dg_status s = device_state(&ds); s != DG_OK) return s;

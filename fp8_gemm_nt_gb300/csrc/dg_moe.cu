@@ -7,11 +7,10 @@
 // 128 x 128 block, or E2M1 with one per row per 32 columns: the grouped GEMMs' operands.
 //
 // At a few tokens an expert has one to a handful of rows, so the time is that of reading the weights
-// of the experts in use, once. Both kernels stream them: every warp has a ring of its own in shared
-// memory that it fills with asynchronous copies, so that no warp waits for another between copies.
-// A warp multiplies 16 weight rows (or 32) by up to 8 tokens (or 16) with m16n8 MMAs: the weights are
-// the M operand, an expert's tokens the N columns. The first product's operands are both E4M3 (E2M1 is
-// one with two exponent bits, moved into place), the second's FP16, which holds E4M3 and E2M1 exactly.
+// of the experts in use, once. Both kernels stream them with TMA into rings in shared memory. A warp
+// multiplies 16 weight rows (or 32) by up to 8 tokens (or 16) with m16n8 MMAs: the weights are the M
+// operand, an expert's tokens the N columns. The first product's operands are both E4M3 (E2M1 is one
+// with two exponent bits, moved into place), the second's FP16, which holds E4M3 and E2M1 exactly.
 // Accumulation is FP32, and the scales are applied to FP32 partial sums.
 //
 // An expert's tokens are compacted into jobs of at most 8 (16) columns; each distinct (expert, token)
@@ -28,6 +27,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "debug_state.h"
 #include "dg.h"
 #include "ptx.cuh"
 #include "runtime.h"
@@ -42,7 +42,6 @@ constexpr int kMaxTopk = 16;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxH = 16384;
 constexpr int kMaxSlots = kMaxTokens * kMaxTopk;
-constexpr int kUpWarps = 8;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kHBytes = 272;            // 128 columns of h of a slot: 256 bytes of FP16, FP32 scales of both halves, padding
 constexpr int kMaxSmem = 216 * 1024;
@@ -60,6 +59,8 @@ struct MoeArgs {
   __nv_bfloat16* y;        // [T, H]
   uint8_t* h;              // [slots, I / 128, kHBytes]
   uint32_t* status;
+  unsigned long long timeout_ns;   // of a wait for a copy
+  int fault;                       // failure injection: no copies
   int T, k, E, H, I;
 };
 
@@ -73,7 +74,7 @@ struct Routing {
   uint8_t job_count[kMaxSlots];
   uint8_t token[kMaxSlots];
   float coef[kMaxSlots];                // weight of a slot (the sum, where a token names an expert twice)
-  int warp_sum[16];
+  int warp_sum[17];
   int jobs;
 };
 
@@ -89,7 +90,7 @@ struct RoutingScratch {
 // every block of both kernels. `kCols`: columns of a job.
 template <int kCols, int kThreads>
 __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& s, bool report) {
-  constexpr int kPer = kMaxExperts / kThreads;
+  constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, slots = a.T * a.k;
   for (int i = tid; i < slots; i += kThreads) {
     s.ids[i] = dg::ld_cg_s32(a.ids + i);
@@ -160,7 +161,7 @@ __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, Rout
 }
 
 // -------------------------------------------------------------------------------------------
-// A warp's piece of the weights: 16 kM rows x 128 columns
+// Elements, MMAs, copies
 // -------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {
@@ -192,6 +193,18 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same on a sum that starts at zero.
+__device__ __forceinline__ void mma_e4m3_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t p) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
@@ -215,182 +228,192 @@ __device__ __forceinline__ uint2 ld_cg_v2(const void* p) {
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ float float_of(const uint4& v, int i) { return __uint_as_float(word_of(v, i)); }
 
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Untiled bulk copy (16-byte aligned addresses and size) that completes on `bar`.
+__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dg::smem_addr(to)),
+               "l"(from), "r"(bytes), "r"(dg::smem_addr(bar))
+               : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // The K order of a product is free. Within 128 columns, lane 4 g + q (g the row or column of the MMA
 // fragment) takes, in the E4M3 form, columns 64 p + 16 q .. + 15 of half p: one 128-bit load of a row holds
 // its fragments of two (four) MMAs. In the E2M1 form it takes columns 32 b + 8 q .. + 7 of block b: the
 // columns of an MMA then share a scale.
 //
-// Rings hold 128-byte rows of E4M3 and 64-byte rows of E2M1, in 16-byte chunks that are permuted so that
-// the lanes of one shared load cover every bank once: two rows of four chunks (128-bit loads of E4M3),
-// eight rows of one (32-bit loads of E2M1), four rows of two (64-bit loads of the E2M1 form's tokens).
-__device__ __forceinline__ int chunk_e4m3(int row, int c) { return row * 128 + ((c ^ ((row & 1) << 2)) << 4); }
-__device__ __forceinline__ int chunk_e2m1(int row, int c) { return row * 64 + ((c ^ ((row >> 1) & 3)) << 4); }
-__device__ __forceinline__ int chunk_pair(int row, int c) { return row * 128 + ((c ^ ((row & 3) << 1)) << 4); }
-
-template <bool kFp4, int kM>
-struct Piece {
-  static constexpr int kRowBytes = kFp4 ? 64 : 128;
-  static constexpr int kBytes = 16 * kM * kRowBytes;
-  static constexpr int kCopyRows = 512 / kRowBytes;         // rows of one copy by a whole warp, 16 bytes a lane
-  static constexpr int kCopies = 16 * kM / kCopyRows;
-  // E4M3: a packed word of one 128-row block (with its neighbours); E2M1: one per row
-  static constexpr int kScaleBytes = kFp4 ? 64 * kM : 16;
-
-  static __device__ __forceinline__ int chunk(int row, int c) { return kFp4 ? chunk_e2m1(row, c) : chunk_e4m3(row, c); }
-  // this lane's row (of the first copy), first byte of it and place in a stage; copy i is kCopyRows rows further
-  static __device__ __forceinline__ int row(int lane) { return lane / (kRowBytes / 16); }
-  static __device__ __forceinline__ int column(int lane) { return lane % (kRowBytes / 16) * 16; }
-  static __device__ __forceinline__ int place(int lane) { return chunk(row(lane), lane % (kRowBytes / 16)); }
-
-  // E2M1: the stage's scales (4 of every row) as FP32, times `by`, at `to` [16 kM][4]. Ends with the warp's
-  // writes visible.
-  static __device__ __forceinline__ void expand_scales(uint32_t scales, float* to, int lane, float by) {
-    if constexpr (kM == 1) {
-      const uint32_t w = lds32(scales + lane / 2 * 4) >> (lane & 1) * 16;
-      reinterpret_cast<float2*>(to)[lane] = make_float2(dg::ue8m0_value(w & 255) * by, dg::ue8m0_value(w >> 8 & 255) * by);
-    } else {
-      const uint32_t w = lds32(scales + lane * 4);
-      reinterpret_cast<float4*>(to)[lane] = make_float4(dg::ue8m0_value(w & 255) * by, dg::ue8m0_value(w >> 8 & 255) * by,
-                                                        dg::ue8m0_value(w >> 16 & 255) * by, dg::ue8m0_value(w >> 24) * by);
-    }
-    __syncwarp();
+// TMA permutes the 16-byte chunks of a row (the 128-byte swizzle for E4M3, the 64-byte one for E2M1).
+// The eight lanes of a 128-bit load's phase are two rows of four chunks; they cover every bank once if the
+// rows differ by four, so row g of a fragment is row g / 2 + 4 (g % 2) of eight in memory. E2M1's 32-bit
+// loads (eight rows of one chunk) meet no bank twice in any order of the rows.
+template <bool kFp4>
+struct Rows {
+  static constexpr int kBytes = kFp4 ? 64 : 128;            // of 128 columns
+  static __device__ __forceinline__ int of(int g) { return kFp4 ? g : g / 2 + 4 * (g & 1); }
+  static __device__ __forceinline__ int chunk(int row, int c) {
+    return kFp4 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4);
   }
 };
-static_assert(Piece<true, 1>::kCopyRows == 8 && Piece<false, 1>::kCopyRows == 4, "the permutations repeat every 2 and 8 rows");
 
-// Shapes. kBig (more than 8 tokens): experts then have several tokens, and reading the tokens' side again
-// for every 16 weight rows would cost as much as the weights; a warp's pieces have 32 rows and 16 columns.
+// FP32 values of the four UE8M0 codes of a word.
+__device__ __forceinline__ float4 four_scales(uint32_t w) {
+  return make_float4(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255), dg::ue8m0_value(w >> 16 & 255), dg::ue8m0_value(w >> 24));
+}
+
+// E2M1: the packed scales of 16 kM rows at `packed` as FP32 at `to` [16 kM][4], each by one lane; visible to
+// the warp at the end.
+template <int kM>
+__device__ __forceinline__ void expand_scales(uint32_t packed, float* to, int lane) {
+  if constexpr (kM == 1) {
+    const uint32_t w = lds32(packed + lane / 2 * 4) >> (lane & 1) * 16;
+    reinterpret_cast<float2*>(to)[lane] = make_float2(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255));
+  } else {
+    reinterpret_cast<float4*>(to)[lane] = four_scales(lds32(packed + lane * 4));
+  }
+  __syncwarp();
+}
+
+// A wait that has run out once is not repeated: the kernel then runs through on what is in its rings, with
+// every barrier met, and the status word says that its results are void.
+__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, const MoeArgs& a, bool ok) {
+  if (ok && dg::mbar_wait(bar, parity, a.timeout_ns)) return true;
+  if (ok) atomicOr(a.status, dg::kTimeoutBit);
+  return false;
+}
+
+constexpr int round_up(int v, int to) { return (v + to - 1) / to * to; }
+
+// Shapes. kBig (more than 8 tokens): experts then have several tokens; 16 columns, and for E2M1, whose
+// tokens' side and conversions cost as much as its bytes, 32 rows a warp.
 template <bool kFp4, bool kBig>
 struct Up {
-  static constexpr int kM = kBig ? 2 : 1, kCols = kBig ? 16 : 8;
-  static constexpr int kBlock = 8 * kM * kUpWarps;          // columns of h of a block
-  static constexpr int kStages = kBig ? (kFp4 ? 5 : 4) : (kFp4 ? 5 : 4);
-  static constexpr int kBlocksPerSm = kBig ? 1 : 2;
-  using P = Piece<kFp4, kM>;
-  static constexpr int kStage = P::kBytes + (kFp4 ? P::kScaleBytes : 0) + kCols * 128;
-  static constexpr int kRing = kUpWarps * kStages * kStage;
-  static constexpr int kExpanded = kFp4 ? kUpWarps * 256 * kM : 0;   // E2M1: the piece's scales as FP32, per warp
+  static constexpr int kM = kFp4 && kBig ? 2 : 1, kCols = kBig ? 16 : 8;
+  static constexpr int kWarps = kBig && !kFp4 ? 16 : 8, kThreads = 32 * kWarps;
+  static constexpr int kBlock = 8 * kM * kWarps;                    // columns of h of a block, 64 or 128
+  static constexpr int kBlocksPerSm = kBig && !kFp4 ? 1 : 2;
+  static constexpr int kStages = kFp4 ? (kBig ? 4 : 8) : 5;
+  static constexpr int kAhead = kStages - 2;                        // copies run this far ahead of the products
+  // a stage: kBlock gate rows and as many up rows of 128 columns, the tokens' 128 bytes, E2M1's scales. A
+  // token's row is spaced so that the lanes of a load of it (two rows of 64 bytes, four of 32) cover the banks.
+  static constexpr int kBox = kBlock * Rows<kFp4>::kBytes;
+  static constexpr int kTokenStride = kFp4 ? 160 : 192;
+  static constexpr int kTokens = 2 * kBox, kScales = kTokens + kCols * kTokenStride;
+  static constexpr int kStage = round_up(kScales + (kFp4 ? 8 * kBlock : 0), 1024);
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kExpanded = kFp4 ? kWarps * 256 * kM : 0;    // E2M1: a warp's scales as FP32
   // then the tokens' scales [groups, T], and for E4M3 each warp's two scales of every group
-  static int smem(int groups, int T) { return kRing + kExpanded + (groups * T + 1) / 2 * 8 + (kFp4 ? 0 : kUpWarps * groups * 8); }
+  static int smem(int groups, int T) { return 1024 + kRing + kExpanded + (groups * T + 1) / 2 * 8 + (kFp4 ? 0 : kWarps * groups * 8); }
 };
 template <bool kFp4, bool kBig>
 struct Down {
-  static constexpr int kM = kBig ? 2 : 1, kCols = kBig ? 16 : 8;
-  static constexpr int kRows = 16 * kM;
-  static constexpr int kWarps = kBig ? 8 : 16;
-  static constexpr int kStages = kFp4 ? 5 : 4;
-  using P = Piece<kFp4, kM>;
-  static constexpr int kStage = P::kBytes + P::kScaleBytes;
-  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kM = kFp4 && kBig ? 2 : 1, kCols = kBig ? 16 : 8;
+  static constexpr int kRows = 16 * kM, kWarps = 16, kThreads = 32 * kWarps;
+  static constexpr int kStages = kFp4 ? (kBig ? 4 : 6) : 4;
+  static constexpr int kBox = kRows * Rows<kFp4>::kBytes;           // a stage of a warp
+  static constexpr int kRing = kWarps * kStages * kBox;
+  // E4M3: the packed word of the rows' 128-row block (with its neighbours); E2M1: a word per row
+  static constexpr int kScaleBytes = kFp4 ? 4 * kRows : 16;
+  static constexpr int kScales = kWarps * kStages * kScaleBytes;
   static constexpr int kExpanded = kFp4 ? kWarps * 256 * kM : 0;
-  // then every warp's sums of a tile, twice: [2][warps][T][kRows]
-  static int smem(int T) { return kRing + kExpanded + 2 * kWarps * T * kRows * 4; }
+  // then every warp's sums of a tile, [warps][T][kRows]
+  static int smem(int T) { return 1024 + kRing + kScales + kExpanded + kWarps * T * kRows * 4; }
 };
+
+__device__ __forceinline__ uint8_t* aligned_1k(uint8_t* p) {
+  return p + ((1024u - (dg::smem_addr(p) & 1023u)) & 1023u);
+}
 
 // -------------------------------------------------------------------------------------------
 // First kernel: h = weight * silu(G x) * (U x)
 // -------------------------------------------------------------------------------------------
+//
+// A unit is kBlock columns of h of a job: kBlock gate rows and kBlock up rows of W13, a warp 8 kM of each. A
+// stage is 128 columns of all of them and of the job's tokens. The warps take turns at issuing its copies,
+// two stages less than the ring is long ahead: a warp may then lag another by two stages before its turn
+// has to wait for it. (A warp for the copies alone would leave the others 96 registers instead of 128.)
 
 template <bool kFp4, bool kBig>
-__global__ void __launch_bounds__(32 * kUpWarps, Up<kFp4, kBig>::kBlocksPerSm) moe_up_kernel(const MoeArgs a) {
+__global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlocksPerSm)
+    moe_up_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
   using C = Up<kFp4, kBig>;
-  using P = typename C::P;
-  constexpr int kM = C::kM, NT = C::kCols / 8, kStages = C::kStages;
-  extern __shared__ __align__(128) uint8_t dyn[];
+  using R = Rows<kFp4>;
+  constexpr int kM = C::kM, NT = C::kCols / 8, kStages = C::kStages, kWarps = C::kWarps;
+  extern __shared__ uint8_t raw[];
   __shared__ Routing r;
-  __shared__ float block_max[2][kUpWarps][C::kCols];
+  __shared__ float block_max[2][kWarps][C::kCols];
+  __shared__ uint64_t full[kStages], empty[kStages];
+  uint8_t* const ring = aligned_1k(raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      dg::mbar_init(&full[i], 1);
+      dg::mbar_init(&empty[i], kWarps);
+    }
+    dg::fence_mbarrier_init();
+    dg::tma_prefetch_desc(&map);
+  }
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g8 = lane / 4, q4 = lane & 3;
   const int t4 = (a.T + 3) / 4 * 4;
   const int groups = a.H / 128, blocks = a.I / C::kBlock;
-  build_routing<C::kCols, 32 * kUpWarps>(a, r, *reinterpret_cast<RoutingScratch*>(dyn), blockIdx.x == 0);
-  float* expanded = reinterpret_cast<float*>(dyn + C::kRing) + warp * 64 * kM;
-  float* sx = reinterpret_cast<float*>(dyn + C::kRing + C::kExpanded);
-  float2* sw = reinterpret_cast<float2*>(sx + (groups * a.T + 1) / 2 * 2) + warp * groups;
-  for (int i = threadIdx.x; i < (groups + 3) / 4 * a.T; i += 32 * kUpWarps) {
+  build_routing<C::kCols, C::kThreads>(a, r, *reinterpret_cast<RoutingScratch*>(ring), blockIdx.x == 0);
+  float* expanded = reinterpret_cast<float*>(ring + C::kRing) + warp * 64 * kM;
+  float* sx = reinterpret_cast<float*>(ring + C::kRing + C::kExpanded);
+  for (int i = threadIdx.x; i < (groups + 3) / 4 * a.T; i += C::kThreads) {
     const int w = i / a.T, t = i % a.T;
     const uint32_t v = dg::ld_cg_s32(a.sfx + w * t4 + t);
     for (int b = 0; b < 4 && 4 * w + b < groups; ++b) sx[(4 * w + b) * a.T + t] = dg::ue8m0_value(v >> (8 * b) & 255);
   }
+  dg::fence_proxy_async_smem();        // the scratch in the ring was written by threads; copies write there next
   __syncthreads();
-
   const int units = r.jobs * blocks;
-  const uint32_t ring = dg::smem_addr(dyn) + warp * kStages * C::kStage;
-  constexpr int kTokens = P::kBytes + (kFp4 ? P::kScaleBytes : 0);  // where a stage's tokens begin
-  const long long row_bytes = kFp4 ? a.H / 2 : a.H;
-  const int n4 = kFp4 ? 2 * a.I : (a.I / 64 + 3) / 4 * 4;           // words of a scale row (2 I is a multiple of 4)
-  // the copies run kStages - 1 pieces ahead of the products, over the block's units one after another
-  int fu = blockIdx.x, fg = 0, fcount = 0;
-  uint32_t fto = ring;
-  const uint8_t* gate_from = nullptr;
-  const uint8_t* up_from = nullptr;
-  const int32_t* scale_from = nullptr;
-  const uint8_t* x_from[2 * NT];                                    // columns lane / 8 + 4 i of the job
-  uint32_t next_gate = 0, next_up = 0;                              // E4M3: packed scale word `lane` of the unit
+  bool ok = true;
+
+  // the stage to copy: column group fg of unit fu, the issued'th of the block
+  int fu = blockIdx.x, fg = 0, fstage = 0, issued = 0;
+  uint32_t fphase = 1;
+  auto fetch = [&] {
+    if (fu >= units) return;
+    if (issued % kWarps == warp && a.fault == 0) {
+      const int job = fu / blocks, e = r.job_expert[job], i0 = fu % blocks * C::kBlock, slot = r.job_slot[job], count = r.job_count[job];
+      ok = wait_full(&empty[fstage], fphase, a, ok);
+      if (__all_sync(kAll, ok)) {
+        uint8_t* to = ring + fstage * C::kStage;
+        if (lane == 0) {
+          const int row = e * 2 * a.I + i0;
+          dg::mbar_arrive_expect_tx(&full[fstage], 2 * C::kBox + count * 128 + (kFp4 ? 8 * C::kBlock : 0));
+          dg::tma_load_2d(to, &map, &full[fstage], fg * R::kBytes, row);
+          dg::tma_load_2d(to + C::kBox, &map, &full[fstage], fg * R::kBytes, row + a.I);
+          if (kFp4) {
+            const int32_t* from = a.sf13 + (static_cast<long long>(e) * groups + fg) * 2 * a.I + i0;
+            bulk_load(to + C::kScales, from, 4 * C::kBlock, &full[fstage]);
+            bulk_load(to + C::kScales + 4 * C::kBlock, from + a.I, 4 * C::kBlock, &full[fstage]);
+          }
+        }
+        __syncwarp();
+        if (lane < count)
+          bulk_load(to + C::kTokens + lane * C::kTokenStride, a.x + static_cast<long long>(r.token[slot + lane]) * a.H + fg * 128, 128, &full[fstage]);
+      }
+    }
+    ++issued;
+    if (++fstage == kStages) fstage = 0, fphase ^= 1;
+    if (++fg == groups) fg = 0, fu += gridDim.x;
+  };
+
+  const int g8 = lane / 4, q4 = lane & 3, row8 = R::of(g8);
+  float2* sw = reinterpret_cast<float2*>(sx + (groups * a.T + 1) / 2 * 2) + warp * groups;
+  // E4M3: packed scale word `lane` of a unit's gate and up rows, read a unit ahead
+  uint32_t next_gate = 0, next_up = 0;
   auto load_scales = [&](int u) {
-    const int e = r.job_expert[u / blocks], i0 = u % blocks * C::kBlock;
+    const int e = r.job_expert[u / blocks], i0 = u % blocks * C::kBlock, n4 = (a.I / 64 + 3) / 4 * 4;
     if (lane < (groups + 3) / 4) {
       const int32_t* sf = a.sf13 + (static_cast<long long>(e) * ((groups + 3) / 4) + lane) * n4;
       next_gate = dg::ld_cg_s32(sf + i0 / 128);
       next_up = dg::ld_cg_s32(sf + (a.I + i0) / 128);
     }
   };
-  auto fetch = [&] {
-    if (fu < units) {
-      if (fg == 0) {
-        const int job = fu / blocks, e = r.job_expert[job], i0 = fu % blocks * C::kBlock + warp * 8 * kM;
-        gate_from = a.w13 + (static_cast<long long>(e) * 2 * a.I + i0 + P::row(lane)) * row_bytes + P::column(lane);
-        up_from = gate_from + a.I * row_bytes;
-        fcount = r.job_count[job];
-#pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-          const int col = lane / 8 + 4 * i;
-          x_from[i] = col < fcount ? a.x + static_cast<long long>(r.token[r.job_slot[job] + col]) * a.H + (lane & 7) * 16 : nullptr;
-        }
-        if (kFp4) {
-          const int part = lane & 3;
-          scale_from = a.sf13 + static_cast<long long>(e) * groups * n4 + i0 + lane / 4 * 8 + (part < 2 ? 4 * part : a.I + 4 * part - 8);
-        } else if (groups >= kStages - 1) {
-          load_scales(fu);
-        }
-      }
-      const uint32_t to = fto + P::place(lane);
-      constexpr int kHalf = 8 / P::kCopyRows;                       // copies of a tile's 8 gate rows, then as many of its up rows
-#pragma unroll
-      for (int i = 0; i < P::kCopies; ++i) {
-        const int rows = i / (2 * kHalf) * 8 + i % kHalf * P::kCopyRows;
-        dg::cp_async_16(to + i * 512, (i / kHalf % 2 ? up_from : gate_from) + rows * row_bytes);
-      }
-      gate_from += P::kRowBytes;
-      up_from += P::kRowBytes;
-      if (kFp4) {
-        if (lane < 4 * kM) dg::cp_async_16(fto + P::kBytes + 16 * lane, scale_from);
-        scale_from += n4;
-      }
-#pragma unroll
-      for (int i = 0; i < 2 * NT; ++i)
-        if (x_from[i]) {
-          const int col = lane / 8 + 4 * i, c = lane & 7;
-          dg::cp_async_16(fto + kTokens + (kFp4 ? chunk_pair(col, c) : chunk_e4m3(col, c)), x_from[i]);
-          x_from[i] += 128;
-        }
-      if (++fg == groups) fg = 0, fu += gridDim.x;
-    }
-    fto = fto + C::kStage == ring + kStages * C::kStage ? ring : fto + C::kStage;
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch();
-
-  int flip = 0;
-  uint32_t at = ring;
+  for (int i = 0; i < C::kAhead; ++i) fetch();
+  if (!kFp4 && static_cast<int>(blockIdx.x) < units) load_scales(blockIdx.x);
+  int stage = 0, flip = 0;
+  uint32_t phase = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x, flip ^= 1) {
     const int job = u / blocks, blk = u % blocks, slot = r.job_slot[job], count = r.job_count[job];
     float sum[kM][NT][4];
@@ -406,104 +429,105 @@ __global__ void __launch_bounds__(32 * kUpWarps, Up<kFp4, kBig>::kBlocksPerSm) m
       }
     }
     if constexpr (!kFp4) {
-      // the unit's scales as FP32, read while the unit before was computed (unless the copies, kStages - 1
-      // pieces ahead, are then past the next unit's start)
-      if (groups < kStages - 1) load_scales(u);
       __syncwarp();
-      if (lane < (groups + 3) / 4)
-        for (int b = 0; b < 4 && 4 * lane + b < groups; ++b)
-          sw[4 * lane + b] = make_float2(dg::ue8m0_value(next_gate >> (8 * b) & 255), dg::ue8m0_value(next_up >> (8 * b) & 255));
+      if (lane < (groups + 3) / 4) {
+        const float4 gate = four_scales(next_gate), up = four_scales(next_up);
+        sw[4 * lane] = make_float2(gate.x, up.x);
+        if (4 * lane + 1 < groups) sw[4 * lane + 1] = make_float2(gate.y, up.y);
+        if (4 * lane + 2 < groups) sw[4 * lane + 2] = make_float2(gate.z, up.z);
+        if (4 * lane + 3 < groups) sw[4 * lane + 3] = make_float2(gate.w, up.w);
+      }
       __syncwarp();
+      if (u + static_cast<int>(gridDim.x) < units) load_scales(u + gridDim.x);
     }
     for (int g = 0; g < groups; ++g) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
       fetch();
-      const uint32_t tokens = at + kTokens;
+      ok = wait_full(&full[stage], phase, a, ok);
+      const uint32_t at = dg::smem_addr(ring) + stage * C::kStage;
+      const uint32_t gate = at + warp * 8 * kM * R::kBytes, up = gate + C::kBox, tokens = at + C::kTokens + g8 * C::kTokenStride;
       float acc[kM][NT][4];
-#pragma unroll
-      for (int m = 0; m < kM; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0;
       if constexpr (!kFp4) {
+        uint4 w0[2], w1[2], x[NT][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          uint4 x[NT];
+          w0[p] = lds128(gate + R::chunk(row8, 4 * p + q4)), w1[p] = lds128(up + R::chunk(row8, 4 * p + q4));
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            if (n == 0 || n * 8 < count) x[n] = lds128(tokens + chunk_e4m3(8 * n + g8, 4 * p + q4));
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            const uint4 w0 = lds128(at + P::chunk(16 * m + g8, 4 * p + q4)), w1 = lds128(at + P::chunk(16 * m + 8 + g8, 4 * p + q4));
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              if (n == 0 || n * 8 < count) {
-                mma_e4m3(acc[m][n], w0.x, w1.x, w0.y, w1.y, x[n].x, x[n].y);
-                mma_e4m3(acc[m][n], w0.z, w1.z, w0.w, w1.w, x[n].z, x[n].w);
-              }
-          }
+            if (n == 0 || n * 8 < count) x[n][p] = lds128(tokens + n * 8 * C::kTokenStride + 64 * p + 16 * q4);
         }
-        const float2 s = sw[g];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float t = sxt[n][i][g * a.T], tx = t * s.x, ty = t * s.y;
-#pragma unroll
-            for (int m = 0; m < kM; ++m) {
-              sum[m][n][i] = fmaf(tx, acc[m][n][i], sum[m][n][i]);
-              sum[m][n][2 + i] = fmaf(ty, acc[m][n][2 + i], sum[m][n][2 + i]);
-            }
+          if (n == 0 || n * 8 < count) {
+            mma_e4m3_zero(acc[0][n], w0[0].x, w1[0].x, w0[0].y, w1[0].y, x[n][0].x, x[n][0].y);
+            mma_e4m3(acc[0][n], w0[0].z, w1[0].z, w0[0].w, w1[0].w, x[n][0].z, x[n][0].w);
+            mma_e4m3(acc[0][n], w0[1].x, w1[1].x, w0[1].y, w1[1].y, x[n][1].x, x[n][1].y);
+            mma_e4m3(acc[0][n], w0[1].z, w1[1].z, w0[1].w, w1[1].w, x[n][1].z, x[n][1].w);
           }
       } else {
-        P::expand_scales(at + P::kBytes, expanded, lane, 64.0f);    // E2M1 enters the MMAs as 2^-6 of itself
+        // the warp's scales: 8 kM gate rows, then as many up rows
+        const uint32_t packed = at + C::kScales + warp * 32 * kM;
+        const uint32_t w = lds32(packed + (kM == 1 ? (lane / 16) * 4 * C::kBlock + lane % 16 / 2 * 4 : (lane / 16) * 4 * C::kBlock + lane % 16 * 4));
+        if constexpr (kM == 1) {
+          const uint32_t v = w >> (lane & 1) * 16;
+          reinterpret_cast<float2*>(expanded)[lane] = make_float2(dg::ue8m0_value(v & 255), dg::ue8m0_value(v >> 8 & 255));
+        } else {
+          reinterpret_cast<float4*>(expanded)[lane] = four_scales(w);
+        }
+        __syncwarp();
         uint4 scale[kM][2];
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) scale[m][i] = reinterpret_cast<const uint4*>(expanded)[16 * m + 8 * i + g8];
+        for (int m = 0; m < kM; ++m) {
+          scale[m][0] = reinterpret_cast<const uint4*>(expanded)[8 * m + g8];
+          scale[m][1] = reinterpret_cast<const uint4*>(expanded)[8 * kM + 8 * m + g8];
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           uint32_t even[NT], odd[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             if (n == 0 || n * 8 < count) {
-              const uint2 x = lds64(tokens + chunk_pair(8 * n + g8, 2 * b + q4 / 2) + 8 * (q4 & 1));
+              const uint2 x = lds64(tokens + n * 8 * C::kTokenStride + 32 * b + 8 * q4);
               even[n] = __byte_perm(x.x, x.y, 0x6420), odd[n] = __byte_perm(x.x, x.y, 0x7531);
             }
 #pragma unroll
           for (int m = 0; m < kM; ++m) {
-            const uint32_t u0 = lds32(at + P::chunk(16 * m + g8, b) + 4 * q4), u1 = lds32(at + P::chunk(16 * m + 8 + g8, b) + 4 * q4);
+            const uint32_t u0 = lds32(gate + m * 8 * R::kBytes + R::chunk(row8, b) + 4 * q4), u1 = lds32(up + m * 8 * R::kBytes + R::chunk(row8, b) + 4 * q4);
             const uint32_t a0 = e4m3_of_even(u0), a1 = e4m3_of_even(u1), a2 = e4m3_of_odd(u0), a3 = e4m3_of_odd(u1);
             const float e0 = float_of(scale[m][0], b), e1 = float_of(scale[m][1], b);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
               if (n == 0 || n * 8 < count) {
-                float part[4] = {0, 0, 0, 0};
-                mma_e4m3(part, a0, a1, a2, a3, even[n], odd[n]);
-                acc[m][n][0] = fmaf(e0, part[0], acc[m][n][0]);
-                acc[m][n][1] = fmaf(e0, part[1], acc[m][n][1]);
-                acc[m][n][2] = fmaf(e1, part[2], acc[m][n][2]);
-                acc[m][n][3] = fmaf(e1, part[3], acc[m][n][3]);
+                float part[4];
+                mma_e4m3_zero(part, a0, a1, a2, a3, even[n], odd[n]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float e = i < 2 ? e0 : e1;
+                  acc[m][n][i] = b == 0 ? e * part[i] : fmaf(e, part[i], acc[m][n][i]);
+                }
               }
           }
         }
+      }
+      __syncwarp();
+      if (lane == 0) dg::mbar_arrive(&empty[stage]);
+      if (++stage == kStages) stage = 0, phase ^= 1;
+      const float2 s = kFp4 ? make_float2(1.0f, 1.0f) : sw[g];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
+        if (n == 0 || n * 8 < count)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float t = sxt[n][i][g * a.T];
+            const float t = sxt[n][i][g * a.T], tx = kFp4 ? t : t * s.x, ty = kFp4 ? t : t * s.y;
 #pragma unroll
             for (int m = 0; m < kM; ++m) {
-              sum[m][n][i] = fmaf(t, acc[m][n][i], sum[m][n][i]);
-              sum[m][n][2 + i] = fmaf(t, acc[m][n][2 + i], sum[m][n][2 + i]);
+              sum[m][n][i] = fmaf(tx, acc[m][n][i], sum[m][n][i]);
+              sum[m][n][2 + i] = fmaf(ty, acc[m][n][2 + i], sum[m][n][2 + i]);
             }
           }
-      }
-      at = at + C::kStage == ring + kStages * C::kStage ? ring : at + C::kStage;
     }
-    // column blk * kBlock + (warp * kM + m) * 8 + g8 of h for tokens 2 q4, 2 q4 + 1 of each eight: gate in
-    // sum[0..1], up in sum[2..3]
+    // column blk * kBlock + (warp * kM + m) * 8 + row8 of h for tokens 2 q4, 2 q4 + 1 of each eight: gate in
+    // sum[0..1], up in sum[2..3] (E2M1 went into the MMAs as 2^-6 of itself)
+    constexpr float kUnit = kFp4 ? 64.0f : 1.0f;
     float hv[kM][NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -514,8 +538,8 @@ __global__ void __launch_bounds__(32 * kUpWarps, Up<kFp4, kBig>::kBlocksPerSm) m
         float top = 0;
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
-          const float gate = sum[m][n][i];
-          hv[m][n][i] = col < count ? w * (gate / (1.0f + expf(-gate)) * sum[m][n][2 + i]) : 0.0f;
+          const float gate = sum[m][n][i] * kUnit;
+          hv[m][n][i] = col < count ? w * (gate / (1.0f + expf(-gate)) * (sum[m][n][2 + i] * kUnit)) : 0.0f;
           const float v = fabsf(hv[m][n][i]);
           top = fmaxf(top, v < INFINITY ? v : 0.0f);
         }
@@ -532,95 +556,93 @@ __global__ void __launch_bounds__(32 * kUpWarps, Up<kFp4, kBig>::kBlocksPerSm) m
         if (col >= count) continue;
         float top = 0;
 #pragma unroll
-        for (int w = 0; w < kUpWarps; ++w) top = fmaxf(top, block_max[flip][w][col]);
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, block_max[flip][w][col]);
         // the largest to [2^14, 2^15); both powers stay normal
         const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 254) - 127 - 14;
-        const float up = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23), down = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        const float to_half = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23), back = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
         uint8_t* row = a.h + (static_cast<long long>(slot + col) * (a.I / 128) + blk * C::kBlock / 128) * kHBytes;
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
           // where the second kernel's lanes find this column of the 128: E4M3 as 16-byte pieces of two loads,
           // each of 64 bytes over four lanes; E2M1 in order
-          const int cc = blk * C::kBlock % 128 + (warp * kM + m) * 8 + g8;
+          const int cc = blk * C::kBlock % 128 + (warp * kM + m) * 8 + row8;
           const int place = kFp4 ? cc * 2 : cc / 64 * 128 + cc % 16 / 8 * 64 + cc % 64 / 16 * 16 + cc % 8 * 2;
-          *reinterpret_cast<__half*>(row + place) = __float2half_rn(hv[m][n][i] * up);
+          *reinterpret_cast<__half*>(row + place) = __float2half_rn(hv[m][n][i] * to_half);
         }
         if (warp == 0 && g8 == 0) {
           float* to = reinterpret_cast<float*>(row + 256);
-          if (kM == 2) to[0] = to[1] = down;
-          else to[blk & 1] = down;
+          if (C::kBlock == 128) to[0] = to[1] = back;
+          else to[blk & 1] = back;
         }
       }
   }
-  cp_async_wait<0>();
+  // no copy may be under way when the block ends
+  if (!ok && a.fault == 0)
+    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      if (!dg::mbar_wait(&full[i % kStages], i / kStages & 1, a.timeout_ns)) break;
 }
 
 // -------------------------------------------------------------------------------------------
 // Second kernel: y = c + W2 h
 // -------------------------------------------------------------------------------------------
+//
+// A tile is kRows output rows and all tokens. Its items are 128 columns of W2 of a job each; a warp takes a
+// run of them, with a ring of its own that its first lane fills. The tokens' side is small, shared by all
+// tiles and stays in L2: a warp reads its fragments of it straight into registers, an item ahead.
 
 template <bool kFp4, bool kBig>
-__global__ void __launch_bounds__(32 * Down<kFp4, kBig>::kWarps, 1) moe_down_kernel(const MoeArgs a) {
+__global__ void __launch_bounds__(Down<kFp4, kBig>::kThreads, 1) moe_down_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
   using C = Down<kFp4, kBig>;
-  using P = typename C::P;
+  using R = Rows<kFp4>;
   constexpr int kM = C::kM, NT = C::kCols / 8, kStages = C::kStages, kWarps = C::kWarps;
-  extern __shared__ __align__(128) uint8_t dyn[];
+  extern __shared__ uint8_t raw[];
   __shared__ Routing r;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g8 = lane / 4, q4 = lane & 3;
+  __shared__ uint64_t full_bars[kWarps][kStages];
+  uint8_t* const rings = aligned_1k(raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g8 = lane / 4, q4 = lane & 3, row8 = R::of(g8);
+  uint64_t* full = full_bars[warp];
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) dg::mbar_init(&full[i], 1);
+    dg::fence_mbarrier_init();
+    if (warp == 0) dg::tma_prefetch_desc(&map);
+  }
   // The first kernel let this one start only after its own wait: ids and weights are there, h is not yet.
-  build_routing<C::kCols, 32 * kWarps>(a, r, *reinterpret_cast<RoutingScratch*>(dyn), false);
+  build_routing<C::kCols, C::kThreads>(a, r, *reinterpret_cast<RoutingScratch*>(rings), false);
 
   const int groups = a.I / 128, items = r.jobs * groups, tiles = a.H / C::kRows;
-  const uint32_t row_bytes = kFp4 ? a.I / 2 : a.I;
   const int n4 = kFp4 ? a.H : (a.H / 128 + 3) / 4 * 4;
-  const uint32_t ring = dg::smem_addr(dyn) + warp * kStages * C::kStage;
-  float* expanded = reinterpret_cast<float*>(dyn + C::kRing) + warp * 64 * kM;
-  // every warp's sums of a tile, [2][warps][T][kRows]: the tile before is being added up meanwhile
-  float* sums = reinterpret_cast<float*>(dyn + C::kRing + C::kExpanded);
-  const int tile_sums = kWarps * a.T * C::kRows;
-  for (int i = threadIdx.x; i < 2 * tile_sums; i += 32 * kWarps) sums[i] = 0;
-
-  // a warp takes a run of the tile's (job, K-group) items
-  const int begin = warp * items / kWarps, end = (warp + 1) * items / kWarps, begin_job = begin / groups, begin_g = begin % groups;
-  int ft = begin < end ? blockIdx.x : tiles, fi = begin, fjob = begin_job, fg = begin_g;
-  uint32_t fto = ring;
-  const uint8_t* w_from = nullptr;
-  const int32_t* scale_from = nullptr;
-  const int scale_row = kFp4 ? n4 : 0;
-  auto aim = [&] {
-    const int e = r.job_expert[fjob];
-    w_from = a.w2 + (static_cast<long long>(e) * a.H + ft * C::kRows + P::row(lane)) * row_bytes + fg * P::kRowBytes + P::column(lane);
-    scale_from = kFp4 ? a.sf2 + (static_cast<long long>(e) * groups + fg) * n4 + ft * C::kRows + 4 * lane
-                      : a.sf2 + static_cast<long long>(e) * ((groups + 3) / 4) * n4 + (ft * C::kRows / 128 & ~3);
-  };
-  if (ft < tiles) aim();
-  auto fetch = [&] {
-    if (ft < tiles) {
-      const uint32_t to = fto + P::place(lane);
-#pragma unroll
-      for (int i = 0; i < P::kCopies; ++i) dg::cp_async_16(to + i * 512, w_from + i * P::kCopyRows * row_bytes);
-      if (lane < P::kScaleBytes / 16) dg::cp_async_16(fto + P::kBytes + 16 * lane, kFp4 ? scale_from : scale_from + fg / 4 * n4);
-      w_from += P::kRowBytes;
-      scale_from += scale_row;
-      ++fg;
-      if (++fi == end) {
-        fi = begin, fjob = begin_job, fg = begin_g, ft += gridDim.x;
-        if (ft < tiles) aim();
-      } else if (fg == groups) {
-        fg = 0, ++fjob;
-        aim();
-      }
-    }
-    fto = fto + C::kStage == ring + kStages * C::kStage ? ring : fto + C::kStage;
-    cp_async_commit();
-  };
+  uint8_t* const ring = rings + warp * kStages * C::kBox;
+  uint8_t* const scales = rings + C::kRing + warp * kStages * C::kScaleBytes;
+  float* expanded = reinterpret_cast<float*>(rings + C::kRing + C::kScales) + warp * 64 * kM;
+  float* sums = reinterpret_cast<float*>(rings + C::kRing + C::kScales + C::kExpanded);
+  for (int i = threadIdx.x; i < kWarps * a.T * C::kRows; i += C::kThreads) sums[i] = 0;
+  dg::fence_proxy_async_smem();        // the scratch in the rings was written by threads; copies write there next
   __syncthreads();
+
+  const int begin = warp * items / kWarps, end = (warp + 1) * items / kWarps, begin_job = begin / groups, begin_g = begin % groups;
+  int ft = begin < end && a.fault == 0 ? blockIdx.x : tiles, fi = begin, fjob = begin_job, fg = begin_g, fstage = 0, issued = 0;
+  auto fetch = [&] {
+    if (ft >= tiles) return;
+    if (lane == 0) {
+      const int e = r.job_expert[fjob], row = ft * C::kRows;
+      dg::mbar_arrive_expect_tx(&full[fstage], C::kBox + C::kScaleBytes);
+      dg::tma_load_2d(ring + fstage * C::kBox, &map, &full[fstage], fg * R::kBytes, e * a.H + row);
+      const int32_t* sf = kFp4 ? a.sf2 + (static_cast<long long>(e) * groups + fg) * n4 + row
+                               : a.sf2 + (static_cast<long long>(e) * ((groups + 3) / 4) + fg / 4) * n4 + (row / 128 & ~3);
+      bulk_load(scales + fstage * C::kScaleBytes, sf, C::kScaleBytes, &full[fstage]);
+    }
+    ++issued;
+    if (++fstage == kStages) fstage = 0;
+    if (++fi == end) fi = begin, fjob = begin_job, fg = begin_g, ft += gridDim.x;
+    else if (++fg == groups) fg = 0, ++fjob;
+  };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch();
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
 
-  // this lane's fragments of an item's tokens (as FP16 pairs) and the scales of its two columns, one item ahead
+  // this lane's fragments of an item's tokens (as FP16 pairs) and the scales of its two columns
+  constexpr bool kAhead = NT == 1;     // sixteen columns' fragments leave no registers for a second set
   uint4 hr[NT][4];
   uint2 hs[NT][2];
 #pragma unroll
@@ -647,10 +669,11 @@ __global__ void __launch_bounds__(32 * Down<kFp4, kBig>::kWarps, 1) moe_down_ker
   };
   if (begin < end && static_cast<int>(blockIdx.x) < tiles) load_h(begin_job, begin_g);
 
-  uint32_t at = ring;
-  int flip = 0;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, flip ^= 1) {
-    float* mine = sums + flip * tile_sums + warp * a.T * C::kRows;
+  bool ok = true;
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    float* mine = sums + warp * a.T * C::kRows;
     float sum[kM][NT][4];
 #pragma unroll
     for (int m = 0; m < kM; ++m)
@@ -659,94 +682,103 @@ __global__ void __launch_bounds__(32 * Down<kFp4, kBig>::kWarps, 1) moe_down_ker
     int job = begin_job, g = begin_g;
     for (int it = begin; it < end; ++it) {
       const int slot = r.job_slot[job], count = r.job_count[job];
-      uint4 hc[NT][4];
-      float sc[NT][2][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) hc[n][i] = hr[n][i];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sc[n][i][0] = __uint_as_float(hs[n][i].x), sc[n][i][1] = __uint_as_float(hs[n][i].y);
-      }
       const bool last = it + 1 == end, turn = g + 1 == groups;
-      if (!last) load_h(turn ? job + 1 : job, turn ? 0 : g + 1);
-      else if (tile + static_cast<int>(gridDim.x) < tiles) load_h(begin_job, begin_g);
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      fetch();
+      auto load_next = [&] {
+        if (!last) load_h(turn ? job + 1 : job, turn ? 0 : g + 1);
+        else if (tile + static_cast<int>(gridDim.x) < tiles) load_h(begin_job, begin_g);
+      };
+      uint4 hc[NT][4];
+      uint2 sc[NT][2];
+      if constexpr (kAhead) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hc[0][i] = hr[0][i];
+        sc[0][0] = hs[0][0], sc[0][1] = hs[0][1];
+        load_next();
+      }
+      auto frag = [&](int n, int i, int w) { return word_of(kAhead ? hc[n][i] : hr[n][i], w); };
+      auto col_scale = [&](int n, int i, int p) {
+        const uint2 v = kAhead ? sc[n][i] : hs[n][i];
+        return __uint_as_float(p ? v.y : v.x);
+      };
+      ok = wait_full(&full[stage], phase, a, ok);
+      const uint32_t at = dg::smem_addr(ring) + stage * C::kBox, packed = dg::smem_addr(scales) + stage * C::kScaleBytes;
       if constexpr (!kFp4) {
-        const float s = dg::ue8m0_value(lds32(at + P::kBytes + (tile * C::kRows / 128 & 3) * 4) >> (8 * (g & 3)) & 255);
+        const float s = dg::ue8m0_value(lds32(packed + (tile * C::kRows / 128 & 3) * 4) >> (8 * (g & 3)) & 255);
+        uint4 w0[2], w1[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) w0[p] = lds128(at + R::chunk(row8, 4 * p + q4)), w1[p] = lds128(at + R::chunk(8 + row8, 4 * p + q4));
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          float t[NT][2];
+          float acc[NT][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) t[n][0] = s * sc[n][0][p], t[n][1] = s * sc[n][1][p];
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            const uint4 w0 = lds128(at + P::chunk(16 * m + g8, 4 * p + q4)), w1 = lds128(at + P::chunk(16 * m + 8 + g8, 4 * p + q4));
-            float acc[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t u0 = word_of(w0, i), u1 = word_of(w1, i);
-              const uint32_t a0 = half2_of_e4m3(u0), a2 = half2_of_e4m3(u0 >> 16), a1 = half2_of_e4m3(u1), a3 = half2_of_e4m3(u1 >> 16);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                if (n == 0 || n * 8 < count)
-                  mma_f16(acc[n], a0, a1, a2, a3, word_of(hc[n][2 * p + i / 2], i % 2 * 2), word_of(hc[n][2 * p + i / 2], i % 2 * 2 + 1));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t u0 = word_of(w0[p], i), u1 = word_of(w1[p], i);
+            const uint32_t a0 = half2_of_e4m3(u0), a2 = half2_of_e4m3(u0 >> 16), a1 = half2_of_e4m3(u1), a3 = half2_of_e4m3(u1 >> 16);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                sum[m][n][i] = fmaf(t[n][i], acc[n][i], sum[m][n][i]);
-                sum[m][n][2 + i] = fmaf(t[n][i], acc[n][2 + i], sum[m][n][2 + i]);
+              if (n == 0 || n * 8 < count) {
+                const uint32_t b0 = frag(n, 2 * p + i / 2, i % 2 * 2), b1 = frag(n, 2 * p + i / 2, i % 2 * 2 + 1);
+                if (i == 0) mma_f16_zero(acc[n], a0, a1, a2, a3, b0, b1);
+                else mma_f16(acc[n], a0, a1, a2, a3, b0, b1);
               }
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (n == 0 || n * 8 < count)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float t = s * col_scale(n, i, p);
+                sum[0][n][i] = fmaf(t, acc[n][i], sum[0][n][i]);
+                sum[0][n][2 + i] = fmaf(t, acc[n][2 + i], sum[0][n][2 + i]);
+              }
         }
       } else {
-        P::expand_scales(at + P::kBytes, expanded, lane, 1.0f);
+        expand_scales<kM>(packed, expanded, lane);
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
           const uint4 s0 = reinterpret_cast<const uint4*>(expanded)[16 * m + g8], s1 = reinterpret_cast<const uint4*>(expanded)[16 * m + 8 + g8];
           float half[NT][4];
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const uint32_t u0 = lds32(at + P::chunk(16 * m + g8, b) + 4 * q4), u1 = lds32(at + P::chunk(16 * m + 8 + g8, b) + 4 * q4);
-            const float e0 = float_of(s0, b), e1 = float_of(s1, b);
+            const uint32_t u0 = lds32(at + R::chunk(16 * m + row8, b) + 4 * q4), u1 = lds32(at + R::chunk(16 * m + 8 + row8, b) + 4 * q4);
             float part[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t v0 = u0 >> (16 * i), v1 = u1 >> (16 * i);
               const uint32_t a0 = half2_of_e2m1(v0 & 255), a1 = half2_of_e2m1(v1 & 255), a2 = half2_of_e2m1(v0 >> 8 & 255), a3 = half2_of_e2m1(v1 >> 8 & 255);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                if (n == 0 || n * 8 < count) mma_f16(part[n], a0, a1, a2, a3, word_of(hc[n][b], 2 * i), word_of(hc[n][b], 2 * i + 1));
+                if (n == 0 || n * 8 < count) {
+                  if (i == 0) mma_f16_zero(part[n], a0, a1, a2, a3, frag(n, b, 0), frag(n, b, 1));
+                  else mma_f16(part[n], a0, a1, a2, a3, frag(n, b, 2), frag(n, b, 3));
+                }
             }
+            const float e0 = float_of(s0, b), e1 = float_of(s1, b);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
+              if (n == 0 || n * 8 < count)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float e = i < 2 ? e0 : e1;
-                half[n][i] = b % 2 == 0 ? e * part[n][i] : fmaf(e, part[n][i], half[n][i]);
-                if (b % 2 == 1) sum[m][n][i] = fmaf(sc[n][i % 2][b / 2], half[n][i], sum[m][n][i]);
-              }
+                for (int i = 0; i < 4; ++i) {
+                  const float e = i < 2 ? e0 : e1;
+                  half[n][i] = b % 2 == 0 ? e * part[n][i] : fmaf(e, part[n][i], half[n][i]);
+                  if (b % 2 == 1) sum[m][n][i] = fmaf(col_scale(n, i % 2, b / 2), half[n][i], sum[m][n][i]);
+                }
           }
         }
       }
-      at = at + C::kStage == ring + kStages * C::kStage ? ring : at + C::kStage;
+      __syncwarp();        // every lane has read the stage
+      if constexpr (!kAhead) load_next();
+      if (++stage == kStages) stage = 0, phase ^= 1;
+      fetch();
       if (last || turn) {
-        // rows g8 and g8 + 8 of each 16 for the job's tokens, into the warp's sums
+        // rows row8 and row8 + 8 of each 16 for the job's tokens, into the warp's sums
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int col = n * 8 + 2 * q4 + i;
             if (col < count) {
-              float* to = mine + r.token[slot + col] * C::kRows + g8;
+              float* to = mine + r.token[slot + col] * C::kRows + row8;
 #pragma unroll
               for (int m = 0; m < kM; ++m) {
                 to[16 * m] += sum[m][n][i];
@@ -762,19 +794,22 @@ __global__ void __launch_bounds__(32 * Down<kFp4, kBig>::kWarps, 1) moe_down_ker
       job += turn;
     }
     __syncthreads();
-    float* all = sums + flip * tile_sums;
-    for (int i = threadIdx.x; i < a.T * C::kRows; i += 32 * kWarps) {
+    for (int i = threadIdx.x; i < a.T * C::kRows; i += C::kThreads) {
       const long long to = static_cast<long long>(i / C::kRows) * a.H + tile * C::kRows + i % C::kRows;
       float v = a.c ? __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(a.c) + to))) : 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        v += all[w * a.T * C::kRows + i];
-        all[w * a.T * C::kRows + i] = 0;
+        v += sums[w * a.T * C::kRows + i];
+        sums[w * a.T * C::kRows + i] = 0;
       }
       a.y[to] = __float2bfloat16_rn(v);
     }
+    __syncthreads();
   }
-  cp_async_wait<0>();
+  // no copy may be under way when the block ends
+  if (!ok && a.fault == 0)
+    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      if (!dg::mbar_wait(&full[i % kStages], i / kStages & 1, a.timeout_ns)) break;
 }
 
 // -------------------------------------------------------------------------------------------
@@ -784,6 +819,7 @@ dg_status run_layer(const MoeArgs& a, const LaunchContext& ctx, cudaStream_t str
   using U = Up<kFp4, kBig>;
   using D = Down<kFp4, kBig>;
   static_assert(sizeof(RoutingScratch) <= U::kRing && sizeof(RoutingScratch) <= D::kRing, "scratch in the rings");
+  static_assert(U::kBlock == 64 || U::kBlock == 128, "h has two scales per 128 columns");
   const int up_smem = U::smem(a.H / 128, a.T), down_smem = D::smem(a.T);
   if (up_smem > kMaxSmem || down_smem > kMaxSmem) return DG_ERR_UNSUPPORTED;
   // once per thread and device: the limit, above what any shape needs
@@ -796,9 +832,14 @@ dg_status run_layer(const MoeArgs& a, const LaunchContext& ctx, cudaStream_t str
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return dg::record_cuda_error(e);
+  const int per = kFp4 ? 2 : 1;
+  CUtensorMap up_map, down_map;
+  if (!dg::byte_rows_map(&up_map, a.w13, static_cast<uint64_t>(a.E) * 2 * a.I, a.H / per, U::kBlock, Rows<kFp4>::kBytes) ||
+      !dg::byte_rows_map(&down_map, a.w2, static_cast<uint64_t>(a.E) * a.H, a.I / per, D::kRows, Rows<kFp4>::kBytes))
+    return DG_ERR_CUDA;
   const unsigned up_grid = static_cast<unsigned>(U::kBlocksPerSm * ctx.sms), down_grid = static_cast<unsigned>(std::min(ctx.sms, a.H / D::kRows));
-  if (dg_status s = dg::launch(moe_up_kernel<kFp4, kBig>, up_grid, 32 * kUpWarps, static_cast<size_t>(up_smem), stream, ctx.pdl, a); s != DG_OK) return s;
-  return dg::launch(moe_down_kernel<kFp4, kBig>, down_grid, 32 * D::kWarps, static_cast<size_t>(down_smem), stream, ctx.pdl, a);
+  if (dg_status s = dg::launch(moe_up_kernel<kFp4, kBig>, up_grid, U::kThreads, static_cast<size_t>(up_smem), stream, ctx.pdl, up_map, a); s != DG_OK) return s;
+  return dg::launch(moe_down_kernel<kFp4, kBig>, down_grid, D::kThreads, static_cast<size_t>(down_smem), stream, ctx.pdl, down_map, a);
 }
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -821,7 +862,7 @@ dg_status few_tokens(const void* x, const int32_t* sfx, const void* w13, const i
   if (dg_status s = ws.acquire(stream, static_cast<size_t>(T) * topk * (I / 128) * kHBytes, &h); s != DG_OK) return s;
   const MoeArgs a{static_cast<const uint8_t*>(x), sfx, static_cast<const uint8_t*>(w13), sf13, static_cast<const uint8_t*>(w2), sf2,
                   ids, weights, static_cast<const __nv_bfloat16*>(c), static_cast<__nv_bfloat16*>(y), static_cast<uint8_t*>(h),
-                  ctx.status, T, topk, E, H, I};
+                  ctx.status, dg::pipeline_wait_timeout_ns(), dg::debug_fault_mode(), T, topk, E, H, I};
   return T <= 8 ? run_layer<kFp4, false>(a, ctx, stream) : run_layer<kFp4, true>(a, ctx, stream);
 }
 

@@ -6,6 +6,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "dg.h"
@@ -23,6 +24,10 @@ dg_status launch_context(LaunchContext* out);
 
 // Records `e` for dg_last_cuda_error and returns DG_ERR_CUDA.
 dg_status record_cuda_error(cudaError_t e);
+
+// Tensor map of a [rows, row_bytes] byte matrix (16-byte aligned rows), copied in boxes of box_rows x box_bytes
+// with the swizzle of that width (64 or 128 bytes). Maps are cached per host thread. False on failure.
+bool byte_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows, uint32_t box_bytes);
 
 // `bytes` of the stream's workspace, past the stream-K arrival counters at its start (which stay
 // zero). Held until the object goes out of scope, which has to be after the launches that use it.

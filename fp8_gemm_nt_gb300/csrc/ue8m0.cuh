@@ -9,7 +9,7 @@
 namespace dg {
 
 // Bits of the device status word (the GEMM kernels set the same ones).
-enum : uint32_t { kBadIndexBit = 1u << 6 };
+enum : uint32_t { kTimeoutBit = 1u << 5, kBadIndexBit = 1u << 6 };
 
 // 2^(e - 127); code 0 is the subnormal 2^-127, code 255 NaN.
 __device__ __forceinline__ float ue8m0_value(uint32_t e) {
