@@ -170,63 +170,53 @@ __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t half2_of_e2m1(uint32_t two) {
-  uint32_t d;
-  asm("{ .reg .b8 b; cvt.u8.u32 b, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(d) : "r"(two));
-  return d;
-}
-
 // Four E2M1 codes as E4M3 of 2^-6 of their values: the sign to bit 7, the two exponent bits and the
 // mantissa bit to the lowest exponent bits and the highest mantissa bit (E2M1's subnormal 0.5 becomes
 // the subnormal 2^-7). Even elements of eight are the low nibbles, odd ones the high nibbles.
 __device__ __forceinline__ uint32_t e4m3_of_even(uint32_t w) { return (w << 4 & 0x80808080u) | (w << 2 & 0x1C1C1C1Cu); }
 __device__ __forceinline__ uint32_t e4m3_of_odd(uint32_t w) { return (w & 0x80808080u) | (w >> 2 & 0x1C1C1C1Cu); }
 
+// The same as the upper bytes of FP16 of 2^-14 of their values (the lower bytes are 0), and two of them as a
+// pair: bytes 0 and 1, or 2 and 3, of b.
+__device__ __forceinline__ uint32_t f16_of_even(uint32_t w) { return (w << 4 & 0x80808080u) | (w << 1 & 0x0E0E0E0Eu); }
+__device__ __forceinline__ uint32_t f16_of_odd(uint32_t w) { return (w & 0x80808080u) | (w >> 3 & 0x0E0E0E0Eu); }
+__device__ __forceinline__ uint32_t lower_pair(uint32_t b) { return __byte_perm(b, 0, 0x1404); }
+__device__ __forceinline__ uint32_t upper_pair(uint32_t b) { return __byte_perm(b, 0, 0x3424); }
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The same on a sum that starts at zero.
 __device__ __forceinline__ void mma_e4m3_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t p) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t p) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(p));
-  return v;
-}
+// Plain loads of shared memory: the waits before them clobber memory, so they stay after those, and the
+// compiler may otherwise move them ahead of other work.
+template <class T>
+__device__ __forceinline__ T lds(const uint8_t* p) { return *reinterpret_cast<const T*>(p); }
 __device__ __forceinline__ uint2 ld_cg_v2(const void* p) {
   uint2 v;
   asm volatile("ld.global.cg.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ float float_of(const uint4& v, int i) { return __uint_as_float(word_of(v, i)); }
+__device__ __forceinline__ float float_of(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // Untiled bulk copy (16-byte aligned addresses and size) that completes on `bar`.
 __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
@@ -253,22 +243,14 @@ struct Rows {
   }
 };
 
-// FP32 values of the four UE8M0 codes of a word.
+// FP32 values of the four UE8M0 codes of a word: the code in the exponent's place, unless a code is 0 (2^-127,
+// a subnormal) or 255 (NaN). A byte of v is 0 where (v - 0x01010101) & ~v has its top bit (or a byte below
+// is 0, which is as good a reason to look closer).
 __device__ __forceinline__ float4 four_scales(uint32_t w) {
-  return make_float4(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255), dg::ue8m0_value(w >> 16 & 255), dg::ue8m0_value(w >> 24));
-}
-
-// E2M1: the packed scales of 16 kM rows at `packed` as FP32 at `to` [16 kM][4], each by one lane; visible to
-// the warp at the end.
-template <int kM>
-__device__ __forceinline__ void expand_scales(uint32_t packed, float* to, int lane) {
-  if constexpr (kM == 1) {
-    const uint32_t w = lds32(packed + lane / 2 * 4) >> (lane & 1) * 16;
-    reinterpret_cast<float2*>(to)[lane] = make_float2(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255));
-  } else {
-    reinterpret_cast<float4*>(to)[lane] = four_scales(lds32(packed + lane * 4));
-  }
-  __syncwarp();
+  if (((w - 0x01010101u) & ~w & 0x80808080u) || ((~w - 0x01010101u) & w & 0x80808080u))
+    return make_float4(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255), dg::ue8m0_value(w >> 16 & 255), dg::ue8m0_value(w >> 24));
+  return make_float4(__uint_as_float(w << 23 & 0x7F800000u), __uint_as_float(w << 15 & 0x7F800000u), __uint_as_float(w << 7 & 0x7F800000u),
+                     __uint_as_float(w >> 1 & 0x7F800000u));
 }
 
 // A wait that has run out once is not repeated: the kernel then runs through on what is in its rings, with
@@ -304,7 +286,10 @@ struct Up {
 };
 template <bool kFp4, bool kBig>
 struct Down {
-  static constexpr int kM = kFp4 && kBig ? 2 : 1, kCols = kBig ? 16 : 8;
+  static constexpr int kM = kFp4 && kBig ? 2 : 1;
+  // with 32 rows, 16 columns' fragments and sums would not fit the registers: an expert of more than 8 tokens
+  // is then two jobs, the second of which finds the weights in L2
+  static constexpr int kCols = kBig && kM == 1 ? 16 : 8;
   static constexpr int kRows = 16 * kM, kWarps = 16, kThreads = 32 * kWarps;
   static constexpr int kStages = kFp4 ? (kBig ? 4 : 6) : 4;
   static constexpr int kBox = kRows * Rows<kFp4>::kBytes;           // a stage of a warp
@@ -443,87 +428,94 @@ __global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlo
     for (int g = 0; g < groups; ++g) {
       fetch();
       ok = wait_full(&full[stage], phase, a, ok);
-      const uint32_t at = dg::smem_addr(ring) + stage * C::kStage;
-      const uint32_t gate = at + warp * 8 * kM * R::kBytes, up = gate + C::kBox, tokens = at + C::kTokens + g8 * C::kTokenStride;
-      float acc[kM][NT][4];
-      if constexpr (!kFp4) {
-        uint4 w0[2], w1[2], x[NT][2];
+      const uint8_t* at = ring + stage * C::kStage;
+      const uint8_t* gate = at + warp * 8 * kM * R::kBytes;
+      const uint8_t* up = gate + C::kBox;
+      const uint8_t* tokens = at + C::kTokens + g8 * C::kTokenStride;
+      // one item, for N eights of columns (a branch for the second eight inside would cost those that have one)
+      auto item = [&](auto eights) {
+        constexpr int N = decltype(eights)::value;
+        float acc[kM][N][4];
+        if constexpr (!kFp4) {
+          uint4 w0[2], w1[2], x[N][2];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          w0[p] = lds128(gate + R::chunk(row8, 4 * p + q4)), w1[p] = lds128(up + R::chunk(row8, 4 * p + q4));
+          for (int p = 0; p < 2; ++p) {
+            w0[p] = lds<uint4>(gate + R::chunk(row8, 4 * p + q4)), w1[p] = lds<uint4>(up + R::chunk(row8, 4 * p + q4));
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n == 0 || n * 8 < count) x[n][p] = lds128(tokens + n * 8 * C::kTokenStride + 64 * p + 16 * q4);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (n == 0 || n * 8 < count) {
-            mma_e4m3_zero(acc[0][n], w0[0].x, w1[0].x, w0[0].y, w1[0].y, x[n][0].x, x[n][0].y);
-            mma_e4m3(acc[0][n], w0[0].z, w1[0].z, w0[0].w, w1[0].w, x[n][0].z, x[n][0].w);
-            mma_e4m3(acc[0][n], w0[1].x, w1[1].x, w0[1].y, w1[1].y, x[n][1].x, x[n][1].y);
-            mma_e4m3(acc[0][n], w0[1].z, w1[1].z, w0[1].w, w1[1].w, x[n][1].z, x[n][1].w);
+            for (int n = 0; n < N; ++n)
+              x[n][p] = lds<uint4>(tokens + n * 8 * C::kTokenStride + 64 * p + 16 * q4);
           }
-      } else {
-        // the warp's scales: 8 kM gate rows, then as many up rows
-        const uint32_t packed = at + C::kScales + warp * 32 * kM;
-        const uint32_t w = lds32(packed + (kM == 1 ? (lane / 16) * 4 * C::kBlock + lane % 16 / 2 * 4 : (lane / 16) * 4 * C::kBlock + lane % 16 * 4));
-        if constexpr (kM == 1) {
-          const uint32_t v = w >> (lane & 1) * 16;
-          reinterpret_cast<float2*>(expanded)[lane] = make_float2(dg::ue8m0_value(v & 255), dg::ue8m0_value(v >> 8 & 255));
-        } else {
-          reinterpret_cast<float4*>(expanded)[lane] = four_scales(w);
-        }
-        __syncwarp();
-        uint4 scale[kM][2];
 #pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          scale[m][0] = reinterpret_cast<const uint4*>(expanded)[8 * m + g8];
-          scale[m][1] = reinterpret_cast<const uint4*>(expanded)[8 * kM + 8 * m + g8];
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t even[NT], odd[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n == 0 || n * 8 < count) {
-              const uint2 x = lds64(tokens + n * 8 * C::kTokenStride + 32 * b + 8 * q4);
-              even[n] = __byte_perm(x.x, x.y, 0x6420), odd[n] = __byte_perm(x.x, x.y, 0x7531);
+          for (int n = 0; n < N; ++n)
+            {
+              mma_e4m3_zero(acc[0][n], w0[0].x, w1[0].x, w0[0].y, w1[0].y, x[n][0].x, x[n][0].y);
+              mma_e4m3(acc[0][n], w0[0].z, w1[0].z, w0[0].w, w1[0].w, x[n][0].z, x[n][0].w);
+              mma_e4m3(acc[0][n], w0[1].x, w1[1].x, w0[1].y, w1[1].y, x[n][1].x, x[n][1].y);
+              mma_e4m3(acc[0][n], w0[1].z, w1[1].z, w0[1].w, w1[1].w, x[n][1].z, x[n][1].w);
             }
+        } else {
+          // the warp's scales, 8 kM gate rows and then as many up rows, as FP32: each converted by one lane
+          const uint8_t* packed = at + C::kScales + warp * 32 * kM + (lane / 16) * 4 * C::kBlock;
+          if constexpr (kM == 1) {
+            const uint32_t w = lds<uint32_t>(packed + lane % 16 / 2 * 4) >> (lane & 1) * 16;
+            reinterpret_cast<float2*>(expanded)[lane] = make_float2(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255));
+          } else {
+            reinterpret_cast<float4*>(expanded)[lane] = four_scales(lds<uint32_t>(packed + lane % 16 * 4));
+          }
+          __syncwarp();
+          float4 scale[kM][2];
 #pragma unroll
           for (int m = 0; m < kM; ++m) {
-            const uint32_t u0 = lds32(gate + m * 8 * R::kBytes + R::chunk(row8, b) + 4 * q4), u1 = lds32(up + m * 8 * R::kBytes + R::chunk(row8, b) + 4 * q4);
-            const uint32_t a0 = e4m3_of_even(u0), a1 = e4m3_of_even(u1), a2 = e4m3_of_odd(u0), a3 = e4m3_of_odd(u1);
-            const float e0 = float_of(scale[m][0], b), e1 = float_of(scale[m][1], b);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              if (n == 0 || n * 8 < count) {
-                float part[4];
-                mma_e4m3_zero(part, a0, a1, a2, a3, even[n], odd[n]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float e = i < 2 ? e0 : e1;
-                  acc[m][n][i] = b == 0 ? e * part[i] : fmaf(e, part[i], acc[m][n][i]);
-                }
-              }
+            scale[m][0] = reinterpret_cast<const float4*>(expanded)[8 * m + g8];
+            scale[m][1] = reinterpret_cast<const float4*>(expanded)[8 * kM + 8 * m + g8];
           }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) dg::mbar_arrive(&empty[stage]);
-      if (++stage == kStages) stage = 0, phase ^= 1;
-      const float2 s = kFp4 ? make_float2(1.0f, 1.0f) : sw[g];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n == 0 || n * 8 < count)
+          for (int b = 0; b < 4; ++b) {
+            uint32_t even[N], odd[N];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float t = sxt[n][i][g * a.T], tx = kFp4 ? t : t * s.x, ty = kFp4 ? t : t * s.y;
+            for (int n = 0; n < N; ++n)
+              {
+                const uint2 x = lds<uint2>(tokens + n * 8 * C::kTokenStride + 32 * b + 8 * q4);
+                even[n] = __byte_perm(x.x, x.y, 0x6420), odd[n] = __byte_perm(x.x, x.y, 0x7531);
+              }
 #pragma unroll
             for (int m = 0; m < kM; ++m) {
-              sum[m][n][i] = fmaf(tx, acc[m][n][i], sum[m][n][i]);
-              sum[m][n][2 + i] = fmaf(ty, acc[m][n][2 + i], sum[m][n][2 + i]);
+              const uint32_t u0 = lds<uint32_t>(gate + m * 8 * R::kBytes + R::chunk(row8, b) + 4 * q4);
+              const uint32_t u1 = lds<uint32_t>(up + m * 8 * R::kBytes + R::chunk(row8, b) + 4 * q4);
+              const uint32_t a0 = e4m3_of_even(u0), a1 = e4m3_of_even(u1), a2 = e4m3_of_odd(u0), a3 = e4m3_of_odd(u1);
+              const float e0 = float_of(scale[m][0], b), e1 = float_of(scale[m][1], b);
+#pragma unroll
+              for (int n = 0; n < N; ++n)
+                {
+                  float part[4];
+                  mma_e4m3_zero(part, a0, a1, a2, a3, even[n], odd[n]);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float e = i < 2 ? e0 : e1;
+                    acc[m][n][i] = b == 0 ? e * part[i] : fmaf(e, part[i], acc[m][n][i]);
+                  }
+                }
             }
           }
+        }
+        __syncwarp();
+        if (lane == 0) dg::mbar_arrive(&empty[stage]);
+        const float2 s = kFp4 ? make_float2(1.0f, 1.0f) : sw[g];
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float t = sxt[n][i][g * a.T], tx = kFp4 ? t : t * s.x, ty = kFp4 ? t : t * s.y;
+#pragma unroll
+              for (int m = 0; m < kM; ++m) {
+                sum[m][n][i] = fmaf(tx, acc[m][n][i], sum[m][n][i]);
+                sum[m][n][2 + i] = fmaf(ty, acc[m][n][2 + i], sum[m][n][2 + i]);
+              }
+            }
+      };
+      if (NT == 1 || count <= 8) item(std::integral_constant<int, 1>());
+      else item(std::integral_constant<int, NT>());
+      if (++stage == kStages) stage = 0, phase ^= 1;
     }
     // column blk * kBlock + (warp * kM + m) * 8 + row8 of h for tokens 2 q4, 2 q4 + 1 of each eight: gate in
     // sum[0..1], up in sum[2..3] (E2M1 went into the MMAs as 2^-6 of itself)
@@ -559,14 +551,15 @@ __global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlo
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, block_max[flip][w][col]);
         // the largest to [2^14, 2^15); both powers stay normal
         const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 254) - 127 - 14;
-        const float to_half = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23), back = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        const float to_half = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        const float back = __uint_as_float(static_cast<uint32_t>(127 + ex + (kFp4 ? 14 : 0)) << 23);   // E2M1 enters the MMAs as 2^-14 of itself
         uint8_t* row = a.h + (static_cast<long long>(slot + col) * (a.I / 128) + blk * C::kBlock / 128) * kHBytes;
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
           // where the second kernel's lanes find this column of the 128: E4M3 as 16-byte pieces of two loads,
-          // each of 64 bytes over four lanes; E2M1 in order
+          // each of 64 bytes over four lanes; E2M1 the even ones of every eight, then the odd ones
           const int cc = blk * C::kBlock % 128 + (warp * kM + m) * 8 + row8;
-          const int place = kFp4 ? cc * 2 : cc / 64 * 128 + cc % 16 / 8 * 64 + cc % 64 / 16 * 16 + cc % 8 * 2;
+          const int place = kFp4 ? (cc / 8 * 8 + cc % 2 * 4 + cc % 8 / 2) * 2 : cc / 64 * 128 + cc % 16 / 8 * 64 + cc % 64 / 16 * 16 + cc % 8 * 2;
           *reinterpret_cast<__half*>(row + place) = __float2half_rn(hv[m][n][i] * to_half);
         }
         if (warp == 0 && g8 == 0) {
@@ -701,71 +694,73 @@ __global__ void __launch_bounds__(Down<kFp4, kBig>::kThreads, 1) moe_down_kernel
         return __uint_as_float(p ? v.y : v.x);
       };
       ok = wait_full(&full[stage], phase, a, ok);
-      const uint32_t at = dg::smem_addr(ring) + stage * C::kBox, packed = dg::smem_addr(scales) + stage * C::kScaleBytes;
-      if constexpr (!kFp4) {
-        const float s = dg::ue8m0_value(lds32(packed + (tile * C::kRows / 128 & 3) * 4) >> (8 * (g & 3)) & 255);
-        uint4 w0[2], w1[2];
+      const uint8_t* at = ring + stage * C::kBox;
+      const uint8_t* packed = scales + stage * C::kScaleBytes;
+      // one item, for N eights of columns
+      auto item = [&](auto eights) {
+        constexpr int N = decltype(eights)::value;
+        if constexpr (!kFp4) {
+          const float s = dg::ue8m0_value(lds<uint32_t>(packed + (tile * C::kRows / 128 & 3) * 4) >> (8 * (g & 3)) & 255);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) w0[p] = lds128(at + R::chunk(row8, 4 * p + q4)), w1[p] = lds128(at + R::chunk(8 + row8, 4 * p + q4));
+          for (int p = 0; p < 2; ++p) {
+            const uint4 w0 = lds<uint4>(at + R::chunk(row8, 4 * p + q4)), w1 = lds<uint4>(at + R::chunk(8 + row8, 4 * p + q4));
+            float acc[N][4];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          float acc[NT][4];
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t u0 = word_of(w0, i), u1 = word_of(w1, i);
+              const uint32_t a0 = half2_of_e4m3(u0), a2 = half2_of_e4m3(u0 >> 16), a1 = half2_of_e4m3(u1), a3 = half2_of_e4m3(u1 >> 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t u0 = word_of(w0[p], i), u1 = word_of(w1[p], i);
-            const uint32_t a0 = half2_of_e4m3(u0), a2 = half2_of_e4m3(u0 >> 16), a1 = half2_of_e4m3(u1), a3 = half2_of_e4m3(u1 >> 16);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              if (n == 0 || n * 8 < count) {
+              for (int n = 0; n < N; ++n) {
                 const uint32_t b0 = frag(n, 2 * p + i / 2, i % 2 * 2), b1 = frag(n, 2 * p + i / 2, i % 2 * 2 + 1);
                 if (i == 0) mma_f16_zero(acc[n], a0, a1, a2, a3, b0, b1);
                 else mma_f16(acc[n], a0, a1, a2, a3, b0, b1);
               }
-          }
+            }
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n == 0 || n * 8 < count)
+            for (int n = 0; n < N; ++n)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const float t = s * col_scale(n, i, p);
                 sum[0][n][i] = fmaf(t, acc[n][i], sum[0][n][i]);
                 sum[0][n][2 + i] = fmaf(t, acc[n][2 + i], sum[0][n][2 + i]);
               }
-        }
-      } else {
-        expand_scales<kM>(packed, expanded, lane);
+          }
+        } else {
+          // the rows' scales as FP32, each converted by one lane
+          if constexpr (kM == 1) {
+            const uint32_t w = lds<uint32_t>(packed + lane / 2 * 4) >> (lane & 1) * 16;
+            reinterpret_cast<float2*>(expanded)[lane] = make_float2(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255));
+          } else {
+            reinterpret_cast<float4*>(expanded)[lane] = four_scales(lds<uint32_t>(packed + lane * 4));
+          }
+          __syncwarp();
 #pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          const uint4 s0 = reinterpret_cast<const uint4*>(expanded)[16 * m + g8], s1 = reinterpret_cast<const uint4*>(expanded)[16 * m + 8 + g8];
-          float half[NT][4];
+          for (int m = 0; m < kM; ++m) {
+            const float4 s0 = reinterpret_cast<const float4*>(expanded)[16 * m + g8], s1 = reinterpret_cast<const float4*>(expanded)[16 * m + 8 + g8];
+            float half[N][4];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t u0 = lds32(at + R::chunk(16 * m + row8, b) + 4 * q4), u1 = lds32(at + R::chunk(16 * m + 8 + row8, b) + 4 * q4);
-            float part[NT][4];
+            for (int b = 0; b < 4; ++b) {
+              const uint32_t u0 = lds<uint32_t>(at + R::chunk(16 * m + row8, b) + 4 * q4), u1 = lds<uint32_t>(at + R::chunk(16 * m + 8 + row8, b) + 4 * q4);
+              const uint32_t even0 = f16_of_even(u0), even1 = f16_of_even(u1), odd0 = f16_of_odd(u0), odd1 = f16_of_odd(u1);
+              const float e0 = float_of(s0, b), e1 = float_of(s1, b);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t v0 = u0 >> (16 * i), v1 = u1 >> (16 * i);
-              const uint32_t a0 = half2_of_e2m1(v0 & 255), a1 = half2_of_e2m1(v1 & 255), a2 = half2_of_e2m1(v0 >> 8 & 255), a3 = half2_of_e2m1(v1 >> 8 & 255);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                if (n == 0 || n * 8 < count) {
-                  if (i == 0) mma_f16_zero(part[n], a0, a1, a2, a3, frag(n, b, 0), frag(n, b, 1));
-                  else mma_f16(part[n], a0, a1, a2, a3, frag(n, b, 2), frag(n, b, 3));
-                }
-            }
-            const float e0 = float_of(s0, b), e1 = float_of(s1, b);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              if (n == 0 || n * 8 < count)
+              for (int n = 0; n < N; ++n) {
+                float part[4];
+                mma_f16_zero(part, lower_pair(even0), lower_pair(even1), upper_pair(even0), upper_pair(even1), frag(n, b, 0), frag(n, b, 1));
+                mma_f16(part, lower_pair(odd0), lower_pair(odd1), upper_pair(odd0), upper_pair(odd1), frag(n, b, 2), frag(n, b, 3));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const float e = i < 2 ? e0 : e1;
-                  half[n][i] = b % 2 == 0 ? e * part[n][i] : fmaf(e, part[n][i], half[n][i]);
+                  half[n][i] = b % 2 == 0 ? e * part[i] : fmaf(e, part[i], half[n][i]);
                   if (b % 2 == 1) sum[m][n][i] = fmaf(col_scale(n, i % 2, b / 2), half[n][i], sum[m][n][i]);
                 }
+              }
+            }
           }
         }
-      }
+      };
+      if (NT == 1 || count <= 8) item(std::integral_constant<int, 1>());
+      else item(std::integral_constant<int, NT>());
       __syncwarp();        // every lane has read the stage
       if constexpr (!kAhead) load_next();
       if (++stage == kStages) stage = 0, phase ^= 1;
