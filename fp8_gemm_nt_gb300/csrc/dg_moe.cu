@@ -19,6 +19,9 @@
 // largest; plain FP32 would double what the second kernel reads). The second kernel owns output rows: a
 // block sums all experts for its 16 (32) rows of W2 and every token, in an order that depends on the
 // sizes alone, and writes each output once. No atomics on values.
+//
+// Where a layer has fewer pieces of work than the GPU has room for blocks, a cluster of blocks shares a
+// piece, each with a part of K, and sums through distributed shared memory in the order of its ranks.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -45,6 +48,7 @@ constexpr int kMaxSlots = kMaxTokens * kMaxTopk;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kHBytes = 272;            // 128 columns of h of a slot: 256 bytes of FP16, FP32 scales of both halves, padding
 constexpr int kMaxSmem = 216 * 1024;
+constexpr int kHalfSm = 104 * 1024;     // dynamic shared memory of a block of which two are resident
 
 struct MoeArgs {
   const uint8_t* x;        // [T, H] E4M3
@@ -261,7 +265,7 @@ __device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, const 
   return false;
 }
 
-constexpr int round_up(int v, int to) { return (v + to - 1) / to * to; }
+__host__ __device__ constexpr int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
 // Shapes. kBig (more than 8 tokens): experts then have several tokens; 16 columns, and for E2M1, whose
 // tokens' side and conversions cost as much as its bytes, 32 rows a warp.
@@ -281,8 +285,13 @@ struct Up {
   static constexpr int kStage = round_up(kScales + (kFp4 ? 8 * kBlock : 0), 1024);
   static constexpr int kRing = kStages * kStage;
   static constexpr int kExpanded = kFp4 ? kWarps * 256 * kM : 0;    // E2M1: a warp's scales as FP32
-  // then the tokens' scales [groups, T], and for E4M3 each warp's two scales of every group
-  static int smem(int groups, int T) { return 1024 + kRing + kExpanded + (groups * T + 1) / 2 * 8 + (kFp4 ? 0 : kWarps * groups * 8); }
+  // then the tokens' scales [groups, T], for E4M3 each warp's two scales of every group, and a cluster's
+  // partial sums of two units
+  static constexpr int kSums = kM * kCols / 2;                      // a thread's
+  static __host__ __device__ int partials(int groups, int T) {
+    return kRing + kExpanded + round_up((groups * T + 1) / 2 * 8 + (kFp4 ? 0 : kWarps * groups * 8), 16);
+  }
+  static int smem(int groups, int T, int cluster) { return 1024 + partials(groups, T) + (cluster > 1 ? 2 * kThreads * kSums * 4 : 0); }
 };
 template <bool kFp4, bool kBig>
 struct Down {
@@ -298,9 +307,21 @@ struct Down {
   static constexpr int kScaleBytes = kFp4 ? 4 * kRows : 16;
   static constexpr int kScales = kWarps * kStages * kScaleBytes;
   static constexpr int kExpanded = kFp4 ? kWarps * 256 * kM : 0;
-  // then every warp's sums of a tile, [warps][T][kRows]
-  static int smem(int T) { return 1024 + kRing + kScales + kExpanded + kWarps * T * kRows * 4; }
+  // then every warp's sums of a tile, [warps][T][kRows], and the block's
+  static int smem(int T) { return 1024 + kRing + kScales + kExpanded + (kWarps + 1) * T * kRows * 4; }
 };
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int cluster_blocks() {
+  int n;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
 
 __device__ __forceinline__ uint8_t* aligned_1k(uint8_t* p) {
   return p + ((1024u - (dg::smem_addr(p) & 1023u)) & 1023u);
@@ -350,10 +371,14 @@ __global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlo
   dg::fence_proxy_async_smem();        // the scratch in the ring was written by threads; copies write there next
   __syncthreads();
   const int units = r.jobs * blocks;
+  // the cluster's share of the units, and this block's of their column groups
+  const int ranks = cluster_blocks(), rank = ranks > 1 ? dg::cluster_cta_rank() : 0;
+  const int first_unit = blockIdx.x / ranks, unit_step = gridDim.x / ranks;
+  const int group_begin = rank * groups / ranks, group_end = (rank + 1) * groups / ranks;
   bool ok = true;
 
   // the stage to copy: column group fg of unit fu, the issued'th of the block
-  int fu = blockIdx.x, fg = 0, fstage = 0, issued = 0;
+  int fu = first_unit, fg = group_begin, fstage = 0, issued = 0;
   uint32_t fphase = 1;
   auto fetch = [&] {
     if (fu >= units) return;
@@ -380,7 +405,7 @@ __global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlo
     }
     ++issued;
     if (++fstage == kStages) fstage = 0, fphase ^= 1;
-    if (++fg == groups) fg = 0, fu += gridDim.x;
+    if (++fg == group_end) fg = group_begin, fu += unit_step;
   };
 
   const int g8 = lane / 4, q4 = lane & 3, row8 = R::of(g8);
@@ -396,10 +421,10 @@ __global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlo
     }
   };
   for (int i = 0; i < C::kAhead; ++i) fetch();
-  if (!kFp4 && static_cast<int>(blockIdx.x) < units) load_scales(blockIdx.x);
+  if (!kFp4 && first_unit < units) load_scales(first_unit);
   int stage = 0, flip = 0;
   uint32_t phase = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x, flip ^= 1) {
+  for (int u = first_unit; u < units; u += unit_step, flip ^= 1) {
     const int job = u / blocks, blk = u % blocks, slot = r.job_slot[job], count = r.job_count[job];
     float sum[kM][NT][4];
     const float* sxt[NT][2];
@@ -423,9 +448,9 @@ __global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlo
         if (4 * lane + 3 < groups) sw[4 * lane + 3] = make_float2(gate.w, up.w);
       }
       __syncwarp();
-      if (u + static_cast<int>(gridDim.x) < units) load_scales(u + gridDim.x);
+      if (u + unit_step < units) load_scales(u + unit_step);
     }
-    for (int g = 0; g < groups; ++g) {
+    for (int g = group_begin; g < group_end; ++g) {
       fetch();
       ok = wait_full(&full[stage], phase, a, ok);
       const uint8_t* at = ring + stage * C::kStage;
@@ -517,6 +542,28 @@ __global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlo
       else item(std::integral_constant<int, NT>());
       if (++stage == kStages) stage = 0, phase ^= 1;
     }
+    if (ranks > 1) {
+      // the first block of the cluster adds the others' sums to its own
+      float4* mine = reinterpret_cast<float4*>(ring + C::partials(groups, a.T)) + flip * C::kThreads * (C::kSums / 4);
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mine[(m * NT + n) * C::kThreads + threadIdx.x] = make_float4(sum[m][n][0], sum[m][n][1], sum[m][n][2], sum[m][n][3]);
+      dg::cluster_sync();
+      if (rank != 0) continue;
+      for (int other = 1; other < ranks; ++other) {
+        const uint32_t theirs = dg::map_to_rank(mine, other);
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 v = dg::ld_shared_cluster_v4(theirs + ((m * NT + n) * C::kThreads + threadIdx.x) * 16);
+            sum[m][n][0] += __uint_as_float(v.x), sum[m][n][1] += __uint_as_float(v.y);
+            sum[m][n][2] += __uint_as_float(v.z), sum[m][n][3] += __uint_as_float(v.w);
+          }
+      }
+    }
     // column blk * kBlock + (warp * kM + m) * 8 + row8 of h for tokens 2 q4, 2 q4 + 1 of each eight: gate in
     // sum[0..1], up in sum[2..3] (E2M1 went into the MMAs as 2^-6 of itself)
     constexpr float kUnit = kFp4 ? 64.0f : 1.0f;
@@ -569,10 +616,11 @@ __global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlo
         }
       }
   }
-  // no copy may be under way when the block ends
+  // no copy may be under way when the block ends, and no block of a cluster be gone whose sums are read
   if (!ok && a.fault == 0)
     for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
       if (!dg::mbar_wait(&full[i % kStages], i / kStages & 1, a.timeout_ns)) break;
+  if (ranks > 1) dg::cluster_sync();
 }
 
 // -------------------------------------------------------------------------------------------
@@ -612,8 +660,12 @@ __global__ void __launch_bounds__(Down<kFp4, kBig>::kThreads, 1) moe_down_kernel
   dg::fence_proxy_async_smem();        // the scratch in the rings was written by threads; copies write there next
   __syncthreads();
 
-  const int begin = warp * items / kWarps, end = (warp + 1) * items / kWarps, begin_job = begin / groups, begin_g = begin % groups;
-  int ft = begin < end && a.fault == 0 ? blockIdx.x : tiles, fi = begin, fjob = begin_job, fg = begin_g, fstage = 0, issued = 0;
+  // the cluster's tiles, and this warp's run of their items among all of the cluster's warps
+  const int ranks = cluster_blocks(), rank = ranks > 1 ? dg::cluster_cta_rank() : 0;
+  const int first_tile = blockIdx.x / ranks, tile_step = gridDim.x / ranks;
+  const int place = rank * kWarps + warp, places = ranks * kWarps;
+  const int begin = place * items / places, end = (place + 1) * items / places, begin_job = begin / groups, begin_g = begin % groups;
+  int ft = begin < end && a.fault == 0 ? first_tile : tiles, fi = begin, fjob = begin_job, fg = begin_g, fstage = 0, issued = 0;
   auto fetch = [&] {
     if (ft >= tiles) return;
     if (lane == 0) {
@@ -626,7 +678,7 @@ __global__ void __launch_bounds__(Down<kFp4, kBig>::kThreads, 1) moe_down_kernel
     }
     ++issued;
     if (++fstage == kStages) fstage = 0;
-    if (++fi == end) fi = begin, fjob = begin_job, fg = begin_g, ft += gridDim.x;
+    if (++fi == end) fi = begin, fjob = begin_job, fg = begin_g, ft += tile_step;
     else if (++fg == groups) fg = 0, ++fjob;
   };
 #pragma unroll
@@ -660,12 +712,12 @@ __global__ void __launch_bounds__(Down<kFp4, kBig>::kThreads, 1) moe_down_kernel
         if (n * 8 + 2 * q4 + i < count) hs[n][i] = ld_cg_v2(base + (n * 8 + 2 * q4 + i) * slot_bytes + 256);
     }
   };
-  if (begin < end && static_cast<int>(blockIdx.x) < tiles) load_h(begin_job, begin_g);
+  if (begin < end && first_tile < tiles) load_h(begin_job, begin_g);
 
   bool ok = true;
   int stage = 0;
   uint32_t phase = 0;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  for (int tile = first_tile; tile < tiles; tile += tile_step) {
     float* mine = sums + warp * a.T * C::kRows;
     float sum[kM][NT][4];
 #pragma unroll
@@ -678,7 +730,7 @@ __global__ void __launch_bounds__(Down<kFp4, kBig>::kThreads, 1) moe_down_kernel
       const bool last = it + 1 == end, turn = g + 1 == groups;
       auto load_next = [&] {
         if (!last) load_h(turn ? job + 1 : job, turn ? 0 : g + 1);
-        else if (tile + static_cast<int>(gridDim.x) < tiles) load_h(begin_job, begin_g);
+        else if (tile + tile_step < tiles) load_h(begin_job, begin_g);
       };
       uint4 hc[NT][4];
       uint2 sc[NT][2];
@@ -789,17 +841,30 @@ __global__ void __launch_bounds__(Down<kFp4, kBig>::kThreads, 1) moe_down_kernel
       job += turn;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * C::kRows; i += C::kThreads) {
-      const long long to = static_cast<long long>(i / C::kRows) * a.H + tile * C::kRows + i % C::kRows;
-      float v = a.c ? __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(a.c) + to))) : 0.0f;
+    // the warps' sums, then the cluster's; each block of a cluster writes its share of the tile
+    const int values = a.T * C::kRows;
+    float* total = sums + kWarps * values;
+    for (int i = threadIdx.x; i < values; i += C::kThreads) {
+      float v = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        v += sums[w * a.T * C::kRows + i];
-        sums[w * a.T * C::kRows + i] = 0;
+        v += sums[w * values + i];
+        sums[w * values + i] = 0;
       }
+      total[i] = v;
+    }
+    if (ranks > 1) dg::cluster_sync();
+    else __syncthreads();
+    for (int i = rank * values / ranks + threadIdx.x; i < (rank + 1) * values / ranks; i += C::kThreads) {
+      const long long to = static_cast<long long>(i / C::kRows) * a.H + tile * C::kRows + i % C::kRows;
+      float v = a.c ? __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(a.c) + to))) : 0.0f;
+      if (ranks == 1) v += total[i];
+      else
+        for (int other = 0; other < ranks; ++other) v += ld_shared_cluster_f32(dg::map_to_rank(total + i, other));
       a.y[to] = __float2bfloat16_rn(v);
     }
-    __syncthreads();
+    if (ranks > 1) dg::cluster_sync();
+    else __syncthreads();
   }
   // no copy may be under way when the block ends
   if (!ok && a.fault == 0)
@@ -815,7 +880,15 @@ dg_status run_layer(const MoeArgs& a, const LaunchContext& ctx, cudaStream_t str
   using D = Down<kFp4, kBig>;
   static_assert(sizeof(RoutingScratch) <= U::kRing && sizeof(RoutingScratch) <= D::kRing, "scratch in the rings");
   static_assert(U::kBlock == 64 || U::kBlock == 128, "h has two scales per 128 columns");
-  const int up_smem = U::smem(a.H / 128, a.T), down_smem = D::smem(a.T);
+  // Blocks of a cluster: as many, a power of two up to 8, as fit the SMs for the units (tiles) that there are at
+  // most, if each still has K groups (items for its warps) to work on.
+  const int groups = a.H / 128, units = std::min(a.T * a.k, a.E) * (a.I / U::kBlock), tiles = a.H / D::kRows;
+  const int items = std::min(a.T * a.k, a.E) * (a.I / 128);
+  const int up_room = ctx.sms * (U::kBlocksPerSm == 2 && U::smem(groups, a.T, 2) <= kHalfSm ? 2 : 1);
+  int up_cluster = 1, down_cluster = 1;
+  while (up_cluster < 8 && 2 * up_cluster * units <= up_room && 2 * up_cluster <= groups) up_cluster *= 2;
+  while (down_cluster < 8 && 2 * down_cluster * tiles <= ctx.sms && 2 * down_cluster * D::kWarps <= items) down_cluster *= 2;
+  const int up_smem = U::smem(groups, a.T, up_cluster), down_smem = D::smem(a.T);
   if (up_smem > kMaxSmem || down_smem > kMaxSmem) return DG_ERR_UNSUPPORTED;
   // once per thread and device: the limit, above what any shape needs
   static thread_local int ready = -1;
@@ -832,9 +905,12 @@ dg_status run_layer(const MoeArgs& a, const LaunchContext& ctx, cudaStream_t str
   if (!dg::byte_rows_map(&up_map, a.w13, static_cast<uint64_t>(a.E) * 2 * a.I, a.H / per, U::kBlock, Rows<kFp4>::kBytes) ||
       !dg::byte_rows_map(&down_map, a.w2, static_cast<uint64_t>(a.E) * a.H, a.I / per, D::kRows, Rows<kFp4>::kBytes))
     return DG_ERR_CUDA;
-  const unsigned up_grid = static_cast<unsigned>(U::kBlocksPerSm * ctx.sms), down_grid = static_cast<unsigned>(std::min(ctx.sms, a.H / D::kRows));
-  if (dg_status s = dg::launch(moe_up_kernel<kFp4, kBig>, up_grid, U::kThreads, static_cast<size_t>(up_smem), stream, ctx.pdl, up_map, a); s != DG_OK) return s;
-  return dg::launch(moe_down_kernel<kFp4, kBig>, down_grid, D::kThreads, static_cast<size_t>(down_smem), stream, ctx.pdl, down_map, a);
+  const int up_clusters = up_cluster > 1 ? units : std::min(units, U::kBlocksPerSm * ctx.sms);
+  const int down_clusters = std::min(tiles, std::max(1, ctx.sms / down_cluster));
+  if (dg_status s = dg::launch_clusters(moe_up_kernel<kFp4, kBig>, static_cast<unsigned>(up_clusters * up_cluster), static_cast<unsigned>(up_cluster),
+                                        U::kThreads, static_cast<size_t>(up_smem), stream, ctx.pdl, up_map, a); s != DG_OK) return s;
+  return dg::launch_clusters(moe_down_kernel<kFp4, kBig>, static_cast<unsigned>(down_clusters * down_cluster), static_cast<unsigned>(down_cluster),
+                             D::kThreads, static_cast<size_t>(down_smem), stream, ctx.pdl, down_map, a);
 }
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -43,23 +43,37 @@ class StreamWorkspace {
   void* lease_ = nullptr;
 };
 
-// Launches `kernel` on `stream`, as a programmatic dependent of the stream's last kernel if `pdl`
-// (the kernel then waits for that one itself, before any access to what it may touch).
+// Launches `kernel` on `stream`, in clusters of `cluster` blocks, as a programmatic dependent of the stream's
+// last kernel if `pdl` (the kernel then waits for that one itself, before any access to what it may touch).
 template <class... Params, class... Args>
-dg_status launch(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, bool pdl,
-                 Args... args) {
+dg_status launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned cluster, unsigned block, size_t smem, cudaStream_t stream, bool pdl,
+                          Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(block, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = n;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
   return e == cudaSuccess ? DG_OK : record_cuda_error(e);
+}
+
+template <class... Params, class... Args>
+dg_status launch(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, bool pdl, Args... args) {
+  return launch_clusters(kernel, grid, 1, block, smem, stream, pdl, args...);
 }
 
 }  // namespace dg
