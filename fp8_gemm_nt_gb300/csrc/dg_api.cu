@@ -986,11 +986,11 @@ dg_status launch_context(LaunchContext* out) {
 
 dg_status record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
-bool byte_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows, uint32_t box_bytes) {
-  const uint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
-  const uint32_t box[2] = {box_bytes, box_rows};
-  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
-                  box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+bool weight_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool e2m1) {
+  const uint64_t dims[2] = {cols, rows}, strides[1] = {e2m1 ? cols / 2 : cols};
+  const uint32_t box[2] = {128, box_rows};
+  return make_map(map, e2m1 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 dg_status StreamWorkspace::acquire(cudaStream_t stream, size_t bytes, void** out) {

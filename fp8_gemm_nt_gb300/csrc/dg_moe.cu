@@ -7,21 +7,26 @@
 // 128 x 128 block, or E2M1 with one per row per 32 columns: the grouped GEMMs' operands.
 //
 // At a few tokens an expert has one to a handful of rows, so the time is that of reading the weights
-// of the experts in use, once. Both kernels stream them with TMA into rings in shared memory. A warp
-// multiplies 16 weight rows (or 32) by up to 8 tokens (or 16) with m16n8 MMAs: the weights are the M
-// operand, an expert's tokens the N columns. The first product's operands are both E4M3 (E2M1 is one
-// with two exponent bits, moved into place), the second's FP16, which holds E4M3 and E2M1 exactly.
-// Accumulation is FP32, and the scales are applied to FP32 partial sums.
+// of the experts in use, once. The grouped GEMMs make the tokens the 128 rows of an MMA and would fill
+// one to four of them; here the weights are the M operand (128 rows) and an expert's tokens the N columns
+// of block-scaled tcgen05 MMAs, which take E4M3 and E2M1 as they are, with their scales: TMA brings the
+// weights to shared memory and no instruction touches them on the way.
 //
-// An expert's tokens are compacted into jobs of at most 8 (16) columns; each distinct (expert, token)
-// pair is a slot. The first kernel writes h = weight * silu(g) * u of every slot to the workspace, in
-// FP16 with one power-of-two scale per 64 or 128 columns (11 bits of every value within 2^-29 of the
-// largest; plain FP32 would double what the second kernel reads). The second kernel owns output rows: a
-// block sums all experts for its 16 (32) rows of W2 and every token, in an order that depends on the
-// sizes alone, and writes each output once. No atomics on values.
+// An expert's tokens are compacted into jobs of at most 16 columns; each distinct (expert, token) pair is
+// a slot. The first kernel computes h = weight * silu(g) * u of every slot. The second product also has to
+// be E4M3 by the weights' type, and three bits of mantissa would be too few: h is written as the sum of
+// three E4M3 terms, the second and third being the remainders times 16 and 256, with one power of two for
+// each 64 columns: 12 bits of every value within 2^-15 of the largest of its 64, and 2^-27 of that largest
+// below. The three terms are three columns, whose scales are 16 and 256 times smaller, and whose sums the
+// second kernel adds up. It owns output rows, sums all experts for 128 rows of W2 and every token in an
+// order that depends on the sizes alone, and writes each output once. No atomics on values.
 //
-// Where a layer has fewer pieces of work than the GPU has room for blocks, a cluster of blocks shares a
-// piece, each with a part of K, and sums through distributed shared memory in the order of its ranks.
+// A pipeline is a warp each for the weights' copies, the tokens' side, the weights' scales and the MMAs, and
+// four that read the sums from TMEM, with a ring of stages of 128 columns. A block (one to an SM) is two
+// pipelines, halves that share nothing but the routing: one thread issuing MMAs does not keep up with HBM.
+// Where there are fewer pieces of work than pipelines (always in the second kernel, whose tiles are few),
+// the halves of a cluster of blocks share a piece, each with a part of K, and sum through (distributed)
+// shared memory in the order of their ranks.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -46,26 +51,33 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxH = 16384;
 constexpr int kMaxSlots = kMaxTokens * kMaxTopk;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kHBytes = 272;            // 128 columns of h of a slot: 256 bytes of FP16, FP32 scales of both halves, padding
-constexpr int kMaxSmem = 216 * 1024;
-constexpr int kHalfSm = 104 * 1024;     // dynamic shared memory of a block of which two are resident
+constexpr int kCols = 16;               // tokens of a job
+constexpr int kTerms = 3;               // E4M3 terms of a value of h
+constexpr int kBlock = 64;              // columns of h of a unit of the first kernel, which share a scale
+constexpr int kHalf = 256;              // threads of a pipeline
+constexpr int kThreads = 2 * kHalf;
+constexpr int kMaxStages = 8;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxSmem = 221 * 1024;    // dynamic
 
 struct MoeArgs {
   const uint8_t* x;        // [T, H] E4M3
   const int32_t* sfx;      // [KP(H), ceil4(T)]
-  const uint8_t* w13;      // [E, 2 I, H] (H / 2 bytes a row for E2M1)
-  const int32_t* sf13;
-  const uint8_t* w2;       // [E, H, I]
-  const int32_t* sf2;
+  const int32_t* sf13;     // scales of w13 [E, 2 I, H]
+  const int32_t* sf2;      // scales of w2 [E, H, I]
   const int32_t* ids;      // [T, k]
   const float* weights;    // [T, k]
   const __nv_bfloat16* c;  // [T, H] or null
   __nv_bfloat16* y;        // [T, H]
-  uint8_t* h;              // [slots, I / 128, kHBytes]
+  uint8_t* h;              // [slots, kTerms, I] E4M3
+  uint32_t* hs;            // [slots, I / 128 up to a multiple of 4]: codes of a slot's four 32-column blocks of 128
   uint32_t* status;
-  unsigned long long timeout_ns;   // of a wait for a copy
-  int fault;                       // failure injection: no copies
+  unsigned long long timeout_ns;   // of a wait
+  int fault;                       // failure injection: no copies of weights
   int T, k, E, H, I;
+  int stages, stage_bytes, token_rows;   // of a pipeline's ring; rows of a stage's tokens
+  int rest_bytes;                        // of a pipeline's shared memory beside the rings
+  int split;                             // the pipelines of a cluster share a piece
 };
 
 // -------------------------------------------------------------------------------------------
@@ -165,62 +177,24 @@ __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, Rout
 }
 
 // -------------------------------------------------------------------------------------------
-// Elements, MMAs, copies
+// The products of both kernels
 // -------------------------------------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(two)));
-  return d;
-}
-
-// Four E2M1 codes as E4M3 of 2^-6 of their values: the sign to bit 7, the two exponent bits and the
-// mantissa bit to the lowest exponent bits and the highest mantissa bit (E2M1's subnormal 0.5 becomes
-// the subnormal 2^-7). Even elements of eight are the low nibbles, odd ones the high nibbles.
-__device__ __forceinline__ uint32_t e4m3_of_even(uint32_t w) { return (w << 4 & 0x80808080u) | (w << 2 & 0x1C1C1C1Cu); }
-__device__ __forceinline__ uint32_t e4m3_of_odd(uint32_t w) { return (w & 0x80808080u) | (w >> 2 & 0x1C1C1C1Cu); }
-
-// The same as the upper bytes of FP16 of 2^-14 of their values (the lower bytes are 0), and two of them as a
-// pair: bytes 0 and 1, or 2 and 3, of b.
-__device__ __forceinline__ uint32_t f16_of_even(uint32_t w) { return (w << 4 & 0x80808080u) | (w << 1 & 0x0E0E0E0Eu); }
-__device__ __forceinline__ uint32_t f16_of_odd(uint32_t w) { return (w & 0x80808080u) | (w >> 3 & 0x0E0E0E0Eu); }
-__device__ __forceinline__ uint32_t lower_pair(uint32_t b) { return __byte_perm(b, 0, 0x1404); }
-__device__ __forceinline__ uint32_t upper_pair(uint32_t b) { return __byte_perm(b, 0, 0x3424); }
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The same on a sum that starts at zero.
-__device__ __forceinline__ void mma_e4m3_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-// Plain loads of shared memory: the waits before them clobber memory, so they stay after those, and the
-// compiler may otherwise move them ahead of other work.
-template <class T>
-__device__ __forceinline__ T lds(const uint8_t* p) { return *reinterpret_cast<const T*>(p); }
-__device__ __forceinline__ uint2 ld_cg_v2(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.cg.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ float float_of(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ int cluster_blocks() {
+  int n;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Untiled bulk copy (16-byte aligned addresses and size) that completes on `bar`.
 __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
@@ -228,689 +202,524 @@ __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t b
                "l"(from), "r"(bytes), "r"(dg::smem_addr(bar))
                : "memory");
 }
+__device__ __forceinline__ void named_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// The K order of a product is free. Within 128 columns, lane 4 g + q (g the row or column of the MMA
-// fragment) takes, in the E4M3 form, columns 64 p + 16 q .. + 15 of half p: one 128-bit load of a row holds
-// its fragments of two (four) MMAs. In the E2M1 form it takes columns 32 b + 8 q .. + 7 of block b: the
-// columns of an MMA then share a scale.
-//
-// TMA permutes the 16-byte chunks of a row (the 128-byte swizzle for E4M3, the 64-byte one for E2M1).
-// The eight lanes of a 128-bit load's phase are two rows of four chunks; they cover every bank once if the
-// rows differ by four, so row g of a fragment is row g / 2 + 4 (g % 2) of eight in memory. E2M1's 32-bit
-// loads (eight rows of one chunk) meet no bank twice in any order of the rows.
-template <bool kFp4>
-struct Rows {
-  static constexpr int kBytes = kFp4 ? 64 : 128;            // of 128 columns
-  static __device__ __forceinline__ int of(int g) { return kFp4 ? g : g / 2 + 4 * (g & 1); }
-  static __device__ __forceinline__ int chunk(int row, int c) {
-    return kFp4 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4);
+// A stage: 128 weight rows of 128 columns (128-byte rows in the 128-byte swizzle; E2M1 spread to one element a
+// byte by TMA), the tokens' rows in the same form, the weights' scale words as loaded (E2M1: one per row), the
+// tokens' as loaded (second kernel: four words per token), and both as tcgen05.cp takes them (row r of 32 holds
+// the words of rows r, r + 32, ...).
+constexpr int kWeights = 128 * 128;
+constexpr int kRawA = 0, kRawB = 512, kTileA = kRawB + kCols * 16, kTileB = kTileA + 512, kScaleArea = kTileB + 512;
+__host__ __device__ constexpr int stage_bytes(int token_rows) { return (kWeights + token_rows * 128 + kScaleArea + 1023) / 1024 * 1024; }
+
+struct Pipe {
+  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], sum_full[2], sum_empty[2], drain;
+};
+struct Shared {
+  Routing r;
+  Pipe pipe[2];
+  uint32_t tmem;
+  volatile uint32_t abort;
+};
+
+// A run of K groups of one job against 128 weight rows (two boxes of 64): one sum in TMEM.
+struct Run {
+  int job, expert, slot, count;
+  int row0, row1;          // of the boxes, in the [E * N, K] weight matrix
+  int begin, end;          // K groups
+  int piece;               // unit (first kernel) or tile (second)
+};
+
+// Who a pipeline is: `rank` of the `ranks` pipelines that share a piece, and the piece's place.
+struct Place {
+  int half, rank, ranks, first, step;
+};
+
+// A pipeline's runs in order. First kernel: units (job, 64 columns of h), each 64 gate rows and their up rows,
+// all K groups of them or the rank's share. Second kernel: one tile of 128 output rows, the rank's share of its
+// (job, K group) items, cut at the jobs.
+template <bool kDown>
+struct Walk {
+  const MoeArgs& a;
+  const Routing& r;
+  int at, end, groups, step, rank, ranks, tile;
+  __device__ __forceinline__ Walk(const MoeArgs& args, const Routing& routing, const Place& p) : a(args), r(routing), step(p.step), rank(p.rank), ranks(p.ranks), tile(p.first) {
+    groups = (kDown ? a.I : a.H) / 128;
+    const int items = r.jobs * groups;
+    at = kDown ? rank * items / ranks : p.first;
+    end = kDown ? (rank + 1) * items / ranks : r.jobs * (a.I / kBlock);
   }
-};
-
-// FP32 values of the four UE8M0 codes of a word: the code in the exponent's place, unless a code is 0 (2^-127,
-// a subnormal) or 255 (NaN). A byte of v is 0 where (v - 0x01010101) & ~v has its top bit (or a byte below
-// is 0, which is as good a reason to look closer).
-__device__ __forceinline__ float4 four_scales(uint32_t w) {
-  if (((w - 0x01010101u) & ~w & 0x80808080u) || ((~w - 0x01010101u) & w & 0x80808080u))
-    return make_float4(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255), dg::ue8m0_value(w >> 16 & 255), dg::ue8m0_value(w >> 24));
-  return make_float4(__uint_as_float(w << 23 & 0x7F800000u), __uint_as_float(w << 15 & 0x7F800000u), __uint_as_float(w << 7 & 0x7F800000u),
-                     __uint_as_float(w >> 1 & 0x7F800000u));
-}
-
-// A wait that has run out once is not repeated: the kernel then runs through on what is in its rings, with
-// every barrier met, and the status word says that its results are void.
-__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, const MoeArgs& a, bool ok) {
-  if (ok && dg::mbar_wait(bar, parity, a.timeout_ns)) return true;
-  if (ok) atomicOr(a.status, dg::kTimeoutBit);
-  return false;
-}
-
-__host__ __device__ constexpr int round_up(int v, int to) { return (v + to - 1) / to * to; }
-
-// Shapes. kBig (more than 8 tokens): experts then have several tokens; 16 columns, and for E2M1, whose
-// tokens' side and conversions cost as much as its bytes, 32 rows a warp.
-template <bool kFp4, bool kBig>
-struct Up {
-  static constexpr int kM = kFp4 && kBig ? 2 : 1, kCols = kBig ? 16 : 8;
-  static constexpr int kWarps = kBig && !kFp4 ? 16 : 8, kThreads = 32 * kWarps;
-  static constexpr int kBlock = 8 * kM * kWarps;                    // columns of h of a block, 64 or 128
-  static constexpr int kBlocksPerSm = kBig && !kFp4 ? 1 : 2;
-  static constexpr int kStages = kFp4 ? (kBig ? 4 : 8) : 5;
-  static constexpr int kAhead = kStages - 2;                        // copies run this far ahead of the products
-  // a stage: kBlock gate rows and as many up rows of 128 columns, the tokens' 128 bytes, E2M1's scales. A
-  // token's row is spaced so that the lanes of a load of it (two rows of 64 bytes, four of 32) cover the banks.
-  static constexpr int kBox = kBlock * Rows<kFp4>::kBytes;
-  static constexpr int kTokenStride = kFp4 ? 160 : 192;
-  static constexpr int kTokens = 2 * kBox, kScales = kTokens + kCols * kTokenStride;
-  static constexpr int kStage = round_up(kScales + (kFp4 ? 8 * kBlock : 0), 1024);
-  static constexpr int kRing = kStages * kStage;
-  static constexpr int kExpanded = kFp4 ? kWarps * 256 * kM : 0;    // E2M1: a warp's scales as FP32
-  // then the tokens' scales [groups, T], for E4M3 each warp's two scales of every group, and a cluster's
-  // partial sums of two units
-  static constexpr int kSums = kM * kCols / 2;                      // a thread's
-  static __host__ __device__ int partials(int groups, int T) {
-    return kRing + kExpanded + round_up((groups * T + 1) / 2 * 8 + (kFp4 ? 0 : kWarps * groups * 8), 16);
-  }
-  static int smem(int groups, int T, int cluster) { return 1024 + partials(groups, T) + (cluster > 1 ? 2 * kThreads * kSums * 4 : 0); }
-};
-template <bool kFp4, bool kBig>
-struct Down {
-  static constexpr int kM = kFp4 && kBig ? 2 : 1;
-  // with 32 rows, 16 columns' fragments and sums would not fit the registers: an expert of more than 8 tokens
-  // is then two jobs, the second of which finds the weights in L2
-  static constexpr int kCols = kBig && kM == 1 ? 16 : 8;
-  static constexpr int kRows = 16 * kM, kWarps = 16, kThreads = 32 * kWarps;
-  static constexpr int kStages = kFp4 ? (kBig ? 4 : 6) : 4;
-  static constexpr int kBox = kRows * Rows<kFp4>::kBytes;           // a stage of a warp
-  static constexpr int kRing = kWarps * kStages * kBox;
-  // E4M3: the packed word of the rows' 128-row block (with its neighbours); E2M1: a word per row
-  static constexpr int kScaleBytes = kFp4 ? 4 * kRows : 16;
-  static constexpr int kScales = kWarps * kStages * kScaleBytes;
-  static constexpr int kExpanded = kFp4 ? kWarps * 256 * kM : 0;
-  // then every warp's sums of a tile, [warps][T][kRows], and the block's
-  static int smem(int T) { return 1024 + kRing + kScales + kExpanded + (kWarps + 1) * T * kRows * 4; }
-};
-
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ int cluster_blocks() {
-  int n;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-
-__device__ __forceinline__ uint8_t* aligned_1k(uint8_t* p) {
-  return p + ((1024u - (dg::smem_addr(p) & 1023u)) & 1023u);
-}
-
-// -------------------------------------------------------------------------------------------
-// First kernel: h = weight * silu(G x) * (U x)
-// -------------------------------------------------------------------------------------------
-//
-// A unit is kBlock columns of h of a job: kBlock gate rows and kBlock up rows of W13, a warp 8 kM of each. A
-// stage is 128 columns of all of them and of the job's tokens. The warps take turns at issuing its copies,
-// two stages less than the ring is long ahead: a warp may then lag another by two stages before its turn
-// has to wait for it. (A warp for the copies alone would leave the others 96 registers instead of 128.)
-
-template <bool kFp4, bool kBig>
-__global__ void __launch_bounds__(Up<kFp4, kBig>::kThreads, Up<kFp4, kBig>::kBlocksPerSm)
-    moe_up_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
-  using C = Up<kFp4, kBig>;
-  using R = Rows<kFp4>;
-  constexpr int kM = C::kM, NT = C::kCols / 8, kStages = C::kStages, kWarps = C::kWarps;
-  extern __shared__ uint8_t raw[];
-  __shared__ Routing r;
-  __shared__ float block_max[2][kWarps][C::kCols];
-  __shared__ uint64_t full[kStages], empty[kStages];
-  uint8_t* const ring = aligned_1k(raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      dg::mbar_init(&full[i], 1);
-      dg::mbar_init(&empty[i], kWarps);
+  __device__ __forceinline__ bool next(Run& s) {
+    if (at >= end) return false;
+    if (kDown) {
+      s.job = at / groups;
+      s.begin = at - s.job * groups;
+      s.end = min(groups, s.begin + end - at);
+      at += s.end - s.begin;
+      s.piece = tile;
+    } else {
+      const int blocks = a.I / kBlock;
+      s.job = at / blocks;
+      s.piece = at - s.job * blocks;
+      s.begin = rank * groups / ranks;
+      s.end = (rank + 1) * groups / ranks;
+      at += step;
     }
+    s.expert = r.job_expert[s.job];
+    s.slot = r.job_slot[s.job];
+    s.count = r.job_count[s.job];
+    s.row0 = kDown ? s.expert * a.H + s.piece * 128 : s.expert * 2 * a.I + s.piece * kBlock;
+    s.row1 = kDown ? s.row0 + 64 : s.row0 + a.I;
+    return true;
+  }
+};
+
+// FP32 value of an E4M3 code.
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(code)));
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(d)));
+}
+
+// The end of a unit of the first kernel, by warps 4 to 7: rows 0 to 63 of the sums (two warps) are the gate's,
+// rows 64 to 127 the up's of the same columns of h. Writes h's three terms and its scale for the job's tokens.
+__device__ __forceinline__ void store_inner(const MoeArgs& a, const Routing& r, const Run& run, float* exchange, const uint32_t (&v)[kCols], int half, int quad, int lane) {
+  float* const up = exchange;                       // [64][17]
+  float* const top = exchange + 64 * 17;            // [2][kCols]
+  const int row = (quad & 1) * 32 + lane;
+  if (quad >= 2) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) up[row * 17 + c] = __uint_as_float(v[c]);
+  }
+  named_barrier(1 + 2 * half, 128);
+  if (quad < 2) {
+    float h[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      h[c] = 0;
+      if (c >= run.count) continue;
+      const float gate = __uint_as_float(v[c]);
+      h[c] = r.coef[run.slot + c] * (gate / (1.0f + expf(-gate)) * up[row * 17 + c]);
+      float m = fabsf(h[c]);
+      m = m < INFINITY ? m : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+      if (lane == 0) top[quad * kCols + c] = m;
+    }
+    named_barrier(2 + 2 * half, 64);
+    const int groups4 = (a.I / 128 + 3) / 4 * 4;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      if (c >= run.count) continue;
+      // the third term's scale is 2^-8 of the first's: its code stays at least 1
+      const int e = max(dg::ue8m0_for_amax(fmaxf(top[c], top[kCols + c])), 9);
+      const float full = h[c] * dg::ue8m0_inverse(e);
+      uint8_t* to = a.h + static_cast<long long>(run.slot + c) * kTerms * a.I + run.piece * kBlock + row;
+      // an infinity (NaN - infinity) becomes NaN
+      float left = full - full == 0.0f ? full : NAN;
+#pragma unroll
+      for (int j = 0; j < kTerms; ++j) {
+        const uint32_t code = dg::pack_e4m3(left, 0, 0, 0) & 255;
+        to[static_cast<long long>(j) * a.I] = static_cast<uint8_t>(code);
+        left = (left - e4m3_value(code)) * 16.0f;
+      }
+      if (quad == 0 && lane == 0)
+        reinterpret_cast<uint16_t*>(a.hs + static_cast<long long>(run.slot + c) * groups4)[run.piece] = static_cast<uint16_t>(e | e << 8);
+    }
+  }
+  named_barrier(1 + 2 * half, 128);               // before the next unit's exchange
+}
+
+template <bool kFp4, bool kDown>
+__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
+  extern __shared__ uint8_t raw[];
+  __shared__ Shared s;
+  uint8_t* const base = raw + ((1024u - (dg::smem_addr(raw) & 1023u)) & 1023u);
+  const int lane = threadIdx.x & 31, half = threadIdx.x / kHalf, warp = threadIdx.x % kHalf / 32;
+  Pipe& pipe = s.pipe[half];
+  constexpr int kSumCols = kDown ? 48 : 16, kTmemCols = kDown ? 128 : 64;     // two sums, then two buffers of each side's scales
+  if (threadIdx.x % kHalf == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      dg::mbar_init(&pipe.full[i], 1);
+      dg::mbar_init(&pipe.ready[i], 2);
+      dg::mbar_init(&pipe.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      dg::mbar_init(&pipe.sum_full[i], 1);
+      dg::mbar_init(&pipe.sum_empty[i], 4);
+    }
+    dg::mbar_init(&pipe.drain, 1);
     dg::fence_mbarrier_init();
+  }
+  if (threadIdx.x == 0) {
+    s.abort = 0;
     dg::tma_prefetch_desc(&map);
   }
-  dg::grid_dependency_wait();
-  dg::grid_launch_dependents();
-  const int t4 = (a.T + 3) / 4 * 4;
-  const int groups = a.H / 128, blocks = a.I / C::kBlock;
-  build_routing<C::kCols, C::kThreads>(a, r, *reinterpret_cast<RoutingScratch*>(ring), blockIdx.x == 0);
-  float* expanded = reinterpret_cast<float*>(ring + C::kRing) + warp * 64 * kM;
-  float* sx = reinterpret_cast<float*>(ring + C::kRing + C::kExpanded);
-  for (int i = threadIdx.x; i < (groups + 3) / 4 * a.T; i += C::kThreads) {
-    const int w = i / a.T, t = i % a.T;
-    const uint32_t v = dg::ld_cg_s32(a.sfx + w * t4 + t);
-    for (int b = 0; b < 4 && 4 * w + b < groups; ++b) sx[(4 * w + b) * a.T + t] = dg::ue8m0_value(v >> (8 * b) & 255);
+  if (threadIdx.x / 32 == 1) {
+    dg::tmem_alloc(&s.tmem, 2 * kTmemCols);
+    dg::tmem_relinquish();
   }
-  dg::fence_proxy_async_smem();        // the scratch in the ring was written by threads; copies write there next
-  __syncthreads();
-  const int units = r.jobs * blocks;
-  // the cluster's share of the units, and this block's of their column groups
-  const int ranks = cluster_blocks(), rank = ranks > 1 ? dg::cluster_cta_rank() : 0;
-  const int first_unit = blockIdx.x / ranks, unit_step = gridDim.x / ranks;
-  const int group_begin = rank * groups / ranks, group_end = (rank + 1) * groups / ranks;
-  bool ok = true;
-
-  // the stage to copy: column group fg of unit fu, the issued'th of the block
-  int fu = first_unit, fg = group_begin, fstage = 0, issued = 0;
-  uint32_t fphase = 1;
-  auto fetch = [&] {
-    if (fu >= units) return;
-    if (issued % kWarps == warp && a.fault == 0) {
-      const int job = fu / blocks, e = r.job_expert[job], i0 = fu % blocks * C::kBlock, slot = r.job_slot[job], count = r.job_count[job];
-      ok = wait_full(&empty[fstage], fphase, a, ok);
-      if (__all_sync(kAll, ok)) {
-        uint8_t* to = ring + fstage * C::kStage;
-        if (lane == 0) {
-          const int row = e * 2 * a.I + i0;
-          dg::mbar_arrive_expect_tx(&full[fstage], 2 * C::kBox + count * 128 + (kFp4 ? 8 * C::kBlock : 0));
-          dg::tma_load_2d(to, &map, &full[fstage], fg * R::kBytes, row);
-          dg::tma_load_2d(to + C::kBox, &map, &full[fstage], fg * R::kBytes, row + a.I);
-          if (kFp4) {
-            const int32_t* from = a.sf13 + (static_cast<long long>(e) * groups + fg) * 2 * a.I + i0;
-            bulk_load(to + C::kScales, from, 4 * C::kBlock, &full[fstage]);
-            bulk_load(to + C::kScales + 4 * C::kBlock, from + a.I, 4 * C::kBlock, &full[fstage]);
-          }
-        }
-        __syncwarp();
-        if (lane < count)
-          bulk_load(to + C::kTokens + lane * C::kTokenStride, a.x + static_cast<long long>(r.token[slot + lane]) * a.H + fg * 128, 128, &full[fstage]);
-      }
-    }
-    ++issued;
-    if (++fstage == kStages) fstage = 0, fphase ^= 1;
-    if (++fg == group_end) fg = group_begin, fu += unit_step;
-  };
-
-  const int g8 = lane / 4, q4 = lane & 3, row8 = R::of(g8);
-  float2* sw = reinterpret_cast<float2*>(sx + (groups * a.T + 1) / 2 * 2) + warp * groups;
-  // E4M3: packed scale word `lane` of a unit's gate and up rows, read a unit ahead
-  uint32_t next_gate = 0, next_up = 0;
-  auto load_scales = [&](int u) {
-    const int e = r.job_expert[u / blocks], i0 = u % blocks * C::kBlock, n4 = (a.I / 64 + 3) / 4 * 4;
-    if (lane < (groups + 3) / 4) {
-      const int32_t* sf = a.sf13 + (static_cast<long long>(e) * ((groups + 3) / 4) + lane) * n4;
-      next_gate = dg::ld_cg_s32(sf + i0 / 128);
-      next_up = dg::ld_cg_s32(sf + (a.I + i0) / 128);
-    }
-  };
-  for (int i = 0; i < C::kAhead; ++i) fetch();
-  if (!kFp4 && first_unit < units) load_scales(first_unit);
-  int stage = 0, flip = 0;
-  uint32_t phase = 0;
-  for (int u = first_unit; u < units; u += unit_step, flip ^= 1) {
-    const int job = u / blocks, blk = u % blocks, slot = r.job_slot[job], count = r.job_count[job];
-    float sum[kM][NT][4];
-    const float* sxt[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int m = 0; m < kM; ++m) sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = n * 8 + 2 * q4 + i;
-        sxt[n][i] = sx + (col < count ? r.token[slot + col] : 0);
-      }
-    }
-    if constexpr (!kFp4) {
-      __syncwarp();
-      if (lane < (groups + 3) / 4) {
-        const float4 gate = four_scales(next_gate), up = four_scales(next_up);
-        sw[4 * lane] = make_float2(gate.x, up.x);
-        if (4 * lane + 1 < groups) sw[4 * lane + 1] = make_float2(gate.y, up.y);
-        if (4 * lane + 2 < groups) sw[4 * lane + 2] = make_float2(gate.z, up.z);
-        if (4 * lane + 3 < groups) sw[4 * lane + 3] = make_float2(gate.w, up.w);
-      }
-      __syncwarp();
-      if (u + unit_step < units) load_scales(u + unit_step);
-    }
-    for (int g = group_begin; g < group_end; ++g) {
-      fetch();
-      ok = wait_full(&full[stage], phase, a, ok);
-      const uint8_t* at = ring + stage * C::kStage;
-      const uint8_t* gate = at + warp * 8 * kM * R::kBytes;
-      const uint8_t* up = gate + C::kBox;
-      const uint8_t* tokens = at + C::kTokens + g8 * C::kTokenStride;
-      // one item, for N eights of columns (a branch for the second eight inside would cost those that have one)
-      auto item = [&](auto eights) {
-        constexpr int N = decltype(eights)::value;
-        float acc[kM][N][4];
-        if constexpr (!kFp4) {
-          uint4 w0[2], w1[2], x[N][2];
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            w0[p] = lds<uint4>(gate + R::chunk(row8, 4 * p + q4)), w1[p] = lds<uint4>(up + R::chunk(row8, 4 * p + q4));
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-              x[n][p] = lds<uint4>(tokens + n * 8 * C::kTokenStride + 64 * p + 16 * q4);
-          }
-#pragma unroll
-          for (int n = 0; n < N; ++n)
-            {
-              mma_e4m3_zero(acc[0][n], w0[0].x, w1[0].x, w0[0].y, w1[0].y, x[n][0].x, x[n][0].y);
-              mma_e4m3(acc[0][n], w0[0].z, w1[0].z, w0[0].w, w1[0].w, x[n][0].z, x[n][0].w);
-              mma_e4m3(acc[0][n], w0[1].x, w1[1].x, w0[1].y, w1[1].y, x[n][1].x, x[n][1].y);
-              mma_e4m3(acc[0][n], w0[1].z, w1[1].z, w0[1].w, w1[1].w, x[n][1].z, x[n][1].w);
-            }
-        } else {
-          // the warp's scales, 8 kM gate rows and then as many up rows, as FP32: each converted by one lane
-          const uint8_t* packed = at + C::kScales + warp * 32 * kM + (lane / 16) * 4 * C::kBlock;
-          if constexpr (kM == 1) {
-            const uint32_t w = lds<uint32_t>(packed + lane % 16 / 2 * 4) >> (lane & 1) * 16;
-            reinterpret_cast<float2*>(expanded)[lane] = make_float2(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255));
-          } else {
-            reinterpret_cast<float4*>(expanded)[lane] = four_scales(lds<uint32_t>(packed + lane % 16 * 4));
-          }
-          __syncwarp();
-          float4 scale[kM][2];
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            scale[m][0] = reinterpret_cast<const float4*>(expanded)[8 * m + g8];
-            scale[m][1] = reinterpret_cast<const float4*>(expanded)[8 * kM + 8 * m + g8];
-          }
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            uint32_t even[N], odd[N];
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-              {
-                const uint2 x = lds<uint2>(tokens + n * 8 * C::kTokenStride + 32 * b + 8 * q4);
-                even[n] = __byte_perm(x.x, x.y, 0x6420), odd[n] = __byte_perm(x.x, x.y, 0x7531);
-              }
-#pragma unroll
-            for (int m = 0; m < kM; ++m) {
-              const uint32_t u0 = lds<uint32_t>(gate + m * 8 * R::kBytes + R::chunk(row8, b) + 4 * q4);
-              const uint32_t u1 = lds<uint32_t>(up + m * 8 * R::kBytes + R::chunk(row8, b) + 4 * q4);
-              const uint32_t a0 = e4m3_of_even(u0), a1 = e4m3_of_even(u1), a2 = e4m3_of_odd(u0), a3 = e4m3_of_odd(u1);
-              const float e0 = float_of(scale[m][0], b), e1 = float_of(scale[m][1], b);
-#pragma unroll
-              for (int n = 0; n < N; ++n)
-                {
-                  float part[4];
-                  mma_e4m3_zero(part, a0, a1, a2, a3, even[n], odd[n]);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const float e = i < 2 ? e0 : e1;
-                    acc[m][n][i] = b == 0 ? e * part[i] : fmaf(e, part[i], acc[m][n][i]);
-                  }
-                }
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) dg::mbar_arrive(&empty[stage]);
-        const float2 s = kFp4 ? make_float2(1.0f, 1.0f) : sw[g];
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float t = sxt[n][i][g * a.T], tx = kFp4 ? t : t * s.x, ty = kFp4 ? t : t * s.y;
-#pragma unroll
-              for (int m = 0; m < kM; ++m) {
-                sum[m][n][i] = fmaf(tx, acc[m][n][i], sum[m][n][i]);
-                sum[m][n][2 + i] = fmaf(ty, acc[m][n][2 + i], sum[m][n][2 + i]);
-              }
-            }
-      };
-      if (NT == 1 || count <= 8) item(std::integral_constant<int, 1>());
-      else item(std::integral_constant<int, NT>());
-      if (++stage == kStages) stage = 0, phase ^= 1;
-    }
-    if (ranks > 1) {
-      // the first block of the cluster adds the others' sums to its own
-      float4* mine = reinterpret_cast<float4*>(ring + C::partials(groups, a.T)) + flip * C::kThreads * (C::kSums / 4);
-#pragma unroll
-      for (int m = 0; m < kM; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mine[(m * NT + n) * C::kThreads + threadIdx.x] = make_float4(sum[m][n][0], sum[m][n][1], sum[m][n][2], sum[m][n][3]);
-      dg::cluster_sync();
-      if (rank != 0) continue;
-      for (int other = 1; other < ranks; ++other) {
-        const uint32_t theirs = dg::map_to_rank(mine, other);
-#pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 v = dg::ld_shared_cluster_v4(theirs + ((m * NT + n) * C::kThreads + threadIdx.x) * 16);
-            sum[m][n][0] += __uint_as_float(v.x), sum[m][n][1] += __uint_as_float(v.y);
-            sum[m][n][2] += __uint_as_float(v.z), sum[m][n][3] += __uint_as_float(v.w);
-          }
-      }
-    }
-    // column blk * kBlock + (warp * kM + m) * 8 + row8 of h for tokens 2 q4, 2 q4 + 1 of each eight: gate in
-    // sum[0..1], up in sum[2..3] (E2M1 went into the MMAs as 2^-6 of itself)
-    constexpr float kUnit = kFp4 ? 64.0f : 1.0f;
-    float hv[kM][NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = n * 8 + 2 * q4 + i;
-        const float w = col < count ? r.coef[slot + col] : 0.0f;
-        float top = 0;
-#pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          const float gate = sum[m][n][i] * kUnit;
-          hv[m][n][i] = col < count ? w * (gate / (1.0f + expf(-gate)) * (sum[m][n][2 + i] * kUnit)) : 0.0f;
-          const float v = fabsf(hv[m][n][i]);
-          top = fmaxf(top, v < INFINITY ? v : 0.0f);
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-        if (g8 == 0) block_max[flip][warp][col] = top;
-      }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = n * 8 + 2 * q4 + i;
-        if (col >= count) continue;
-        float top = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, block_max[flip][w][col]);
-        // the largest to [2^14, 2^15); both powers stay normal
-        const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 254) - 127 - 14;
-        const float to_half = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        const float back = __uint_as_float(static_cast<uint32_t>(127 + ex + (kFp4 ? 14 : 0)) << 23);   // E2M1 enters the MMAs as 2^-14 of itself
-        uint8_t* row = a.h + (static_cast<long long>(slot + col) * (a.I / 128) + blk * C::kBlock / 128) * kHBytes;
-#pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          // where the second kernel's lanes find this column of the 128: E4M3 as 16-byte pieces of two loads,
-          // each of 64 bytes over four lanes; E2M1 the even ones of every eight, then the odd ones
-          const int cc = blk * C::kBlock % 128 + (warp * kM + m) * 8 + row8;
-          const int place = kFp4 ? (cc / 8 * 8 + cc % 2 * 4 + cc % 8 / 2) * 2 : cc / 64 * 128 + cc % 16 / 8 * 64 + cc % 64 / 16 * 16 + cc % 8 * 2;
-          *reinterpret_cast<__half*>(row + place) = __float2half_rn(hv[m][n][i] * to_half);
-        }
-        if (warp == 0 && g8 == 0) {
-          float* to = reinterpret_cast<float*>(row + 256);
-          if (C::kBlock == 128) to[0] = to[1] = back;
-          else to[blk & 1] = back;
-        }
-      }
+  if (!kDown) {
+    dg::grid_dependency_wait();
+    dg::grid_launch_dependents();
   }
-  // no copy may be under way when the block ends, and no block of a cluster be gone whose sums are read
-  if (!ok && a.fault == 0)
-    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-      if (!dg::mbar_wait(&full[i % kStages], i / kStages & 1, a.timeout_ns)) break;
-  if (ranks > 1) dg::cluster_sync();
-}
-
-// -------------------------------------------------------------------------------------------
-// Second kernel: y = c + W2 h
-// -------------------------------------------------------------------------------------------
-//
-// A tile is kRows output rows and all tokens. Its items are 128 columns of W2 of a job each; a warp takes a
-// run of them, with a ring of its own that its first lane fills. The tokens' side is small, shared by all
-// tiles and stays in L2: a warp reads its fragments of it straight into registers, an item ahead.
-
-template <bool kFp4, bool kBig>
-__global__ void __launch_bounds__(Down<kFp4, kBig>::kThreads, 1) moe_down_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
-  using C = Down<kFp4, kBig>;
-  using R = Rows<kFp4>;
-  constexpr int kM = C::kM, NT = C::kCols / 8, kStages = C::kStages, kWarps = C::kWarps;
-  extern __shared__ uint8_t raw[];
-  __shared__ Routing r;
-  __shared__ uint64_t full_bars[kWarps][kStages];
-  uint8_t* const rings = aligned_1k(raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g8 = lane / 4, q4 = lane & 3, row8 = R::of(g8);
-  uint64_t* full = full_bars[warp];
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) dg::mbar_init(&full[i], 1);
-    dg::fence_mbarrier_init();
-    if (warp == 0) dg::tma_prefetch_desc(&map);
+  // (The first kernel let the second start only after its own wait: ids and weights are there, h is not yet.)
+  build_routing<kCols, kThreads>(a, s.r, *reinterpret_cast<RoutingScratch*>(base), !kDown && blockIdx.x == 0);
+  // the halves' rings, then for each half: the first kernel's token scales [KP, T] and its exchange of sums
+  // (of 64 rows and their maxima, or all 128 rows where a piece is split); the second's output [T][128]
+  uint8_t* const ring = base + half * a.stages * a.stage_bytes;
+  uint8_t* const rest = base + 2 * a.stages * a.stage_bytes + half * a.rest_bytes;
+  uint32_t* const sfx = reinterpret_cast<uint32_t*>(rest);
+  const int kp = (a.H / 128 + 3) / 4;
+  float* const exchange = reinterpret_cast<float*>(rest + (kDown ? 0 : kp * a.T * 4));
+  float* const out = reinterpret_cast<float*>(rest);
+  if (kDown) {
+    for (int i = threadIdx.x % kHalf; i < a.T * 128; i += kHalf) out[i] = 0;
+  } else {
+    const int t4 = (a.T + 3) / 4 * 4;
+    for (int i = threadIdx.x % kHalf; i < kp * a.T; i += kHalf) sfx[i] = dg::ld_cg_s32(a.sfx + i / a.T * t4 + i % a.T);
   }
-  // The first kernel let this one start only after its own wait: ids and weights are there, h is not yet.
-  build_routing<C::kCols, C::kThreads>(a, r, *reinterpret_cast<RoutingScratch*>(rings), false);
-
-  const int groups = a.I / 128, items = r.jobs * groups, tiles = a.H / C::kRows;
-  const int n4 = kFp4 ? a.H : (a.H / 128 + 3) / 4 * 4;
-  uint8_t* const ring = rings + warp * kStages * C::kBox;
-  uint8_t* const scales = rings + C::kRing + warp * kStages * C::kScaleBytes;
-  float* expanded = reinterpret_cast<float*>(rings + C::kRing + C::kScales) + warp * 64 * kM;
-  float* sums = reinterpret_cast<float*>(rings + C::kRing + C::kScales + C::kExpanded);
-  for (int i = threadIdx.x; i < kWarps * a.T * C::kRows; i += C::kThreads) sums[i] = 0;
   dg::fence_proxy_async_smem();        // the scratch in the rings was written by threads; copies write there next
+  dg::tc_fence_before();
   __syncthreads();
+  dg::tc_fence_after();
 
-  // the cluster's tiles, and this warp's run of their items among all of the cluster's warps
-  const int ranks = cluster_blocks(), rank = ranks > 1 ? dg::cluster_cta_rank() : 0;
-  const int first_tile = blockIdx.x / ranks, tile_step = gridDim.x / ranks;
-  const int place = rank * kWarps + warp, places = ranks * kWarps;
-  const int begin = place * items / places, end = (place + 1) * items / places, begin_job = begin / groups, begin_g = begin % groups;
-  int ft = begin < end && a.fault == 0 ? first_tile : tiles, fi = begin, fjob = begin_job, fg = begin_g, fstage = 0, issued = 0;
-  auto fetch = [&] {
-    if (ft >= tiles) return;
-    if (lane == 0) {
-      const int e = r.job_expert[fjob], row = ft * C::kRows;
-      dg::mbar_arrive_expect_tx(&full[fstage], C::kBox + C::kScaleBytes);
-      dg::tma_load_2d(ring + fstage * C::kBox, &map, &full[fstage], fg * R::kBytes, e * a.H + row);
-      const int32_t* sf = kFp4 ? a.sf2 + (static_cast<long long>(e) * groups + fg) * n4 + row
-                               : a.sf2 + (static_cast<long long>(e) * ((groups + 3) / 4) + fg / 4) * n4 + (row / 128 & ~3);
-      bulk_load(scales + fstage * C::kScaleBytes, sf, C::kScaleBytes, &full[fstage]);
-    }
-    ++issued;
-    if (++fstage == kStages) fstage = 0;
-    if (++fi == end) fi = begin, fjob = begin_job, fg = begin_g, ft += tile_step;
-    else if (++fg == groups) fg = 0, ++fjob;
+  const int blocks = cluster_blocks();
+  Place place;
+  place.half = half;
+  place.rank = a.split ? 2 * (blocks > 1 ? dg::cluster_cta_rank() : 0) + half : 0;
+  place.ranks = a.split ? 2 * blocks : 1;
+  place.first = a.split ? blockIdx.x / blocks : 2 * blockIdx.x + half;
+  place.step = a.split ? gridDim.x / blocks : 2 * gridDim.x;
+  const int groups = (kDown ? a.I : a.H) / 128;
+  const uint32_t tmem = s.tmem + half * kTmemCols;
+  Walk<kDown> walk(a, s.r, place);
+  Run run;
+  // A wait that runs out is recorded, and every role then leaves its loop (the epilogue runs through it without
+  // waiting, since its warps meet at barriers).
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (s.abort) return false;
+    if (dg::mbar_wait(bar, parity, a.timeout_ns)) return true;
+    atomicOr(a.status, dg::kTimeoutBit);
+    s.abort = 1;
+    return false;
   };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch();
-  dg::grid_dependency_wait();
-  dg::grid_launch_dependents();
 
-  // this lane's fragments of an item's tokens (as FP16 pairs) and the scales of its two columns
-  constexpr bool kAhead = NT == 1;     // sixteen columns' fragments leave no registers for a second set
-  uint4 hr[NT][4];
-  uint2 hs[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    hs[n][0] = hs[n][1] = make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) hr[n][i] = make_uint4(0, 0, 0, 0);
-  }
-  const uint32_t slot_bytes = groups * kHBytes;                     // at most 512 slots of 128 groups: 32 bits are enough
-  auto load_h = [&](int job, int g) {
-    const int slot = r.job_slot[job], count = r.job_count[job];
-    const uint8_t* base = a.h + (slot * slot_bytes + g * kHBytes);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (n * 8 + g8 < count) {
-        const uint8_t* from = base + (n * 8 + g8) * slot_bytes + q4 * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) hr[n][i] = dg::ld_cg_v4(from + i * 64);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (n * 8 + 2 * q4 + i < count) hs[n][i] = ld_cg_v2(base + (n * 8 + 2 * q4 + i) * slot_bytes + 256);
-    }
-  };
-  if (begin < end && first_tile < tiles) load_h(begin_job, begin_g);
-
-  bool ok = true;
-  int stage = 0;
-  uint32_t phase = 0;
-  for (int tile = first_tile; tile < tiles; tile += tile_step) {
-    float* mine = sums + warp * a.T * C::kRows;
-    float sum[kM][NT][4];
-#pragma unroll
-    for (int m = 0; m < kM; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0;
-    int job = begin_job, g = begin_g;
-    for (int it = begin; it < end; ++it) {
-      const int slot = r.job_slot[job], count = r.job_count[job];
-      const bool last = it + 1 == end, turn = g + 1 == groups;
-      auto load_next = [&] {
-        if (!last) load_h(turn ? job + 1 : job, turn ? 0 : g + 1);
-        else if (tile + tile_step < tiles) load_h(begin_job, begin_g);
-      };
-      uint4 hc[NT][4];
-      uint2 sc[NT][2];
-      if constexpr (kAhead) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) hc[0][i] = hr[0][i];
-        sc[0][0] = hs[0][0], sc[0][1] = hs[0][1];
-        load_next();
-      }
-      auto frag = [&](int n, int i, int w) { return word_of(kAhead ? hc[n][i] : hr[n][i], w); };
-      auto col_scale = [&](int n, int i, int p) {
-        const uint2 v = kAhead ? sc[n][i] : hs[n][i];
-        return __uint_as_float(p ? v.y : v.x);
-      };
-      ok = wait_full(&full[stage], phase, a, ok);
-      const uint8_t* at = ring + stage * C::kBox;
-      const uint8_t* packed = scales + stage * C::kScaleBytes;
-      // one item, for N eights of columns
-      auto item = [&](auto eights) {
-        constexpr int N = decltype(eights)::value;
-        if constexpr (!kFp4) {
-          const float s = dg::ue8m0_value(lds<uint32_t>(packed + (tile * C::kRows / 128 & 3) * 4) >> (8 * (g & 3)) & 255);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint4 w0 = lds<uint4>(at + R::chunk(row8, 4 * p + q4)), w1 = lds<uint4>(at + R::chunk(8 + row8, 4 * p + q4));
-            float acc[N][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t u0 = word_of(w0, i), u1 = word_of(w1, i);
-              const uint32_t a0 = half2_of_e4m3(u0), a2 = half2_of_e4m3(u0 >> 16), a1 = half2_of_e4m3(u1), a3 = half2_of_e4m3(u1 >> 16);
-#pragma unroll
-              for (int n = 0; n < N; ++n) {
-                const uint32_t b0 = frag(n, 2 * p + i / 2, i % 2 * 2), b1 = frag(n, 2 * p + i / 2, i % 2 * 2 + 1);
-                if (i == 0) mma_f16_zero(acc[n], a0, a1, a2, a3, b0, b1);
-                else mma_f16(acc[n], a0, a1, a2, a3, b0, b1);
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float t = s * col_scale(n, i, p);
-                sum[0][n][i] = fmaf(t, acc[n][i], sum[0][n][i]);
-                sum[0][n][2 + i] = fmaf(t, acc[n][2 + i], sum[0][n][2 + i]);
-              }
+  if (warp == 0) {
+    // ---------------------------------------------- the weights' copies
+    if (lane == 0 && a.fault == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 1;
+      const int n4 = kDown ? a.H : 2 * a.I;
+      bool ok = true;
+      while (ok && walk.next(run)) {
+        for (int g = run.begin; g < run.end; ++g) {
+          if (!(ok = wait(&pipe.empty[stage], phase))) break;
+          uint8_t* to = ring + stage * a.stage_bytes;
+          uint64_t* bar = &pipe.full[stage];
+          dg::mbar_arrive_expect_tx(bar, kFp4 ? kWeights / 2 + 512 : kWeights);
+          dg::tma_load_2d(to, &map, bar, g * 128, run.row0);
+          dg::tma_load_2d(to + kWeights / 2, &map, bar, g * 128, run.row1);
+          if (kFp4) {
+            // scale words [E, groups, N]
+            const int32_t* sf = (kDown ? a.sf2 : a.sf13) + (static_cast<long long>(run.expert) * groups + g) * n4 - static_cast<long long>(run.expert) * n4;
+            uint8_t* scales = to + kWeights + a.token_rows * 128 + kRawA;
+            bulk_load(scales, sf + run.row0, 256, bar);
+            bulk_load(scales + 256, sf + run.row1, 256, bar);
           }
-        } else {
-          // the rows' scales as FP32, each converted by one lane
-          if constexpr (kM == 1) {
-            const uint32_t w = lds<uint32_t>(packed + lane / 2 * 4) >> (lane & 1) * 16;
-            reinterpret_cast<float2*>(expanded)[lane] = make_float2(dg::ue8m0_value(w & 255), dg::ue8m0_value(w >> 8 & 255));
-          } else {
-            reinterpret_cast<float4*>(expanded)[lane] = four_scales(lds<uint32_t>(packed + lane * 4));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            const float4 s0 = reinterpret_cast<const float4*>(expanded)[16 * m + g8], s1 = reinterpret_cast<const float4*>(expanded)[16 * m + 8 + g8];
-            float half[N][4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint32_t u0 = lds<uint32_t>(at + R::chunk(16 * m + row8, b) + 4 * q4), u1 = lds<uint32_t>(at + R::chunk(16 * m + 8 + row8, b) + 4 * q4);
-              const uint32_t even0 = f16_of_even(u0), even1 = f16_of_even(u1), odd0 = f16_of_odd(u0), odd1 = f16_of_odd(u1);
-              const float e0 = float_of(s0, b), e1 = float_of(s1, b);
-#pragma unroll
-              for (int n = 0; n < N; ++n) {
-                float part[4];
-                mma_f16_zero(part, lower_pair(even0), lower_pair(even1), upper_pair(even0), upper_pair(even1), frag(n, b, 0), frag(n, b, 1));
-                mma_f16(part, lower_pair(odd0), lower_pair(odd1), upper_pair(odd0), upper_pair(odd1), frag(n, b, 2), frag(n, b, 3));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float e = i < 2 ? e0 : e1;
-                  half[n][i] = b % 2 == 0 ? e * part[i] : fmaf(e, part[i], half[n][i]);
-                  if (b % 2 == 1) sum[m][n][i] = fmaf(col_scale(n, i % 2, b / 2), half[n][i], sum[m][n][i]);
-                }
-              }
-            }
-          }
+          ++issued;
+          if (++stage == a.stages) stage = 0, phase ^= 1;
         }
-      };
-      if (NT == 1 || count <= 8) item(std::integral_constant<int, 1>());
-      else item(std::integral_constant<int, NT>());
-      __syncwarp();        // every lane has read the stage
-      if constexpr (!kAhead) load_next();
-      if (++stage == kStages) stage = 0, phase ^= 1;
-      fetch();
-      if (last || turn) {
-        // rows row8 and row8 + 8 of each 16 for the job's tokens, into the warp's sums
+      }
+      // no copy may be under way when the block ends
+      for (int i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i)
+        if (!dg::mbar_wait(&pipe.full[i % a.stages], i / a.stages & 1, a.timeout_ns)) break;
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------- the MMAs
+    if (lane == 0) {
+      const uint64_t a_desc = dg::make_smem_desc(dg::smem_addr(ring), 16, 1024, dg::kLayoutSwizzle128B);
+      const uint64_t b_desc = a_desc + (kWeights >> 4);
+      const uint64_t sf_desc = dg::make_smem_desc(dg::smem_addr(ring) + kWeights + a.token_rows * 128, 0, 128, dg::kLayoutNone);
+      int stage = 0;
+      uint32_t phase = 0, n = 0, buffer = 0;
+      bool ok = true;
+      while (ok && walk.next(run)) {
+        const uint32_t sum = n & 1, d = tmem + sum * kSumCols;
+        if (!(ok = wait(&pipe.sum_empty[sum], (n >> 1 & 1) ^ 1))) break;
+        dg::tc_fence_after();
+        const uint32_t cols = kDown ? (kTerms * run.count + 15) / 16 * 16 : 16;
+        const uint32_t idesc = dg::make_idesc_mxf8_e4m3(128, 0) | (cols >> 3) << 17 | (kFp4 ? 5u << 7 : 0u);
+        for (int g = run.begin; g < run.end; ++g) {
+          if (!(ok = wait(&pipe.full[stage], phase) && wait(&pipe.ready[stage], phase))) break;
+          dg::tc_fence_after();
+          const uint64_t off = static_cast<uint64_t>(stage * a.stage_bytes) >> 4;
+          const uint32_t sfa = tmem + 2 * kSumCols + 4 * buffer, sfb = sfa + 8;
+          buffer ^= 1;
+          dg::tmem_copy_32x128b_warpx4(sfa, sf_desc + off + (kTileA >> 4));
+          dg::tmem_copy_32x128b_warpx4(sfb, sf_desc + off + (kTileB >> 4));
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int col = n * 8 + 2 * q4 + i;
-            if (col < count) {
-              float* to = mine + r.token[slot + col] * C::kRows + row8;
-#pragma unroll
-              for (int m = 0; m < kM; ++m) {
-                to[16 * m] += sum[m][n][i];
-                to[16 * m + 8] += sum[m][n][2 + i];
-              }
-            }
-#pragma unroll
-            for (int m = 0; m < kM; ++m) sum[m][n][i] = sum[m][n][2 + i] = 0;
+          for (int k = 0; k < 4; ++k) {
+            // bytes of the scale words: the four 32-column blocks of E2M1 rows and of h, or the K group of four
+            const uint32_t id = dg::idesc_with_sf_id(idesc, kFp4 ? k : g & 3, kDown ? k : g & 3);
+            dg::mma_mxf8_block_scale(d, a_desc + off + 2 * k, b_desc + off + 2 * k, id, sfa, sfb, g != run.begin || k != 0);
           }
-        __syncwarp();
+          dg::tc_commit(&pipe.empty[stage]);
+          if (++stage == a.stages) stage = 0, phase ^= 1;
+        }
+        if (ok) dg::tc_commit(&pipe.sum_full[sum]);
+        ++n;
       }
-      g = turn ? 0 : g + 1;
-      job += turn;
+      // all that was issued has to be done before TMEM is given back
+      dg::tc_commit(&pipe.drain);
+      dg::mbar_wait(&pipe.drain, 0, a.timeout_ns);
     }
-    __syncthreads();
-    // the warps' sums, then the cluster's; each block of a cluster writes its share of the tile
-    const int values = a.T * C::kRows;
-    float* total = sums + kWarps * values;
-    for (int i = threadIdx.x; i < values; i += C::kThreads) {
-      float v = 0;
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------- the tokens' side: copied up to `stages` - 2 stages ahead
+    // (one further, and each stage's MMAs would have to end before the next one's tokens are handed over)
+    const int most_ahead = max(1, a.stages - 2);
+    if (kDown) {
+      dg::grid_dependency_wait();
+      dg::grid_launch_dependents();
+    }
+    const int hs_row = (groups + 3) / 4 * 4;
+    Walk<kDown> done_walk = walk;
+    Run done;
+    int done_g = 0, copied = 0, finished = 0, stage = 0, done_stage = 0;
+    uint32_t phase = 1;
+    bool ok = true, have_done = false;
+    auto finish = [&] {
+      // the oldest stage's rows have arrived: its scales to the form of tcgen05.cp, and over to the MMAs
+      if (!have_done || ++done_g == done.end) {
+        done_walk.next(done);
+        done_g = done.begin;
+        have_done = true;
+      }
+      uint8_t* area = ring + done_stage * a.stage_bytes + kWeights + a.token_rows * 128;
+      uint32_t w[2];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        v += sums[w * values + i];
-        sums[w * values + i] = 0;
+      for (int j = 0; j < 2; ++j) {
+        const int row = lane + 32 * j;
+        w[j] = 0;
+        if (kDown) {
+          if (row < kTerms * done.count) w[j] = *reinterpret_cast<uint32_t*>(area + kRawB + row / kTerms * 16 + (done_g & 3) * 4) - row % kTerms * 0x04040404u;
+        } else if (row < done.count) {
+          w[j] = sfx[done_g / 4 * a.T + s.r.token[done.slot + row]];
+        }
       }
-      total[i] = v;
+      dg::st_shared_v4(dg::smem_addr(area) + kTileB + 16 * lane, w[0], w[1], 0, 0);
+      dg::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) dg::mbar_arrive(&pipe.ready[done_stage]);
+      if (++done_stage == a.stages) done_stage = 0;
+      ++finished;
+    };
+    auto settle = [&](int left) {
+      // copies of all but the last `left` stages have arrived
+      switch (left) {
+        case 0: cp_async_wait<0>(); break;
+        case 1: cp_async_wait<1>(); break;
+        case 2: cp_async_wait<2>(); break;
+        case 3: cp_async_wait<3>(); break;
+        case 4: cp_async_wait<4>(); break;
+        case 5: cp_async_wait<5>(); break;
+        case 6: cp_async_wait<6>(); break;
+        default: cp_async_wait<7>(); break;
+      }
+      __syncwarp();
+    };
+    while (ok && walk.next(run)) {
+      const int rows = kDown ? kTerms * run.count : run.count;
+      for (int g = run.begin; g < run.end; ++g) {
+        ok = __all_sync(kAll, wait(&pipe.empty[stage], phase));
+        if (!ok) break;
+        uint8_t* to = ring + stage * a.stage_bytes + kWeights;
+        for (int i = lane; i < rows * 8; i += 32) {
+          const int row = i / 8, c = i & 7;
+          const uint8_t* from = kDown ? a.h + static_cast<long long>(run.slot * kTerms + row) * a.I : a.x + static_cast<long long>(s.r.token[run.slot + row]) * a.H;
+          dg::cp_async_16(dg::smem_addr(to) + row * 128 + ((c ^ (row & 7)) << 4), from + g * 128 + c * 16);
+        }
+        if (kDown && lane < run.count)
+          dg::cp_async_16(dg::smem_addr(to) + a.token_rows * 128 + kRawB + lane * 16, a.hs + static_cast<long long>(run.slot + lane) * hs_row + (g & ~3));
+        cp_async_commit();
+        ++copied;
+        if (++stage == a.stages) stage = 0, phase ^= 1;
+        if (copied - finished > most_ahead) {
+          settle(most_ahead);
+          finish();
+        }
+      }
     }
-    if (ranks > 1) dg::cluster_sync();
-    else __syncthreads();
-    for (int i = rank * values / ranks + threadIdx.x; i < (rank + 1) * values / ranks; i += C::kThreads) {
-      const long long to = static_cast<long long>(i / C::kRows) * a.H + tile * C::kRows + i % C::kRows;
-      float v = a.c ? __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(a.c) + to))) : 0.0f;
-      if (ranks == 1) v += total[i];
-      else
-        for (int other = 0; other < ranks; ++other) v += ld_shared_cluster_f32(dg::map_to_rank(total + i, other));
-      a.y[to] = __float2bfloat16_rn(v);
+    while (ok && finished < copied) {
+      settle(copied - finished - 1);
+      finish();
     }
-    if (ranks > 1) dg::cluster_sync();
-    else __syncthreads();
+    cp_async_wait<0>();
+  } else if (warp == 3) {
+    // ---------------------------------------------- the weights' scales to the form of tcgen05.cp
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    // E4M3: packed word `lane` of the boxes' 128-row blocks, loaded a run ahead
+    Walk<kDown> ahead = walk;
+    Run next_run;
+    uint32_t next0 = 0, next1 = 0;
+    auto load_words = [&] {
+      if (!ahead.next(next_run)) return;
+      const int n = kDown ? a.H : 2 * a.I, n4 = (n / 128 + 3) / 4 * 4, words = (groups + 3) / 4;
+      const int32_t* sf = (kDown ? a.sf2 : a.sf13) + (static_cast<long long>(next_run.expert) * words + lane) * n4;
+      if (lane < words) {
+        next0 = dg::ld_cg_s32(sf + (next_run.row0 - next_run.expert * n) / 128);
+        next1 = dg::ld_cg_s32(sf + (next_run.row1 - next_run.expert * n) / 128);
+      }
+    };
+    if (!kFp4) load_words();
+    while (ok && walk.next(run)) {
+      const uint32_t word0 = next0, word1 = next1;
+      if (!kFp4) load_words();
+      for (int g = run.begin; g < run.end; ++g) {
+        // E2M1's words come with the weights; E4M3's are here, and wait only for the stage to be free
+        ok = __all_sync(kAll, kFp4 ? wait(&pipe.full[stage], phase) : wait(&pipe.empty[stage], phase ^ 1));
+        if (!ok) break;
+        const uint32_t area = dg::smem_addr(ring) + stage * a.stage_bytes + kWeights + a.token_rows * 128;
+        uint32_t w[4];
+        if (kFp4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = dg::ld_shared_u32(area + kRawA + 4 * (lane + 32 * j));
+        } else {
+          w[0] = w[1] = __shfl_sync(kAll, word0, g / 4);
+          w[2] = w[3] = __shfl_sync(kAll, word1, g / 4);
+        }
+        dg::st_shared_v4(area + kTileA + 16 * lane, w[0], w[1], w[2], w[3]);
+        dg::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) dg::mbar_arrive(&pipe.ready[stage]);
+        if (++stage == a.stages) stage = 0, phase ^= 1;
+      }
+    }
+  } else {
+    // ---------------------------------------------- the sums: warps 4 to 7, a row of 128 per thread
+    const int quad = warp - 4, row = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    uint32_t n = 0;
+    while (walk.next(run)) {
+      const uint32_t sum = n & 1;
+      wait(&pipe.sum_full[sum], n >> 1 & 1);
+      __syncwarp();
+      dg::tc_fence_after();
+      uint32_t v[kSumCols];
+#pragma unroll
+      for (int i = 0; i < kSumCols; i += 16)
+        if (i < (kDown ? kTerms : 1) * run.count) dg::tmem_load_32x32b_x16(tmem + lanes + sum * kSumCols + i, v + i);
+      dg::tmem_load_wait();
+      dg::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) dg::mbar_arrive(&pipe.sum_empty[sum]);
+      ++n;
+      if constexpr (kDown) {
+        // this row of the job's tokens: no other thread has it
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (c < run.count)
+            out[s.r.token[run.slot + c] * 128 + row] += __uint_as_float(v[kTerms * c]) + __uint_as_float(v[kTerms * c + 1]) + __uint_as_float(v[kTerms * c + 2]);
+      } else if (a.split) {
+        // a rank's share of K: added up at the end (of its only unit)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) exchange[row * 17 + c] = __uint_as_float(v[c]);
+      } else {
+        store_inner(a, s.r, run, exchange, v, half, quad, lane);
+      }
+    }
   }
-  // no copy may be under way when the block ends
-  if (!ok && a.fault == 0)
-    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-      if (!dg::mbar_wait(&full[i % kStages], i / kStages & 1, a.timeout_ns)) break;
+
+  __syncwarp();
+  __syncthreads();
+  if (blocks > 1) dg::cluster_sync();
+  if (warp >= 4 && a.split) {
+    const int quad = warp - 4, row = quad * 32 + lane;
+    // rank r's pipeline is half r % 2 of block r / 2
+    auto of_rank = [&](const float* mine, int r) {
+      return ld_shared_cluster_f32(dg::map_to_rank(mine + (r % 2 - half) * (a.rest_bytes / 4), r / 2));
+    };
+    if constexpr (kDown) {
+      // each pipeline writes its share of the tokens
+      for (int t = place.rank; t < a.T; t += place.ranks) {
+        const long long to = static_cast<long long>(t) * a.H + place.first * 128 + row;
+        float sum = a.c ? __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(a.c) + to))) : 0.0f;
+        for (int r = 0; r < place.ranks; ++r) sum += of_rank(out + t * 128 + row, r);
+        a.y[to] = __float2bfloat16_rn(sum);
+      }
+    } else if (place.rank == 0) {
+      Walk<kDown> again(a, s.r, place);
+      if (again.next(run)) {
+        uint32_t v[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          float sum = 0;
+          if (c < run.count)
+            for (int r = 0; r < place.ranks; ++r) sum += of_rank(exchange + row * 17 + c, r);
+          v[c] = __float_as_uint(sum);
+        }
+        named_barrier(1, 128);         // before the exchange is written again
+        store_inner(a, s.r, run, exchange, v, half, quad, lane);
+      }
+    }
+  }
+  if (blocks > 1) dg::cluster_sync();  // no block may be gone whose sums are read
+  else __syncthreads();
+  if (threadIdx.x / 32 == 1) dg::tmem_dealloc(s.tmem, 2 * kTmemCols);
 }
 
 // -------------------------------------------------------------------------------------------
 
-template <bool kFp4, bool kBig>
-dg_status run_layer(const MoeArgs& a, const LaunchContext& ctx, cudaStream_t stream) {
-  using U = Up<kFp4, kBig>;
-  using D = Down<kFp4, kBig>;
-  static_assert(sizeof(RoutingScratch) <= U::kRing && sizeof(RoutingScratch) <= D::kRing, "scratch in the rings");
-  static_assert(U::kBlock == 64 || U::kBlock == 128, "h has two scales per 128 columns");
-  // Blocks of a cluster: as many, a power of two up to 8, as fit the SMs for the units (tiles) that there are at
-  // most, if each still has K groups (items for its warps) to work on.
-  const int groups = a.H / 128, units = std::min(a.T * a.k, a.E) * (a.I / U::kBlock), tiles = a.H / D::kRows;
-  const int items = std::min(a.T * a.k, a.E) * (a.I / 128);
-  const int up_room = ctx.sms * (U::kBlocksPerSm == 2 && U::smem(groups, a.T, 2) <= kHalfSm ? 2 : 1);
-  int up_cluster = 1, down_cluster = 1;
-  while (up_cluster < 8 && 2 * up_cluster * units <= up_room && 2 * up_cluster <= groups) up_cluster *= 2;
-  while (down_cluster < 8 && 2 * down_cluster * tiles <= ctx.sms && 2 * down_cluster * D::kWarps <= items) down_cluster *= 2;
-  const int up_smem = U::smem(groups, a.T, up_cluster), down_smem = D::smem(a.T);
-  if (up_smem > kMaxSmem || down_smem > kMaxSmem) return DG_ERR_UNSUPPORTED;
+template <bool kFp4>
+dg_status run_layer(MoeArgs a, const void* w13, const void* w2, const LaunchContext& ctx, cudaStream_t stream) {
   // once per thread and device: the limit, above what any shape needs
   static thread_local int ready = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && ready != dev) {
-    e = cudaFuncSetAttribute(moe_up_kernel<kFp4, kBig>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_down_kernel<kFp4, kBig>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    e = cudaFuncSetAttribute(moe_kernel<kFp4, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_kernel<kFp4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return dg::record_cuda_error(e);
-  const int per = kFp4 ? 2 : 1;
   CUtensorMap up_map, down_map;
-  if (!dg::byte_rows_map(&up_map, a.w13, static_cast<uint64_t>(a.E) * 2 * a.I, a.H / per, U::kBlock, Rows<kFp4>::kBytes) ||
-      !dg::byte_rows_map(&down_map, a.w2, static_cast<uint64_t>(a.E) * a.H, a.I / per, D::kRows, Rows<kFp4>::kBytes))
+  if (!dg::weight_rows_map(&up_map, w13, static_cast<uint64_t>(a.E) * 2 * a.I, a.H, 64, kFp4) ||
+      !dg::weight_rows_map(&down_map, w2, static_cast<uint64_t>(a.E) * a.H, a.I, 64, kFp4))
     return DG_ERR_CUDA;
-  const int up_clusters = up_cluster > 1 ? units : std::min(units, U::kBlocksPerSm * ctx.sms);
-  const int down_clusters = std::min(tiles, std::max(1, ctx.sms / down_cluster));
-  if (dg_status s = dg::launch_clusters(moe_up_kernel<kFp4, kBig>, static_cast<unsigned>(up_clusters * up_cluster), static_cast<unsigned>(up_cluster),
-                                        U::kThreads, static_cast<size_t>(up_smem), stream, ctx.pdl, up_map, a); s != DG_OK) return s;
-  return dg::launch_clusters(moe_down_kernel<kFp4, kBig>, static_cast<unsigned>(down_clusters * down_cluster), static_cast<unsigned>(down_cluster),
-                             D::kThreads, static_cast<size_t>(down_smem), stream, ctx.pdl, down_map, a);
+  // jobs, at most: one per slot, and one per expert and for every 16 slots
+  const int jobs = std::min(a.T * a.k, a.E + (a.T * a.k + kCols - 1) / kCols);
+  const int cols = std::min(a.T, kCols);
+  auto ring = [&](MoeArgs& m, int rows, int rest) {
+    m.token_rows = (rows + 15) / 16 * 16;
+    m.stage_bytes = stage_bytes(m.token_rows);
+    m.rest_bytes = (rest + 15) / 16 * 16;
+    m.stages = std::min(kMaxStages, (kMaxSmem - 1024 - 2 * m.rest_bytes) / (2 * m.stage_bytes));
+    return static_cast<size_t>(1024 + 2 * (m.stages * m.stage_bytes + m.rest_bytes));
+  };
+
+  // First kernel: units to pipelines, or where there are fewer units than SMs, each to the pipelines of a
+  // cluster, of as many blocks as fit, if each pipeline still has K groups.
+  const int units = jobs * (a.I / kBlock), groups = a.H / 128;
+  MoeArgs up = a;
+  up.split = units <= ctx.sms && groups >= 2;
+  const size_t up_smem = ring(up, cols, (groups + 3) / 4 * a.T * 4 + (up.split ? 128 * 17 : 64 * 17 + 2 * kCols) * 4);
+  int cluster = 1;
+  while (up.split && cluster < kMaxCluster && 2 * cluster * units <= ctx.sms && 4 * cluster <= groups) cluster *= 2;
+  const int up_grid = up.split ? units * cluster : std::min((units + 1) / 2, ctx.sms);
+  if (dg_status s = dg::launch_clusters(moe_kernel<kFp4, false>, static_cast<unsigned>(up_grid), static_cast<unsigned>(cluster), kThreads, up_smem,
+                                        stream, ctx.pdl, up_map, up); s != DG_OK) return s;
+
+  // Second kernel: a cluster per tile, of as many blocks as fit, if each pipeline still has a few items.
+  const int tiles = a.H / 128, items = jobs * (a.I / 128);
+  cluster = std::max(1, std::min({kMaxCluster, ctx.sms / tiles, items / 4}));
+  MoeArgs down = a;
+  down.split = 1;
+  const size_t down_smem = ring(down, kTerms * cols, a.T * 128 * 4);
+  return dg::launch_clusters(moe_kernel<kFp4, true>, static_cast<unsigned>(tiles * cluster), static_cast<unsigned>(cluster), kThreads, down_smem, stream,
+                             ctx.pdl, down_map, down);
 }
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -926,15 +735,20 @@ dg_status few_tokens(const void* x, const int32_t* sfx, const void* w13, const i
   if (!aligned(x, 16) || !aligned(sfx, 16) || !aligned(w13, 16) || !aligned(sf13, 16) || !aligned(w2, 16) || !aligned(sf2, 16) ||
       !aligned(ids, 4) || !aligned(weights, 4) || !aligned(c, 16) || !aligned(y, 16))
     return DG_ERR_MISALIGNED;
+  if (kFp4 && (!aligned(w13, 32) || !aligned(w2, 32))) return DG_ERR_MISALIGNED;
   LaunchContext ctx;
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+  const size_t slots = static_cast<size_t>(T) * topk, scale_words = slots * ((I / 128 + 3) / 4 * 4);
   dg::StreamWorkspace ws;
-  void* h = nullptr;
-  if (dg_status s = ws.acquire(stream, static_cast<size_t>(T) * topk * (I / 128) * kHBytes, &h); s != DG_OK) return s;
-  const MoeArgs a{static_cast<const uint8_t*>(x), sfx, static_cast<const uint8_t*>(w13), sf13, static_cast<const uint8_t*>(w2), sf2,
-                  ids, weights, static_cast<const __nv_bfloat16*>(c), static_cast<__nv_bfloat16*>(y), static_cast<uint8_t*>(h),
-                  ctx.status, dg::pipeline_wait_timeout_ns(), dg::debug_fault_mode(), T, topk, E, H, I};
-  return T <= 8 ? run_layer<kFp4, false>(a, ctx, stream) : run_layer<kFp4, true>(a, ctx, stream);
+  void* scratch = nullptr;
+  if (dg_status s = ws.acquire(stream, scale_words * 4 + slots * kTerms * I, &scratch); s != DG_OK) return s;
+  MoeArgs a{};
+  a.x = static_cast<const uint8_t*>(x), a.sfx = sfx, a.sf13 = sf13, a.sf2 = sf2, a.ids = ids, a.weights = weights;
+  a.c = static_cast<const __nv_bfloat16*>(c), a.y = static_cast<__nv_bfloat16*>(y);
+  a.hs = static_cast<uint32_t*>(scratch), a.h = static_cast<uint8_t*>(scratch) + scale_words * 4;
+  a.status = ctx.status, a.timeout_ns = dg::pipeline_wait_timeout_ns(), a.fault = dg::debug_fault_mode();
+  a.T = T, a.k = topk, a.E = E, a.H = H, a.I = I;
+  return run_layer<kFp4>(a, w13, w2, ctx, stream);
 }
 
 }  // namespace

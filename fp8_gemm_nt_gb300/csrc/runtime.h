@@ -25,9 +25,10 @@ dg_status launch_context(LaunchContext* out);
 // Records `e` for dg_last_cuda_error and returns DG_ERR_CUDA.
 dg_status record_cuda_error(cudaError_t e);
 
-// Tensor map of a [rows, row_bytes] byte matrix (16-byte aligned rows), copied in boxes of box_rows x box_bytes
-// with the swizzle of that width (64 or 128 bytes). Maps are cached per host thread. False on failure.
-bool byte_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows, uint32_t box_bytes);
+// Tensor map of a [rows, cols] weight matrix, E4M3 or packed E2M1 (spread to a byte an element as it is copied),
+// copied in boxes of box_rows x 128 columns with the 128-byte swizzle. Maps are cached per host thread. False on
+// failure.
+bool weight_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool e2m1);
 
 // `bytes` of the stream's workspace, past the stream-K arrival counters at its start (which stay
 // zero). Held until the object goes out of scope, which has to be after the launches that use it.

@@ -374,7 +374,7 @@ dg_status dg_moe_fp8_few_tokens(const void* x, const int32_t* sfx, const void* w
 /*
  * The same layer with the experts' weights in E2M1: w13 uint8 [E, 2 I, H/2] with sf13 int32 [E, H/128,
  * ceil4(2 I)], w2 uint8 [E, H, I/2] with sf2 int32 [E, I/128, ceil4(H)], as b and sfb of the FP8 x FP4
- * GEMMs (16-byte alignment is enough here).
+ * GEMMs (32-byte aligned).
  */
 dg_status dg_moe_fp8_fp4_few_tokens(const void* x, const int32_t* sfx, const void* w13, const int32_t* sf13, const void* w2,
                                     const int32_t* sf2, const int32_t* topk_ids, const float* topk_weights, const void* c,
