@@ -997,6 +997,7 @@ dg_status StreamWorkspace::acquire(cudaStream_t stream, size_t bytes, void** out
   DeviceState* ds = nullptr;
   if (dg_status s = device_state(&ds); s != DG_OK) return s;
   constexpr size_t kCounters = kSkCounterInts * sizeof(int);
+  static_assert(kSkCounterInts == kArrivalCounters, "runtime.h's count");
   auto* lease = new (std::nothrow) WorkspaceLease;
   if (!lease) return cuda_fail(cudaErrorMemoryAllocation);
   if (dg_status s = stream_workspace(*ds, stream, kCounters + bytes, lease); s != DG_OK) {
@@ -1004,6 +1005,7 @@ dg_status StreamWorkspace::acquire(cudaStream_t stream, size_t bytes, void** out
     return s;
   }
   lease_ = lease;
+  counters_ = static_cast<int*>(lease->ptr);
   *out = static_cast<char*>(lease->ptr) + kCounters;
   return DG_OK;
 }

@@ -24,9 +24,11 @@
 // A pipeline is a warp each for the weights' copies, the tokens' side, the weights' scales and the MMAs, and
 // four that read the sums from TMEM, with a ring of stages of 128 columns. A block (one to an SM) is two
 // pipelines, halves that share nothing but the routing: one thread issuing MMAs does not keep up with HBM.
-// Where there are fewer pieces of work than pipelines (always in the second kernel, whose tiles are few),
-// the halves of a cluster of blocks share a piece, each with a part of K, and sum through (distributed)
-// shared memory in the order of their ranks.
+//
+// The pieces (64 columns of h of a job; 128 output rows) are few and large, so their stages are dealt out
+// evenly, each pipeline a run of them. A piece that is cut is summed by the last of its pipelines to finish:
+// each writes its FP32 part to the workspace, and the last adds all parts in the order of the pipelines, so
+// that the result does not depend on which one it was. Nobody waits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -57,7 +59,7 @@ constexpr int kBlock = 64;              // columns of h of a unit of the first k
 constexpr int kHalf = 256;              // threads of a pipeline
 constexpr int kThreads = 2 * kHalf;
 constexpr int kMaxStages = 8;
-constexpr int kMaxCluster = 8;
+constexpr int kMinShare = 4;            // stages of a pipeline, at least, where there are that few
 constexpr int kMaxSmem = 221 * 1024;    // dynamic
 
 struct MoeArgs {
@@ -77,7 +79,8 @@ struct MoeArgs {
   int T, k, E, H, I;
   int stages, stage_bytes, token_rows;   // of a pipeline's ring; rows of a stage's tokens
   int rest_bytes;                        // of a pipeline's shared memory beside the rings
-  int split;                             // the pipelines of a cluster share a piece
+  float* parts;                          // [pipelines][2] parts of cut pieces: [128][16], [T][128]
+  int* arrivals;                         // per first pipeline of a cut piece; zero between launches
 };
 
 // -------------------------------------------------------------------------------------------
@@ -180,16 +183,6 @@ __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, Rout
 // The products of both kernels
 // -------------------------------------------------------------------------------------------
 
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ int cluster_blocks() {
-  int n;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -219,6 +212,7 @@ struct Shared {
   Routing r;
   Pipe pipe[2];
   uint32_t tmem;
+  int arrived[2];
   volatile uint32_t abort;
 };
 
@@ -227,44 +221,55 @@ struct Run {
   int job, expert, slot, count;
   int row0, row1;          // of the boxes, in the [E * N, K] weight matrix
   int begin, end;          // K groups
-  int piece;               // unit (first kernel) or tile (second)
+  int unit;                // first kernel: (job, 64 columns of h); `piece` the columns' index
+  int piece;               // second kernel: the tile
+  bool done;               // the pipeline's last run of the piece
 };
 
-// Who a pipeline is: `rank` of the `ranks` pipelines that share a piece, and the piece's place.
-struct Place {
-  int half, rank, ranks, first, step;
+// The stages of all pieces, dealt out to `pipes` pipelines in runs of equal length (to one).
+struct Deal {
+  long long stages;
+  int pipes;
+  __device__ __forceinline__ Deal(long long stages_, int most) : stages(stages_) {
+    const long long wanted = (stages + kMinShare - 1) / kMinShare;
+    pipes = static_cast<int>(wanted < most ? (wanted > 0 ? wanted : 1) : most);
+  }
+  __device__ __forceinline__ long long begin(int p) const { return p < pipes ? p * stages / pipes : stages; }
+  __device__ __forceinline__ int owner(long long stage) const { return static_cast<int>(((stage + 1) * pipes - 1) / stages); }
 };
 
-// A pipeline's runs in order. First kernel: units (job, 64 columns of h), each 64 gate rows and their up rows,
-// all K groups of them or the rank's share. Second kernel: one tile of 128 output rows, the rank's share of its
-// (job, K group) items, cut at the jobs.
+// A pipeline's runs in order. First kernel: the pieces are units (job, 64 columns of h), each 64 gate rows and
+// their up rows, a stage a K group. Second kernel: tiles of 128 output rows, a stage a (job, K group); a run ends
+// with its job.
 template <bool kDown>
 struct Walk {
   const MoeArgs& a;
   const Routing& r;
-  int at, end, groups, step, rank, ranks, tile;
-  __device__ __forceinline__ Walk(const MoeArgs& args, const Routing& routing, const Place& p) : a(args), r(routing), step(p.step), rank(p.rank), ranks(p.ranks), tile(p.first) {
+  long long at, end;
+  int groups, per;         // K groups, and stages of a piece
+  __device__ __forceinline__ Walk(const MoeArgs& args, const Routing& routing, const Deal& deal, int pipe) : a(args), r(routing) {
     groups = (kDown ? a.I : a.H) / 128;
-    const int items = r.jobs * groups;
-    at = kDown ? rank * items / ranks : p.first;
-    end = kDown ? (rank + 1) * items / ranks : r.jobs * (a.I / kBlock);
+    per = kDown ? r.jobs * groups : groups;
+    at = deal.begin(pipe);
+    end = deal.begin(pipe + 1);
   }
   __device__ __forceinline__ bool next(Run& s) {
     if (at >= end) return false;
+    const int piece = static_cast<int>(at / per), in = static_cast<int>(at - static_cast<long long>(piece) * per);
     if (kDown) {
-      s.job = at / groups;
-      s.begin = at - s.job * groups;
-      s.end = min(groups, s.begin + end - at);
-      at += s.end - s.begin;
-      s.piece = tile;
+      s.job = in / groups;
+      s.piece = piece;
+      s.begin = in - s.job * groups;
     } else {
       const int blocks = a.I / kBlock;
-      s.job = at / blocks;
-      s.piece = at - s.job * blocks;
-      s.begin = rank * groups / ranks;
-      s.end = (rank + 1) * groups / ranks;
-      at += step;
+      s.unit = piece;
+      s.job = piece / blocks;
+      s.piece = piece - s.job * blocks;
+      s.begin = in;
     }
+    s.end = static_cast<int>(min(static_cast<long long>(groups), s.begin + end - at));
+    at += s.end - s.begin;
+    s.done = at >= end || at % per == 0;
     s.expert = r.job_expert[s.job];
     s.slot = r.job_slot[s.job];
     s.count = r.job_count[s.job];
@@ -273,6 +278,8 @@ struct Walk {
     return true;
   }
 };
+
+__device__ __forceinline__ void add(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
 // FP32 value of an E4M3 code.
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
@@ -365,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   }
   // (The first kernel let the second start only after its own wait: ids and weights are there, h is not yet.)
   build_routing<kCols, kThreads>(a, s.r, *reinterpret_cast<RoutingScratch*>(base), !kDown && blockIdx.x == 0);
-  // the halves' rings, then for each half: the first kernel's token scales [KP, T] and its exchange of sums
-  // (of 64 rows and their maxima, or all 128 rows where a piece is split); the second's output [T][128]
+  // the halves' rings, then for each half: the first kernel's token scales [KP, T] and its exchange of sums (64
+  // rows and their maxima); the second's output [T][128]
   uint8_t* const ring = base + half * a.stages * a.stage_bytes;
   uint8_t* const rest = base + 2 * a.stages * a.stage_bytes + half * a.rest_bytes;
   uint32_t* const sfx = reinterpret_cast<uint32_t*>(rest);
@@ -384,16 +391,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   __syncthreads();
   dg::tc_fence_after();
 
-  const int blocks = cluster_blocks();
-  Place place;
-  place.half = half;
-  place.rank = a.split ? 2 * (blocks > 1 ? dg::cluster_cta_rank() : 0) + half : 0;
-  place.ranks = a.split ? 2 * blocks : 1;
-  place.first = a.split ? blockIdx.x / blocks : 2 * blockIdx.x + half;
-  place.step = a.split ? gridDim.x / blocks : 2 * gridDim.x;
   const int groups = (kDown ? a.I : a.H) / 128;
   const uint32_t tmem = s.tmem + half * kTmemCols;
-  Walk<kDown> walk(a, s.r, place);
+  const int me = 2 * blockIdx.x + half;
+  const long long pieces = kDown ? a.H / 128 : static_cast<long long>(s.r.jobs) * (a.I / kBlock);
+  const Deal deal(pieces * (kDown ? s.r.jobs * groups : groups), 2 * gridDim.x);
+  Walk<kDown> walk(a, s.r, deal, me);
   Run run;
   // A wait that runs out is recorded, and every role then leaves its loop (the epilogue runs through it without
   // waiting, since its warps meet at barriers).
@@ -608,66 +611,125 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       wait(&pipe.sum_full[sum], n >> 1 & 1);
       __syncwarp();
       dg::tc_fence_after();
-      uint32_t v[kSumCols];
+      uint32_t v[kCols];
+      if constexpr (kDown) {
+        // this row of the job's tokens, the sum of three terms each: no other thread has it
+#pragma unroll 1
+        for (int i = 0; i < kTerms * run.count; i += 16) {
+          dg::tmem_load_32x32b_x16(tmem + lanes + sum * kSumCols + i, v);
+          dg::tmem_load_wait();
 #pragma unroll
-      for (int i = 0; i < kSumCols; i += 16)
-        if (i < (kDown ? kTerms : 1) * run.count) dg::tmem_load_32x32b_x16(tmem + lanes + sum * kSumCols + i, v + i);
-      dg::tmem_load_wait();
+          for (int j = 0; j < 16; ++j)
+            if (i + j < kTerms * run.count) out[s.r.token[run.slot + (i + j) / kTerms] * 128 + row] += __uint_as_float(v[j]);
+        }
+      } else {
+        dg::tmem_load_32x32b_x16(tmem + lanes + sum * kSumCols, v);
+        dg::tmem_load_wait();
+      }
       dg::tc_fence_before();
       __syncwarp();
       if (lane == 0) dg::mbar_arrive(&pipe.sum_empty[sum]);
       ++n;
+      // a piece that other pipelines have parts of: 1 if this one is the last to bring its own
+      auto last_of = [&](long long piece_begin, int per, int* first, int* last) {
+        *first = deal.owner(piece_begin);
+        *last = deal.owner(piece_begin + per - 1);
+        __threadfence();
+        named_barrier(1 + 2 * half, 128);
+        if (warp == 4 && lane == 0) {
+          const int before = atomicAdd(a.arrivals + *first, 1);
+          s.arrived[half] = before == *last - *first;
+          if (before == *last - *first) a.arrivals[*first] = 0;
+        }
+        named_barrier(1 + 2 * half, 128);
+        __threadfence();
+        return s.arrived[half] != 0;
+      };
+      // where pipeline p put its part of the piece: a piece that it did not begin is its first
+      auto part_of = [&](int p, long long piece_begin, int floats) {
+        return a.parts + (2ll * p + (deal.begin(p) > piece_begin ? 0 : 1)) * floats;
+      };
       if constexpr (kDown) {
-        // this row of the job's tokens: no other thread has it
+        if (!run.done) continue;
+        const int per = s.r.jobs * groups;
+        const long long begin = static_cast<long long>(run.piece) * per;
+        const bool whole = deal.begin(me) <= begin && deal.begin(me + 1) >= begin + per;
+        int first = me, last = me;
+        bool write = true;
+        if (!whole) {
+          float* mine = part_of(me, begin, a.T * 128);
+#pragma unroll 1
+          for (int t = 0; t < a.T; ++t) mine[t * 128 + row] = out[t * 128 + row];
+          write = last_of(begin, per, &first, &last);
+        }
+        if (whole || write) {
+          // four columns of a token each: a warp a token, and as many of its parts at once as the registers hold
+          if (whole) named_barrier(1 + 2 * half, 128);
+          for (int t = quad; t < a.T; t += 4) {
+            const long long to = static_cast<long long>(t) * a.H + run.piece * 128 + 4 * lane;
+            float4 total = make_float4(0, 0, 0, 0);
+            if (a.c) {
+              const uint2 c = __ldcg(reinterpret_cast<const uint2*>(a.c + to));
+              dg::unpack_bf16(c.x, total.x, total.y);
+              dg::unpack_bf16(c.y, total.z, total.w);
+            }
+            if (whole) add(total, *reinterpret_cast<const float4*>(out + t * 128 + 4 * lane));
+            else
+              for (int p = first; p <= last; p += 8) {
+                float4 part[8];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (c < run.count)
-            out[s.r.token[run.slot + c] * 128 + row] += __uint_as_float(v[kTerms * c]) + __uint_as_float(v[kTerms * c + 1]) + __uint_as_float(v[kTerms * c + 2]);
-      } else if (a.split) {
-        // a rank's share of K: added up at the end (of its only unit)
+                for (int i = 0; i < 8; ++i)
+                  part[i] = p + i <= last ? __ldcg(reinterpret_cast<const float4*>(part_of(p + i, begin, a.T * 128) + t * 128) + lane) : make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) exchange[row * 17 + c] = __uint_as_float(v[c]);
+                for (int i = 0; i < 8; ++i) add(total, part[i]);
+              }
+            *reinterpret_cast<uint2*>(a.y + to) = make_uint2(dg::pack_bf16(total.x, total.y), dg::pack_bf16(total.z, total.w));
+          }
+          if (whole) named_barrier(1 + 2 * half, 128);
+        }
+#pragma unroll 4
+        for (int t = 0; t < a.T; ++t) out[t * 128 + row] = 0;
       } else {
+        if (run.end - run.begin < groups) {
+          const long long begin = static_cast<long long>(run.unit) * groups;
+          float4* mine = reinterpret_cast<float4*>(part_of(me, begin, 128 * kCols)) + row * (kCols / 4);
+#pragma unroll
+          for (int i = 0; i < kCols / 4; ++i)
+            if (4 * i < run.count) mine[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+          int first, last;
+          if (!last_of(begin, groups, &first, &last)) continue;
+          float total[kCols];
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) total[i] = 0;
+          for (int p = first; p <= last; p += 3) {
+            float4 f[3][kCols / 4];
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+#pragma unroll
+              for (int i = 0; i < kCols / 4; ++i)
+                f[j][i] = p + j <= last && 4 * i < run.count ? __ldcg(reinterpret_cast<const float4*>(part_of(p + j, begin, 128 * kCols)) + row * (kCols / 4) + i)
+                                                             : make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+#pragma unroll
+              for (int i = 0; i < kCols / 4; ++i)
+                total[4 * i] += f[j][i].x, total[4 * i + 1] += f[j][i].y, total[4 * i + 2] += f[j][i].z, total[4 * i + 3] += f[j][i].w;
+          }
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) v[i] = __float_as_uint(total[i]);
+        }
         store_inner(a, s.r, run, exchange, v, half, quad, lane);
       }
+    }
+    if (kDown && s.r.jobs == 0) {
+      // no expert at all: the addend alone
+      for (int i = me * 128 + row; i < a.T * a.H; i += 2 * gridDim.x * 128)
+        a.y[i] = a.c ? a.c[i] : __float2bfloat16_rn(0.0f);
     }
   }
 
   __syncwarp();
   __syncthreads();
-  if (blocks > 1) dg::cluster_sync();
-  if (warp >= 4 && a.split) {
-    const int quad = warp - 4, row = quad * 32 + lane;
-    // rank r's pipeline is half r % 2 of block r / 2
-    auto of_rank = [&](const float* mine, int r) {
-      return ld_shared_cluster_f32(dg::map_to_rank(mine + (r % 2 - half) * (a.rest_bytes / 4), r / 2));
-    };
-    if constexpr (kDown) {
-      // each pipeline writes its share of the tokens
-      for (int t = place.rank; t < a.T; t += place.ranks) {
-        const long long to = static_cast<long long>(t) * a.H + place.first * 128 + row;
-        float sum = a.c ? __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(a.c) + to))) : 0.0f;
-        for (int r = 0; r < place.ranks; ++r) sum += of_rank(out + t * 128 + row, r);
-        a.y[to] = __float2bfloat16_rn(sum);
-      }
-    } else if (place.rank == 0) {
-      Walk<kDown> again(a, s.r, place);
-      if (again.next(run)) {
-        uint32_t v[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          float sum = 0;
-          if (c < run.count)
-            for (int r = 0; r < place.ranks; ++r) sum += of_rank(exchange + row * 17 + c, r);
-          v[c] = __float_as_uint(sum);
-        }
-        named_barrier(1, 128);         // before the exchange is written again
-        store_inner(a, s.r, run, exchange, v, half, quad, lane);
-      }
-    }
-  }
-  if (blocks > 1) dg::cluster_sync();  // no block may be gone whose sums are read
-  else __syncthreads();
   if (threadIdx.x / 32 == 1) dg::tmem_dealloc(s.tmem, 2 * kTmemCols);
 }
 
@@ -700,26 +762,15 @@ dg_status run_layer(MoeArgs a, const void* w13, const void* w2, const LaunchCont
     return static_cast<size_t>(1024 + 2 * (m.stages * m.stage_bytes + m.rest_bytes));
   };
 
-  // First kernel: units to pipelines, or where there are fewer units than SMs, each to the pipelines of a
-  // cluster, of as many blocks as fit, if each pipeline still has K groups.
-  const int units = jobs * (a.I / kBlock), groups = a.H / 128;
-  MoeArgs up = a;
-  up.split = units <= ctx.sms && groups >= 2;
-  const size_t up_smem = ring(up, cols, (groups + 3) / 4 * a.T * 4 + (up.split ? 128 * 17 : 64 * 17 + 2 * kCols) * 4);
-  int cluster = 1;
-  while (up.split && cluster < kMaxCluster && 2 * cluster * units <= ctx.sms && 4 * cluster <= groups) cluster *= 2;
-  const int up_grid = up.split ? units * cluster : std::min((units + 1) / 2, ctx.sms);
-  if (dg_status s = dg::launch_clusters(moe_kernel<kFp4, false>, static_cast<unsigned>(up_grid), static_cast<unsigned>(cluster), kThreads, up_smem,
-                                        stream, ctx.pdl, up_map, up); s != DG_OK) return s;
-
-  // Second kernel: a cluster per tile, of as many blocks as fit, if each pipeline still has a few items.
-  const int tiles = a.H / 128, items = jobs * (a.I / 128);
-  cluster = std::max(1, std::min({kMaxCluster, ctx.sms / tiles, items / 4}));
-  MoeArgs down = a;
-  down.split = 1;
+  // as many blocks as there are SMs, or shares of stages for two pipelines each
+  auto grid = [&](long long stages) { return static_cast<unsigned>(std::max(1ll, std::min<long long>(ctx.sms, (stages + 2 * kMinShare - 1) / (2 * kMinShare)))); };
+  const int up_groups = a.H / 128, down_groups = a.I / 128;
+  MoeArgs up = a, down = a;
+  const size_t up_smem = ring(up, cols, (up_groups + 3) / 4 * a.T * 4 + (64 * 17 + 2 * kCols) * 4);
+  if (dg_status s = dg::launch(moe_kernel<kFp4, false>, grid(static_cast<long long>(jobs) * (a.I / kBlock) * up_groups), kThreads, up_smem, stream, ctx.pdl,
+                               up_map, up); s != DG_OK) return s;
   const size_t down_smem = ring(down, kTerms * cols, a.T * 128 * 4);
-  return dg::launch_clusters(moe_kernel<kFp4, true>, static_cast<unsigned>(tiles * cluster), static_cast<unsigned>(cluster), kThreads, down_smem, stream,
-                             ctx.pdl, down_map, down);
+  return dg::launch(moe_kernel<kFp4, true>, grid(static_cast<long long>(a.H / 128) * jobs * down_groups), kThreads, down_smem, stream, ctx.pdl, down_map, down);
 }
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -739,13 +790,15 @@ dg_status few_tokens(const void* x, const int32_t* sfx, const void* w13, const i
   LaunchContext ctx;
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   const size_t slots = static_cast<size_t>(T) * topk, scale_words = slots * ((I / 128 + 3) / 4 * 4);
+  const size_t part_floats = 2ull * 2 * ctx.sms * 128 * std::max(kCols, T), h_bytes = (slots * kTerms * I + 15) / 16 * 16;
   dg::StreamWorkspace ws;
   void* scratch = nullptr;
-  if (dg_status s = ws.acquire(stream, scale_words * 4 + slots * kTerms * I, &scratch); s != DG_OK) return s;
+  if (dg_status s = ws.acquire(stream, scale_words * 4 + h_bytes + part_floats * 4, &scratch); s != DG_OK) return s;
   MoeArgs a{};
   a.x = static_cast<const uint8_t*>(x), a.sfx = sfx, a.sf13 = sf13, a.sf2 = sf2, a.ids = ids, a.weights = weights;
   a.c = static_cast<const __nv_bfloat16*>(c), a.y = static_cast<__nv_bfloat16*>(y);
   a.hs = static_cast<uint32_t*>(scratch), a.h = static_cast<uint8_t*>(scratch) + scale_words * 4;
+  a.parts = reinterpret_cast<float*>(a.h + h_bytes), a.arrivals = ws.counters();
   a.status = ctx.status, a.timeout_ns = dg::pipeline_wait_timeout_ns(), a.fault = dg::debug_fault_mode();
   a.T = T, a.k = topk, a.E = E, a.H = H, a.I = I;
   return run_layer<kFp4>(a, w13, w2, ctx, stream);

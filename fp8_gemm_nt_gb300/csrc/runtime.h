@@ -30,8 +30,9 @@ dg_status record_cuda_error(cudaError_t e);
 // failure.
 bool weight_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool e2m1);
 
-// `bytes` of the stream's workspace, past the stream-K arrival counters at its start (which stay
-// zero). Held until the object goes out of scope, which has to be after the launches that use it.
+// `bytes` of the stream's workspace, past the arrival counters at its start (kArrivalCounters of them, zero
+// between launches: a kernel that counts in them leaves them so). Held until the object goes out of scope, which has to be after the launches that use it.
+constexpr int kArrivalCounters = 4096;
 class StreamWorkspace {
  public:
   StreamWorkspace() = default;
@@ -39,9 +40,11 @@ class StreamWorkspace {
   StreamWorkspace(const StreamWorkspace&) = delete;
   StreamWorkspace& operator=(const StreamWorkspace&) = delete;
   dg_status acquire(cudaStream_t stream, size_t bytes, void** out);
+  int* counters() const { return counters_; }
 
  private:
   void* lease_ = nullptr;
+  int* counters_ = nullptr;
 };
 
 // Launches `kernel` on `stream`, in clusters of `cluster` blocks, as a programmatic dependent of the stream's
