@@ -226,16 +226,19 @@ struct Run {
   bool done;               // the pipeline's last run of the piece
 };
 
-// The stages of all pieces, dealt out to `pipes` pipelines in runs of equal length (to one).
+// The stages of all pieces, dealt out to `pipes` pipelines in runs of equal length (to one). At most 2^24 stages.
 struct Deal {
-  long long stages;
-  int pipes;
-  __device__ __forceinline__ Deal(long long stages_, int most) : stages(stages_) {
-    const long long wanted = (stages + kMinShare - 1) / kMinShare;
-    pipes = static_cast<int>(wanted < most ? (wanted > 0 ? wanted : 1) : most);
+  int pipes, share, longer;        // `longer` pipelines have `share` + 1 stages, the others `share`
+  __device__ __forceinline__ Deal(int stages, int most) {
+    pipes = max(1, min(most, (stages + kMinShare - 1) / kMinShare));
+    share = stages / pipes;
+    longer = stages - share * pipes;
   }
-  __device__ __forceinline__ long long begin(int p) const { return p < pipes ? p * stages / pipes : stages; }
-  __device__ __forceinline__ int owner(long long stage) const { return static_cast<int>(((stage + 1) * pipes - 1) / stages); }
+  __device__ __forceinline__ int begin(int p) const { return min(p, pipes) * share + min(p, longer); }
+  __device__ __forceinline__ int owner(int stage) const {
+    const int before = longer * (share + 1);
+    return stage < before ? stage / (share + 1) : longer + (stage - before) / share;
+  }
 };
 
 // A pipeline's runs in order. First kernel: the pieces are units (job, 64 columns of h), each 64 gate rows and
@@ -245,7 +248,7 @@ template <bool kDown>
 struct Walk {
   const MoeArgs& a;
   const Routing& r;
-  long long at, end;
+  int at, end;
   int groups, per;         // K groups, and stages of a piece
   __device__ __forceinline__ Walk(const MoeArgs& args, const Routing& routing, const Deal& deal, int pipe) : a(args), r(routing) {
     groups = (kDown ? a.I : a.H) / 128;
@@ -255,7 +258,7 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(Run& s) {
     if (at >= end) return false;
-    const int piece = static_cast<int>(at / per), in = static_cast<int>(at - static_cast<long long>(piece) * per);
+    const int piece = at / per, in = at - piece * per;
     if (kDown) {
       s.job = in / groups;
       s.piece = piece;
@@ -267,9 +270,9 @@ struct Walk {
       s.piece = piece - s.job * blocks;
       s.begin = in;
     }
-    s.end = static_cast<int>(min(static_cast<long long>(groups), s.begin + end - at));
+    s.end = min(groups, s.begin + end - at);
     at += s.end - s.begin;
-    s.done = at >= end || at % per == 0;
+    s.done = at >= end || in + s.end - s.begin == per;
     s.expert = r.job_expert[s.job];
     s.slot = r.job_slot[s.job];
     s.count = r.job_count[s.job];
@@ -288,53 +291,35 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(d)));
 }
 
-// The end of a unit of the first kernel, by warps 4 to 7: rows 0 to 63 of the sums (two warps) are the gate's,
-// rows 64 to 127 the up's of the same columns of h. Writes h's three terms and its scale for the job's tokens.
-__device__ __forceinline__ void store_inner(const MoeArgs& a, const Routing& r, const Run& run, float* exchange, const uint32_t (&v)[kCols], int half, int quad, int lane) {
-  float* const up = exchange;                       // [64][17]
-  float* const top = exchange + 64 * 17;            // [2][kCols]
-  const int row = (quad & 1) * 32 + lane;
-  if (quad >= 2) {
+// 64 columns of h of a slot, by a warp, two columns a lane: their three terms and their scale, from the sums of
+// the gate's rows and of the up's.
+__device__ __forceinline__ void store_inner(const MoeArgs& a, float coef, int slot, int block, float2 gate, float2 up, int lane) {
+  float h[2] = {coef * (gate.x / (1.0f + expf(-gate.x)) * up.x), coef * (gate.y / (1.0f + expf(-gate.y)) * up.y)};
+  float top = 0;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) up[row * 17 + c] = __uint_as_float(v[c]);
+  for (int i = 0; i < 2; ++i) {
+    const float m = fabsf(h[i]);
+    top = m < INFINITY ? fmaxf(top, m) : top;
   }
-  named_barrier(1 + 2 * half, 128);
-  if (quad < 2) {
-    float h[kCols];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      h[c] = 0;
-      if (c >= run.count) continue;
-      const float gate = __uint_as_float(v[c]);
-      h[c] = r.coef[run.slot + c] * (gate / (1.0f + expf(-gate)) * up[row * 17 + c]);
-      float m = fabsf(h[c]);
-      m = m < INFINITY ? m : 0.0f;
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  // the third term's scale is 2^-8 of the first's: its code stays at least 1
+  const int e = max(dg::ue8m0_for_amax(top), 9);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-      if (lane == 0) top[quad * kCols + c] = m;
-    }
-    named_barrier(2 + 2 * half, 64);
-    const int groups4 = (a.I / 128 + 3) / 4 * 4;
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      if (c >= run.count) continue;
-      // the third term's scale is 2^-8 of the first's: its code stays at least 1
-      const int e = max(dg::ue8m0_for_amax(fmaxf(top[c], top[kCols + c])), 9);
-      const float full = h[c] * dg::ue8m0_inverse(e);
-      uint8_t* to = a.h + static_cast<long long>(run.slot + c) * kTerms * a.I + run.piece * kBlock + row;
-      // an infinity (NaN - infinity) becomes NaN
-      float left = full - full == 0.0f ? full : NAN;
-#pragma unroll
-      for (int j = 0; j < kTerms; ++j) {
-        const uint32_t code = dg::pack_e4m3(left, 0, 0, 0) & 255;
-        to[static_cast<long long>(j) * a.I] = static_cast<uint8_t>(code);
-        left = (left - e4m3_value(code)) * 16.0f;
-      }
-      if (quad == 0 && lane == 0)
-        reinterpret_cast<uint16_t*>(a.hs + static_cast<long long>(run.slot + c) * groups4)[run.piece] = static_cast<uint16_t>(e | e << 8);
-    }
+  for (int i = 0; i < 2; ++i) {
+    const float full = h[i] * dg::ue8m0_inverse(e);
+    h[i] = full - full == 0.0f ? full : NAN;        // an infinity (NaN - infinity) becomes NaN
   }
-  named_barrier(1 + 2 * half, 128);               // before the next unit's exchange
+  uint8_t* to = a.h + static_cast<long long>(slot) * kTerms * a.I + block * kBlock + 2 * lane;
+#pragma unroll
+  for (int j = 0; j < kTerms; ++j) {
+    const uint32_t code = dg::pack_e4m3(h[0], h[1], 0, 0);
+    *reinterpret_cast<uint16_t*>(to + static_cast<long long>(j) * a.I) = static_cast<uint16_t>(code);
+    h[0] = (h[0] - e4m3_value(code & 255)) * 16.0f;
+    h[1] = (h[1] - e4m3_value(code >> 8 & 255)) * 16.0f;
+  }
+  const int words = (a.I / 128 + 3) / 4 * 4;
+  if (lane == 0) reinterpret_cast<uint16_t*>(a.hs + static_cast<long long>(slot) * words)[block] = static_cast<uint16_t>(e | e << 8);
 }
 
 template <bool kFp4, bool kDown>
@@ -372,13 +357,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   }
   // (The first kernel let the second start only after its own wait: ids and weights are there, h is not yet.)
   build_routing<kCols, kThreads>(a, s.r, *reinterpret_cast<RoutingScratch*>(base), !kDown && blockIdx.x == 0);
-  // the halves' rings, then for each half: the first kernel's token scales [KP, T] and its exchange of sums (64
-  // rows and their maxima); the second's output [T][128]
+  // the halves' rings, then for each half: the first kernel's sums [kCols][128] and token scales [KP, T]; the
+  // second's output [T][128]
   uint8_t* const ring = base + half * a.stages * a.stage_bytes;
   uint8_t* const rest = base + 2 * a.stages * a.stage_bytes + half * a.rest_bytes;
-  uint32_t* const sfx = reinterpret_cast<uint32_t*>(rest);
+  float* const exchange = reinterpret_cast<float*>(rest);
+  uint32_t* const sfx = reinterpret_cast<uint32_t*>(rest + kCols * 128 * 4);
   const int kp = (a.H / 128 + 3) / 4;
-  float* const exchange = reinterpret_cast<float*>(rest + (kDown ? 0 : kp * a.T * 4));
   float* const out = reinterpret_cast<float*>(rest);
   if (kDown) {
     for (int i = threadIdx.x % kHalf; i < a.T * 128; i += kHalf) out[i] = 0;
@@ -394,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const int groups = (kDown ? a.I : a.H) / 128;
   const uint32_t tmem = s.tmem + half * kTmemCols;
   const int me = 2 * blockIdx.x + half;
-  const long long pieces = kDown ? a.H / 128 : static_cast<long long>(s.r.jobs) * (a.I / kBlock);
-  const Deal deal(pieces * (kDown ? s.r.jobs * groups : groups), 2 * gridDim.x);
+  const int pieces = kDown ? a.H / 128 : s.r.jobs * (a.I / kBlock);
+  const Deal deal(pieces * (kDown ? s.r.jobs * groups : groups), 2 * static_cast<int>(gridDim.x));
   Walk<kDown> walk(a, s.r, deal, me);
   Run run;
   // A wait that runs out is recorded, and every role then leaves its loop (the epilogue runs through it without
@@ -631,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       if (lane == 0) dg::mbar_arrive(&pipe.sum_empty[sum]);
       ++n;
       // a piece that other pipelines have parts of: 1 if this one is the last to bring its own
-      auto last_of = [&](long long piece_begin, int per, int* first, int* last) {
+      auto last_of = [&](int piece_begin, int per, int* first, int* last) {
         *first = deal.owner(piece_begin);
         *last = deal.owner(piece_begin + per - 1);
         __threadfence();
@@ -646,13 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         return s.arrived[half] != 0;
       };
       // where pipeline p put its part of the piece: a piece that it did not begin is its first
-      auto part_of = [&](int p, long long piece_begin, int floats) {
+      auto part_of = [&](int p, int piece_begin, int floats) {
         return a.parts + (2ll * p + (deal.begin(p) > piece_begin ? 0 : 1)) * floats;
       };
       if constexpr (kDown) {
         if (!run.done) continue;
         const int per = s.r.jobs * groups;
-        const long long begin = static_cast<long long>(run.piece) * per;
+        const int begin = run.piece * per;
         const bool whole = deal.begin(me) <= begin && deal.begin(me + 1) >= begin + per;
         int first = me, last = me;
         bool write = true;
@@ -690,35 +675,43 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 #pragma unroll 4
         for (int t = 0; t < a.T; ++t) out[t * 128 + row] = 0;
       } else {
-        if (run.end - run.begin < groups) {
-          const long long begin = static_cast<long long>(run.unit) * groups;
-          float4* mine = reinterpret_cast<float4*>(part_of(me, begin, 128 * kCols)) + row * (kCols / 4);
+        // sums as [token][row]; rows 0 to 63 are the gate's, 64 to 127 the up's of the same columns of h. The loop
+        // over the tokens is a loop in the code too: it runs once or twice per launch, and unrolled over 16 tokens
+        // its instructions took 15 us to arrive from memory
+        const bool whole = run.end - run.begin == groups;
+        const int begin = run.unit * groups;
+        float* mine = whole ? exchange : part_of(me, begin, 128 * kCols);
 #pragma unroll
-          for (int i = 0; i < kCols / 4; ++i)
-            if (4 * i < run.count) mine[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
-          int first, last;
-          if (!last_of(begin, groups, &first, &last)) continue;
-          float total[kCols];
+        for (int i = 0; i < kCols; ++i)
+          if (i < run.count) mine[i * 128 + row] = __uint_as_float(v[i]);
+        int first = me, last = me;
+        if (whole) named_barrier(1 + 2 * half, 128);
+        else if (!last_of(begin, groups, &first, &last)) continue;
+#pragma unroll 1
+        for (int i = quad; i < run.count; i += 4) {
+          float2 gate = make_float2(0, 0), up = make_float2(0, 0);
+          if (whole) {
+            gate = *reinterpret_cast<const float2*>(exchange + i * 128 + 2 * lane);
+            up = *reinterpret_cast<const float2*>(exchange + i * 128 + 64 + 2 * lane);
+          } else {
+#pragma unroll 1
+            for (int p = first; p <= last; p += 4) {
+              float2 part[4][2];
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) total[i] = 0;
-          for (int p = first; p <= last; p += 3) {
-            float4 f[3][kCols / 4];
+              for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 3; ++j)
+                for (int n = 0; n < 2; ++n)
+                  part[j][n] = p + j <= last ? __ldcg(reinterpret_cast<const float2*>(part_of(p + j, begin, 128 * kCols) + i * 128 + n * 64) + lane) : make_float2(0, 0);
 #pragma unroll
-              for (int i = 0; i < kCols / 4; ++i)
-                f[j][i] = p + j <= last && 4 * i < run.count ? __ldcg(reinterpret_cast<const float4*>(part_of(p + j, begin, 128 * kCols)) + row * (kCols / 4) + i)
-                                                             : make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-#pragma unroll
-              for (int i = 0; i < kCols / 4; ++i)
-                total[4 * i] += f[j][i].x, total[4 * i + 1] += f[j][i].y, total[4 * i + 2] += f[j][i].z, total[4 * i + 3] += f[j][i].w;
+              for (int j = 0; j < 4; ++j) {
+                gate.x += part[j][0].x, gate.y += part[j][0].y;
+                up.x += part[j][1].x, up.y += part[j][1].y;
+              }
+            }
           }
-#pragma unroll
-          for (int i = 0; i < kCols; ++i) v[i] = __float_as_uint(total[i]);
+          store_inner(a, s.r.coef[run.slot + i], run.slot + i, run.piece, gate, up, lane);
         }
-        store_inner(a, s.r, run, exchange, v, half, quad, lane);
+        if (whole) named_barrier(1 + 2 * half, 128);
       }
     }
     if (kDown && s.r.jobs == 0) {
@@ -766,7 +759,7 @@ dg_status run_layer(MoeArgs a, const void* w13, const void* w2, const LaunchCont
   auto grid = [&](long long stages) { return static_cast<unsigned>(std::max(1ll, std::min<long long>(ctx.sms, (stages + 2 * kMinShare - 1) / (2 * kMinShare)))); };
   const int up_groups = a.H / 128, down_groups = a.I / 128;
   MoeArgs up = a, down = a;
-  const size_t up_smem = ring(up, cols, (up_groups + 3) / 4 * a.T * 4 + (64 * 17 + 2 * kCols) * 4);
+  const size_t up_smem = ring(up, cols, (up_groups + 3) / 4 * a.T * 4 + kCols * 128 * 4);
   if (dg_status s = dg::launch(moe_kernel<kFp4, false>, grid(static_cast<long long>(jobs) * (a.I / kBlock) * up_groups), kThreads, up_smem, stream, ctx.pdl,
                                up_map, up); s != DG_OK) return s;
   const size_t down_smem = ring(down, kTerms * cols, a.T * 128 * 4);
