@@ -106,7 +106,7 @@ struct RoutingScratch {
 };
 
 // Builds the routing of the block from the ids, in the order of experts and tokens: the same in
-// every block of both kernels. `kCols`: columns of a job.
+// every block of both kernels. `kCols`: columns of a job. Ends without a barrier.
 template <int kCols, int kThreads>
 __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& s, bool report) {
   constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
@@ -176,7 +176,6 @@ __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, Rout
       r.coef[slot] = w;
     }
   }
-  __syncthreads();
 }
 
 // -------------------------------------------------------------------------------------------
@@ -194,6 +193,10 @@ __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t b
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dg::smem_addr(to)),
                "l"(from), "r"(bytes), "r"(dg::smem_addr(bar))
                : "memory");
+}
+// Asynchronous copy of one word.
+__device__ __forceinline__ void cp_async_4(const void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dg::smem_addr(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ void named_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
@@ -280,6 +283,11 @@ struct Walk {
     s.row1 = kDown ? s.row0 + 64 : s.row0 + a.I;
     return true;
   }
+  // E2M1's scale words [E, groups, N]: those of a K group of the run's expert, to be indexed by row of the matrix
+  __device__ __forceinline__ const int32_t* scale_words(const Run& s, int g) const {
+    const int n = kDown ? a.H : 2 * a.I;
+    return (kDown ? a.sf2 : a.sf13) + (static_cast<long long>(s.expert) * groups + g) * n - static_cast<long long>(s.expert) * n;
+  }
 };
 
 __device__ __forceinline__ void add(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
@@ -355,22 +363,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     dg::grid_dependency_wait();
     dg::grid_launch_dependents();
   }
-  // (The first kernel let the second start only after its own wait: ids and weights are there, h is not yet.)
-  build_routing<kCols, kThreads>(a, s.r, *reinterpret_cast<RoutingScratch*>(base), !kDown && blockIdx.x == 0);
   // the halves' rings, then for each half: the first kernel's sums [kCols][128] and token scales [KP, T]; the
   // second's output [T][128]
   uint8_t* const ring = base + half * a.stages * a.stage_bytes;
   uint8_t* const rest = base + 2 * a.stages * a.stage_bytes + half * a.rest_bytes;
   float* const exchange = reinterpret_cast<float*>(rest);
   uint32_t* const sfx = reinterpret_cast<uint32_t*>(rest + kCols * 128 * 4);
-  const int kp = (a.H / 128 + 3) / 4;
   float* const out = reinterpret_cast<float*>(rest);
   if (kDown) {
     for (int i = threadIdx.x % kHalf; i < a.T * 128; i += kHalf) out[i] = 0;
   } else {
-    const int t4 = (a.T + 3) / 4 * 4;
-    for (int i = threadIdx.x % kHalf; i < kp * a.T; i += kHalf) sfx[i] = dg::ld_cg_s32(a.sfx + i / a.T * t4 + i % a.T);
+    const int t4 = (a.T + 3) / 4 * 4, words = (a.H / 128 + 3) / 4 * a.T;
+    for (int i = threadIdx.x % kHalf; i < words; i += kHalf) cp_async_4(sfx + i, a.sfx + i / a.T * t4 + i % a.T);
+    cp_async_commit();
   }
+  // (The first kernel let the second start only after its own wait: ids and weights are there, h is not yet.)
+  build_routing<kCols, kThreads>(a, s.r, *reinterpret_cast<RoutingScratch*>(base), !kDown && blockIdx.x == 0);
+  if (!kDown) cp_async_wait<0>();
   dg::fence_proxy_async_smem();        // the scratch in the rings was written by threads; copies write there next
   dg::tc_fence_before();
   __syncthreads();
@@ -398,7 +407,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     if (lane == 0 && a.fault == 0) {
       int stage = 0, issued = 0;
       uint32_t phase = 1;
-      const int n4 = kDown ? a.H : 2 * a.I;
       bool ok = true;
       while (ok && walk.next(run)) {
         for (int g = run.begin; g < run.end; ++g) {
@@ -409,11 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           dg::tma_load_2d(to, &map, bar, g * 128, run.row0);
           dg::tma_load_2d(to + kWeights / 2, &map, bar, g * 128, run.row1);
           if (kFp4) {
-            // scale words [E, groups, N]
-            const int32_t* sf = (kDown ? a.sf2 : a.sf13) + (static_cast<long long>(run.expert) * groups + g) * n4 - static_cast<long long>(run.expert) * n4;
+            const int32_t* words = walk.scale_words(run, g);
             uint8_t* scales = to + kWeights + a.token_rows * 128 + kRawA;
-            bulk_load(scales, sf + run.row0, 256, bar);
-            bulk_load(scales + 256, sf + run.row1, 256, bar);
+            bulk_load(scales, words + run.row0, 256, bar);
+            bulk_load(scales + 256, words + run.row1, 256, bar);
           }
           ++issued;
           if (++stage == a.stages) stage = 0, phase ^= 1;
@@ -759,11 +766,12 @@ dg_status run_layer(MoeArgs a, const void* w13, const void* w2, const LaunchCont
   auto grid = [&](long long stages) { return static_cast<unsigned>(std::max(1ll, std::min<long long>(ctx.sms, (stages + 2 * kMinShare - 1) / (2 * kMinShare)))); };
   const int up_groups = a.H / 128, down_groups = a.I / 128;
   MoeArgs up = a, down = a;
+  const unsigned up_blocks = grid(static_cast<long long>(jobs) * (a.I / kBlock) * up_groups);
+  const unsigned down_blocks = grid(static_cast<long long>(a.H / 128) * jobs * down_groups);
   const size_t up_smem = ring(up, cols, (up_groups + 3) / 4 * a.T * 4 + kCols * 128 * 4);
-  if (dg_status s = dg::launch(moe_kernel<kFp4, false>, grid(static_cast<long long>(jobs) * (a.I / kBlock) * up_groups), kThreads, up_smem, stream, ctx.pdl,
-                               up_map, up); s != DG_OK) return s;
+  if (dg_status s = dg::launch(moe_kernel<kFp4, false>, up_blocks, kThreads, up_smem, stream, ctx.pdl, up_map, up); s != DG_OK) return s;
   const size_t down_smem = ring(down, kTerms * cols, a.T * 128 * 4);
-  return dg::launch(moe_kernel<kFp4, true>, grid(static_cast<long long>(a.H / 128) * jobs * down_groups), kThreads, down_smem, stream, ctx.pdl, down_map, down);
+  return dg::launch(moe_kernel<kFp4, true>, down_blocks, kThreads, down_smem, stream, ctx.pdl, down_map, down);
 }
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
