@@ -53,7 +53,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxH = 16384;
 constexpr int kMaxSlots = kMaxTokens * kMaxTopk;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kCols = 16;               // tokens of a job
+constexpr int kCols = 16;               // tokens of a job of the first kernel
 constexpr int kTerms = 3;               // E4M3 terms of a value of h
 constexpr int kBlock = 64;              // columns of h of a unit of the first kernel, which share a scale
 constexpr int kHalf = 256;              // threads of a pipeline
@@ -72,14 +72,15 @@ struct MoeArgs {
   const __nv_bfloat16* c;  // [T, H] or null
   __nv_bfloat16* y;        // [T, H]
   uint8_t* h;              // [slots, kTerms, I] E4M3
-  uint32_t* hs;            // [slots, I / 128 up to a multiple of 4]: codes of a slot's four 32-column blocks of 128
+  uint32_t* hs;            // [I / 128, slots, kTerms]: the codes of a term's four 32-column blocks of 128
   uint32_t* status;
   unsigned long long timeout_ns;   // of a wait
   int fault;                       // failure injection: no copies of weights
   int T, k, E, H, I;
-  int stages, stage_bytes, token_rows;   // of a pipeline's ring; rows of a stage's tokens
+  int cols;                              // tokens of a job, at most
+  int stages, stage_bytes, scale_bytes;  // of a pipeline's ring
   int rest_bytes;                        // of a pipeline's shared memory beside the rings
-  float* parts;                          // [pipelines][2] parts of cut pieces: [128][16], [T][128]
+  float* parts;                          // [pipelines][2] parts of cut pieces: [kCols][128], [T][128]
   int* arrivals;                         // per first pipeline of a cut piece; zero between launches
 };
 
@@ -106,8 +107,8 @@ struct RoutingScratch {
 };
 
 // Builds the routing of the block from the ids, in the order of experts and tokens: the same in
-// every block of both kernels. `kCols`: columns of a job. Ends without a barrier.
-template <int kCols, int kThreads>
+// every block of both kernels. Ends without a barrier.
+template <int kThreads>
 __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& s, bool report) {
   constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, slots = a.T * a.k;
@@ -129,7 +130,7 @@ __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, Rout
   for (int i = 0; i < kPer; ++i) {
     const int e = kPer * tid + i;
     const int tokens = e < a.E ? __popc(s.mask[e]) : 0;
-    n[i] = ((tokens + kCols - 1) / kCols) << 16 | tokens;
+    n[i] = ((tokens + a.cols - 1) / a.cols) << 16 | tokens;
     sum += n[i];
   }
   int before = sum;
@@ -149,10 +150,10 @@ __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, Rout
       const int slot = before & 0xFFFF, tokens = n[i] & 0xFFFF;
       s.first_slot[e] = static_cast<uint16_t>(slot);
       int job = before >> 16;
-      for (int c = 0; c < tokens; c += kCols, ++job) {
+      for (int c = 0; c < tokens; c += a.cols, ++job) {
         r.job_expert[job] = static_cast<uint16_t>(e);
         r.job_slot[job] = static_cast<uint16_t>(slot + c);
-        r.job_count[job] = static_cast<uint8_t>(min(kCols, tokens - c));
+        r.job_count[job] = static_cast<uint8_t>(min(a.cols, tokens - c));
       }
       before += n[i];
     }
@@ -182,31 +183,27 @@ __device__ __forceinline__ void build_routing(const MoeArgs& a, Routing& r, Rout
 // The products of both kernels
 // -------------------------------------------------------------------------------------------
 
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
 // Untiled bulk copy (16-byte aligned addresses and size) that completes on `bar`.
 __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dg::smem_addr(to)),
                "l"(from), "r"(bytes), "r"(dg::smem_addr(bar))
                : "memory");
 }
-// Asynchronous copy of one word.
-__device__ __forceinline__ void cp_async_4(const void* to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dg::smem_addr(to)), "l"(from) : "memory");
+// Asynchronous copy of a word, and the thread's arrival at a barrier when its copies so far are done.
+__device__ __forceinline__ void cp_async_4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(dg::smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void named_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// A stage: 128 weight rows of 128 columns (128-byte rows in the 128-byte swizzle; E2M1 spread to one element a
-// byte by TMA), the tokens' rows in the same form, the weights' scale words as loaded (E2M1: one per row), the
-// tokens' as loaded (second kernel: four words per token), and both as tcgen05.cp takes them (row r of 32 holds
-// the words of rows r, r + 32, ...).
-constexpr int kWeights = 128 * 128;
-constexpr int kRawA = 0, kRawB = 512, kTileA = kRawB + kCols * 16, kTileB = kTileA + 512, kScaleArea = kTileB + 512;
-__host__ __device__ constexpr int stage_bytes(int token_rows) { return (kWeights + token_rows * 128 + kScaleArea + 1023) / 1024 * 1024; }
+// A stage: 128 weight rows of 128 columns (128-byte rows in the 128-byte swizzle; E2M1 spread by TMA, 16 elements to 8 bytes
+// and 8 of padding), the tokens' rows in the same form, and scale words as tcgen05.cp takes them, 32 rows of 16 bytes (row
+// r: the words of rows r, r + 32, ...): the weights', the tokens', and for E2M1 the weights' as loaded, one per row.
+constexpr int kWeights = 128 * 128, kTile = 512;
+constexpr int kTileA = 0, kTileB = kTile, kRaw = 2 * kTile;
 
 struct Pipe {
   uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], sum_full[2], sum_empty[2], drain;
@@ -283,11 +280,6 @@ struct Walk {
     s.row1 = kDown ? s.row0 + 64 : s.row0 + a.I;
     return true;
   }
-  // E2M1's scale words [E, groups, N]: those of a K group of the run's expert, to be indexed by row of the matrix
-  __device__ __forceinline__ const int32_t* scale_words(const Run& s, int g) const {
-    const int n = kDown ? a.H : 2 * a.I;
-    return (kDown ? a.sf2 : a.sf13) + (static_cast<long long>(s.expert) * groups + g) * n - static_cast<long long>(s.expert) * n;
-  }
 };
 
 __device__ __forceinline__ void add(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
@@ -319,15 +311,15 @@ __device__ __forceinline__ void store_inner(const MoeArgs& a, float coef, int sl
     h[i] = full - full == 0.0f ? full : NAN;        // an infinity (NaN - infinity) becomes NaN
   }
   uint8_t* to = a.h + static_cast<long long>(slot) * kTerms * a.I + block * kBlock + 2 * lane;
+  uint16_t* code_to = reinterpret_cast<uint16_t*>(a.hs + (static_cast<long long>(block / 2) * a.T * a.k + slot) * kTerms) + block % 2;
 #pragma unroll
   for (int j = 0; j < kTerms; ++j) {
     const uint32_t code = dg::pack_e4m3(h[0], h[1], 0, 0);
     *reinterpret_cast<uint16_t*>(to + static_cast<long long>(j) * a.I) = static_cast<uint16_t>(code);
     h[0] = (h[0] - e4m3_value(code & 255)) * 16.0f;
     h[1] = (h[1] - e4m3_value(code >> 8 & 255)) * 16.0f;
+    if (lane == 0) code_to[2 * j] = static_cast<uint16_t>((e - 4 * j) * 0x0101);
   }
-  const int words = (a.I / 128 + 3) / 4 * 4;
-  if (lane == 0) reinterpret_cast<uint16_t*>(a.hs + static_cast<long long>(slot) * words)[block] = static_cast<uint16_t>(e | e << 8);
 }
 
 template <bool kFp4, bool kDown>
@@ -337,11 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   uint8_t* const base = raw + ((1024u - (dg::smem_addr(raw) & 1023u)) & 1023u);
   const int lane = threadIdx.x & 31, half = threadIdx.x / kHalf, warp = threadIdx.x % kHalf / 32;
   Pipe& pipe = s.pipe[half];
-  constexpr int kSumCols = kDown ? 48 : 16, kTmemCols = kDown ? 128 : 64;     // two sums, then two buffers of each side's scales
+  constexpr int kSumCols = kDown ? 32 : 16, kTmemCols = kDown ? 128 : 64;     // two sums, then two buffers of each side's scales
   if (threadIdx.x % kHalf == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       dg::mbar_init(&pipe.full[i], 1);
-      dg::mbar_init(&pipe.ready[i], 2);
+      dg::mbar_init(&pipe.ready[i], 33);
       dg::mbar_init(&pipe.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -363,24 +355,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     dg::grid_dependency_wait();
     dg::grid_launch_dependents();
   }
-  // the halves' rings, then for each half: the first kernel's sums [kCols][128] and token scales [KP, T]; the
-  // second's output [T][128]
+  // the halves' rings and their scales, then for each half the first kernel's sums of a unit, the second's output
+  // [T][128]
   uint8_t* const ring = base + half * a.stages * a.stage_bytes;
-  uint8_t* const rest = base + 2 * a.stages * a.stage_bytes + half * a.rest_bytes;
-  float* const exchange = reinterpret_cast<float*>(rest);
-  uint32_t* const sfx = reinterpret_cast<uint32_t*>(rest + kCols * 128 * 4);
-  float* const out = reinterpret_cast<float*>(rest);
-  if (kDown) {
-    for (int i = threadIdx.x % kHalf; i < a.T * 128; i += kHalf) out[i] = 0;
-  } else {
-    const int t4 = (a.T + 3) / 4 * 4, words = (a.H / 128 + 3) / 4 * a.T;
-    for (int i = threadIdx.x % kHalf; i < words; i += kHalf) cp_async_4(sfx + i, a.sfx + i / a.T * t4 + i % a.T);
-    cp_async_commit();
-  }
+  uint8_t* const scales = base + 2 * a.stages * a.stage_bytes + half * a.stages * a.scale_bytes;
+  float* const rest = reinterpret_cast<float*>(base + 2 * a.stages * (a.stage_bytes + a.scale_bytes) + half * a.rest_bytes);
+  if (kDown)
+    for (int i = threadIdx.x % kHalf; i < a.T * 128; i += kHalf) rest[i] = 0;
   // (The first kernel let the second start only after its own wait: ids and weights are there, h is not yet.)
-  build_routing<kCols, kThreads>(a, s.r, *reinterpret_cast<RoutingScratch*>(base), !kDown && blockIdx.x == 0);
-  if (!kDown) cp_async_wait<0>();
-  dg::fence_proxy_async_smem();        // the scratch in the rings was written by threads; copies write there next
+  build_routing<kThreads>(a, s.r, *reinterpret_cast<RoutingScratch*>(base), !kDown && blockIdx.x == 0);
+  dg::fence_proxy_async_smem();        // written by threads, read and overwritten by copies and MMAs
   dg::tc_fence_before();
   __syncthreads();
   dg::tc_fence_after();
@@ -413,21 +397,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           if (!(ok = wait(&pipe.empty[stage], phase))) break;
           uint8_t* to = ring + stage * a.stage_bytes;
           uint64_t* bar = &pipe.full[stage];
-          dg::mbar_arrive_expect_tx(bar, kFp4 ? kWeights / 2 + 512 : kWeights);
+          dg::mbar_arrive_expect_tx(bar, kFp4 ? kWeights / 2 + kTile : kWeights);
           dg::tma_load_2d(to, &map, bar, g * 128, run.row0);
           dg::tma_load_2d(to + kWeights / 2, &map, bar, g * 128, run.row1);
           if (kFp4) {
-            const int32_t* words = walk.scale_words(run, g);
-            uint8_t* scales = to + kWeights + a.token_rows * 128 + kRawA;
-            bulk_load(scales, words + run.row0, 256, bar);
-            bulk_load(scales + 256, words + run.row1, 256, bar);
+            // scale words [E, groups, N]
+            const int n = kDown ? a.H : 2 * a.I;
+            const int32_t* words = (kDown ? a.sf2 : a.sf13) + (static_cast<long long>(run.expert) * groups + g) * n - static_cast<long long>(run.expert) * n;
+            uint8_t* raw_words = scales + stage * a.scale_bytes + kRaw;
+            bulk_load(raw_words, words + run.row0, kTile / 2, bar);
+            bulk_load(raw_words + kTile / 2, words + run.row1, kTile / 2, bar);
           }
           ++issued;
           if (++stage == a.stages) stage = 0, phase ^= 1;
         }
       }
       // no copy may be under way when the block ends
-      for (int i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i)
+      for (int i = max(issued - a.stages, 0); i < issued; ++i)
         if (!dg::mbar_wait(&pipe.full[i % a.stages], i / a.stages & 1, a.timeout_ns)) break;
     }
   } else if (warp == 1) {
@@ -435,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     if (lane == 0) {
       const uint64_t a_desc = dg::make_smem_desc(dg::smem_addr(ring), 16, 1024, dg::kLayoutSwizzle128B);
       const uint64_t b_desc = a_desc + (kWeights >> 4);
-      const uint64_t sf_desc = dg::make_smem_desc(dg::smem_addr(ring) + kWeights + a.token_rows * 128, 0, 128, dg::kLayoutNone);
+      const uint64_t sf_desc = dg::make_smem_desc(dg::smem_addr(scales), 0, 128, dg::kLayoutNone);
       int stage = 0;
       uint32_t phase = 0, n = 0, buffer = 0;
       bool ok = true;
@@ -443,16 +429,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         const uint32_t sum = n & 1, d = tmem + sum * kSumCols;
         if (!(ok = wait(&pipe.sum_empty[sum], (n >> 1 & 1) ^ 1))) break;
         dg::tc_fence_after();
-        const uint32_t cols = kDown ? (kTerms * run.count + 15) / 16 * 16 : 16;
+        // rows past the last of the tokens' hold anything: they are columns of the sums that nobody reads
+        const uint32_t cols = kDown && kTerms * run.count > 16 ? 32 : 16;
         const uint32_t idesc = dg::make_idesc_mxf8_e4m3(128, 0) | (cols >> 3) << 17 | (kFp4 ? 5u << 7 : 0u);
         for (int g = run.begin; g < run.end; ++g) {
           if (!(ok = wait(&pipe.full[stage], phase) && wait(&pipe.ready[stage], phase))) break;
+          dg::fence_proxy_async_smem();       // of what the barriers say has arrived by cp.async
           dg::tc_fence_after();
-          const uint64_t off = static_cast<uint64_t>(stage * a.stage_bytes) >> 4;
+          const uint64_t off = static_cast<uint64_t>(stage * a.stage_bytes) >> 4, sf_off = static_cast<uint64_t>(stage * a.scale_bytes) >> 4;
           const uint32_t sfa = tmem + 2 * kSumCols + 4 * buffer, sfb = sfa + 8;
           buffer ^= 1;
-          dg::tmem_copy_32x128b_warpx4(sfa, sf_desc + off + (kTileA >> 4));
-          dg::tmem_copy_32x128b_warpx4(sfb, sf_desc + off + (kTileB >> 4));
+          dg::tmem_copy_32x128b_warpx4(sfa, sf_desc + sf_off + (kTileA >> 4));
+          dg::tmem_copy_32x128b_warpx4(sfb, sf_desc + sf_off + (kTileB >> 4));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             // bytes of the scale words: the four 32-column blocks of E2M1 rows and of h, or the K group of four
@@ -471,86 +459,35 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ---------------------------------------------- the tokens' side: copied up to `stages` - 2 stages ahead
-    // (one further, and each stage's MMAs would have to end before the next one's tokens are handed over)
-    const int most_ahead = max(1, a.stages - 2);
+    // ---------------------------------------------- the tokens' side: rows and scale words
     if (kDown) {
       dg::grid_dependency_wait();
       dg::grid_launch_dependents();
     }
-    const int hs_row = (groups + 3) / 4 * 4;
-    Walk<kDown> done_walk = walk;
-    Run done;
-    int done_g = 0, copied = 0, finished = 0, stage = 0, done_stage = 0;
+    int stage = 0;
     uint32_t phase = 1;
-    bool ok = true, have_done = false;
-    auto finish = [&] {
-      // the oldest stage's rows have arrived: its scales to the form of tcgen05.cp, and over to the MMAs
-      if (!have_done || ++done_g == done.end) {
-        done_walk.next(done);
-        done_g = done.begin;
-        have_done = true;
-      }
-      uint8_t* area = ring + done_stage * a.stage_bytes + kWeights + a.token_rows * 128;
-      uint32_t w[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = lane + 32 * j;
-        w[j] = 0;
-        if (kDown) {
-          if (row < kTerms * done.count) w[j] = *reinterpret_cast<uint32_t*>(area + kRawB + row / kTerms * 16 + (done_g & 3) * 4) - row % kTerms * 0x04040404u;
-        } else if (row < done.count) {
-          w[j] = sfx[done_g / 4 * a.T + s.r.token[done.slot + row]];
-        }
-      }
-      dg::st_shared_v4(dg::smem_addr(area) + kTileB + 16 * lane, w[0], w[1], 0, 0);
-      dg::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) dg::mbar_arrive(&pipe.ready[done_stage]);
-      if (++done_stage == a.stages) done_stage = 0;
-      ++finished;
-    };
-    auto settle = [&](int left) {
-      // copies of all but the last `left` stages have arrived
-      switch (left) {
-        case 0: cp_async_wait<0>(); break;
-        case 1: cp_async_wait<1>(); break;
-        case 2: cp_async_wait<2>(); break;
-        case 3: cp_async_wait<3>(); break;
-        case 4: cp_async_wait<4>(); break;
-        case 5: cp_async_wait<5>(); break;
-        case 6: cp_async_wait<6>(); break;
-        default: cp_async_wait<7>(); break;
-      }
-      __syncwarp();
-    };
+    bool ok = true;
+    const int t4 = (a.T + 3) / 4 * 4;
     while (ok && walk.next(run)) {
       const int rows = kDown ? kTerms * run.count : run.count;
       for (int g = run.begin; g < run.end; ++g) {
         ok = __all_sync(kAll, wait(&pipe.empty[stage], phase));
         if (!ok) break;
-        uint8_t* to = ring + stage * a.stage_bytes + kWeights;
+        const uint32_t to = dg::smem_addr(ring) + stage * a.stage_bytes + kWeights;
         for (int i = lane; i < rows * 8; i += 32) {
           const int row = i / 8, c = i & 7;
           const uint8_t* from = kDown ? a.h + static_cast<long long>(run.slot * kTerms + row) * a.I : a.x + static_cast<long long>(s.r.token[run.slot + row]) * a.H;
-          dg::cp_async_16(dg::smem_addr(to) + row * 128 + ((c ^ (row & 7)) << 4), from + g * 128 + c * 16);
+          dg::cp_async_16(to + row * 128 + ((c ^ (row & 7)) << 4), from + g * 128 + c * 16);
         }
-        if (kDown && lane < run.count)
-          dg::cp_async_16(dg::smem_addr(to) + a.token_rows * 128 + kRawB + lane * 16, a.hs + static_cast<long long>(run.slot + lane) * hs_row + (g & ~3));
-        cp_async_commit();
-        ++copied;
+        if (lane < rows)
+          cp_async_4(dg::smem_addr(scales) + stage * a.scale_bytes + kTileB + lane * 16,
+                     kDown ? reinterpret_cast<const int32_t*>(a.hs) + (static_cast<long long>(g) * a.T * a.k + run.slot) * kTerms + lane
+                           : a.sfx + g / 4 * t4 + s.r.token[run.slot + lane]);
+        cp_async_arrive(&pipe.ready[stage]);
         if (++stage == a.stages) stage = 0, phase ^= 1;
-        if (copied - finished > most_ahead) {
-          settle(most_ahead);
-          finish();
-        }
       }
     }
-    while (ok && finished < copied) {
-      settle(copied - finished - 1);
-      finish();
-    }
-    cp_async_wait<0>();
+    cp_async_wait_all();
   } else if (warp == 3) {
     // ---------------------------------------------- the weights' scales to the form of tcgen05.cp
     int stage = 0;
@@ -577,11 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         // E2M1's words come with the weights; E4M3's are here, and wait only for the stage to be free
         ok = __all_sync(kAll, kFp4 ? wait(&pipe.full[stage], phase) : wait(&pipe.empty[stage], phase ^ 1));
         if (!ok) break;
-        const uint32_t area = dg::smem_addr(ring) + stage * a.stage_bytes + kWeights + a.token_rows * 128;
+        const uint32_t area = dg::smem_addr(scales) + stage * a.scale_bytes;
         uint32_t w[4];
         if (kFp4) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = dg::ld_shared_u32(area + kRawA + 4 * (lane + 32 * j));
+          for (int j = 0; j < 4; ++j) w[j] = dg::ld_shared_u32(area + kRaw + 4 * (lane + 32 * j));
         } else {
           w[0] = w[1] = __shfl_sync(kAll, word0, g / 4);
           w[2] = w[3] = __shfl_sync(kAll, word1, g / 4);
@@ -599,29 +536,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t n = 0;
     while (walk.next(run)) {
-      const uint32_t sum = n & 1;
+      const uint32_t sum = n & 1, from = tmem + lanes + sum * kSumCols;
       wait(&pipe.sum_full[sum], n >> 1 & 1);
       __syncwarp();
       dg::tc_fence_after();
-      uint32_t v[kCols];
-      if constexpr (kDown) {
-        // this row of the job's tokens, the sum of three terms each: no other thread has it
-#pragma unroll 1
-        for (int i = 0; i < kTerms * run.count; i += 16) {
-          dg::tmem_load_32x32b_x16(tmem + lanes + sum * kSumCols + i, v);
-          dg::tmem_load_wait();
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (i + j < kTerms * run.count) out[s.r.token[run.slot + (i + j) / kTerms] * 128 + row] += __uint_as_float(v[j]);
-        }
-      } else {
-        dg::tmem_load_32x32b_x16(tmem + lanes + sum * kSumCols, v);
-        dg::tmem_load_wait();
-      }
-      dg::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) dg::mbar_arrive(&pipe.sum_empty[sum]);
-      ++n;
+      auto release = [&] {
+        dg::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dg::mbar_arrive(&pipe.sum_empty[sum]);
+        ++n;
+      };
       // a piece that other pipelines have parts of: 1 if this one is the last to bring its own
       auto last_of = [&](int piece_begin, int per, int* first, int* last) {
         *first = deal.owner(piece_begin);
@@ -638,10 +562,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         return s.arrived[half] != 0;
       };
       // where pipeline p put its part of the piece: a piece that it did not begin is its first
-      auto part_of = [&](int p, int piece_begin, int floats) {
-        return a.parts + (2ll * p + (deal.begin(p) > piece_begin ? 0 : 1)) * floats;
+      auto part_of = [&](int p, int piece_begin) {
+        return a.parts + (2ll * p + (deal.begin(p) > piece_begin ? 0 : 1)) * (128 * (kDown ? a.T : kCols));
       };
       if constexpr (kDown) {
+        // this row of the job's tokens, the sum of three terms each: no other thread has it
+        float* const out = rest;
+#pragma unroll 1
+        for (int i = 0; i < run.count; i += 8) {
+          uint32_t v[kTerms * 8];
+#pragma unroll
+          for (int j = 0; j < kTerms; ++j) dg::tmem_load_32x32b_x8(from + kTerms * i + 8 * j, v + 8 * j);
+          dg::tmem_load_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (i + j < run.count)
+              out[s.r.token[run.slot + i + j] * 128 + row] += __uint_as_float(v[3 * j]) + __uint_as_float(v[3 * j + 1]) + __uint_as_float(v[3 * j + 2]);
+        }
+        release();
         if (!run.done) continue;
         const int per = s.r.jobs * groups;
         const int begin = run.piece * per;
@@ -649,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         int first = me, last = me;
         bool write = true;
         if (!whole) {
-          float* mine = part_of(me, begin, a.T * 128);
+          float* mine = part_of(me, begin);
 #pragma unroll 1
           for (int t = 0; t < a.T; ++t) mine[t * 128 + row] = out[t * 128 + row];
           write = last_of(begin, per, &first, &last);
@@ -671,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 float4 part[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  part[i] = p + i <= last ? __ldcg(reinterpret_cast<const float4*>(part_of(p + i, begin, a.T * 128) + t * 128) + lane) : make_float4(0, 0, 0, 0);
+                  part[i] = p + i <= last ? __ldcg(reinterpret_cast<const float4*>(part_of(p + i, begin) + t * 128) + lane) : make_float4(0, 0, 0, 0);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) add(total, part[i]);
               }
@@ -685,9 +623,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         // sums as [token][row]; rows 0 to 63 are the gate's, 64 to 127 the up's of the same columns of h. The loop
         // over the tokens is a loop in the code too: it runs once or twice per launch, and unrolled over 16 tokens
         // its instructions took 15 us to arrive from memory
+        uint32_t v[kCols];
+        dg::tmem_load_32x32b_x16(from, v);
+        dg::tmem_load_wait();
+        release();
         const bool whole = run.end - run.begin == groups;
         const int begin = run.unit * groups;
-        float* mine = whole ? exchange : part_of(me, begin, 128 * kCols);
+        float* mine = whole ? rest : part_of(me, begin);
 #pragma unroll
         for (int i = 0; i < kCols; ++i)
           if (i < run.count) mine[i * 128 + row] = __uint_as_float(v[i]);
@@ -698,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         for (int i = quad; i < run.count; i += 4) {
           float2 gate = make_float2(0, 0), up = make_float2(0, 0);
           if (whole) {
-            gate = *reinterpret_cast<const float2*>(exchange + i * 128 + 2 * lane);
-            up = *reinterpret_cast<const float2*>(exchange + i * 128 + 64 + 2 * lane);
+            gate = *reinterpret_cast<const float2*>(rest + i * 128 + 2 * lane);
+            up = *reinterpret_cast<const float2*>(rest + i * 128 + 64 + 2 * lane);
           } else {
 #pragma unroll 1
             for (int p = first; p <= last; p += 4) {
@@ -708,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
               for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
-                  part[j][n] = p + j <= last ? __ldcg(reinterpret_cast<const float2*>(part_of(p + j, begin, 128 * kCols) + i * 128 + n * 64) + lane) : make_float2(0, 0);
+                  part[j][n] = p + j <= last ? __ldcg(reinterpret_cast<const float2*>(part_of(p + j, begin) + i * 128 + n * 64) + lane) : make_float2(0, 0);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 gate.x += part[j][0].x, gate.y += part[j][0].y;
@@ -747,31 +689,33 @@ dg_status run_layer(MoeArgs a, const void* w13, const void* w2, const LaunchCont
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return dg::record_cuda_error(e);
+  // Tokens of a job: 16 are the least columns of an MMA. In the second product each is three rows, 32 at most:
+  // 8 tokens a job leave room for a fifth stage where T * 128 outputs take no more than 8 KB a half.
+  MoeArgs up = a, down = a;
+  up.cols = kCols;
+  down.cols = a.T <= 16 ? 8 : 10;
   CUtensorMap up_map, down_map;
   if (!dg::weight_rows_map(&up_map, w13, static_cast<uint64_t>(a.E) * 2 * a.I, a.H, 64, kFp4) ||
       !dg::weight_rows_map(&down_map, w2, static_cast<uint64_t>(a.E) * a.H, a.I, 64, kFp4))
     return DG_ERR_CUDA;
-  // jobs, at most: one per slot, and one per expert and for every 16 slots
-  const int jobs = std::min(a.T * a.k, a.E + (a.T * a.k + kCols - 1) / kCols);
-  const int cols = std::min(a.T, kCols);
-  auto ring = [&](MoeArgs& m, int rows, int rest) {
-    m.token_rows = (rows + 15) / 16 * 16;
-    m.stage_bytes = stage_bytes(m.token_rows);
-    m.rest_bytes = (rest + 15) / 16 * 16;
-    m.stages = std::min(kMaxStages, (kMaxSmem - 1024 - 2 * m.rest_bytes) / (2 * m.stage_bytes));
-    return static_cast<size_t>(1024 + 2 * (m.stages * m.stage_bytes + m.rest_bytes));
+  // as many blocks as there are SMs, or shares of stages for two pipelines each of the jobs there are at most
+  auto grid = [&](const MoeArgs& m, long long stages_of_a_job) {
+    const int jobs = std::min(a.T * a.k, a.E + (a.T * a.k + m.cols - 1) / m.cols);
+    return static_cast<unsigned>(std::max(1ll, std::min<long long>(ctx.sms, (jobs * stages_of_a_job + 2 * kMinShare - 1) / (2 * kMinShare))));
   };
-
-  // as many blocks as there are SMs, or shares of stages for two pipelines each
-  auto grid = [&](long long stages) { return static_cast<unsigned>(std::max(1ll, std::min<long long>(ctx.sms, (stages + 2 * kMinShare - 1) / (2 * kMinShare)))); };
-  const int up_groups = a.H / 128, down_groups = a.I / 128;
-  MoeArgs up = a, down = a;
-  const unsigned up_blocks = grid(static_cast<long long>(jobs) * (a.I / kBlock) * up_groups);
-  const unsigned down_blocks = grid(static_cast<long long>(a.H / 128) * jobs * down_groups);
-  const size_t up_smem = ring(up, cols, (up_groups + 3) / 4 * a.T * 4 + kCols * 128 * 4);
-  if (dg_status s = dg::launch(moe_kernel<kFp4, false>, up_blocks, kThreads, up_smem, stream, ctx.pdl, up_map, up); s != DG_OK) return s;
-  const size_t down_smem = ring(down, kTerms * cols, a.T * 128 * 4);
-  return dg::launch(moe_kernel<kFp4, true>, down_blocks, kThreads, down_smem, stream, ctx.pdl, down_map, down);
+  auto shared_bytes = [&](MoeArgs& m, int rows, int rest) {
+    m.stage_bytes = kWeights + (rows + 7) / 8 * 1024;
+    m.scale_bytes = kTile * (kFp4 ? 3 : 2);
+    m.rest_bytes = rest;
+    m.stages = std::min(kMaxStages, (kMaxSmem - 1024 - 2 * rest) / (2 * (m.stage_bytes + m.scale_bytes)));
+    return static_cast<size_t>(1024 + 2 * (m.stages * (m.stage_bytes + m.scale_bytes) + rest));
+  };
+  const int up_rows = std::min(a.T, kCols);
+  const size_t up_smem = shared_bytes(up, up_rows, up_rows * 128 * 4);
+  const size_t down_smem = shared_bytes(down, kTerms * std::min(a.T, down.cols), a.T * 128 * 4);
+  if (dg_status s = dg::launch(moe_kernel<kFp4, false>, grid(up, static_cast<long long>(a.I / kBlock) * (a.H / 128)), kThreads, up_smem, stream, ctx.pdl,
+                               up_map, up); s != DG_OK) return s;
+  return dg::launch(moe_kernel<kFp4, true>, grid(down, static_cast<long long>(a.H / 128) * (a.I / 128)), kThreads, down_smem, stream, ctx.pdl, down_map, down);
 }
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -790,8 +734,8 @@ dg_status few_tokens(const void* x, const int32_t* sfx, const void* w13, const i
   if (kFp4 && (!aligned(w13, 32) || !aligned(w2, 32))) return DG_ERR_MISALIGNED;
   LaunchContext ctx;
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
-  const size_t slots = static_cast<size_t>(T) * topk, scale_words = slots * ((I / 128 + 3) / 4 * 4);
-  const size_t part_floats = 2ull * 2 * ctx.sms * 128 * std::max(kCols, T), h_bytes = (slots * kTerms * I + 15) / 16 * 16;
+  const size_t slots = static_cast<size_t>(T) * topk, scale_words = (slots * (I / 128) * kTerms + 3) / 4 * 4;
+  const size_t part_floats = 2ull * 2 * ctx.sms * 128 * std::max(T, kCols), h_bytes = (slots * kTerms * I + 15) / 16 * 16;
   dg::StreamWorkspace ws;
   void* scratch = nullptr;
   if (dg_status s = ws.acquire(stream, scale_words * 4 + h_bytes + part_floats * 4, &scratch); s != DG_OK) return s;
