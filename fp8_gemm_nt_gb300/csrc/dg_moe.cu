@@ -19,7 +19,7 @@
 // each 64 columns: 12 bits of every value within 2^-15 of the largest of its 64, and 2^-27 of that largest
 // below. The three terms are three columns, whose scales are 16 and 256 times smaller, and whose sums the
 // second kernel adds up. It owns output rows, sums all experts for 128 rows of W2 and every token in an
-// order that depends on the sizes alone, and writes each output once. No atomics on values.
+// order that depends on the sizes and the ids alone, and writes each output once. No atomics on values.
 //
 // A pipeline is a warp each for the weights' copies, the tokens' side, the weights' scales and the MMAs, and
 // four that read the sums from TMEM, with a ring of stages of 128 columns. A block (one to an SM) is two

@@ -362,7 +362,8 @@ dg_status dg_moe_route_backward(const void* logits, const int32_t* topk_ids, con
  *              gets c[t] (or 0). An id outside [-1, E) is taken as -1 and sets DG_ERR_BAD_INDEX on the device.
  *   c        : BF16 [T, H] addend (a shared expert's output, the residual) or NULL; may be y.
  *   y        : BF16 [T, H].
- * FP32 accumulation; the experts' inner values are held in FP16 with a power-of-two scale per 64 columns,
+ * FP32 accumulation; the experts' inner values (weight * silu * up) are held as sums of three E4M3 terms
+ * with a power-of-two scale per 64 columns: within 2^-12 of themselves, or 2^-27 of the largest of the 64.
  * y is rounded once. The values of experts that a token does not name never reach it.
  * Limits: T <= 32, topk <= 16, E <= 1024, H and I <= 16384 (DG_ERR_UNSUPPORTED above); H and I positive
  * multiples of 128. Pointers 16-byte aligned (topk_ids, topk_weights: 4). Uses the stream's workspace.
@@ -487,8 +488,9 @@ int dg_last_cuda_error(void);
 /*
  * Test hook for the failure-detection path (no counterpart on the pages).
  *   fault_mode      : 0 = none (default); 1 = the TMA producer of every later GEMM launch
- *                     issues no loads, so the MMA and epilogue waits run out and the
- *                     kernel exits with DG_ERR_TIMEOUT recorded in the status word.
+ *                     issues no loads (of the few-token layer: none of the weights), so the MMA
+ *                     and epilogue waits run out and the kernel exits with DG_ERR_TIMEOUT
+ *                     recorded in the status word.
  *   wait_timeout_ns : limit of every pipeline wait in later launches; 0 = default (2 s).
  * Process-wide; affects launches made after the call. Returns DG_ERR_INVALID_ARG for an
  * unknown fault_mode.

@@ -1,9 +1,9 @@
 """The mixture-of-experts layer for a few tokens against the FP64 oracle.
 
-Tolerances, from the arithmetic: products of E4M3, E2M1 and FP16 values are exact in FP32; a dot
+Tolerances, from the arithmetic: products of E4M3 and E2M1 values are exact in FP32; a dot
 product accumulates in FP32 in chains of at most H / 128 + 8 roundings or truncations at 2^-23, so it is
-within 2^-15 of the sum of its terms' magnitudes. The inner values are held in FP16 under a shared
-scale: 2^-11 of themselves. The oracle carries both through to y; storing y in BF16 adds 2^-8 of it."""
+within 2^-15 of the sum of its terms' magnitudes. The inner values are held to 11 bits or more under a
+shared scale: 2^-11 of themselves. The oracle carries both through to y; storing y in BF16 adds 2^-8 of it."""
 from __future__ import annotations
 
 import numpy as np
@@ -82,7 +82,7 @@ class Layer:
 def check(y, want, err):
     got = y.double().cpu().numpy()
     assert (np.abs(got - want) <= 1.01 * (BF16_REL * np.abs(want) + err)).all(), np.abs(got - want).max()
-    # and in the mean: BF16's rounding is at most 2^-8 / sqrt(3) of the values, FP16's far below
+    # and in the mean: BF16's rounding is at most 2^-8 / sqrt(3) of the values, the inner values' far below
     assert np.linalg.norm(got - want) <= 0.75 * BF16_REL * np.linalg.norm(want)
 
 
@@ -242,6 +242,27 @@ def test_experts_past_four_gib(lib):
     assert torch.equal(*out) and out[0].abs().sum() > 0
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_a_wait_that_runs_out_is_reported(lib, fmt):
+    p = Layer(6, 4, 2, 512, 384, fmt, seed=17)
+    base = p.run(lib)
+    lib.dg_set_debug(1, 20_000_000)          # no weights are copied; waits give up after 20 ms
+    try:
+        p.run(lib)
+        assert lib.dg_get_device_status() == 5   # DG_ERR_TIMEOUT
+    finally:
+        lib.dg_set_debug(0, 0)
+    assert torch.equal(p.run(lib), base) and lib.dg_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T, E, k", [(32, 1, 1), (32, 2, 2), (11, 1, 1), (16, 3, 2), (25, 2, 1), (32, 3, 1)])
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_many_tokens_of_an_expert(lib, T, E, k, fmt):
+    # more of them than one MMA takes as columns, in either product
+    p = Layer(T, E, k, 384, 256, fmt, seed=T + E, c=False)
+    check(p.run(lib), *p.oracle())
+
+
 def test_binding_refuses(lib):
     p = Layer(2, 3, 2, 128, 128, "e4m3", seed=14)
     d = {n: torch.from_numpy(getattr(p, n)).cuda() for n in ("x", "sfx", "w13", "sf13", "w2", "sf2", "ids", "weights")}
@@ -256,6 +277,12 @@ def test_binding_refuses(lib):
                 dict(y=y.float()), dict(c=y[:1]), dict(fn=lib.dg_moe_fp8_fp4_few_tokens)):
         with pytest.raises(ValueError):
             call(**bad)
+    f = Layer(2, 3, 2, 128, 128, "e2m1", seed=14)
+    d4 = {n: torch.from_numpy(getattr(f, n)).cuda() for n in ("w13", "sf13", "w2", "sf2")}
+    call(fn=lib.dg_moe_fp8_fp4_few_tokens, **d4)
+    off16 = torch.empty(3 * 128 * 64 + 16, dtype=torch.uint8, device="cuda")[16:].view(3, 128, 64)
+    with pytest.raises(lib.DGError, match="MISALIGNED"):
+        call(fn=lib.dg_moe_fp8_fp4_few_tokens, **{**d4, "w2": off16})
     odd = torch.empty(3 * 256 * 128 + 8, dtype=torch.uint8, device="cuda")[8:].view(3, 256, 128)
     with pytest.raises(lib.DGError, match="MISALIGNED"):
         call(w13=odd)
