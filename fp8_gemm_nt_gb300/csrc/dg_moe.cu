@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   // A wait that runs out is recorded, and every role then leaves its loop (the epilogue runs through it without
   // waiting, since its warps meet at barriers).
   auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (dg::mbar_try_wait(dg::smem_addr(bar), parity)) return true;
     if (s.abort) return false;
     if (dg::mbar_wait(bar, parity, a.timeout_ns)) return true;
     atomicOr(a.status, dg::kTimeoutBit);
@@ -417,28 +418,30 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         if (!dg::mbar_wait(&pipe.full[i % a.stages], i / a.stages & 1, a.timeout_ns)) break;
     }
   } else if (warp == 1) {
-    // ---------------------------------------------- the MMAs
-    if (lane == 0) {
-      const uint64_t a_desc = dg::make_smem_desc(dg::smem_addr(ring), 16, 1024, dg::kLayoutSwizzle128B);
-      const uint64_t b_desc = a_desc + (kWeights >> 4);
-      const uint64_t sf_desc = dg::make_smem_desc(dg::smem_addr(scales), 0, 128, dg::kLayoutNone);
-      int stage = 0;
-      uint32_t phase = 0, n = 0, buffer = 0;
-      bool ok = true;
-      while (ok && walk.next(run)) {
-        const uint32_t sum = n & 1, d = tmem + sum * kSumCols;
-        if (!(ok = wait(&pipe.sum_empty[sum], (n >> 1 & 1) ^ 1))) break;
+    // ---------------------------------------------- the MMAs. The whole warp runs the loop and one elected thread
+    // issues: behind a branch on the lane, the seven instructions of a stage took 530 clocks to issue (the compiler
+    // did not know the descriptors to be uniform), which bounded E2M1: 16 tokens, 174 us that way, 135 us this way.
+    const uint64_t a_desc = dg::make_smem_desc(dg::smem_addr(ring), 16, 1024, dg::kLayoutSwizzle128B);
+    const uint64_t b_desc = a_desc + (kWeights >> 4);
+    const uint64_t sf_desc = dg::make_smem_desc(dg::smem_addr(scales), 0, 128, dg::kLayoutNone);
+    int stage = 0;
+    uint32_t phase = 0, n = 0, buffer = 0;
+    bool ok = true;
+    while (ok && walk.next(run)) {
+      const uint32_t sum = n & 1, d = tmem + sum * kSumCols;
+      if (!(ok = __all_sync(kAll, wait(&pipe.sum_empty[sum], (n >> 1 & 1) ^ 1)))) break;
+      dg::tc_fence_after();
+      // rows past the last of the tokens' hold anything: they are columns of the sums that nobody reads
+      const uint32_t cols = kDown && kTerms * run.count > 16 ? 32 : 16;
+      const uint32_t idesc = dg::make_idesc_mxf8_e4m3(128, 0) | (cols >> 3) << 17 | (kFp4 ? 5u << 7 : 0u);
+      for (int g = run.begin; g < run.end; ++g) {
+        if (!(ok = __all_sync(kAll, wait(&pipe.full[stage], phase) && wait(&pipe.ready[stage], phase)))) break;
+        dg::fence_proxy_async_smem();       // of what the barriers say has arrived by cp.async
         dg::tc_fence_after();
-        // rows past the last of the tokens' hold anything: they are columns of the sums that nobody reads
-        const uint32_t cols = kDown && kTerms * run.count > 16 ? 32 : 16;
-        const uint32_t idesc = dg::make_idesc_mxf8_e4m3(128, 0) | (cols >> 3) << 17 | (kFp4 ? 5u << 7 : 0u);
-        for (int g = run.begin; g < run.end; ++g) {
-          if (!(ok = wait(&pipe.full[stage], phase) && wait(&pipe.ready[stage], phase))) break;
-          dg::fence_proxy_async_smem();       // of what the barriers say has arrived by cp.async
-          dg::tc_fence_after();
-          const uint64_t off = static_cast<uint64_t>(stage * a.stage_bytes) >> 4, sf_off = static_cast<uint64_t>(stage * a.scale_bytes) >> 4;
-          const uint32_t sfa = tmem + 2 * kSumCols + 4 * buffer, sfb = sfa + 8;
-          buffer ^= 1;
+        const uint64_t off = static_cast<uint64_t>(stage * a.stage_bytes) >> 4, sf_off = static_cast<uint64_t>(stage * a.scale_bytes) >> 4;
+        const uint32_t sfa = tmem + 2 * kSumCols + 4 * buffer, sfb = sfa + 8;
+        buffer ^= 1;
+        if (dg::elect_one()) {
           dg::tmem_copy_32x128b_warpx4(sfa, sf_desc + sf_off + (kTileA >> 4));
           dg::tmem_copy_32x128b_warpx4(sfb, sf_desc + sf_off + (kTileB >> 4));
 #pragma unroll
@@ -448,15 +451,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             dg::mma_mxf8_block_scale(d, a_desc + off + 2 * k, b_desc + off + 2 * k, id, sfa, sfb, g != run.begin || k != 0);
           }
           dg::tc_commit(&pipe.empty[stage]);
-          if (++stage == a.stages) stage = 0, phase ^= 1;
+          if (g + 1 == run.end) dg::tc_commit(&pipe.sum_full[sum]);
         }
-        if (ok) dg::tc_commit(&pipe.sum_full[sum]);
-        ++n;
+        __syncwarp();
+        if (++stage == a.stages) stage = 0, phase ^= 1;
       }
-      // all that was issued has to be done before TMEM is given back
-      dg::tc_commit(&pipe.drain);
-      dg::mbar_wait(&pipe.drain, 0, a.timeout_ns);
+      ++n;
     }
+    // all that was issued has to be done before TMEM is given back
+    if (dg::elect_one()) dg::tc_commit(&pipe.drain);
+    dg::mbar_wait(&pipe.drain, 0, a.timeout_ns);
     __syncwarp();
   } else if (warp == 2) {
     // ---------------------------------------------- the tokens' side: rows and scale words

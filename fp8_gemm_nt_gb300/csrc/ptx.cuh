@@ -162,6 +162,13 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// True in one thread of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(yes)::"memory");
+  return yes != 0;
+}
+
 // Arrive once on `bar` when every tcgen05 async operation issued so far by this thread
 // (MMAs, shared->TMEM copies) has completed.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
