@@ -13,6 +13,7 @@ B: per 128x128 block), FP32 accumulation and a BF16 result.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -419,12 +420,28 @@ class _RouteDesc(ctypes.Structure):
 
 
 # These calls are short (a few microseconds on the device), so their checks read each property of a
-# tensor once and build a message only where one fails.
+# tensor once and build a message only where one fails, and a descriptor is built once for its values.
+
+@functools.lru_cache(maxsize=256)
+def _norm_desc(*values):
+    return ctypes.byref(_NormDesc(*values))
+
+
+@functools.lru_cache(maxsize=256)
+def _route_desc(*values):
+    return ctypes.byref(_RouteDesc(*values))
+
 
 def _device(t: torch.Tensor, name: str) -> int:
     """The device of a call's first tensor, which has to be the current one."""
-    _here(t, name)
-    return t.get_device()
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _here(t, name)
+    return dev
+
+
+def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _refuse(t: torch.Tensor, name: str, dtypes, shape, dev: int):
@@ -446,14 +463,17 @@ def _rows(t: torch.Tensor, name: str, dtypes, shape, dev: int):
     """Pointer and row stride of a 2-D tensor whose columns are contiguous."""
     if t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
         ld, step = t.stride()
-        _need(step == 1 or shape[1] <= 1, f"{name} must have contiguous columns")
+        if step != 1 and shape[1] > 1:
+            raise ValueError(f"{name} must have contiguous columns")
         return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
     _refuse(t, name, dtypes, shape, dev)
 
 
 def _two_d(t: torch.Tensor, name: str):
-    _need(t.dim() == 2, f"{name} must be 2-D")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return shape
 
 
 def dg_add_rms_norm(x, residual, weight, eps, residual_out=None, y=None, q=None, sf=None, rstd=None, stream=None) -> None:
@@ -484,9 +504,8 @@ def dg_add_rms_norm(x, residual, weight, eps, residual_out=None, y=None, q=None,
         ps = _arg(sf, "sf", _I32_ONLY, (-(-H // 512), 4 * (-(-T // 4))), dev)
     if rstd is not None:
         pd = _arg(rstd, "rstd", _F32_ONLY, (T,), dev)
-    desc = _NormDesc(T, H, ldx, ldr, ldo, _TYPES[rt], _TYPES[weight.dtype], eps)
-    _check("dg_add_rms_norm", (_lib or load_library()).dg_add_rms_norm(px, pr, pw, po, py, pq, ps, pd, ctypes.byref(desc),
-                                                                      _stream(stream)))
+    desc = _norm_desc(T, H, ldx, ldr, ldo, _TYPES[rt], _TYPES[weight.dtype], eps)
+    _check("dg_add_rms_norm", (_lib or load_library()).dg_add_rms_norm(px, pr, pw, po, py, pq, ps, pd, desc, _stream_of(stream, dev)))
 
 
 def dg_add_rms_norm_backward(dy, s, weight, rstd, ds, dx, dresidual, dw, stream=None) -> None:
@@ -507,7 +526,7 @@ def dg_add_rms_norm_backward(dy, s, weight, rstd, ds, dx, dresidual, dw, stream=
     pdw = _arg(dw, "dw", _F32_ONLY, (H,), dev)
     _check("dg_add_rms_norm_backward",
            (_lib or load_library()).dg_add_rms_norm_backward(pdy, ps, pw, pr, pds, pdx, pdr, pdw, T, H, _TYPES[s.dtype],
-                                                             _TYPES[weight.dtype], _stream(stream)))
+                                                             _TYPES[weight.dtype], _stream_of(stream, dev)))
 
 
 def _route_args(logits, topk_ids, scoring, renormalize, scale):
@@ -516,8 +535,8 @@ def _route_args(logits, topk_ids, scoring, renormalize, scale):
     p, ld = _rows(logits, "logits", _STREAM_DTYPES, shape, dev)
     k = _two_d(topk_ids, "topk_ids")[1]
     _need(scoring in _SCORING, "scoring must be softmax or sigmoid")
-    desc = _RouteDesc(T, E, k, ld, _TYPES[logits.dtype], _SCORING[scoring], bool(renormalize), scale)
-    return dev, shape, (T, k), p, ctypes.byref(desc)
+    desc = _route_desc(T, E, k, ld, _TYPES[logits.dtype], _SCORING[scoring], bool(renormalize), scale)
+    return dev, shape, (T, k), p, desc
 
 
 def dg_moe_route(logits, topk_ids, topk_weights, scoring="softmax", renormalize=True, scale=1.0, stream=None):
@@ -527,7 +546,7 @@ def dg_moe_route(logits, topk_ids, topk_weights, scoring="softmax", renormalize=
     dev, _, slots, p, desc = _route_args(logits, topk_ids, scoring, renormalize, scale)
     pi = _arg(topk_ids, "topk_ids", _I32_ONLY, slots, dev)
     pw = _arg(topk_weights, "topk_weights", _F32_ONLY, slots, dev)
-    _check("dg_moe_route", (_lib or load_library()).dg_moe_route(p, pi, pw, desc, _stream(stream)))
+    _check("dg_moe_route", (_lib or load_library()).dg_moe_route(p, pi, pw, desc, _stream_of(stream, dev)))
     return topk_ids, topk_weights
 
 
@@ -538,7 +557,7 @@ def dg_moe_route_backward(logits, topk_ids, dweights, dlogits, scoring="softmax"
     pi = _arg(topk_ids, "topk_ids", _I32_ONLY, slots, dev)
     pw = _arg(dweights, "dweights", _F32_ONLY, slots, dev)
     po = _arg(dlogits, "dlogits", (logits.dtype,), shape, dev)
-    _check("dg_moe_route_backward", (_lib or load_library()).dg_moe_route_backward(p, pi, pw, po, desc, _stream(stream)))
+    _check("dg_moe_route_backward", (_lib or load_library()).dg_moe_route_backward(p, pi, pw, po, desc, _stream_of(stream, dev)))
     return dlogits
 
 
@@ -564,7 +583,7 @@ def _few_tokens(name, fp4, x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c
     pw = _arg(topk_weights, "topk_weights", _F32_ONLY, (T, k), dev)
     pc = None if c is None else _arg(c, "c", _BF16_ONLY, shape, dev)
     py = _arg(y, "y", _BF16_ONLY, shape, dev)
-    _check(name, getattr(_lib or load_library(), name)(px, psx, p13, ps13, p2, ps2, pi, pw, pc, py, T, k, E, H, I, _stream(stream)))
+    _check(name, getattr(_lib or load_library(), name)(px, psx, p13, ps13, p2, ps2, pi, pw, pc, py, T, k, E, H, I, _stream_of(stream, dev)))
     return y
 
 
