@@ -7,14 +7,16 @@
 // An expert whose logit is -inf or NaN is masked: never chosen, and no part of the softmax. Slots for
 // which no expert is left get id -1 and weight 0.
 //
-// One warp per row, its logits in registers. A choice of k among all E by
+// A warp takes a row, its logits in registers. A choice of k among all E by
 // k rounds over every register costs about 50 instructions a round, more than reading the row allows; so
 // most of the row is sorted out first. The k-th largest of the 32 lanes' own maxima is a lower bound of
 // the k-th largest logit; what reaches it (k and a few) is gathered, one per lane, and each candidate
 // counts those before it. Rows with more than 32 candidates (large k, many equal logits) take the rounds
-// over all. 65536 rows of 256 FP32 logits, k = 8: 30 us, 2.3 TB/s, bound by issued instructions (500 a row,
-// 85 % of the issue slots); the rounds alone took 70 us. Blocks that loop over rows with the next row's
-// loads in flight were slower (34 us: the registers cost more warps than the loads cost time).
+// over all. Where there are many rows and k is at most 8, a warp takes two.
+//
+// 65536 rows of 256 FP32 logits, k = 8: 24 us, 2.9 TB/s, bound by issued instructions (29.4 us with a row a warp, 500
+// instructions a row; 70 us by rounds alone). Blocks that loop over rows with the next row's loads in flight
+// were slower (34 us: the registers cost more warps than the loads cost time).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,6 +35,11 @@ using dg::LaunchContext;
 constexpr int kWarps = 8;               // rows per block
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 32;            // a lane of the warp holds a slot
+// Two rows a warp: for k that seldom leaves more than 16 candidates, few enough logits per lane to hold both rows, and
+// rows enough for half the warps to fill the SMs (256 FP32 logits, k = 8, two rows against one: 65536 rows 24.0 and
+// 29.1 us, 16384 rows 7.6 and 8.9, 4096 rows 3.7 and 3.8, 1024 rows 3.3 and 2.7; k = 12: 32.0 and 34.9, k = 16: 42.7
+// and 41.2; 512 logits: 36.8 and 38.5).
+constexpr int kPairTopk = 8, kPairLogits = 8, kPairRows = 8192;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float load_logit(const float* p) { return __ldcg(p); }
@@ -118,72 +125,82 @@ struct RouteArgs {
   float scale;
 };
 
-template <class L, int J, int kVec>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs<L> a) {
-  using At = Lane<L, J, kVec>;
-  constexpr int P = At::kCount;
-  __shared__ float2 gathered[kWarps][32], chosen[kWarps][32];
-  dg::grid_dependency_wait();
-  dg::grid_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  // (logit, expert) of the candidates, and of the chosen by slot
-  float2* const candidates = gathered[threadIdx.x / 32];
-  float2* const slots = chosen[threadIdx.x / 32];
-  const long long t = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
-  if (t >= a.T) return;
-  float v[P];
-  At::load(a.logits + t * a.ld, lane, a.E, v);
+// What is known of a row once its candidates, n of them, have been gathered as (logit, expert).
+struct Candidates {
+  float top, total;      // the largest logit, and the softmax's sum over every expert relative to it
+  int n;
+};
+
+template <class At, int P, class L>
+__device__ __forceinline__ Candidates gather(const RouteArgs<L>& a, float (&v)[P], int lane, float2* candidates) {
 #pragma unroll
   for (int i = 0; i < P; ++i) v[i] = fmaxf(v[i], -INFINITY);        // NaN is masked as -inf is
   const float mine = max_of(v), top = warp_max(mine);
-  float total = 0;   // of the softmax over every expert, relative to the largest
+  float total = 0;
   if (!a.sigmoid && !a.renorm && top > -INFINITY) {
 #pragma unroll
     for (int i = 0; i < P; ++i) total += expf(v[i] - top);
     total = warp_sum(total);
   }
-  int found = 0, n = 32;
-  float2 cand = make_float2(v[0], __int_as_float(lane));
   if (P == 1) {
-    candidates[lane] = cand;
+    candidates[lane] = make_float2(v[0], __int_as_float(lane));
     __syncwarp();
-  } else {
-    float left = mine, bound = top;
-    for (int i = 1; i < a.k; ++i) {
-      left = left == bound ? -INFINITY : left;
-      bound = warp_max(left);
-    }
-    bound = fmaxf(bound, -3.402823466e38f);                       // any logit that is not masked
-    int count = 0;
-#pragma unroll
-    for (int i = 0; i < P; ++i) count += v[i] >= bound;
-    int at = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kAll, at, o);
-      if (lane >= o) at += x;
-    }
-    n = __shfl_sync(kAll, at, 31);
-    if (n <= 32) {
-      at -= count;
-      if (count > 0) {
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-          if (v[i] >= bound) candidates[at++] = make_float2(v[i], __int_as_float(At::index(lane, i)));
-      }
-      __syncwarp();
-      if (lane < n) cand = candidates[lane];
-    }
+    return {top, total, 32};
   }
+  float left = mine, bound = top;
+  for (int i = 1; i < a.k; ++i) {
+    left = left == bound ? -INFINITY : left;
+    bound = warp_max(left);
+  }
+  bound = fmaxf(bound, -3.402823466e38f);                       // any logit that is not masked
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) count += v[i] >= bound;
+  int at = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAll, at, o);
+    if (lane >= o) at += x;
+  }
+  const int n = __shfl_sync(kAll, at, 31);
   if (n <= 32) {
-    // how many candidates come before this lane's: larger ones, and equal ones of a lower index
-    const int id = __float_as_int(cand.y);
-    const bool live = lane < n && cand.x > -INFINITY;
-    int before = 0;
-    for (int i = 0; i < n; ++i) {
-      const float2 c = candidates[i];
-      before += c.x > cand.x || (c.x == cand.x && __float_as_int(c.y) < id);
+    at -= count;
+    if (count > 0) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (v[i] >= bound) candidates[at++] = make_float2(v[i], __int_as_float(At::index(lane, i)));
     }
+    __syncwarp();
+  }
+  return {top, total, n};
+}
+
+// How many of n candidates come before one: larger ones, and equal ones of a lower index.
+__device__ __forceinline__ int rank_of(float2 cand, const float2* candidates, int n) {
+  const int id = __float_as_int(cand.y);
+  int before = 0;
+  for (int i = 0; i < n; ++i) {
+    const float2 c = candidates[i];
+    before += c.x > cand.x || (c.x == cand.x && __float_as_int(c.y) < id);
+  }
+  return before;
+}
+
+// The weight of a chosen expert before `scale`; `total`: of the softmax or, renormalised, of the chosen.
+template <class L>
+__device__ __forceinline__ float weight_of(const RouteArgs<L>& a, float w, float total) {
+  if (!a.renorm && a.sigmoid) return w;
+  return total > 0 ? w / total : total == 0 ? 0.0f : NAN;
+}
+
+// A row's choice and its outputs, by the whole warp.
+template <class At, int P, class L>
+__device__ __forceinline__ void choose(const RouteArgs<L>& a, long long t, float (&v)[P], const Candidates& row, int lane, const float2* candidates, float2* slots) {
+  int found = 0;
+  if (row.n <= 32) {
+    const float2 cand = lane < row.n ? candidates[lane] : make_float2(-INFINITY, 0);
+    const bool live = cand.x > -INFINITY;
+    const int before = rank_of(cand, candidates, row.n);
     found = min(a.k, __popc(__ballot_sync(kAll, live)));
     if (live && before < a.k) slots[before] = cand;
   } else {
@@ -205,12 +222,77 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs<L> a
   const bool have = lane < found;
   const float2 slot = slots[lane];
   float w = 0;
-  if (have) w = a.sigmoid ? sigmoid(slot.x) : expf(slot.x - top);
-  if (a.renorm) total = warp_sum(w);
-  if (a.renorm || !a.sigmoid) w = total > 0 ? w / total : total == 0 ? 0.0f : NAN;
+  if (have) w = a.sigmoid ? sigmoid(slot.x) : expf(slot.x - row.top);
+  w = weight_of(a, w, a.renorm ? warp_sum(w) : row.total);
   if (lane < a.k) {
     a.ids[t * a.k + lane] = have ? __float_as_int(slot.y) : -1;
     a.weights[t * a.k + lane] = have ? a.scale * w : 0.0f;
+  }
+}
+
+template <class L, int J, int kVec>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs<L> a) {
+  using At = Lane<L, J, kVec>;
+  __shared__ float2 gathered[kWarps][32], chosen[kWarps][32];
+  dg::grid_dependency_wait();
+  dg::grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const long long t = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  if (t >= a.T) return;
+  float v[At::kCount];
+  At::load(a.logits + t * a.ld, lane, a.E, v);
+  const Candidates row = gather<At>(a, v, lane, gathered[warp]);
+  choose<At>(a, t, v, row, lane, gathered[warp], chosen[warp]);
+}
+
+// Two rows a warp. Each is gathered by all lanes; the order of its candidates, the weights and the outputs, which
+// need few, by 16 lanes for either row at once, if neither has more candidates.
+template <class L, int J, int kVec>
+__global__ void __launch_bounds__(kWarps * 32) route_pair_kernel(const RouteArgs<L> a) {
+  using At = Lane<L, J, kVec>;
+  __shared__ float2 gathered[kWarps][2][32], chosen[kWarps][32];
+  dg::grid_dependency_wait();
+  dg::grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const long long t = 2 * (static_cast<long long>(blockIdx.x) * kWarps + warp);
+  if (t >= a.T) return;
+  const bool two = t + 1 < a.T;
+  float v[2][At::kCount];
+  At::load(a.logits + t * a.ld, lane, a.E, v[0]);
+  At::load(a.logits + (two ? t + 1 : t) * a.ld, lane, a.E, v[1]);
+  float2(&candidates)[2][32] = gathered[warp];
+  float2* const slots = chosen[warp];
+  const Candidates row0 = gather<At>(a, v[0], lane, candidates[0]), row1 = gather<At>(a, v[1], lane, candidates[1]);
+  if (max(row0.n, row1.n) > 16) {
+    choose<At>(a, t, v[0], row0, lane, candidates[0], slots);
+    __syncwarp();
+    if (two) choose<At>(a, t + 1, v[1], row1, lane, candidates[1], slots);
+    return;
+  }
+  const int at = lane & 15;
+  const bool second = lane >= 16;
+  const int n = second ? row1.n : row0.n;
+  const float2* const mine = candidates[second];
+  const float2 cand = at < n ? mine[at] : make_float2(-INFINITY, 0);
+  const bool live = cand.x > -INFINITY;
+  const int before = rank_of(cand, mine, n);
+  const int found = min(a.k, __popc(__ballot_sync(kAll, live) & (second ? 0xFFFF0000u : 0xFFFFu)));
+  if (live && before < a.k) slots[16 * second + before] = cand;
+  __syncwarp();
+  const bool have = at < found;
+  const float2 slot = slots[lane];
+  float w = 0, total = second ? row1.total : row0.total;
+  if (have) w = a.sigmoid ? sigmoid(slot.x) : expf(slot.x - (second ? row1.top : row0.top));
+  if (a.renorm) {
+    total = w;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  }
+  w = weight_of(a, w, total);
+  if (at < a.k && (two || !second)) {
+    const long long to = (t + second) * a.k + at;
+    a.ids[to] = have ? __float_as_int(slot.y) : -1;
+    a.weights[to] = have ? a.scale * w : 0.0f;
   }
 }
 
@@ -352,7 +434,14 @@ dg_status dg_moe_route(const void* logits, int32_t* topk_ids, float* topk_weight
     using L = std::remove_pointer_t<decltype(type)>;
     const RouteArgs<L> a{static_cast<const L*>(logits), topk_ids, topk_weights, desc->T, desc->E, desc->topk, desc->ld,
                          desc->scoring == DG_ROUTE_SIGMOID, desc->renormalize, desc->scale};
-    return with_shape<L>(desc->E, whole_pieces<L>(logits, desc->ld, desc->E), [&](auto j, auto vec) {
+    // 16-byte loads only where every lane has one: the bound is among the lanes' maxima (65536 rows of 64 BF16 logits,
+    // k = 8: 25 us, against 39 us with 8 lanes at work)
+    const bool wide = desc->E >= 32 * static_cast<int>(16 / sizeof(L)) && whole_pieces<L>(logits, desc->ld, desc->E);
+    return with_shape<L>(desc->E, wide, [&](auto j, auto vec) {
+      constexpr int kLogits = decltype(j)::value * decltype(vec)::value;
+      if constexpr (kLogits > 1 && kLogits <= kPairLogits)
+        if (desc->topk <= kPairTopk && desc->T >= kPairRows)
+          return dg::launch(route_pair_kernel<L, decltype(j)::value, decltype(vec)::value>, row_blocks((desc->T + 1) / 2), kWarps * 32, 0, stream, ctx.pdl, a);
       return dg::launch(route_kernel<L, decltype(j)::value, decltype(vec)::value>, row_blocks(desc->T), kWarps * 32, 0, stream, ctx.pdl, a);
     });
   };

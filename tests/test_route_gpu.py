@@ -70,6 +70,28 @@ def test_route_and_gradient(lib, T, E, k, dtype, scoring, renorm):
     assert lib.dg_get_device_status() == 0
 
 
+@pytest.mark.parametrize("T, E, k", [(8193, 64, 8), (8192, 40, 1), (9001, 250, 5), (8200, 256, 8), (8193, 100, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scoring, renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_two_rows_a_warp(lib, T, E, k, dtype, scoring, renorm):
+    # two rows a warp, among them rows of ties, which have many candidates, and rows with few or no experts left;
+    # the same bits as in calls of fewer rows
+    x = make(T, E, dtype, seed=T + E + k)
+    x[5::7] = x[5::7].round()
+    x[100:300:3] = 1.0
+    x[301:320] = -float("inf")
+    x[310:315, E // 2] = -3.0
+    x[T - 1] = float("nan")
+    x[T - 2, : E // 2] = 2.0
+    ids, w = route(lib, x, k, scoring, renorm, 0.5)
+    few = [route(lib, x[i:i + 3000], k, scoring, renorm, 0.5) for i in range(0, T, 3000)]
+    assert torch.equal(ids, torch.cat([f[0] for f in few])) and torch.equal(w, torch.cat([f[1] for f in few]))
+    some = np.r_[0:700, T - 300:T]
+    want_ids, want = OL.moe_route(x[torch.from_numpy(some).cuda()].double().cpu().numpy(), k, scoring, renorm, 0.5)
+    assert (ids.cpu().numpy()[some] == want_ids).all()
+    assert (np.abs(w.double().cpu().numpy()[some] - want) <= REL * np.abs(want)).all()
+
+
 def test_infinite_and_extreme_logits(lib):
     inf = float("inf")
     x = torch.tensor([[inf, 0.0, 1.0], [-200.0, -300.0, -inf], [3e38, -3e38, 0.0], [float("nan")] * 3], device="cuda")
