@@ -12,6 +12,9 @@
 // copies its own columns of the row after it asynchronously to shared memory while it works on one, so
 // that loads stay in flight through the row's reduction and stores, and no thread waits for another's
 // copies. Blocks are persistent: weight (and the gradient's share of dw) stay in registers over the rows.
+// 32768 rows of 7168 in BF16 to E4M3: 240 us, 6.9 TB/s, as fast as a copy (321 us with scalar arithmetic, which
+// bounded it; 361 us with a block per row). Gradient of 16384 rows: 137 us, 6.9 TB/s (373 us with a block per row).
+// With an FP32 stream 0.73 to 0.80 and 0.65 to 0.72 of a copy's rate, with no unit saturated.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
