@@ -441,7 +441,7 @@ dg_status dg_moe_route(const void* logits, int32_t* topk_ids, float* topk_weight
       constexpr int kLogits = decltype(j)::value * decltype(vec)::value;
       if constexpr (kLogits > 1 && kLogits <= kPairLogits)
         if (desc->topk <= kPairTopk && desc->T >= kPairRows)
-          return dg::launch(route_pair_kernel<L, decltype(j)::value, decltype(vec)::value>, row_blocks((desc->T + 1) / 2), kWarps * 32, 0, stream, ctx.pdl, a);
+          return dg::launch(route_pair_kernel<L, decltype(j)::value, decltype(vec)::value>, row_blocks(desc->T / 2 + desc->T % 2), kWarps * 32, 0, stream, ctx.pdl, a);
       return dg::launch(route_kernel<L, decltype(j)::value, decltype(vec)::value>, row_blocks(desc->T), kWarps * 32, 0, stream, ctx.pdl, a);
     });
   };
