@@ -31,7 +31,8 @@ dg_status record_cuda_error(cudaError_t e);
 bool weight_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool e2m1);
 
 // `bytes` of the stream's workspace, past the arrival counters at its start (kArrivalCounters of them, zero
-// between launches: a kernel that counts in them leaves them so). Held until the object goes out of scope, which has to be after the launches that use it.
+// between launches: a kernel that counts in them leaves them so). Held until the object goes out of scope, which
+// has to be after the launches that use it.
 constexpr int kArrivalCounters = 4096;
 class StreamWorkspace {
  public:
@@ -47,37 +48,22 @@ class StreamWorkspace {
   int* counters_ = nullptr;
 };
 
-// Launches `kernel` on `stream`, in clusters of `cluster` blocks, as a programmatic dependent of the stream's
-// last kernel if `pdl` (the kernel then waits for that one itself, before any access to what it may touch).
+// Launches `kernel` on `stream`, as a programmatic dependent of the stream's last kernel if `pdl` (the kernel then
+// waits for that one itself, before any access to what it may touch).
 template <class... Params, class... Args>
-dg_status launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned cluster, unsigned block, size_t smem, cudaStream_t stream, bool pdl,
-                          Args... args) {
+dg_status launch(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, bool pdl, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (pdl) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(block, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
   return e == cudaSuccess ? DG_OK : record_cuda_error(e);
-}
-
-template <class... Params, class... Args>
-dg_status launch(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, bool pdl, Args... args) {
-  return launch_clusters(kernel, grid, 1, block, smem, stream, pdl, args...);
 }
 
 }  // namespace dg

@@ -11,11 +11,6 @@ namespace dg {
 // Bits of the device status word (the GEMM kernels set the same ones).
 enum : uint32_t { kTimeoutBit = 1u << 5, kBadIndexBit = 1u << 6 };
 
-// 2^(e - 127); code 0 is the subnormal 2^-127, code 255 NaN.
-__device__ __forceinline__ float ue8m0_value(uint32_t e) {
-  return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
-}
-
 // Least code e in [1, 254] with amax <= 448 * 2^(e - 127); for 0 the least of all, 1.
 // 448 = 1.75 * 2^8: the exponent of amax less 8, one more if the mantissa is above 0.75 = 0x600000 / 2^23,
 // which is when adding 0x1FFFFF carries into the exponent.
