@@ -571,15 +571,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       auto last_of = [&](int piece_begin, int per, int* first, int* last) {
         *first = deal.owner(piece_begin);
         *last = deal.owner(piece_begin + per - 1);
-        __threadfence();
         named_barrier(1 + 2 * half, 128);
         if (warp == 4 && lane == 0) {
+          // the fences stand between the barriers and the count, in the thread that counts: the first then covers what
+          // all 128 threads wrote, the second what they read next
+          __threadfence();
           const int before = atomicAdd(a.arrivals + *first, 1);
+          __threadfence();
           s.arrived[half] = before == *last - *first;
           if (before == *last - *first) a.arrivals[*first] = 0;
         }
         named_barrier(1 + 2 * half, 128);
-        __threadfence();
         return s.arrived[half] != 0;
       };
       // where pipeline p put its part of the piece: a piece that it did not begin is its first
