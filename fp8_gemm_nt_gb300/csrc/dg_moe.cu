@@ -556,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const int quad = warp - 4, row = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t n = 0;
+    // Parts and counts are the first kernel's until it has ended, and the waits below do not keep to that when they run out.
+    if (kDown) dg::grid_dependency_wait();
     while (walk.next(run)) {
       const uint32_t sum = n & 1, from = tmem + lanes + sum * kSumCols;
       wait(&pipe.sum_full[sum], n >> 1 & 1);

@@ -29,3 +29,21 @@ def test_cut_pieces_give_the_same_bits_every_time(lib, T, E, k, H, I, fmt):  # n
     torch.cuda.synchronize()
     assert (many == y).all()
     assert lib.dg_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T, E, k, H, I", CUT)
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_waits_that_run_out_leave_the_counts_at_zero(lib, T, E, k, H, I, fmt):  # noqa: F811
+    # every pipeline still counts its parts, in the second kernel only once the first has ended: the calls after it, before
+    # the status is read (which clears the workspaces), are right
+    p = Layer(T, E, k, H, I, fmt, seed=T + H + 1, c=False)
+    y = p.run(lib)
+    lib.dg_set_debug(1, 5_000_000)           # no weights are copied; waits give up after 5 ms
+    try:
+        p.run(lib)
+    finally:
+        lib.dg_set_debug(0, 0)
+    for _ in range(3):
+        assert torch.equal(p.run(lib), y)
+    assert lib.dg_get_device_status() == 5   # DG_ERR_TIMEOUT, from the second call
+    assert torch.equal(p.run(lib), y) and lib.dg_get_device_status() == 0
