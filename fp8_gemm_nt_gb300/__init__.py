@@ -465,7 +465,7 @@ def _rows(t: torch.Tensor, name: str, dtypes, shape, dev: int):
         ld, step = t.stride()
         if step != 1 and shape[1] > 1:
             raise ValueError(f"{name} must have contiguous columns")
-        return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
+        return t.data_ptr(), ld if shape[0] > 1 else shape[1]     # of a single row the stride says nothing
     _refuse(t, name, dtypes, shape, dev)
 
 

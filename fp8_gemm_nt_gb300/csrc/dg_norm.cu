@@ -531,14 +531,15 @@ dg_status dg_add_rms_norm(const void* x, const void* residual, const void* weigh
                           int32_t* sf, float* rstd, const dg_norm_desc* desc, cudaStream_t stream) {
   if (!desc) return DG_ERR_INVALID_ARG;
   const int T = desc->T, H = desc->H, residual_type = desc->residual_type, weight_type = desc->weight_type;
-  const size_t ldx = desc->ldx, ldr = desc->ldr, ldo = desc->ldo;
+  // a stride matters where there is a next row
+  const size_t cols = H > 0 ? static_cast<size_t>(H) : 0;
+  const size_t ldx = T > 1 ? desc->ldx : cols, ldr = T > 1 ? desc->ldr : cols, ldo = T > 1 ? desc->ldo : cols;
   const float eps = desc->eps;
   if (T < 0 || H <= 0 || H % kVec != 0 || !known_type(residual_type) || !known_type(weight_type)) return DG_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !(eps < INFINITY)) return DG_ERR_INVALID_ARG;
   if ((q != nullptr) != (sf != nullptr) || (T > 0 && !q && !y && !residual_out) || (q && H % 128 != 0)) return DG_ERR_INVALID_ARG;
   if (H > kMaxH) return DG_ERR_UNSUPPORTED;
   if (T == 0) return DG_OK;
-  const size_t cols = static_cast<size_t>(H);
   if (!x || !weight || ldx < cols || (residual && ldr < cols) || (residual_out && ldo < cols)) return DG_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(y) ||
       !aligned16(q) || !aligned16(sf) || (reinterpret_cast<uintptr_t>(rstd) & 3u) || row_bytes(ldx, DG_BF16) % 16 ||

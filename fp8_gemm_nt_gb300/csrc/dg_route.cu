@@ -402,10 +402,13 @@ bool whole_pieces(const void* p, size_t ld, int E) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % kWide == 0 && E % kWide == 0;
 }
 
+// Elements between the rows of the logits; a single row has no next one, whatever its stride says.
+size_t row_stride(const dg_route_desc& d) { return d.T > 1 ? d.ld : static_cast<size_t>(d.E); }
+
 dg_status check(const void* logits, const void* ids, const void* weights, const dg_route_desc* desc) {
   if (!desc) return DG_ERR_INVALID_ARG;
   const auto [T, E, topk, ld, logits_type, scoring, renormalize, scale] = *desc;
-  if (T < 0 || E <= 0 || topk <= 0 || topk > E || ld < static_cast<size_t>(E) || (logits_type != DG_BF16 && logits_type != DG_F32))
+  if (T < 0 || E <= 0 || topk <= 0 || topk > E || row_stride(*desc) < static_cast<size_t>(E) || (logits_type != DG_BF16 && logits_type != DG_F32))
     return DG_ERR_INVALID_ARG;
   if ((scoring != DG_ROUTE_SOFTMAX && scoring != DG_ROUTE_SIGMOID) || (renormalize != 0 && renormalize != 1) || !std::isfinite(scale))
     return DG_ERR_INVALID_ARG;
@@ -430,13 +433,14 @@ dg_status dg_moe_route(const void* logits, int32_t* topk_ids, float* topk_weight
   if (desc->T == 0) return DG_OK;
   LaunchContext ctx;
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+  const size_t ld = row_stride(*desc);
   auto run = [&](auto* type) {
     using L = std::remove_pointer_t<decltype(type)>;
-    const RouteArgs<L> a{static_cast<const L*>(logits), topk_ids, topk_weights, desc->T, desc->E, desc->topk, desc->ld,
+    const RouteArgs<L> a{static_cast<const L*>(logits), topk_ids, topk_weights, desc->T, desc->E, desc->topk, ld,
                          desc->scoring == DG_ROUTE_SIGMOID, desc->renormalize, desc->scale};
     // 16-byte loads only where every lane has one: the bound is among the lanes' maxima (65536 rows of 64 BF16 logits,
     // k = 8: 25 us, against 39 us with 8 lanes at work)
-    const bool wide = desc->E >= 32 * static_cast<int>(16 / sizeof(L)) && whole_pieces<L>(logits, desc->ld, desc->E);
+    const bool wide = desc->E >= 32 * static_cast<int>(16 / sizeof(L)) && whole_pieces<L>(logits, ld, desc->E);
     return with_shape<L>(desc->E, wide, [&](auto j, auto vec) {
       constexpr int kLogits = decltype(j)::value * decltype(vec)::value;
       if constexpr (kLogits > 1 && kLogits <= kPairLogits)
@@ -456,11 +460,12 @@ dg_status dg_moe_route_backward(const void* logits, const int32_t* topk_ids, con
   if (reinterpret_cast<uintptr_t>(dlogits) & (desc->logits_type == DG_BF16 ? 1u : 3u)) return DG_ERR_MISALIGNED;
   LaunchContext ctx;
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+  const size_t ld = row_stride(*desc);
   auto run = [&](auto* type) {
     using L = std::remove_pointer_t<decltype(type)>;
     const RouteGradArgs<L> a{static_cast<const L*>(logits), topk_ids, dweights, static_cast<L*>(dlogits), ctx.status,
-                             desc->T, desc->E, desc->topk, desc->ld, desc->scoring == DG_ROUTE_SIGMOID, desc->renormalize, desc->scale};
-    const bool aligned = whole_pieces<L>(logits, desc->ld, desc->E) && whole_pieces<L>(dlogits, desc->E, desc->E);
+                             desc->T, desc->E, desc->topk, ld, desc->scoring == DG_ROUTE_SIGMOID, desc->renormalize, desc->scale};
+    const bool aligned = whole_pieces<L>(logits, ld, desc->E) && whole_pieces<L>(dlogits, desc->E, desc->E);
     return with_shape<L>(desc->E, aligned, [&](auto j, auto vec) {
       return dg::launch(route_grad_kernel<L, decltype(j)::value, decltype(vec)::value>, row_blocks(desc->T), kWarps * 32, 0, stream, ctx.pdl, a);
     });

@@ -264,7 +264,7 @@ typedef enum { DG_BF16 = 0, DG_F32 = 1 } dg_type;
 /* Sizes, strides (in elements) and options of dg_add_rms_norm. */
 typedef struct {
   int T, H;
-  size_t ldx, ldr, ldo;               /* row strides of x, residual, residual_out */
+  size_t ldx, ldr, ldo;               /* row strides of x, residual, residual_out (not read if T <= 1) */
   int residual_type, weight_type;     /* dg_type */
   float eps;
 } dg_norm_desc;
@@ -317,7 +317,7 @@ typedef enum { DG_ROUTE_SOFTMAX = 0, DG_ROUTE_SIGMOID = 1 } dg_route_scoring;
 /* Sizes and options of the router. */
 typedef struct {
   int T, E, topk;
-  size_t ld;                          /* row stride of logits, in elements */
+  size_t ld;                          /* row stride of logits, in elements (not read if T <= 1) */
   int logits_type;                    /* dg_type */
   int scoring;                        /* dg_route_scoring */
   int renormalize;                    /* 0 or 1 */
