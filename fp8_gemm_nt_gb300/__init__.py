@@ -407,6 +407,7 @@ _SCORING = {"softmax": 0, "sigmoid": 1}             # dg_route_scoring
 _STREAM_DTYPES = (torch.bfloat16, torch.float32)
 _BF16_ONLY, _F32_ONLY, _I32_ONLY = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _FP8_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+_MAX_SIZE = 2 ** 31 - 1      # sizes are ints at the C entries, and ctypes would cut off what is above
 
 
 class _NormDesc(ctypes.Structure):
@@ -473,6 +474,8 @@ def _two_d(t: torch.Tensor, name: str):
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
+    if shape[0] > _MAX_SIZE or shape[1] > _MAX_SIZE:
+        raise ValueError(f"{name} has a size above {_MAX_SIZE}: {tuple(shape)}")
     return shape
 
 

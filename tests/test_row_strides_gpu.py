@@ -1,4 +1,4 @@
-"""Row strides at the ends of their range: of a single row, which has no next one."""
+"""Row strides and sizes at the ends of their range."""
 from __future__ import annotations
 
 import ctypes
@@ -57,3 +57,19 @@ def test_router_of_one_row_with_any_stride(lib, dtype, E):  # noqa: F811
         out.append((ids, w, dx))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for o in out[1:] for a, b in zip(o, out[0]))
+
+
+def test_more_rows_than_an_int_counts_are_refused(lib):  # noqa: F811
+    # 2^32 + 3 rows must not pass for 3; they are views of one, so they take no memory
+    T = 2 ** 32 + 3
+    x = torch.zeros(1, 8, dtype=torch.bfloat16, device="cuda").expand(T, 8)
+    w, y = torch.ones(8, device="cuda"), x
+    with pytest.raises(ValueError, match="size above"):
+        lib.dg_add_rms_norm(x, None, w, 1e-6, y=y)
+    with pytest.raises(ValueError, match="size above"):
+        lib.dg_add_rms_norm_backward(x, x, w, w, None, y, None, w)
+    ids, weights = (torch.zeros(1, 2, dtype=d, device="cuda").expand(T, 2) for d in (torch.int32, torch.float32))
+    with pytest.raises(ValueError, match="size above"):
+        lib.dg_moe_route(x, ids, weights)
+    with pytest.raises(ValueError, match="size above"):
+        lib.dg_moe_route(x[:1], ids[:1].expand(1, 2)[:, :1].expand(1, T), weights)
