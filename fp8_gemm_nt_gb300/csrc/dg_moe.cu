@@ -12,14 +12,16 @@
 // of block-scaled tcgen05 MMAs, which take E4M3 and E2M1 as they are, with their scales: TMA brings the
 // weights to shared memory and no instruction touches them on the way.
 //
-// An expert's tokens are compacted into jobs (of at most 16 in the first product, 8 or 10 in the second); each
-// distinct (expert, token) pair is a slot. The first kernel computes h = weight * silu(g) * u of every slot. The second product also has to
-// be E4M3 by the weights' type, and three bits of mantissa would be too few: h is written as the sum of
-// three E4M3 terms, the second and third being the remainders times 16 and 256, with one power of two for
-// each 64 columns: 12 bits of every value within 2^-15 of the largest of its 64, and 2^-27 of that largest
-// below. The three terms are three columns, whose scales are 16 and 256 times smaller, and whose sums the
-// second kernel adds up. It owns output rows, sums all experts for 128 rows of W2 and every token in an
-// order that depends on the sizes and the ids alone, and writes each output once. No atomics on values.
+// An expert's tokens are compacted into jobs (of at most 16 in the first product, 8 in the second); each distinct
+// (expert, token) pair is a slot. The first kernel computes h = weight * silu(g) * u of every slot. The second product also
+// has to be E4M3 by the weights' type, and four bits would be too few: h is written as the sum of four E4M3 terms, each the
+// remainder of those before it times 16, under one power of two for each 64 columns that brings their largest to
+// (224, 448]. A term rounds to within 2^-4 of itself or 2^-10 of its scale, so h is within 2^-16 of itself or 2^-22 of
+// the scale, which is 2^-29.8 of the largest: with that y is as near to the exact sum as its rounding to BF16 lets it be
+// (a sum whose leading bits c cancels is 2^-18.5 off, 2^-16 with three terms, which are up to 4 % faster, with many tokens of few experts). The four
+// terms are four columns, whose scales are 16 times smaller each, and whose sums the second kernel adds up. It owns
+// output rows, sums all experts for 128 rows of W2 and every token in an order that depends on the sizes and the ids
+// alone, and writes each output once. No atomics on values.
 //
 // A pipeline is a warp each for the weights' copies, the tokens' side, the weights' scales and the MMAs, and
 // four that read the sums from TMEM, with a ring of stages of 128 columns. A block (one to an SM) is two
@@ -60,7 +62,8 @@ constexpr int kMaxH = 16384;
 constexpr int kMaxSlots = kMaxTokens * kMaxTopk;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kCols = 16;               // tokens of a job of the first kernel
-constexpr int kTerms = 3;               // E4M3 terms of a value of h
+constexpr int kTerms = 4;               // E4M3 terms of a value of h
+constexpr int kDownCols = 8;            // tokens of a job of the second kernel: 32 columns of their terms
 constexpr int kBlock = 64;              // columns of h of a unit of the first kernel, which share a scale
 constexpr int kHalf = 256;              // threads of a pipeline
 constexpr int kThreads = 2 * kHalf;
@@ -308,7 +311,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(d)));
 }
 
-// 64 columns of h of a slot, by a warp, two columns a lane: their three terms and their scale, from the sums of
+// 64 columns of h of a slot, by a warp, two columns a lane: their terms and their scale, from the sums of
 // the gate's rows and of the up's.
 __device__ __forceinline__ void store_inner(const MoeArgs& a, float coef, int slot, int block, float2 gate, float2 up, int lane) {
   float h[2] = {coef * (gate.x / (1.0f + expf(-gate.x)) * up.x), coef * (gate.y / (1.0f + expf(-gate.y)) * up.y)};
@@ -320,8 +323,8 @@ __device__ __forceinline__ void store_inner(const MoeArgs& a, float coef, int sl
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-  // the third term's scale is 2^-8 of the first's: its code stays at least 1
-  const int e = max(dg::ue8m0_for_amax(top), 9);
+  // the last term's scale is 2^-12 of the first's: its code stays at least 1
+  const int e = max(dg::ue8m0_for_amax(top), 4 * kTerms - 3);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float full = h[i] * dg::ue8m0_inverse(e);
@@ -591,19 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         return a.parts + (2ll * p + (deal.begin(p) > piece_begin ? 0 : 1)) * (128 * (kDown ? a.T : kCols));
       };
       if constexpr (kDown) {
-        // this row of the job's tokens, the sum of three terms each: no other thread has it
+        // this row of the job's tokens, the sum of four terms each: no other thread has it
         float* const out = rest;
-#pragma unroll 1
-        for (int i = 0; i < run.count; i += 8) {
-          uint32_t v[kTerms * 8];
+        uint32_t v[kTerms * kDownCols];
+        dg::tmem_load_32x32b_x32(from, v);
+        dg::tmem_load_wait();
 #pragma unroll
-          for (int j = 0; j < kTerms; ++j) dg::tmem_load_32x32b_x8(from + kTerms * i + 8 * j, v + 8 * j);
-          dg::tmem_load_wait();
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (i + j < run.count)
-              out[s.r.token[run.slot + i + j] * 128 + row] += __uint_as_float(v[3 * j]) + __uint_as_float(v[3 * j + 1]) + __uint_as_float(v[3 * j + 2]);
-        }
+        for (int i = 0; i < kDownCols; ++i)
+          if (i < run.count)
+            out[s.r.token[run.slot + i] * 128 + row] +=
+                (__uint_as_float(v[4 * i]) + __uint_as_float(v[4 * i + 1])) + (__uint_as_float(v[4 * i + 2]) + __uint_as_float(v[4 * i + 3]));
         release();
         if (!run.done) continue;
         const int per = s.r.jobs * groups;
@@ -714,11 +714,10 @@ dg_status run_layer(MoeArgs a, const void* w13, const void* w2, const LaunchCont
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return dg::record_cuda_error(e);
-  // Tokens of a job: 16 are the least columns of an MMA. In the second product each is three rows, 32 at most:
-  // 8 tokens a job leave room for a fifth stage where T * 128 outputs take no more than 8 KB a half.
+  // Tokens of a job: 16 are the least columns of an MMA. In the second product each is four rows, 32 at most.
   MoeArgs up = a, down = a;
   up.cols = kCols;
-  down.cols = a.T <= 16 ? 8 : 10;
+  down.cols = kDownCols;
   CUtensorMap up_map, down_map;
   if (!dg::weight_rows_map(&up_map, w13, static_cast<uint64_t>(a.E) * 2 * a.I, a.H, 64, kFp4) ||
       !dg::weight_rows_map(&down_map, w2, static_cast<uint64_t>(a.E) * a.H, a.I, 64, kFp4))

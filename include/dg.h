@@ -362,8 +362,9 @@ dg_status dg_moe_route_backward(const void* logits, const int32_t* topk_ids, con
  *              gets c[t] (or 0). An id outside [-1, E) is taken as -1 and sets DG_ERR_BAD_INDEX on the device.
  *   c        : BF16 [T, H] addend (a shared expert's output, the residual) or NULL; may be y.
  *   y        : BF16 [T, H].
- * FP32 accumulation; the experts' inner values (weight * silu * up) are held as sums of three E4M3 terms
- * with a power-of-two scale per 64 columns: within 2^-12 of themselves, or 2^-27 of the largest of the 64.
+ * FP32 accumulation; the experts' inner values (weight * silu * up) are held as sums of four E4M3 terms
+ * with a power-of-two scale per 64 columns: within 2^-16 of themselves, 2^-29 of the largest of the 64, or
+ * 2^-136, whichever is most.
  * y is rounded once. The values of experts that a token does not name never reach it.
  * Limits: T <= 32, topk <= 16, E <= 1024, H and I <= 16384 (DG_ERR_UNSUPPORTED above); H and I positive
  * multiples of 128. Pointers 16-byte aligned (topk_ids, topk_weights: 4). Uses the stream's workspace.
