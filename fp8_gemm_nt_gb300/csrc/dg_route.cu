@@ -36,9 +36,10 @@ constexpr int kWarps = 8;               // rows per block
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 32;            // a lane of the warp holds a slot
 // Two rows a warp: for k that seldom leaves more than 16 candidates, few enough logits per lane to hold both rows, and
-// rows enough for half the warps to fill the SMs (256 FP32 logits, k = 8, two rows against one: 65536 rows 24.0 and
-// 29.1 us, 16384 rows 7.6 and 8.9, 4096 rows 3.7 and 3.8, 1024 rows 3.3 and 2.7; k = 12: 32.0 and 34.9, k = 16: 42.7
-// and 41.2; 512 logits: 36.8 and 38.5).
+// rows enough for half the warps to fill the SMs. Two rows against one, 256 FP32 logits, k = 8: 65536 rows 24.0 and
+// 29.1 us, 16384 rows 7.6 and 8.9, 4096 rows 3.7 and 3.8, 1024 rows 3.3 and 2.7; 65536 rows of k = 12: 32.0 and 34.9,
+// k = 16: 42.7 and 41.2; of 512 logits 36.8 and 38.5. The limits keep to where it gains a tenth or more, short of
+// where it begins to gain: at 4096 rows, k = 12 and 512 logits it would by 3 to 8 %, at 1024 rows and k = 16 it loses.
 constexpr int kPairTopk = 8, kPairLogits = 8, kPairRows = 8192;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
