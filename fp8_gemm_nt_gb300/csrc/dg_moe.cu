@@ -13,15 +13,16 @@
 // weights to shared memory and no instruction touches them on the way.
 //
 // An expert's tokens are compacted into jobs (of at most 16 in the first product, 8 in the second); each distinct
-// (expert, token) pair is a slot. The first kernel computes h = weight * silu(g) * u of every slot. The second product also
-// has to be E4M3 by the weights' type, and four bits would be too few: h is written as the sum of four E4M3 terms, each the
-// remainder of those before it times 16, under one power of two for each 64 columns that brings their largest to
-// (224, 448]. A term rounds to within 2^-4 of itself or 2^-10 of its scale, so h is within 2^-16 of itself or 2^-22 of
-// the scale, which is 2^-29.8 of the largest: with that y is as near to the exact sum as its rounding to BF16 lets it be
-// (a sum whose leading bits c cancels is 2^-18.5 off, 2^-16 with three terms, which are up to 4 % faster, with many tokens of few experts). The four
-// terms are four columns, whose scales are 16 times smaller each, and whose sums the second kernel adds up. It owns
-// output rows, sums all experts for 128 rows of W2 and every token in an order that depends on the sizes and the ids
-// alone, and writes each output once. No atomics on values.
+// (expert, token) pair is a slot. The first kernel computes h = weight * silu(g) * u of every slot. The second
+// product also has to be E4M3 by the weights' type, and four bits would be too few: h is written as the sum of four
+// E4M3 terms, each the remainder of those before it times 16, under one power of two for each 64 columns that brings
+// their largest to (224, 448]. A term rounds to within 2^-4 of itself or 2^-10 of its scale, so h is within 2^-16 of
+// itself or 2^-22 of the scale, which is 2^-29.8 of the largest: with that y is as near to the exact sum as its
+// rounding to BF16 lets it be (a sum whose leading bits c cancels is 2^-18.5 off, 2^-16 with three terms, which are
+// up to 4 % faster, with many tokens of few experts). The four terms are four columns, whose scales are 16 times
+// smaller each, and whose sums the second kernel adds up. It owns output rows, sums all experts for 128 rows of W2
+// and every token in an order that depends on the sizes and the ids alone, and writes each output once. No atomics on
+// values.
 //
 // A pipeline is a warp each for the weights' copies, the tokens' side, the weights' scales and the MMAs, and
 // four that read the sums from TMEM, with a ring of stages of 128 columns. A block (one to an SM) is two
@@ -34,8 +35,8 @@
 // in the order of the pipelines, so that the result does not depend on which one it was. Nobody waits.
 //
 // Bound by HBM, but for about 15 us at the ends (ids to the first weights, last sums of h to the second product,
-// joins). Experts of 7168 x 2048: E4M3, 32 tokens of 8 experts each among 64 (2.76 GB): 425 us, 6.5 TB/s; one token
-// (352 MB): 65 us; E2M1, 16 tokens among 32 (736 MB): 136 us. With mma.sync, whose E4M3 products are emulated by
+// joins). Experts of 7168 x 2048: E4M3, 32 tokens of 8 experts each among 64 (2.76 GB): 428 us, 6.4 TB/s; one token
+// (352 MB): 65 us; E2M1, 16 tokens among 32 (736 MB): 137 us. With mma.sync, whose E4M3 products are emulated by
 // FP16 ones, it was 464, 67 and 256 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
