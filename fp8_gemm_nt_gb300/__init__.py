@@ -66,6 +66,14 @@ SIGNATURES = [
     ("dg_last_cuda_error", _I, []),
     ("dg_set_debug", _I, [_I, ctypes.c_ulonglong]),
     ("dg_measure_fp8_mma_tflops", _I, [_I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+    ("dg_quantize_fp4", _I, [_P, _P, _P, _P, _P, _P]),
+    ("dg_swiglu_quantize_fp4", _I, [_P, _P, _P, _P, _P, _P]),
+    ("dg_swiglu_backward", _I, [_P, _P, _P, _P, _P, _P]),
+    ("dg_moe_balance_loss", _I, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    ("dg_moe_balance_loss_backward", _I, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    ("dg_fp4_gemm_nt", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    ("dg_m_grouped_fp4_gemm_nt_contiguous", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    ("dg_m_grouped_fp4_gemm_nt_masked", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     ("dg_fp8_gemm_nt_no_alloc", _I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
 ]
 
@@ -420,6 +428,15 @@ class _RouteDesc(ctypes.Structure):
                 ("renormalize", _I), ("scale", ctypes.c_float)]
 
 
+class _BalanceDesc(ctypes.Structure):
+    _fields_ = [("T", _I), ("E", _I), ("topk", _I), ("ld", ctypes.c_size_t), ("logits_type", _I), ("scoring", _I),
+                ("coef", ctypes.c_float)]
+
+
+class _RowsDesc(ctypes.Structure):
+    _fields_ = [("G", _I), ("M", _I), ("K", _I), ("ldx", ctypes.c_size_t), ("ldg", ctypes.c_size_t), ("x_type", _I)]
+
+
 # These calls are short (a few microseconds on the device), so their checks read each property of a
 # tensor once and build a message only where one fails, and a descriptor is built once for its values.
 
@@ -431,6 +448,16 @@ def _norm_desc(*values):
 @functools.lru_cache(maxsize=256)
 def _route_desc(*values):
     return ctypes.byref(_RouteDesc(*values))
+
+
+@functools.lru_cache(maxsize=256)
+def _balance_desc(*values):
+    return ctypes.byref(_BalanceDesc(*values))
+
+
+@functools.lru_cache(maxsize=256)
+def _rows_desc(*values):
+    return ctypes.byref(_RowsDesc(*values))
 
 
 def _device(t: torch.Tensor, name: str) -> int:
@@ -602,6 +629,164 @@ def dg_moe_fp8_fp4_few_tokens(x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights
     """dg_moe_fp8_few_tokens with the weights in packed E2M1: w13 [E, 2I, H/2] with sf13 [E, H/128, ceil4(2I)],
     w2 [E, H, I/2] with sf2 [E, I/128, ceil4(H)]."""
     return _few_tokens("dg_moe_fp8_fp4_few_tokens", True, x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights, c, y, stream)
+
+
+def _balance_args(logits, scoring, coef, topk):
+    dev = _device(logits, "logits")
+    T, E = shape = _two_d(logits, "logits")
+    p, ld = _rows(logits, "logits", _STREAM_DTYPES, shape, dev)
+    _need(scoring in _SCORING, "scoring must be softmax or sigmoid")
+    return dev, shape, p, _balance_desc(T, E, topk, ld, _TYPES[logits.dtype], _SCORING[scoring], coef)
+
+
+def dg_moe_balance_loss(logits, topk_ids, counts, live_rows, prob_mean, loss, scoring="softmax", coef=1.0, stream=None):
+    """Balance loss of a router: with p the probabilities of each row of logits [T, E] bf16 or float32 (rows may be
+    strided; -inf and NaN mask an expert; softmax, or sigmoids divided by their sum) and f the experts' shares of the
+    slots of topk_ids [T, k] int32, loss [1] float32 = coef * E * sum(f * mean of p over the live rows). Also writes
+    counts [E] int32 (slots per expert), live_rows [1] int32 and prob_mean [E] float32. Returns loss."""
+    k = _two_d(topk_ids, "topk_ids")[1]
+    dev, (T, E), p, desc = _balance_args(logits, scoring, coef, k)
+    pi = _arg(topk_ids, "topk_ids", _I32_ONLY, (T, k), dev)
+    pc = _arg(counts, "counts", _I32_ONLY, (E,), dev)
+    pl = _arg(live_rows, "live_rows", _I32_ONLY, (1,), dev)
+    pm = _arg(prob_mean, "prob_mean", _F32_ONLY, (E,), dev)
+    po = _arg(loss, "loss", _F32_ONLY, (1,), dev)
+    _check("dg_moe_balance_loss", (_lib or load_library()).dg_moe_balance_loss(p, pi, pc, pl, pm, po, desc, _stream_of(stream, dev)))
+    return loss
+
+
+def dg_moe_balance_loss_backward(logits, counts, live_rows, dloss, dlogits, base=None, scoring="softmax", coef=1.0,
+                                 stream=None) -> torch.Tensor:
+    """Gradient of dg_moe_balance_loss with respect to logits, plus `base`: dlogits [T, E] (contiguous, logits' type)
+    from the forward call's counts [E] and live_rows [1] and dloss [1] float32. base [T, E] of logits' type (the
+    gradient by other paths, or None) may be dlogits."""
+    dev, (T, E), p, desc = _balance_args(logits, scoring, coef, 1)
+    same = (logits.dtype,)
+    pc = _arg(counts, "counts", _I32_ONLY, (E,), dev)
+    pl = _arg(live_rows, "live_rows", _I32_ONLY, (1,), dev)
+    pd = _arg(dloss, "dloss", _F32_ONLY, (1,), dev)
+    pb = None if base is None else _arg(base, "base", same, (T, E), dev)
+    po = _arg(dlogits, "dlogits", same, (T, E), dev)
+    _check("dg_moe_balance_loss_backward",
+           (_lib or load_library()).dg_moe_balance_loss_backward(p, pc, pl, pd, pb, po, desc, _stream_of(stream, dev)))
+    return dlogits
+
+
+# --------------------------------------------------------------------------------------
+# FP4: quantisation of rows, and the GEMMs of two FP4 operands. Packed E2M1 and scales as above
+# --------------------------------------------------------------------------------------
+
+def _fp4_rows(x, per, dtypes, masked_m):
+    """Device, (groups or None, rows, result columns), pointers of x and masked_m, descriptor."""
+    dev = _device(x, "x")
+    shape = tuple(x.shape)
+    _need(len(shape) in (2, 3), "x must be [M, K] or [G, M, K]")
+    _need(x.dtype in dtypes, f"x must have type {' or '.join(str(d).replace('torch.', '') for d in dtypes)}")
+    _need(max(shape) <= _MAX_SIZE, f"x has a size above {_MAX_SIZE}: {shape}")
+    strides = x.stride()
+    _need(strides[-1] == 1 or shape[-1] == 1, "x must have contiguous columns")
+    _need(shape[-1] % (128 * per) == 0, f"x must have a multiple of {128 * per} columns")
+    M, K = shape[-2], shape[-1] // per
+    grouped = len(shape) == 3
+    G = shape[0] if grouped else 1
+    pm = None
+    if masked_m is not None:
+        _need(grouped, "masked_m needs x with groups, [G, M, K]")
+        pm = _arg(masked_m, "masked_m", _I32_ONLY, (G,), dev)
+    desc = _rows_desc(G, M, K, strides[-2] if M > 1 else shape[-1], strides[0] if grouped and G > 1 else 0, _TYPES[x.dtype])
+    return dev, (shape[:1] if grouped else ()), M, K, x.data_ptr(), pm, desc
+
+
+def _quantize(name, per, dtypes, x, q, sf, masked_m, stream):
+    dev, lead, M, K, px, pm, desc = _fp4_rows(x, per, dtypes, masked_m)
+    pq = _arg(q, "q", _FP4_DTYPES, (*lead, M, K // 2), dev)
+    ps = _arg(sf, "sf", _I32_ONLY, (*lead, K // 128, 4 * (-(-M // 4))), dev)
+    _check(name, getattr(_lib or load_library(), name)(px, pm, pq, ps, desc, _stream_of(stream, dev)))
+    return q, sf
+
+
+def dg_quantize_fp4(x, q, sf, masked_m=None, stream=None):
+    """Rows to FP4: x [M, K] or [G, M, K] bf16 or float32 (rows and groups may be strided) -> q [.., M, K/2] packed
+    E2M1 and sf [.., K/128, ceil4(M)] int32, one UE8M0 scale per row per 32 columns: the operands of the FP4 GEMMs and
+    the FP4 weights of the FP8 x FP4 ones. With masked_m [G] int32 on the device only the first masked_m[g] rows of each
+    group are read and written."""
+    return _quantize("dg_quantize_fp4", 1, _STREAM_DTYPES, x, q, sf, masked_m, stream)
+
+
+def dg_swiglu_quantize_fp4(x, q, sf, masked_m=None, stream=None):
+    """dg_quantize_fp4 of silu(gate) * up, for x [M, 2K] or [G, M, 2K] bf16 whose first K columns are the gate and
+    last K columns up."""
+    return _quantize("dg_swiglu_quantize_fp4", 2, _BF16_ONLY, x, q, sf, masked_m, stream)
+
+
+def dg_swiglu_backward(x, dy, dx, masked_m=None, stream=None) -> torch.Tensor:
+    """Gradient of silu(gate) * up: dx [.., M, 2K] bf16 from x [.., M, 2K] (gate | up; rows may be strided) and dy
+    [.., M, K] bf16. dx may be x where x is contiguous. Rows behind masked_m are not written."""
+    dev, lead, M, K, px, pm, desc = _fp4_rows(x, 2, _BF16_ONLY, masked_m)
+    pd = _arg(dy, "dy", _BF16_ONLY, (*lead, M, K), dev)
+    po = _arg(dx, "dx", _BF16_ONLY, (*lead, M, 2 * K), dev)
+    _check("dg_swiglu_backward", (_lib or load_library()).dg_swiglu_backward(px, pd, pm, po, desc, _stream_of(stream, dev)))
+    return dx
+
+
+def _sizes(*sizes):
+    for n in sizes:
+        _need(n <= _MAX_SIZE, f"a size is above {_MAX_SIZE}: {n}")
+
+
+def dg_fp4_gemm_nt(a, sfa, b, sfb, c, d, stream=None) -> torch.Tensor:
+    """D = C + A @ B.T of two FP4 operands. a [M, K/2] packed E2M1 with sfa [K/128, ceil4(M)] int32, b [N, K/2] with
+    sfb [K/128, ceil4(N)], c [M, N] bf16 or None (may be d), d [M, N] bf16 (written)."""
+    dev = _device(a, "a")
+    M, Kh = _two_d(a, "a")
+    N = _two_d(b, "b")[0]
+    _sizes(2 * Kh)
+    pa = _arg(a, "a", _FP4_DTYPES, (M, Kh), dev)
+    pb = _arg(b, "b", _FP4_DTYPES, (N, Kh), dev)
+    psa = _arg(sfa, "sfa", _I32_ONLY, sf_fp4_shape(M, 2 * Kh), dev)
+    psb = _arg(sfb, "sfb", _I32_ONLY, sf_fp4_shape(N, 2 * Kh), dev)
+    pc = None if c is None else _arg(c, "c", _BF16_ONLY, (M, N), dev)
+    pd = _arg(d, "d", _BF16_ONLY, (M, N), dev)
+    _check("dg_fp4_gemm_nt", (_lib or load_library()).dg_fp4_gemm_nt(pa, psa, pb, psb, pc, pd, M, N, 2 * Kh, _stream_of(stream, dev)))
+    return d
+
+
+def dg_m_grouped_fp4_gemm_nt_contiguous(a, sfa, b, sfb, d, m_indices, stream=None) -> torch.Tensor:
+    """Contiguous M-grouped FP4 GEMM: a [M_total, K/2] packed E2M1, sfa [K/128, ceil4(M_total)], b [G, N, K/2], sfb
+    [G, K/128, ceil4(N)], d [M_total, N] bf16, m_indices [M_total] int32 (-1 = pad)."""
+    dev = _device(a, "a")
+    M, Kh = _two_d(a, "a")
+    _need(b.dim() == 3, "b must be 3-D")
+    G, N = b.shape[:2]
+    _sizes(2 * Kh, G, N)
+    pa = _arg(a, "a", _FP4_DTYPES, (M, Kh), dev)
+    pb = _arg(b, "b", _FP4_DTYPES, (G, N, Kh), dev)
+    psa = _arg(sfa, "sfa", _I32_ONLY, sf_fp4_shape(M, 2 * Kh), dev)
+    psb = _arg(sfb, "sfb", _I32_ONLY, sf_fp4_shape(N, 2 * Kh, G), dev)
+    pd = _arg(d, "d", _BF16_ONLY, (M, N), dev)
+    pi = _arg(m_indices, "m_indices", _I32_ONLY, (M,), dev)
+    _check("dg_m_grouped_fp4_gemm_nt_contiguous",
+           (_lib or load_library()).dg_m_grouped_fp4_gemm_nt_contiguous(pa, psa, pb, psb, pd, pi, M, N, 2 * Kh, G, _stream_of(stream, dev)))
+    return d
+
+
+def dg_m_grouped_fp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, stream=None) -> torch.Tensor:
+    """Masked M-grouped FP4 GEMM: a [G, max_m, K/2] packed E2M1, sfa [G, K/128, ceil4(max_m)], b [G, N, K/2], sfb
+    [G, K/128, ceil4(N)], d [G, max_m, N] bf16, masked_m [G] int32 on the device."""
+    dev = _device(a, "a")
+    _need(a.dim() == 3 and b.dim() == 3, "a and b must be 3-D")
+    G, max_m, Kh = a.shape
+    N = b.shape[1]
+    _sizes(2 * Kh, G, N, max_m)
+    pa = _arg(a, "a", _FP4_DTYPES, (G, max_m, Kh), dev)
+    pb = _arg(b, "b", _FP4_DTYPES, (G, N, Kh), dev)
+    psa = _arg(sfa, "sfa", _I32_ONLY, sf_fp4_shape(max_m, 2 * Kh, G), dev)
+    psb = _arg(sfb, "sfb", _I32_ONLY, sf_fp4_shape(N, 2 * Kh, G), dev)
+    pd = _arg(d, "d", _BF16_ONLY, (G, max_m, N), dev)
+    pm = _arg(masked_m, "masked_m", _I32_ONLY, (G,), dev)
+    _check("dg_m_grouped_fp4_gemm_nt_masked",
+           (_lib or load_library()).dg_m_grouped_fp4_gemm_nt_masked(pa, psa, pb, psb, pd, pm, G, max_m, N, 2 * Kh, _stream_of(stream, dev)))
+    return d
 
 
 def dg_get_mk_alignment_for_contiguous_layout() -> int:

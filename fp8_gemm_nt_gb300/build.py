@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdg.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("dg_api.cu", "dg_no_alloc.cu", "dg_diag.cu", "dg_norm.cu", "dg_route.cu", "dg_moe.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("dg_api.cu", "dg_no_alloc.cu", "dg_diag.cu", "dg_norm.cu", "dg_route.cu", "dg_moe.cu",
+                                            "dg_quantize.cu", "dg_balance.cu", "dg_fp4.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

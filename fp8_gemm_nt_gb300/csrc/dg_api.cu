@@ -993,6 +993,11 @@ bool weight_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box, CUtensorMapSwizzle swizzle) {
+  return make_map(map, type, rank, base, dims, strides, box, swizzle);
+}
+
 dg_status StreamWorkspace::acquire(cudaStream_t stream, size_t bytes, void** out) {
   DeviceState* ds = nullptr;
   if (dg_status s = device_state(&ds); s != DG_OK) return s;

@@ -1,0 +1,318 @@
+// Balance loss of a mixture of experts' router with its counts per expert, and its gradient.
+//
+//   p = softmax over a row's experts that are not masked, of x or of log sigmoid(x)
+//   f = counts / sum of counts,   P = mean of p over the live rows,   loss = coef E sum f P
+//   dloss/dx_e = coef E / live p_e (f_e - sum_j p_j f_j), with sigmoid scores times 1 - sigmoid(x_e)
+//
+// A warp takes rows in turn, the next row's loads in flight while it works on one, and keeps its sums over rows (or
+// f, the same for every row) in registers. Sums are joined per block, then over the blocks by the last one to finish,
+// in a fixed order; the counts are integers, whose atomics have no order to keep.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "dg.h"
+#include "logit_rows.cuh"
+#include "ptx.cuh"
+#include "runtime.h"
+#include "ue8m0.cuh"
+
+namespace {
+
+using namespace dg::rows;
+using dg::LaunchContext;
+
+// Warps of a block: 16, or 8 where a lane holds 16 or 32 logits, which takes more registers than 16 warps leave it.
+template <int P>
+constexpr int kWarpsOf = P >= 16 ? 8 : 16;
+constexpr int kMaxExperts = 1024, kMaxTopk = 32;
+
+// Scores of a row up to a common factor, and the factor that makes them add up to one (0 for a row without any).
+// Sigmoids are taken relative to the largest where all are small, which keeps them from underflowing together:
+// sigmoid(x) / sigmoid(top) is exp(x - top) / (1 + exp(x)) but for a factor that the row has in common.
+template <int P>
+__device__ __forceinline__ float scores(const float (&x)[P], bool sig, float (&p)[P], bool* live) {
+  float clean[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) clean[i] = fmaxf(x[i], -INFINITY);            // NaN is masked as -inf is
+  const float top = warp_max(max_of(clean)), base = top > -INFINITY ? top : 0.0f;
+  float total = 0;
+  if (sig) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = base > 0 ? sigmoid(clean[i]) : expf(clean[i] - base) / (1.0f + expf(clean[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = expf(clean[i] - base);
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) total += p[i];
+  total = warp_sum(total);
+  *live = top > -INFINITY;
+  return *live ? 1.0f / total : 0.0f;
+}
+
+template <class L>
+struct BalanceArgs {
+  const L* logits;
+  const int32_t* ids;
+  int32_t* counts;
+  int32_t* live_rows;
+  float* prob_mean;
+  float* loss;
+  float* partial;       // [blocks][E]
+  int* counters;        // blocks that have finished, live rows, and from kCountsAt on the counts; zero between launches
+  uint32_t* status;
+  int T, E, slots;
+  size_t ld;
+  int sigmoid;
+  float coef;
+};
+constexpr int kCountsAt = 64;
+
+template <class L, int J, int kVec>
+__global__ void __launch_bounds__(kWarpsOf<J * kVec> * 32, 1) balance_kernel(const BalanceArgs<L> a) {
+  using At = Lane<L, J, kVec>;
+  constexpr int P = At::kCount, kWarps = kWarpsOf<P>;
+  extern __shared__ float sums[];                           // [kWarps][E], then [E] counts
+  int* const hist = reinterpret_cast<int*>(sums + kWarps * a.E);
+  __shared__ int live_warps[kWarps];
+  __shared__ float joined[kWarps];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  for (int e = threadIdx.x; e < a.E; e += kWarps * 32) hist[e] = 0;
+  __syncthreads();
+  dg::grid_dependency_wait();
+  dg::grid_launch_dependents();
+
+  const long long step = static_cast<long long>(gridDim.x) * kWarps;
+  long long t = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  float next[P], acc[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) acc[i] = 0;
+  if (t < a.T) At::load(a.logits + t * a.ld, lane, a.E, next);
+  // the block's share of the slots, while the first rows arrive
+  for (long long s = static_cast<long long>(blockIdx.x) * (kWarps * 32) + threadIdx.x; s < a.slots; s += step * 32) {
+    const int id = __ldcg(a.ids + s);
+    if (id >= 0 && id < a.E)
+      atomicAdd(hist + id, 1);
+    else if (id != -1)
+      atomicOr(a.status, dg::kBadIndexBit);
+  }
+  int rows = 0;
+  while (t < a.T) {
+    float x[P], p[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = next[i];
+    t += step;
+    if (t < a.T) At::load(a.logits + t * a.ld, lane, a.E, next);
+    bool live;
+    const float by = scores(x, a.sigmoid, p, &live);
+    rows += live;
+#pragma unroll
+    for (int i = 0; i < P; ++i) acc[i] += p[i] * by;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int e = At::index(lane, i);
+    if (e < a.E) sums[warp * a.E + e] = acc[i];
+  }
+  if (lane == 0) live_warps[warp] = rows;
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kWarps * 32) {
+    float s = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += sums[w * a.E + e];
+    a.partial[static_cast<size_t>(blockIdx.x) * a.E + e] = s;
+    if (hist[e] > 0) atomicAdd(a.counters + kCountsAt + e, hist[e]);
+  }
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int w = 0; w < kWarps; ++w) n += live_warps[w];
+    if (n > 0) atomicAdd(a.counters + 1, n);
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.counters, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+
+  const int live = __ldcg(a.counters + 1);
+  const float inv = 1.0f / static_cast<float>(max(live, 1));
+  float inner = 0;
+  int total = 0;
+  for (int e = threadIdx.x; e < a.E; e += kWarps * 32) {
+    float s = 0;
+    for (unsigned b = 0; b < gridDim.x; ++b) s += __ldcg(a.partial + static_cast<size_t>(b) * a.E + e);
+    const int c = __ldcg(a.counters + kCountsAt + e);
+    a.counters[kCountsAt + e] = 0;
+    a.counts[e] = c;
+    a.prob_mean[e] = s * inv;
+    inner += static_cast<float>(c) * (s * inv);
+    total += c;
+  }
+  inner = warp_sum(inner);
+  total = __reduce_add_sync(kAll, total);
+  if (lane == 0) joined[warp] = inner, live_warps[warp] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0;
+    int c = 0;
+    for (int w = 0; w < kWarps; ++w) s += joined[w], c += live_warps[w];
+    *a.live_rows = live;
+    *a.loss = a.coef * static_cast<float>(a.E) * (s / static_cast<float>(max(c, 1)));
+    a.counters[0] = a.counters[1] = 0;
+  }
+}
+
+template <class L>
+struct BalanceGradArgs {
+  const L* logits;
+  const int32_t* counts;
+  const int32_t* live_rows;
+  const float* dloss;
+  const L* base;
+  L* dlogits;
+  int T, E;
+  size_t ld;
+  int sigmoid;
+  float coef;
+};
+
+template <class L, int J, int kVec>
+__global__ void __launch_bounds__(kWarpsOf<J * kVec> * 32, 1) balance_grad_kernel(const BalanceGradArgs<L> a) {
+  using At = Lane<L, J, kVec>;
+  constexpr int P = At::kCount, kWarps = kWarpsOf<P>;
+  dg::grid_dependency_wait();
+  dg::grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long step = static_cast<long long>(gridDim.x) * kWarps;
+  long long t = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
+  if (t >= a.T) return;
+  float next[P], add[P], f[P];
+  At::load(a.logits + t * a.ld, lane, a.E, next);
+  if (a.base) At::load(a.base + t * a.E, lane, a.E, add);
+  long long total = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int e = At::index(lane, i), c = e < a.E ? max(__ldcg(a.counts + e), 0) : 0;
+    total += c;
+    f[i] = static_cast<float>(c);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  const float inv = 1.0f / static_cast<float>(total > 1 ? total : 1);
+#pragma unroll
+  for (int i = 0; i < P; ++i) f[i] *= inv;
+  const float scale = __ldcg(a.dloss) * (a.coef * static_cast<float>(a.E)) / static_cast<float>(max(__ldcg(a.live_rows), 1));
+  while (t < a.T) {
+    float x[P], p[P], d[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = next[i], d[i] = a.base ? add[i] : 0.0f;
+    L* const to = a.dlogits + t * a.E;
+    t += step;
+    if (t < a.T) {
+      At::load(a.logits + t * a.ld, lane, a.E, next);
+      if (a.base) At::load(a.base + t * a.E, lane, a.E, add);
+    }
+    bool live;
+    const float by = scores(x, a.sigmoid, p, &live);
+    float inner = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) inner += p[i] * f[i];
+    inner = warp_sum(inner) * by;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float g = scale * by * p[i] * (f[i] - inner);
+      if (a.sigmoid) g *= 1.0f / (1.0f + expf(x[i]));      // 1 - sigmoid, without the cancellation
+      if (x[i] > -INFINITY) d[i] += g;
+    }
+    At::store(to, lane, a.E, d);
+  }
+}
+
+size_t row_stride(const dg_balance_desc& d) { return d.T > 1 ? d.ld : static_cast<size_t>(d.E); }
+
+dg_status check(const void* logits, const dg_balance_desc* desc) {
+  if (!desc) return DG_ERR_INVALID_ARG;
+  if (desc->T < 0 || desc->E <= 0 || row_stride(*desc) < static_cast<size_t>(desc->E)) return DG_ERR_INVALID_ARG;
+  if (desc->logits_type != DG_BF16 && desc->logits_type != DG_F32) return DG_ERR_INVALID_ARG;
+  if ((desc->scoring != DG_ROUTE_SOFTMAX && desc->scoring != DG_ROUTE_SIGMOID) || !std::isfinite(desc->coef)) return DG_ERR_INVALID_ARG;
+  if (desc->E > kMaxExperts) return DG_ERR_UNSUPPORTED;
+  if (desc->T == 0) return DG_OK;
+  if (!logits) return DG_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(logits) & (desc->logits_type == DG_BF16 ? 1 : 3) ? DG_ERR_MISALIGNED : DG_OK;
+}
+bool words(std::initializer_list<const void*> all) {
+  uintptr_t any = 0;
+  for (const void* p : all) any |= reinterpret_cast<uintptr_t>(p);
+  return (any & 3u) == 0;
+}
+
+// Blocks whose warps take a row at a time, `most` at most.
+unsigned blocks_for(int T, int warps, int most) {
+  return static_cast<unsigned>(std::max(1, std::min(T / warps + (T % warps != 0), most)));
+}
+
+}  // namespace
+
+extern "C" {
+
+dg_status dg_moe_balance_loss(const void* logits, const int32_t* topk_ids, int32_t* counts, int32_t* live_rows, float* prob_mean,
+                              float* loss, const dg_balance_desc* desc, cudaStream_t stream) {
+  if (dg_status s = check(logits, desc); s != DG_OK) return s;
+  if (desc->topk <= 0 || !counts || !live_rows || !prob_mean || !loss || (desc->T > 0 && !topk_ids)) return DG_ERR_INVALID_ARG;
+  if (desc->topk > kMaxTopk || static_cast<long long>(desc->T) * desc->topk > 0x7FFFFFFFll) return DG_ERR_UNSUPPORTED;
+  if (!words({topk_ids, counts, live_rows, prob_mean, loss})) return DG_ERR_MISALIGNED;
+  LaunchContext ctx;
+  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+  const size_t ld = row_stride(*desc);
+  dg::StreamWorkspace ws;
+  void* scratch = nullptr;
+  if (dg_status s = ws.acquire(stream, static_cast<size_t>(ctx.sms) * desc->E * sizeof(float), &scratch); s != DG_OK) return s;
+  auto run = [&](auto* type) {
+    using L = std::remove_pointer_t<decltype(type)>;
+    const BalanceArgs<L> a{static_cast<const L*>(logits), topk_ids, counts, live_rows, prob_mean, loss, static_cast<float*>(scratch),
+                           ws.counters(), ctx.status, desc->T, desc->E, desc->T * desc->topk, ld, desc->scoring == DG_ROUTE_SIGMOID, desc->coef};
+    return with_shape<L>(desc->E, whole_pieces<L>(logits, ld, desc->E), [&](auto j, auto vec) {
+      constexpr int kWarps = kWarpsOf<decltype(j)::value * decltype(vec)::value>;
+      const size_t smem = static_cast<size_t>(kWarps + 1) * desc->E * sizeof(float);
+      auto kernel = balance_kernel<L, decltype(j)::value, decltype(vec)::value>;
+      if (smem > 48 * 1024)
+        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)); e != cudaSuccess)
+          return dg::record_cuda_error(e);
+      return dg::launch(kernel, blocks_for(desc->T, kWarps, ctx.sms), kWarps * 32, smem, stream, ctx.pdl, a);
+    });
+  };
+  return desc->logits_type == DG_BF16 ? run(static_cast<__nv_bfloat16*>(nullptr)) : run(static_cast<float*>(nullptr));
+}
+
+dg_status dg_moe_balance_loss_backward(const void* logits, const int32_t* counts, const int32_t* live_rows, const float* dloss,
+                                       const void* base, void* dlogits, const dg_balance_desc* desc, cudaStream_t stream) {
+  if (dg_status s = check(logits, desc); s != DG_OK) return s;
+  if (desc->T == 0) return DG_OK;
+  if (!counts || !live_rows || !dloss || !dlogits) return DG_ERR_INVALID_ARG;
+  const uintptr_t of = desc->logits_type == DG_BF16 ? 1 : 3;
+  if (!words({counts, live_rows, dloss}) || ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(dlogits)) & of))
+    return DG_ERR_MISALIGNED;
+  LaunchContext ctx;
+  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+  const size_t ld = row_stride(*desc);
+  auto run = [&](auto* type) {
+    using L = std::remove_pointer_t<decltype(type)>;
+    const BalanceGradArgs<L> a{static_cast<const L*>(logits), counts, live_rows, dloss, static_cast<const L*>(base), static_cast<L*>(dlogits),
+                               desc->T, desc->E, ld, desc->scoring == DG_ROUTE_SIGMOID, desc->coef};
+    const bool aligned = whole_pieces<L>(logits, ld, desc->E) && whole_pieces<L>(dlogits, desc->E, desc->E) && whole_pieces<L>(base, desc->E, desc->E);
+    return with_shape<L>(desc->E, aligned, [&](auto j, auto vec) {
+      constexpr int kWarps = kWarpsOf<decltype(j)::value * decltype(vec)::value>;
+      return dg::launch(balance_grad_kernel<L, decltype(j)::value, decltype(vec)::value>, blocks_for(desc->T, kWarps, 2 * ctx.sms), kWarps * 32, 0,
+                        stream, ctx.pdl, a);
+    });
+  };
+  return desc->logits_type == DG_BF16 ? run(static_cast<__nv_bfloat16*>(nullptr)) : run(static_cast<float*>(nullptr));
+}
+
+}  // extern "C"

@@ -1,0 +1,190 @@
+// Host side of the FP4 x FP4 GEMMs: checks, tensor maps, choice of kernel and launch. The kernels are in fp4_gemm.cuh.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "debug_state.h"
+#include "dg.h"
+#include "fp4_gemm.cuh"
+#include "pair_list.cuh"
+#include "runtime.h"
+
+namespace {
+
+using dg::LaunchContext;
+using dg::fp4::Form;
+using dg::fp4::Params;
+using dg::fp4::up;
+
+constexpr int kRowBox = dg::fp4::kRows;
+constexpr int kMaxSize = 1 << 30;          // of a row count, N or K
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+// Packed codes [G, rows, K / 2], in boxes of 128 bytes of box_rows rows.
+bool codes_map(CUtensorMap* m, const void* base, int G, int rows, int K, int box_rows) {
+  const uint64_t bytes = static_cast<uint64_t>(K) / 2;
+  const uint64_t dims[3] = {bytes, static_cast<uint64_t>(rows), static_cast<uint64_t>(G)}, strides[2] = {bytes, bytes * rows};
+  const uint32_t box[3] = {128, static_cast<uint32_t>(box_rows), 1};
+  return dg::tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Scale words [G, K / 128, ceil4(rows)], in boxes of box_rows rows' two words.
+bool scales_map(CUtensorMap* m, const int32_t* base, int G, int rows, int K, int box_rows) {
+  const uint64_t w = 4 * ((static_cast<uint64_t>(rows) + 3) / 4), k = static_cast<uint64_t>(K) / 128;
+  const uint64_t dims[3] = {w, k, static_cast<uint64_t>(G)}, strides[2] = {4 * w, 4 * w * k};
+  const uint32_t box[3] = {static_cast<uint32_t>(box_rows), 2, 1};
+  return dg::tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+struct Operands {
+  const void* a;
+  const int32_t* sfa;
+  const void* b;
+  const int32_t* sfb;
+};
+
+template <class Kernel, class... More>
+dg_status launch(Kernel kernel, int smem, int grid, int threads, int cluster, cudaStream_t stream, bool pdl, const CUtensorMap& ta,
+                 const CUtensorMap& tb, const CUtensorMap& tsa, const CUtensorMap& tsb, const Params& p, More... more) {
+  // (set per device; a call costs less than a microsecond)
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e != cudaSuccess)
+    return dg::record_cuda_error(e);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, tsa, tsb, p, more...);
+  return e == cudaSuccess ? DG_OK : dg::record_cuda_error(e);
+}
+
+// pair_rows: 256-row strips of all groups, or a bound of their number.
+template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
+dg_status run_pair(const LaunchContext& ctx, const Operands& o, const Params& p, long long pair_rows, cudaStream_t stream) {
+  using S = dg::fp4::PairShape<BN, kAccum, kStages>;
+  const int ga = kForm == Form::Masked ? p.G : 1, gb = kForm == Form::Dense ? 1 : p.G;
+  CUtensorMap ta, tb, tsa, tsb;
+  if (!codes_map(&ta, o.a, ga, p.M, p.K, kRowBox) || !codes_map(&tb, o.b, gb, p.N, p.K, BN / 2) || !scales_map(&tsa, o.sfa, ga, p.M, p.K, kRowBox) ||
+      !scales_map(&tsb, o.sfb, gb, p.N, p.K, 128 * S::kChunks))
+    return DG_ERR_CUDA;
+  const long long tiles = pair_rows * up(p.N, BN);
+  if (tiles > (1ll << 30)) return DG_ERR_UNSUPPORTED;
+  const int clusters = static_cast<int>(std::min<long long>(std::max(1, ctx.sms / 2), tiles));
+  return launch(dg::fp4::fp4_pair_kernel<kForm, BN, kAccum, kStages, kHasC>, S::smem(kForm), 2 * clusters, S::kThreads, 2, stream, ctx.pdl, ta, tb,
+                tsa, tsb, p);
+}
+
+template <int BN, int kStages, bool kHasC>
+dg_status run_split(const LaunchContext& ctx, const Operands& o, Params p, int ways, cudaStream_t stream) {
+  using S = dg::fp4::SplitShape<BN, kStages>;
+  // no more rows of A than there are, in whole swizzle atoms of eight
+  const int rows = std::min(kRowBox, 8 * up(std::min(p.M, kRowBox), 8));
+  p.a_bytes = static_cast<uint32_t>(rows) * 128;
+  CUtensorMap ta, tb, tsa, tsb;
+  if (!codes_map(&ta, o.a, 1, p.M, p.K, rows) || !codes_map(&tb, o.b, 1, p.N, p.K, BN) || !scales_map(&tsa, o.sfa, 1, p.M, p.K, kRowBox) ||
+      !scales_map(&tsb, o.sfb, 1, p.N, p.K, 128 * S::kChunks))
+    return DG_ERR_CUDA;
+  const long long grid = static_cast<long long>(up(p.M, kRowBox)) * up(p.N, BN) * ways;
+  if (grid > (1ll << 30)) return DG_ERR_UNSUPPORTED;
+  return launch(dg::fp4::fp4_split_kernel<BN, kStages, kHasC>, S::SMEM, static_cast<int>(grid), S::kThreads, ways, stream, ctx.pdl, ta, tb, tsa, tsb, p,
+                ways);
+}
+
+// rows: of A, in each group.
+dg_status check(const Operands& o, const void* c, const void* d, int rows, int N, int K) {
+  if (rows < 0 || K <= 0 || K % 128 != 0 || N <= 0 || N % 16 != 0) return DG_ERR_INVALID_ARG;
+  if (rows > kMaxSize || N > kMaxSize || K > kMaxSize) return DG_ERR_UNSUPPORTED;
+  if (rows == 0) return DG_OK;
+  if (!o.a || !o.sfa || !o.b || !o.sfb || !d) return DG_ERR_INVALID_ARG;
+  if (misaligned(o.a, 16) || misaligned(o.sfa, 16) || misaligned(o.b, 16) || misaligned(o.sfb, 16) || misaligned(c, 16) || misaligned(d, 16))
+    return DG_ERR_MISALIGNED;
+  return DG_OK;
+}
+
+Params params(const LaunchContext& ctx, const void* c, void* d, int M, int N, int K, int G) {
+  Params p{};
+  p.M = M, p.N = N, p.K = K, p.G = G;
+  p.c = static_cast<const __nv_bfloat16*>(c), p.d = static_cast<__nv_bfloat16*>(d);
+  p.wide = !misaligned(d, 32);
+  p.status = ctx.status, p.timeout_ns = dg::pipeline_wait_timeout_ns(), p.fault = dg::debug_fault_mode();
+  return p;
+}
+
+__global__ void __launch_bounds__(256) pair_list_kernel(const dg::PairListArgs a) {
+  dg::grid_dependency_wait();
+  dg::grid_launch_dependents();
+  dg::build_pair_list(a);
+}
+
+template <bool kHasC>
+dg_status dense(const LaunchContext& ctx, const Operands& o, const Params& p, cudaStream_t stream) {
+  const long long pair_tiles = static_cast<long long>(up(p.M, 256)) * up(p.N, 256);
+  if (p.M > 128 && pair_tiles * 4 >= ctx.sms) return run_pair<Form::Dense, 256, 1, 6, kHasC>(ctx, o, p, up(p.M, 256), stream);
+  const int stages = up(p.K, dg::fp4::kStageK);
+  const long long tiles = static_cast<long long>(up(p.M, 128)) * up(p.N, 128);
+  int ways = 1;
+  while (ways < 8 && tiles * ways * 2 <= ctx.sms && 2 * ways <= stages) ways *= 2;
+  return run_split<128, 6, kHasC>(ctx, o, p, ways, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+dg_status dg_fp4_gemm_nt(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, const void* c, void* d, int M, int N, int K,
+                         cudaStream_t stream) {
+  const Operands o{a, sfa, b, sfb};
+  if (dg_status s = check(o, c, d, M, N, K); s != DG_OK || M == 0) return s;
+  LaunchContext ctx;
+  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+  const Params p = params(ctx, c, d, M, N, K, 1);
+  return c ? dense<true>(ctx, o, p, stream) : dense<false>(ctx, o, p, stream);
+}
+
+dg_status dg_m_grouped_fp4_gemm_nt_contiguous(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, void* d,
+                                              const int32_t* m_indices, int M_total, int N, int K, int G, cudaStream_t stream) {
+  const Operands o{a, sfa, b, sfb};
+  if (G <= 0) return DG_ERR_INVALID_ARG;
+  if (dg_status s = check(o, nullptr, d, M_total, N, K); s != DG_OK || M_total == 0) return s;
+  if (!m_indices) return DG_ERR_INVALID_ARG;
+  if (misaligned(m_indices, 4)) return DG_ERR_MISALIGNED;
+  LaunchContext ctx;
+  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+  Params p = params(ctx, nullptr, d, M_total, N, K, G);
+  const int blocks = up(M_total, kRowBox);
+  dg::StreamWorkspace ws;
+  void* scratch = nullptr;
+  if (dg_status s = ws.acquire(stream, (4 + 3 * static_cast<size_t>(blocks)) * sizeof(int), &scratch); s != DG_OK) return s;
+  dg::PairListArgs list{};
+  list.m_indices = m_indices, list.num_mb = blocks, list.groups_g = G, list.status = ctx.status;
+  list.pair_count = static_cast<int*>(scratch), list.pair_list = list.pair_count + 4;
+  if (dg_status s = dg::launch(pair_list_kernel, 1, 256, 0, stream, ctx.pdl, list); s != DG_OK) return s;
+  p.m_indices = m_indices, p.pair_count = list.pair_count, p.pair_list = list.pair_list;
+  return run_pair<Form::Contiguous, 256, 1, 6, false>(ctx, o, p, blocks, stream);
+}
+
+dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, void* d, const int32_t* masked_m,
+                                          int G, int max_m, int N, int K, cudaStream_t stream) {
+  const Operands o{a, sfa, b, sfb};
+  if (G <= 0) return DG_ERR_INVALID_ARG;
+  if (dg_status s = check(o, nullptr, d, max_m, N, K); s != DG_OK || max_m == 0) return s;
+  if (!masked_m) return DG_ERR_INVALID_ARG;
+  if (misaligned(masked_m, 4)) return DG_ERR_MISALIGNED;
+  LaunchContext ctx;
+  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+  Params p = params(ctx, nullptr, d, max_m, N, K, G);
+  p.masked_m = masked_m;
+  return run_pair<Form::Masked, 256, 1, 6, false>(ctx, o, p, static_cast<long long>(G) * up(max_m, 256), stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,680 @@
+// Products of two FP4 operands for sm_103a: D = C + A @ B.T with A and B in packed E2M1, one UE8M0 scale per row per
+// 32 K, on block-scaled tcgen05.mma.kind::mxf4 (K = 64 an instruction, FP32 accumulation in TMEM).
+//
+// A pipeline stage holds 256 K: rows of 128 bytes in the 128-byte swizzle, and two packed scale words per row. The MMA
+// reads the scales of 128 rows from four TMEM columns, row r's word in lane r % 32 of column r / 32, so a warp turns
+// every 128 words as they were loaded into that order in shared memory before tcgen05.cp takes them.
+//
+// Two kernels: fp4_pair_kernel, persistent, a CTA pair to a 256 x BN tile (many rows, and the grouped forms), and
+// fp4_split_kernel, a 128 x BN tile to a cluster whose CTAs share out K (few tiles).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "ue8m0.cuh"
+
+namespace dg {
+namespace fp4 {
+
+enum class Form { Dense, Contiguous, Masked };
+
+constexpr int kRows = 128;                 // rows of A of a CTA
+constexpr int kStageK = 256;               // K of a stage: 128 bytes of a row, two scale words
+constexpr int kCountCache = 1024;          // masked form: counts held in shared memory (more are read at L2)
+constexpr unsigned long long kDrainNs = 50000000ull;
+enum : int { kFaultProducerSilent = 1 };
+
+struct Params {
+  int M, N, K, G;                          // M: rows of A, of each group in the masked form
+  const int32_t* m_indices;                // contiguous form
+  const int32_t* masked_m;                 // masked form
+  const int* pair_list;                    // contiguous form: first block, expert and own blocks of every pair row
+  const int* pair_count;
+  const __nv_bfloat16* c;
+  __nv_bfloat16* d;
+  int wide;                                // d is 32-byte aligned
+  uint32_t a_bytes;                        // split kernel: bytes of A that a stage loads
+  uint32_t* status;
+  unsigned long long timeout_ns;
+  int fault;
+};
+
+__host__ __device__ constexpr int up(int a, int b) { return (a + b - 1) / b; }
+
+// Instruction descriptor of kind::mxf4: A and B E2M1 (1 in bits 7 and 10), N / 8 in bits 17 on, UE8M0 scales (bit 23),
+// M / 128 in bits 27 on; bits 4 and 29 take the first of the two scale bytes (0 or 2) that B and A use of their words.
+__host__ __device__ constexpr uint32_t instruction(uint32_t M, uint32_t N) {
+  return 1u << 7 | 1u << 10 | (N >> 3) << 17 | 1u << 23 | (M >> 7) << 27;
+}
+
+template <bool kPair>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+
+// mbar_wait that also sees what threads of other CTAs of the cluster wrote before they arrived.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+  if (!mbar_wait(bar, parity, timeout_ns)) return false;
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return true;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, volatile uint32_t* abort_flag) {
+  return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(bar, parity, timeout_ns));
+}
+
+// Turns kChunks x 128 scale words from the order of their rows into the order of tcgen05.cp, in place, by a warp: the
+// words of rows l, l + 32, l + 64 and l + 96 to the 16 bytes of lane l.
+template <int kChunks>
+__device__ __forceinline__ void arrange_scales(uint32_t at, uint32_t lane) {
+  uint32_t w[kChunks][4];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[c][i] = ld_shared_u32(at + 512 * c + 4 * (lane + 32 * i));
+  }
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) st_shared_v4(at + 512 * c + 16 * lane, w[c][0], w[c][1], w[c][2], w[c][3]);
+}
+
+// Sixteen columns of a row of D: v, and C's where there is one, rounded to BF16.
+template <bool kHasC>
+__device__ __forceinline__ void store_columns(const Params& p, size_t at, const uint32_t* bits) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(bits[i]);
+  uint32_t w[8];
+  if constexpr (kHasC) {
+    const uint4 lo = ld_cg_v4(p.c + at), hi = ld_cg_v4(p.c + at + 8);
+    const uint32_t cw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      unpack_bf16(cw[i], a, b);
+      w[i] = pack_bf16(a + v[2 * i], b + v[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  }
+  __nv_bfloat16* const d = p.d + at;
+  if (p.wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    st_global_v4(d, w[0], w[1], w[2], w[3]);
+    st_global_v4(d + 8, w[4], w[5], w[6], w[7]);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// CTA pairs
+// ------------------------------------------------------------------------------------
+template <int kBN, int kAccums, int kStages_>
+struct PairShape {
+  static constexpr int BN = kBN, kAccum = kAccums, kStages = kStages_;
+  static constexpr int kEpilogueWarps = 8, kThreads = (4 + kEpilogueWarps) * 32;
+  static constexpr int kChunks = up(BN, 128);                       // 128-row chunks of B's scale words
+  static constexpr int A_BYTES = kRows * 128, B_BYTES = BN / 2 * 128;
+  static constexpr int SFA_BYTES = 2 * 512, SFB_BYTES = 2 * kChunks * 512, SF_BYTES = SFA_BYTES + SFB_BYTES;
+  static constexpr int OFF_B = kStages * A_BYTES, OFF_SF = OFF_B + kStages * B_BYTES, OFF_BAR = OFF_SF + kStages * SF_BYTES;
+  // TMEM: the accumulators, then a buffer of scales for each stage, or for as many as there are columns for
+  static constexpr int kSfCols = 8 + 8 * kChunks;
+  static constexpr int kSfFit = (512 - kAccum * BN) / kSfCols, kSfBufs = kSfFit < kStages ? kSfFit : kStages;
+  static_assert(kSfBufs >= 2 && B_BYTES % 1024 == 0 && BN % 32 == 0, "tile width");
+  static constexpr int kBars = 5 * kStages + 2 * kAccum + kSfBufs + 2;
+  static constexpr int OFF_COUNTS = OFF_BAR + kBars * 8 + 16;
+  static constexpr int smem(Form f) { return OFF_COUNTS + (f == Form::Masked ? kCountCache * 4 : 0) + 1024; }
+};
+
+// A tile: the pair's rows from m0 in its group's rows of A, `valid` of them (may be more than the tile has); its columns
+// from n0; the group of A and D, and of B.
+struct Tile {
+  int m0, valid, n0, ga, gb;
+};
+
+// The tiles of cluster `t`, t + step, ...: every role of a CTA walks the same ones.
+template <Form kForm, int BN>
+struct Walk {
+  int t, step, total, num_n;
+  int g = 0, first = 0, tiles = 0;         // masked form: the group that t is in, its first tile and its tiles
+  const int* counts;
+
+  __device__ __forceinline__ Walk(const Params& p, const int* counts_) : counts(counts_) {
+    t = blockIdx.x / 2;
+    step = gridDim.x / 2;
+    num_n = up(p.N, BN);
+    total = kForm == Form::Dense ? up(p.M, 2 * kRows) * num_n : kForm == Form::Contiguous ? ld_cg_s32(p.pair_count) * num_n : 0;
+    if (kForm == Form::Masked) tiles = tiles_of(p, 0);
+  }
+  __device__ __forceinline__ int count(const Params& p, int group) const {
+    return group < kCountCache ? counts[group] : min(max(ld_cg_s32(p.masked_m + group), 0), p.M);
+  }
+  __device__ __forceinline__ int tiles_of(const Params& p, int group) const { return up(count(p, group), 2 * kRows) * num_n; }
+
+  __device__ __forceinline__ bool next(const Params& p, Tile& s) {
+    if constexpr (kForm == Form::Masked) {
+      while (t - first >= tiles) {
+        first += tiles;
+        if (++g >= p.G) return false;
+        tiles = tiles_of(p, g);
+      }
+      // pair rows of the same columns one after the other: they share B's rows
+      const int local = t - first, pairs = tiles / num_n;
+      s = {local % pairs * 2 * kRows, 0, local / pairs * BN, g, g};
+      s.valid = count(p, g) - s.m0;
+    } else {
+      if (t >= total) return false;
+      const int pair = t / num_n;
+      s = {pair * 2 * kRows, 0, t % num_n * BN, 0, 0};
+      if constexpr (kForm == Form::Contiguous) {
+        s.m0 = ld_cg_s32(p.pair_list + 3 * pair) * kRows;
+        s.gb = ld_cg_s32(p.pair_list + 3 * pair + 1);
+        s.valid = ld_cg_s32(p.pair_list + 3 * pair + 2) * kRows;
+      } else {
+        s.valid = p.M - s.m0;
+      }
+    }
+    t += step;
+    return true;
+  }
+};
+
+// Roles of a CTA (both of a pair run the same code):
+//   warp 0     TMA: its 128 rows of A, its half of B's rows (both counted by the leader's barrier), its rows' and all of
+//              the tile's columns' scale words (counted by its own)
+//   warp 1     (leader) issues the MMAs; allocates TMEM
+//   warp 2     arranges the scale words of each stage
+//   warp 3     (leader) copies both CTAs' scales to TMEM once a stage has arrived, which keeps copies and waits out of
+//              the MMA thread's stream
+//   warps 4..  epilogue: 32 columns at a time from TMEM to registers to D, whole 32-byte sectors a lane
+template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
+__global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
+    fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                    const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb, const Params p) {
+  using S = PairShape<BN, kAccum, kStages>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);   // leader: A and B of both CTAs
+  uint64_t* const sf_full = full + kStages;        // each CTA: its scale words
+  uint64_t* const sf_ready = sf_full + kStages;    // leader: both CTAs' scale words are arranged
+  uint64_t* const ready = sf_ready + kStages;      // leader: and in TMEM
+  uint64_t* const empty = ready + kStages;         // both CTAs: the stage's MMAs are done
+  uint64_t* const acc_full = empty + kStages;      // both CTAs
+  uint64_t* const acc_empty = acc_full + kAccum;   // leader: epilogue warps of both CTAs
+  uint64_t* const sf_free = acc_empty + kAccum;    // leader: the MMAs that read a TMEM buffer of scales are done
+  uint64_t* const drain = sf_free + S::kSfBufs;    // MMA thread, copying thread
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  volatile uint32_t* const abort_flag = tmem_slot + 1;
+  int* const counts = reinterpret_cast<int*>(smem + S::OFF_COUNTS);
+
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_cta_rank() & 1u;
+  const bool leader = rank == 0;
+  const int stages_k = up(p.K, kStageK);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_ready[s], 2);
+      mbar_init(&ready[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < kAccum; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * S::kEpilogueWarps);
+    }
+    for (int b = 0; b < S::kSfBufs; ++b) mbar_init(&sf_free[b], 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_sfa);
+    tma_prefetch_desc(&tm_sfb);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  grid_dependency_wait();   // programmatic dependent launch: no global access before this
+  if constexpr (kForm == Form::Masked) {
+    for (int g = threadIdx.x; g < p.G; g += S::kThreads) {
+      const int c = ld_cg_s32(p.masked_m + g), in = min(max(c, 0), p.M);
+      if (c != in && blockIdx.x == 0) atomicOr(p.status, kBadIndexBit);
+      if (g < kCountCache) counts[g] = in;
+    }
+  }
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto on_timeout = [&]() {
+    atomicOr(p.status, kTimeoutBit);
+    *abort_flag = 1;
+  };
+  Walk<kForm, BN> walk(p, counts);
+  Tile tile;
+  uint32_t stage = 0, phase = 0;
+  auto advance = [&]() {
+    if (++stage == kStages) stage = 0, phase ^= 1;
+  };
+
+  if (warp == 0) {
+    if (lane == 0 && p.fault != kFaultProducerSilent) {
+      uint32_t issued = 0;
+      bool ok = true;
+      while (ok && walk.next(p, tile)) {
+        const bool rows = tile.valid > static_cast<int>(rank) * kRows;      // this CTA has rows of the tile
+        const uint32_t bytes = (tile.valid > kRows ? 2 : 1) * S::A_BYTES + 2 * S::B_BYTES;
+        const int m0 = tile.m0 + static_cast<int>(rank) * kRows;
+        for (int kb = 0; kb < stages_k; ++kb) {
+          if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1, p.timeout_ns)) {
+            on_timeout();
+            ok = false;
+            break;
+          }
+          uint8_t* const sf = smem + S::OFF_SF + stage * S::SF_BYTES;
+          const uint32_t bar = map_to_rank(&full[stage], 0);
+          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          if (rows) tma_load_3d_pair(smem + stage * S::A_BYTES, &tm_a, bar, kb * 128, m0, tile.ga);
+          tma_load_3d_pair(smem + S::OFF_B + stage * S::B_BYTES, &tm_b, bar, kb * 128, tile.n0 + static_cast<int>(rank) * (BN / 2), tile.gb);
+          mbar_arrive_expect_tx(&sf_full[stage], (rows ? S::SFA_BYTES : 0) + S::SFB_BYTES);
+          if (rows) tma_load_3d(sf, &tm_sfa, &sf_full[stage], m0, 2 * kb, tile.ga);
+          tma_load_3d(sf + S::SFA_BYTES, &tm_sfb, &sf_full[stage], tile.n0, 2 * kb, tile.gb);
+          ++issued;
+          advance();
+        }
+      }
+      grid_launch_dependents();
+      // no copy is in flight when the CTA leaves
+      for (uint32_t s = 0; s < kStages && s < issued; ++s) {
+        const uint32_t last = (issued - 1 - s) / kStages & 1;
+        mbar_wait(&sf_full[s], last, kDrainNs);
+        if (leader) mbar_wait(&full[s], last, kDrainNs);
+      }
+    }
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      constexpr uint32_t kIdesc = instruction(2 * kRows, BN);
+      const uint64_t a0 = make_smem_desc(smem_addr(smem), 16, 1024, kLayoutSwizzle128B);
+      const uint64_t b0 = make_smem_desc(smem_addr(smem + S::OFF_B), 16, 1024, kLayoutSwizzle128B);
+      uint32_t tiles = 0, buf = 0;
+      bool ok = true;
+      while (ok && walk.next(p, tile)) {
+        const uint32_t acc = tiles % kAccum;
+        if (*abort_flag || !mbar_wait(&acc_empty[acc], (tiles / kAccum & 1) ^ 1, p.timeout_ns)) {
+          on_timeout();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + acc * BN;
+        for (int kb = 0; kb < stages_k; ++kb) {
+          if (!mbar_wait(&ready[stage], phase, p.timeout_ns)) {
+            on_timeout();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a = a0 + (stage * S::A_BYTES >> 4), b = b0 + (stage * S::B_BYTES >> 4);
+          const uint32_t sfa = tmem + kAccum * BN + buf * S::kSfCols, sfb = sfa + 8;
+          const bool whole = p.K - kb * kStageK >= kStageK;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t id = 2u * (k & 1);
+            if (k < 2 || whole)
+              mma<true>(d, a + 2 * k, b + 2 * k, kIdesc | id << 4 | id << 29, sfa + 4 * (k / 2), sfb + 4 * S::kChunks * (k / 2), (kb | k) != 0);
+          }
+          tc_commit_pair(&empty[stage]);
+          if constexpr (S::kSfBufs < kStages) tc_commit_pair(&sf_free[buf]);
+          if (++buf == S::kSfBufs) buf = 0;
+          advance();
+        }
+        if (ok) tc_commit_pair(&acc_full[acc]);
+        ++tiles;
+      }
+      tc_commit_pair(&drain[0]);
+      mbar_wait(&drain[0], 0, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    bool ok = true;
+    while (ok && walk.next(p, tile)) {
+      for (int kb = 0; kb < stages_k; ++kb) {
+        if (!warp_wait(&sf_full[stage], phase, p.timeout_ns, abort_flag)) {
+          if (lane == 0) on_timeout();
+          ok = false;
+          break;
+        }
+        arrange_scales<S::SF_BYTES / 512>(smem_addr(smem + S::OFF_SF + stage * S::SF_BYTES), lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(&sf_ready[stage], 0));
+        advance();
+      }
+    }
+  } else if (warp == 3) {
+    if (leader && lane == 0) {
+      const uint64_t sf0 = make_smem_desc(smem_addr(smem + S::OFF_SF), 0, 128, kLayoutNone);
+      uint32_t buf = 0, round = 0;
+      bool ok = true;
+      while (ok && walk.next(p, tile)) {
+        for (int kb = 0; kb < stages_k; ++kb) {
+          if (*abort_flag || !mbar_wait(&full[stage], phase, p.timeout_ns) || !mbar_wait_cluster(&sf_ready[stage], phase, p.timeout_ns) ||
+              (S::kSfBufs < kStages && !mbar_wait(&sf_free[buf], (round & 1) ^ 1, p.timeout_ns))) {
+            on_timeout();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t to = tmem + kAccum * BN + buf * S::kSfCols;
+          const uint64_t from = sf0 + (stage * S::SF_BYTES >> 4);
+#pragma unroll
+          for (int c = 0; c < S::SF_BYTES / 512; ++c) tmem_copy_32x128b_warpx4_pair(to + 4 * c, from + 32 * c);
+          tc_commit_pair(&ready[stage]);
+          if (++buf == S::kSfBufs) buf = 0, ++round;
+          advance();
+        }
+      }
+      tc_commit_pair(&drain[1]);
+      mbar_wait(&drain[1], 0, kDrainNs);
+    }
+    __syncwarp();
+  } else {
+    const int quad = warp % 4, half = (warp - 4) / 4;
+    uint32_t tiles = 0;
+    while (walk.next(p, tile)) {
+      const uint32_t acc = tiles % kAccum;
+      if (!warp_wait(&acc_full[acc], tiles / kAccum & 1, p.timeout_ns, abort_flag)) {
+        if (lane == 0) on_timeout();
+        break;
+      }
+      ++tiles;
+      tc_fence_after();
+      const int r = static_cast<int>(rank) * kRows + quad * 32 + static_cast<int>(lane);
+      const int row = tile.m0 + r;
+      bool live = r < tile.valid;
+      if constexpr (kForm == Form::Contiguous) {
+        if (live) {
+          const int expert = row < p.M ? ld_cg_s32(p.m_indices + row) : -1;
+          if (expert != tile.gb && expert != -1 && tile.n0 == 0 && half == 0) atomicOr(p.status, kBadIndexBit);
+          live = expert == tile.gb;
+        }
+      }
+      const size_t at = (static_cast<size_t>(tile.ga) * p.M + row) * p.N + tile.n0;
+      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
+      constexpr int kPieces = BN / 32;
+#pragma unroll
+      for (int i = 0; i < (kPieces + 1) / 2; ++i) {
+        const int piece = 2 * i + half;
+        uint32_t v[32];
+        if (piece < kPieces) tmem_load_32x32b_x32(from + 32 * piece, v);
+        tmem_load_wait();
+        if (i == (kPieces + 1) / 2 - 1) {
+          // the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(&acc_empty[acc], 0));
+        }
+        if (live && piece < kPieces) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (tile.n0 + 32 * piece + 16 * h < p.N) store_columns<kHasC>(p, at + 32 * piece + 16 * h, v + 16 * h);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (*abort_flag) {
+    // a peer's copy may still be in flight towards this CTA: let it land
+    for (int i = 0; i < 1000; ++i) nanosleep_ns(1000);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// few tiles: K shared out over the CTAs of a cluster
+// ------------------------------------------------------------------------------------
+template <int kBN, int kStages_>
+struct SplitShape {
+  static constexpr int BN = kBN, kStages = kStages_, kThreads = 256;
+  static constexpr int kChunks = up(BN, 128);
+  static constexpr int A_BYTES = kRows * 128, B_BYTES = BN * 128;
+  static constexpr int SFA_BYTES = 2 * 512, SFB_BYTES = 2 * kChunks * 512, SF_BYTES = SFA_BYTES + SFB_BYTES;
+  static constexpr int OFF_B = kStages * A_BYTES, OFF_SF = OFF_B + kStages * B_BYTES, OFF_BAR = OFF_SF + kStages * SF_BYTES;
+  static constexpr int kSfCols = 8 + 8 * kChunks, kAccCols = BN <= 128 ? 128 : 256;
+  static constexpr int kTmemCols = kAccCols + kStages * kSfCols <= 256 ? 256 : 512;
+  static_assert(kAccCols + kStages * kSfCols <= 512, "a TMEM buffer of scales for each stage");
+  static constexpr int OFF_MISC = OFF_BAR + (3 * kStages + 1) * 8;
+  static constexpr int kLd = BN + 4;                        // floats between the rows of a partial sum
+  static_assert(kRows * kLd * 4 <= OFF_SF, "the ring holds a partial sum");
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+};
+
+// A cluster's tile: 128 rows x BN columns, CTA r of S taking its r-th share of K's stages. The partial sums meet in
+// shared memory: CTA r adds up, in the order of ranks, and stores columns [r, r + 1) * BN / S.
+//   warp 0     TMA      warp 1     copies scales to TMEM and issues the MMAs     warp 2     arranges the scale words
+//   warps 4..  TMEM to D (S = 1) or to the partial sum
+template <int BN, int kStages, bool kHasC>
+__global__ void __launch_bounds__(256)
+    fp4_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb, const Params p, const int S_) {
+  using S = SplitShape<BN, kStages>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
+  uint64_t* const ready = full + kStages;          // the scale words are arranged
+  uint64_t* const empty = ready + kStages;
+  uint64_t* const acc_full = empty + kStages;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_MISC);
+  volatile uint32_t* const abort_flag = tmem_slot + 1;
+
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = threadIdx.x % 32;
+  const int rank = static_cast<int>(cluster_cta_rank());
+  const int m_tiles = up(p.M, kRows), of = blockIdx.x / S_;
+  const int m0 = of % m_tiles * kRows, n0 = of / m_tiles * BN;
+  const int stages_k = up(p.K, kStageK);
+  const int k_begin = static_cast<int>(static_cast<long long>(rank) * stages_k / S_), k_end = static_cast<int>(static_cast<long long>(rank + 1) * stages_k / S_);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&ready[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_sfa);
+    tma_prefetch_desc(&tm_sfb);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, S::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  auto on_timeout = [&]() {
+    atomicOr(p.status, kTimeoutBit);
+    *abort_flag = 1;
+  };
+  uint32_t stage = 0, phase = 0;
+  auto advance = [&]() {
+    if (++stage == kStages) stage = 0, phase ^= 1;
+  };
+
+  if (warp == 0) {
+    if (lane == 0 && p.fault != kFaultProducerSilent) {
+      uint32_t issued = 0;
+      for (int kb = k_begin; kb < k_end; ++kb) {
+        if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1, p.timeout_ns)) {
+          on_timeout();
+          break;
+        }
+        uint8_t* const sf = smem + S::OFF_SF + stage * S::SF_BYTES;
+        mbar_arrive_expect_tx(&full[stage], p.a_bytes + S::B_BYTES + S::SF_BYTES);
+        tma_load_3d(smem + S::OFF_B + stage * S::B_BYTES, &tm_b, &full[stage], kb * 128, n0, 0);
+        tma_load_3d(smem + stage * S::A_BYTES, &tm_a, &full[stage], kb * 128, m0, 0);
+        tma_load_3d(sf + S::SFA_BYTES, &tm_sfb, &full[stage], n0, 2 * kb, 0);
+        tma_load_3d(sf, &tm_sfa, &full[stage], m0, 2 * kb, 0);
+        ++issued;
+        advance();
+      }
+      grid_launch_dependents();
+      for (uint32_t s = 0; s < kStages && s < issued; ++s) mbar_wait(&full[s], (issued - 1 - s) / kStages & 1, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = instruction(kRows, BN);
+      const uint64_t a0 = make_smem_desc(smem_addr(smem), 16, 1024, kLayoutSwizzle128B);
+      const uint64_t b0 = make_smem_desc(smem_addr(smem + S::OFF_B), 16, 1024, kLayoutSwizzle128B);
+      const uint64_t sf0 = make_smem_desc(smem_addr(smem + S::OFF_SF), 0, 128, kLayoutNone);
+      for (int kb = k_begin; kb < k_end; ++kb) {
+        if (*abort_flag || !mbar_wait(&full[stage], phase, p.timeout_ns) || !mbar_wait(&ready[stage], phase, p.timeout_ns)) {
+          on_timeout();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sfa = tmem + S::kAccCols + stage * S::kSfCols, sfb = sfa + 8;
+        const uint64_t from = sf0 + (stage * S::SF_BYTES >> 4);
+#pragma unroll
+        for (int c = 0; c < S::SF_BYTES / 512; ++c) tmem_copy_32x128b_warpx4(sfa + 4 * c, from + 32 * c);
+        const uint64_t a = a0 + (stage * S::A_BYTES >> 4), b = b0 + (stage * S::B_BYTES >> 4);
+        const bool whole = p.K - kb * kStageK >= kStageK;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t id = 2u * (k & 1);
+          if (k < 2 || whole)
+            mma<false>(tmem, a + 2 * k, b + 2 * k, kIdesc | id << 4 | id << 29, sfa + 4 * (k / 2), sfb + 4 * S::kChunks * (k / 2), kb != k_begin || k != 0);
+        }
+        tc_commit(&empty[stage]);
+        advance();
+      }
+      tc_commit(acc_full);
+      mbar_wait(acc_full, 0, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    for (int kb = k_begin; kb < k_end; ++kb) {
+      if (!warp_wait(&full[stage], phase, p.timeout_ns, abort_flag)) {
+        if (lane == 0) on_timeout();
+        break;
+      }
+      arrange_scales<S::SF_BYTES / 512>(smem_addr(smem + S::OFF_SF + stage * S::SF_BYTES), lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready[stage]);
+      advance();
+    }
+  } else if (warp >= 4) {
+    const int quad = warp - 4, row = quad * 32 + static_cast<int>(lane);
+    // the MMA thread commits on every path; a wait that ran out elsewhere leaves no whole sum
+    const bool ok = warp_wait(acc_full, 0, p.timeout_ns, abort_flag) && *abort_flag == 0;
+    if (!ok) {
+      if (lane == 0) on_timeout();
+    } else if (m0 + quad * 32 < p.M) {
+      tc_fence_after();
+      const bool live = m0 + row < p.M;
+      const size_t at = static_cast<size_t>(m0 + row) * p.N + n0;
+      float* const partial = reinterpret_cast<float*>(smem) + row * S::kLd;
+#pragma unroll
+      for (int piece = 0; piece < BN / 32; ++piece) {
+        uint32_t v[32];
+        tmem_load_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + 32 * piece, v);
+        tmem_load_wait();
+        if (!live) continue;
+        if (S_ == 1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (n0 + 32 * piece + 16 * h < p.N) store_columns<kHasC>(p, at + 32 * piece + 16 * h, v + 16 * h);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) st_shared_v4(smem_addr(partial + 32 * piece + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (S_ > 1) {
+    cluster_sync();
+    tc_fence_after();
+    const int width = BN / S_, per = width / 8, rows = min(p.M - m0, kRows);
+    if (*abort_flag == 0) {
+      for (int i = threadIdx.x; i < rows * per; i += S::kThreads) {
+        const int r = i / per, col = rank * width + i % per * 8;
+        if (n0 + col >= p.N) continue;
+        float v[8] = {};
+        for (int s = 0; s < S_; ++s) {
+          const uint32_t from = map_to_rank(reinterpret_cast<float*>(smem) + r * S::kLd + col, s);
+          const uint4 lo = ld_shared_cluster_v4(from), hi = ld_shared_cluster_v4(from + 16);
+          v[0] += __uint_as_float(lo.x), v[1] += __uint_as_float(lo.y), v[2] += __uint_as_float(lo.z), v[3] += __uint_as_float(lo.w);
+          v[4] += __uint_as_float(hi.x), v[5] += __uint_as_float(hi.y), v[6] += __uint_as_float(hi.z), v[7] += __uint_as_float(hi.w);
+        }
+        const size_t at = static_cast<size_t>(m0 + r) * p.N + n0 + col;
+        if constexpr (kHasC) {
+          const uint4 c = ld_cg_v4(p.c + at);
+          const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x, y;
+            unpack_bf16(cw[j], x, y);
+            v[2 * j] += x, v[2 * j + 1] += y;
+          }
+        }
+        st_global_v4(p.d + at, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      }
+    }
+    cluster_sync();     // no CTA leaves while another reads its sums
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmemCols);
+  }
+}
+
+}  // namespace fp4
+}  // namespace dg

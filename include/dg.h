@@ -382,6 +382,122 @@ dg_status dg_moe_fp8_fp4_few_tokens(const void* x, const int32_t* sfx, const voi
                                     const int32_t* sf2, const int32_t* topk_ids, const float* topk_weights, const void* c,
                                     void* y, int T, int topk, int E, int H, int I, cudaStream_t stream);
 
+/* Sizes and strides (in elements) of the rows that the FP4 quantisers and the SwiGLU's gradient read. */
+typedef struct {
+  int G, M, K;                        /* groups (1 where there are none), rows of each, columns of the result */
+  size_t ldx, ldg;                    /* strides of x between rows (not read if M <= 1) and groups (not read if G == 1) */
+  int x_type;                         /* dg_type */
+} dg_rows_desc;
+
+/*
+ * Quantisation of rows to FP4 (an extra entry point of this library): packed E2M1 with one UE8M0 scale per row
+ * per 32 columns, as the FP4 operands of the GEMMs are. For every row and block b of 32 columns
+ *     e_b = the least code in [1, 254] with max|x_b| <= 6 * 2^(e_b - 127), 127 for a block of zeros
+ *     q   = E2M1(x * 2^(127 - e_b)), to nearest, ties to the even code
+ * A block with a value that is not finite gets e_b = 255 (NaN: E2M1 has none) and codes 0.
+ *   x        : [G, M, K] of desc->x_type, rows desc->ldx and groups desc->ldg elements apart.
+ *   masked_m : DEVICE int32 [G] or NULL. With it, of group g only rows r < masked_m[g] are quantised, as the masked
+ *              GEMMs read them; q and sf of the others are not written. A count above M is clamped to M and a
+ *              negative one is treated as 0; both set DG_ERR_BAD_INDEX on the device.
+ *   q        : uint8 [G, M, K/2], element 2j of a row in the low nibble of byte j.
+ *   sf       : int32 [G, K/128, ceil4(M)], word (k, m) holding the scales of columns 128k + 32j of row m in byte j
+ *              (words of the padding rows 0).
+ * Limits: G > 0, M >= 0, K a positive multiple of 128 and at most 2^30 (DG_ERR_UNSUPPORTED above). Base pointers
+ * and strides are multiples of 16 bytes (masked_m: 4).
+ */
+dg_status dg_quantize_fp4(const void* x, const int32_t* masked_m, void* q, int32_t* sf, const dg_rows_desc* desc,
+                          cudaStream_t stream);
+
+/*
+ * SwiGLU and quantisation to FP4, the step between the two products of a feed-forward layer: dg_quantize_fp4 of
+ *     y[m, k] = silu(x[m, k]) * x[m, K + k],     silu(v) = v / (1 + exp(-v))
+ * computed in FP32.
+ *   x : BF16 [G, M, 2 K], the K gate columns before the K up columns; K at most 2^29. Everything else as above.
+ */
+dg_status dg_swiglu_quantize_fp4(const void* x, const int32_t* masked_m, void* q, int32_t* sf, const dg_rows_desc* desc,
+                                 cudaStream_t stream);
+
+/*
+ * Gradient of that SwiGLU (the rounding to FP4 passes it through). With g and u the gate and up columns of a row and
+ * s = 1 / (1 + exp(-g)):     dg = dy * u * s * (1 + g * (1 - s)),     du = dy * g * s
+ * in FP32, rounded once.
+ *   x        : BF16 [G, M, 2 K] as above.      dy : BF16 [G, M, K], contiguous.
+ *   masked_m : as above; rows behind the count are not written.
+ *   dx       : BF16 [G, M, 2 K], contiguous; may be x where x is contiguous.
+ */
+dg_status dg_swiglu_backward(const void* x, const void* dy, const int32_t* masked_m, void* dx, const dg_rows_desc* desc,
+                             cudaStream_t stream);
+
+/* Sizes and options of the router's balance loss. */
+typedef struct {
+  int T, E, topk;                     /* topk: not read by the gradient */
+  size_t ld;                          /* row stride of logits, in elements (not read if T <= 1) */
+  int logits_type;                    /* dg_type */
+  int scoring;                        /* dg_route_scoring */
+  float coef;
+} dg_balance_desc;
+
+/*
+ * Balance loss of a router and its counts per expert (an extra entry point of this library). With p[t] the softmax of
+ * row t's logits or, with DG_ROUTE_SIGMOID, their sigmoids divided by the sum of them, over the experts that are not
+ * masked (-infinity and NaN mask one, as in dg_moe_route); a row whose experts are all masked is not live and has p = 0:
+ *     counts[e]    = slots of topk_ids that name e                 f[e] = counts[e] / (sum of counts, at least 1)
+ *     prob_mean[e] = (sum over t of p[t, e]) / (live rows, at least 1)
+ *     loss         = coef * E * (sum over e of f[e] * prob_mean[e])
+ *   logits   : [T, E] of desc->logits_type, rows desc->ld elements apart.
+ *   topk_ids : int32 [T, topk] as dg_moe_route writes them; -1 is an empty slot. An id outside [-1, E) is taken as -1
+ *              and sets DG_ERR_BAD_INDEX on the device.
+ *   counts   : int32 [E]; the masked GEMMs' masked_m where each expert's tokens are gathered.
+ *   live_rows: int32 [1].      prob_mean : float32 [E].      loss : float32 [1].
+ * All four are written (zeros for T = 0). Sums are FP32 in a fixed order: the same inputs give the same bits on the
+ * same number of SMs. Limits: E <= 1024, topk <= 32, T * topk < 2^31 (DG_ERR_UNSUPPORTED above); topk > 0, coef finite.
+ * Pointers are aligned to their element. Uses the stream's workspace.
+ */
+dg_status dg_moe_balance_loss(const void* logits, const int32_t* topk_ids, int32_t* counts, int32_t* live_rows,
+                              float* prob_mean, float* loss, const dg_balance_desc* desc, cudaStream_t stream);
+
+/*
+ * Gradient of dg_moe_balance_loss's loss with respect to its logits (counts are constants in it):
+ *     dlogits[t, e] = base[t, e] + dloss * coef * E / live_rows * p[t, e] * (f[e] - sum over j of p[t, j] * f[j])
+ * times 1 - sigmoid(logits[t, e]) with DG_ROUTE_SIGMOID; a masked expert's is base[t, e].
+ *   counts, live_rows : as the forward call wrote them, or sums of them over several batches. A negative count counts
+ *                       as 0.
+ *   dloss             : float32 [1] on the device.
+ *   base              : [T, E] of logits_type, contiguous, the gradient that reaches the logits by other paths (of
+ *                       dg_moe_route_backward), or NULL.
+ *   dlogits           : [T, E] of logits_type, contiguous, fully written; may be base.
+ */
+dg_status dg_moe_balance_loss_backward(const void* logits, const int32_t* counts, const int32_t* live_rows,
+                                       const float* dloss, const void* base, void* dlogits, const dg_balance_desc* desc,
+                                       cudaStream_t stream);
+
+/*
+ * FP4 x FP4 GEMMs (extra entry points of this library): D = C + A @ B.T with both operands in FP4.
+ *   a   : uint8 [M, K/2], sfa : int32 [K/128, ceil4(M)]; b : uint8 [N, K/2], sfb : int32 [K/128, ceil4(N)]: packed E2M1
+ *         and its scales as dg_quantize_fp4 writes them.
+ *   c, d: BF16 as in dg_fp8_gemm_nt. D[m, n] = C[m, n] + sum_k sA[m, k / 32] * sB[n, k / 32] * A[m, k] * B[n, k],
+ *         accumulated in FP32. A scale of 255 makes its row's (column's) results NaN.
+ * All base pointers are 16-byte aligned. Shape limits and errors as dg_fp8_gemm_nt.
+ */
+dg_status dg_fp4_gemm_nt(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, const void* c, void* d,
+                         int M, int N, int K, cudaStream_t stream);
+
+/*
+ * Contiguous M-grouped FP4 x FP4 GEMM: a uint8 [M_total, K/2] with sfa [K/128, ceil4(M_total)], b uint8 [G, N, K/2]
+ * with sfb [G, K/128, ceil4(N)]; d, m_indices and the layout as dg_m_grouped_fp8_gemm_nt_contiguous. Uses the stream's
+ * workspace.
+ */
+dg_status dg_m_grouped_fp4_gemm_nt_contiguous(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+                                              void* d, const int32_t* m_indices, int M_total, int N, int K, int G,
+                                              cudaStream_t stream);
+
+/*
+ * Masked M-grouped FP4 x FP4 GEMM: a uint8 [G, max_m, K/2] with sfa [G, K/128, ceil4(max_m)], b uint8 [G, N, K/2] with
+ * sfb [G, K/128, ceil4(N)]; d, masked_m and the layout as dg_m_grouped_fp8_gemm_nt_masked.
+ */
+dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, void* d,
+                                          const int32_t* masked_m, int G, int max_m, int N, int K, cudaStream_t stream);
+
 /*
  * Dense GEMM that allocates no device memory (the pages have no counterpart: this is an
  * extra entry point of this library).
