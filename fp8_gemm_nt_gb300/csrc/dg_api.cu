@@ -198,9 +198,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // (the common case: weights, activations and outputs reused every step) skip the encode.
 struct MapKey {
   const void* base;
-  uint64_t dims[3];
-  uint64_t strides[2];
-  uint32_t box[3];
+  uint64_t dims[4];
+  uint64_t strides[3];
+  uint32_t box[4];
+  uint32_t steps[4];
   int dt, rank, swz;
 };
 
@@ -216,9 +217,9 @@ thread_local int g_map_cache_next = 0;
 
 bool same_key(const MapKey& a, const MapKey& b) { return std::memcmp(&a, &b, sizeof(MapKey)) == 0; }
 
-// dims/box innermost first; strides in bytes for dims 1..rank-1.
+// dims/box innermost first; strides in bytes for dims 1..rank-1; steps: every how many elements of a dim the box takes (1).
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
-              const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz) {
+              const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz, const uint32_t* steps = nullptr) {
   MapKey key;
   std::memset(&key, 0, sizeof(key));
   key.base = base;
@@ -228,6 +229,7 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base
   for (int i = 0; i < rank; ++i) {
     key.dims[i] = dims[i];
     key.box[i] = box[i];
+    key.steps[i] = steps ? steps[i] : 1;
   }
   for (int i = 0; i + 1 < rank; ++i) key.strides[i] = strides[i];
   for (int i = 0; i < kMapCacheSize; ++i) {
@@ -239,6 +241,7 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) elem_strides[i] = key.steps[i];
   cuuint64_t d[5], st[4];
   cuuint32_t b[5];
   for (int i = 0; i < rank; ++i) {
@@ -994,8 +997,8 @@ bool weight_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
 }
 
 bool tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
-                const uint32_t* box, CUtensorMapSwizzle swizzle) {
-  return make_map(map, type, rank, base, dims, strides, box, swizzle);
+                const uint32_t* box, CUtensorMapSwizzle swizzle, const uint32_t* steps) {
+  return make_map(map, type, rank, base, dims, strides, box, swizzle, steps);
 }
 
 dg_status StreamWorkspace::acquire(cudaStream_t stream, size_t bytes, void** out) {

@@ -30,6 +30,22 @@ bool codes_map(CUtensorMap* m, const void* base, int G, int rows, int K, int box
   return dg::tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Rows of packed codes four apart: [rows / 4] of every fourth row, then the four, then the groups; in boxes of 32 rows of
+// each of `of_four`. Row 4 j + c of a box comes at its row 32 c + j. Rows past the last whole four are not in it.
+bool apart_map(CUtensorMap* m, const void* base, int G, int rows, int K, int of_four) {
+  const uint64_t bytes = static_cast<uint64_t>(K) / 2;
+  const uint64_t dims[4] = {bytes, static_cast<uint64_t>(rows / 4), 4, static_cast<uint64_t>(G)}, strides[3] = {4 * bytes, bytes, bytes * rows};
+  const uint32_t box[4] = {128, 32, static_cast<uint32_t>(of_four), 1};
+  return dg::tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// All rows, in boxes of every fourth of 128.
+bool every_fourth_map(CUtensorMap* m, const void* base, int G, int rows, int K) {
+  const uint64_t bytes = static_cast<uint64_t>(K) / 2;
+  const uint64_t dims[3] = {bytes, static_cast<uint64_t>(rows), static_cast<uint64_t>(G)}, strides[2] = {bytes, bytes * rows};
+  const uint32_t box[3] = {128, 128, 1}, steps[3] = {1, 4, 1};
+  return dg::tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, steps);
+}
+
 // Scale words [G, K / 128, ceil4(rows)], in boxes of box_rows rows' two words.
 bool scales_map(CUtensorMap* m, const int32_t* base, int G, int rows, int K, int box_rows) {
   const uint64_t w = 4 * ((static_cast<uint64_t>(rows) + 3) / 4), k = static_cast<uint64_t>(K) / 128;
@@ -45,9 +61,8 @@ struct Operands {
   const int32_t* sfb;
 };
 
-template <class Kernel, class... More>
-dg_status launch(Kernel kernel, int smem, int grid, int threads, int cluster, cudaStream_t stream, bool pdl, const CUtensorMap& ta,
-                 const CUtensorMap& tb, const CUtensorMap& tsa, const CUtensorMap& tsb, const Params& p, More... more) {
+template <class Kernel, class... Args>
+dg_status launch(Kernel kernel, int smem, int grid, int threads, int cluster, cudaStream_t stream, bool pdl, const Args&... args) {
   // (set per device; a call costs less than a microsecond)
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e != cudaSuccess)
     return dg::record_cuda_error(e);
@@ -64,7 +79,7 @@ dg_status launch(Kernel kernel, int smem, int grid, int threads, int cluster, cu
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, tsa, tsb, p, more...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   return e == cudaSuccess ? DG_OK : dg::record_cuda_error(e);
 }
 
@@ -73,15 +88,17 @@ template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
 dg_status run_pair(const LaunchContext& ctx, const Operands& o, const Params& p, long long pair_rows, cudaStream_t stream) {
   using S = dg::fp4::PairShape<BN, kAccum, kStages>;
   const int ga = kForm == Form::Masked ? p.G : 1, gb = kForm == Form::Dense ? 1 : p.G;
-  CUtensorMap ta, tb, tsa, tsb;
-  if (!codes_map(&ta, o.a, ga, p.M, p.K, kRowBox) || !codes_map(&tb, o.b, gb, p.N, p.K, BN / 2) || !scales_map(&tsa, o.sfa, ga, p.M, p.K, kRowBox) ||
-      !scales_map(&tsb, o.sfb, gb, p.N, p.K, 128 * S::kChunks))
+  CUtensorMap ta, ta_edge, tb, tsa, tsb;
+  if (!every_fourth_map(&ta_edge, o.a, ga, p.M, p.K) || !apart_map(&tb, o.b, gb, p.N, p.K, BN / 64) || !scales_map(&tsa, o.sfa, ga, p.M, p.K, kRowBox) ||
+      !scales_map(&tsb, o.sfb, gb, p.N, p.K, BN))
     return DG_ERR_CUDA;
+  ta = ta_edge;      // (where A has fewer than four rows, none of its tiles is an inner one)
+  if (p.M >= 4 && !apart_map(&ta, o.a, ga, p.M, p.K, 4)) return DG_ERR_CUDA;
   const long long tiles = pair_rows * up(p.N, BN);
   if (tiles > (1ll << 30)) return DG_ERR_UNSUPPORTED;
   const int clusters = static_cast<int>(std::min<long long>(std::max(1, ctx.sms / 2), tiles));
-  return launch(dg::fp4::fp4_pair_kernel<kForm, BN, kAccum, kStages, kHasC>, S::smem(kForm), 2 * clusters, S::kThreads, 2, stream, ctx.pdl, ta, tb,
-                tsa, tsb, p);
+  return launch(dg::fp4::fp4_pair_kernel<kForm, BN, kAccum, kStages, kHasC>, S::smem(kForm), 2 * clusters, S::kThreads, 2, stream, ctx.pdl, ta,
+                ta_edge, tb, tsa, tsb, p);
 }
 
 template <int BN, int kStages, bool kHasC>
@@ -184,7 +201,7 @@ dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const int32_t* sfa, con
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   Params p = params(ctx, nullptr, d, max_m, N, K, G);
   p.masked_m = masked_m;
-  return run_pair<Form::Masked, 256, 1, 6, false>(ctx, o, p, static_cast<long long>(G) * up(max_m, 256), stream);
+  return run_pair<Form::Masked, 256, 1, 5, false>(ctx, o, p, static_cast<long long>(G) * up(max_m, 256), stream);
 }
 
 }  // extern "C"

@@ -66,12 +66,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         : "memory");
 }
 
-// mbar_wait that also sees what threads of other CTAs of the cluster wrote before they arrived.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
-  if (!mbar_wait(bar, parity, timeout_ns)) return false;
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return true;
-}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, volatile uint32_t* abort_flag) {
   return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(bar, parity, timeout_ns));
 }
@@ -125,21 +119,27 @@ __device__ __forceinline__ void store_columns(const Params& p, size_t at, const 
 // ------------------------------------------------------------------------------------
 // CTA pairs
 // ------------------------------------------------------------------------------------
+// The scales go from global memory to TMEM as they are: 128 words of consecutive rows, of which tcgen05.cp gives lane j
+// the four of rows 4 j .. 4 j + 3. So the rows are put where their scales are: row 32 c + j of an MMA's operand is row
+// 4 j + c of the tile. TMA loads them in that order, through a map that takes four rows apart ([rows / 4] of every
+// fourth row, then the four); a lane of the accumulator is row 4 lane + quadrant, and its columns 32 c + j, c = 0 .. 3,
+// are columns 4 j + c of D. Rows of A past the last whole four go by a second map, of every fourth row from a given one.
 template <int kBN, int kAccums, int kStages_>
 struct PairShape {
   static constexpr int BN = kBN, kAccum = kAccums, kStages = kStages_;
   static constexpr int kEpilogueWarps = 8, kThreads = (4 + kEpilogueWarps) * 32;
-  static constexpr int kChunks = up(BN, 128);                       // 128-row chunks of B's scale words
+  static constexpr int kChunks = BN / 128;                          // of 128 scale words of B
   static constexpr int A_BYTES = kRows * 128, B_BYTES = BN / 2 * 128;
   static constexpr int SFA_BYTES = 2 * 512, SFB_BYTES = 2 * kChunks * 512, SF_BYTES = SFA_BYTES + SFB_BYTES;
-  static constexpr int OFF_B = kStages * A_BYTES, OFF_SF = OFF_B + kStages * B_BYTES, OFF_BAR = OFF_SF + kStages * SF_BYTES;
-  // TMEM: the accumulators, then a buffer of scales for each stage, or for as many as there are columns for
+  static constexpr int EPI_BYTES = 32 * 64;                         // of a warp: 32 rows of 32 columns
+  static constexpr int OFF_B = kStages * A_BYTES, OFF_SF = OFF_B + kStages * B_BYTES, OFF_EPI = OFF_SF + kStages * SF_BYTES;
+  static constexpr int OFF_BAR = OFF_EPI + kEpilogueWarps * EPI_BYTES;
+  // TMEM: the accumulators, then a buffer of scales for each stage
   static constexpr int kSfCols = 8 + 8 * kChunks;
-  static constexpr int kSfFit = (512 - kAccum * BN) / kSfCols, kSfBufs = kSfFit < kStages ? kSfFit : kStages;
-  static_assert(kSfBufs >= 2 && B_BYTES % 1024 == 0 && BN % 32 == 0, "tile width");
-  static constexpr int kBars = 5 * kStages + 2 * kAccum + kSfBufs + 2;
+  static_assert(BN % 128 == 0 && kAccum * BN + kStages * kSfCols <= 512, "TMEM columns");
+  static constexpr int kBars = 3 * kStages + 2 * kAccum + 2;
   static constexpr int OFF_COUNTS = OFF_BAR + kBars * 8 + 16;
-  static constexpr int smem(Form f) { return OFF_COUNTS + (f == Form::Masked ? kCountCache * 4 : 0) + 1024; }
+  static constexpr int smem(Form f) { return OFF_COUNTS + (f == Form::Masked ? kCountCache * 4 : 0); }
 };
 
 // A tile: the pair's rows from m0 in its group's rows of A, `valid` of them (may be more than the tile has); its columns
@@ -195,30 +195,27 @@ struct Walk {
   }
 };
 
-// Roles of a CTA (both of a pair run the same code):
-//   warp 0     TMA: its 128 rows of A, its half of B's rows (both counted by the leader's barrier), its rows' and all of
-//              the tile's columns' scale words (counted by its own)
+// Roles of a CTA (both of a pair run the same code; a warp's loop stays converged and one elected thread issues):
+//   warp 0     TMA: its 128 rows of A and their scales, its half of B's rows and all of the tile's scales of B, all counted
+//              by the leader's barrier
 //   warp 1     (leader) issues the MMAs; allocates TMEM
-//   warp 2     arranges the scale words of each stage
-//   warp 3     (leader) copies both CTAs' scales to TMEM once a stage has arrived, which keeps copies and waits out of
+//   warp 2     (leader) copies both CTAs' scales to TMEM once a stage has arrived, which keeps copies and waits out of
 //              the MMA thread's stream
-//   warps 4..  epilogue: 32 columns at a time from TMEM to registers to D, whole 32-byte sectors a lane
+//   warps 4..  epilogue: 32 columns at a time from TMEM to registers to the warp's staging buffer, from which D's rows
+//              leave in pieces of 64 bytes
 template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
 __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
-    fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                    const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb, const Params p) {
+    fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_edge,
+                    const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_sfa,
+                    const __grid_constant__ CUtensorMap tm_sfb, const Params p) {
   using S = PairShape<BN, kAccum, kStages>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);   // leader: A and B of both CTAs
-  uint64_t* const sf_full = full + kStages;        // each CTA: its scale words
-  uint64_t* const sf_ready = sf_full + kStages;    // leader: both CTAs' scale words are arranged
-  uint64_t* const ready = sf_ready + kStages;      // leader: and in TMEM
-  uint64_t* const empty = ready + kStages;         // both CTAs: the stage's MMAs are done
+  extern __shared__ __align__(1024) uint8_t smem[];   // at a multiple of 1024: nothing static lies before it
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);   // leader: the stage of both CTAs
+  uint64_t* const ready = full + kStages;          // leader: its scales are in TMEM
+  uint64_t* const empty = ready + kStages;         // both CTAs: its MMAs are done
   uint64_t* const acc_full = empty + kStages;      // both CTAs
   uint64_t* const acc_empty = acc_full + kAccum;   // leader: epilogue warps of both CTAs
-  uint64_t* const sf_free = acc_empty + kAccum;    // leader: the MMAs that read a TMEM buffer of scales are done
-  uint64_t* const drain = sf_free + S::kSfBufs;    // MMA thread, copying thread
+  uint64_t* const drain = acc_empty + kAccum;      // MMA thread, copying thread
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile uint32_t* const abort_flag = tmem_slot + 1;
   int* const counts = reinterpret_cast<int*>(smem + S::OFF_COUNTS);
@@ -232,8 +229,6 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&sf_full[s], 1);
-      mbar_init(&sf_ready[s], 2);
       mbar_init(&ready[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -241,7 +236,6 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 2 * S::kEpilogueWarps);
     }
-    for (int b = 0; b < S::kSfBufs; ++b) mbar_init(&sf_free[b], 1);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     *abort_flag = 0;
@@ -284,127 +278,130 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0 && p.fault != kFaultProducerSilent) {
+    if (p.fault != kFaultProducerSilent) {
       uint32_t issued = 0;
       bool ok = true;
       while (ok && walk.next(p, tile)) {
+        const int m0 = tile.m0 + static_cast<int>(rank) * kRows, n0 = tile.n0;
         const bool rows = tile.valid > static_cast<int>(rank) * kRows;      // this CTA has rows of the tile
-        const uint32_t bytes = (tile.valid > kRows ? 2 : 1) * S::A_BYTES + 2 * S::B_BYTES;
-        const int m0 = tile.m0 + static_cast<int>(rank) * kRows;
+        const bool inner = m0 + kRows <= (p.M & ~3);
+        const uint32_t bytes = (tile.valid > kRows ? 2 : 1) * (S::A_BYTES + S::SFA_BYTES) + 2 * (S::B_BYTES + S::SFB_BYTES);
         for (int kb = 0; kb < stages_k; ++kb) {
-          if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1, p.timeout_ns)) {
-            on_timeout();
+          if (!warp_wait(&empty[stage], phase ^ 1, p.timeout_ns, abort_flag)) {
+            if (lane == 0) on_timeout();
             ok = false;
             break;
           }
-          uint8_t* const sf = smem + S::OFF_SF + stage * S::SF_BYTES;
-          const uint32_t bar = map_to_rank(&full[stage], 0);
-          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-          if (rows) tma_load_3d_pair(smem + stage * S::A_BYTES, &tm_a, bar, kb * 128, m0, tile.ga);
-          tma_load_3d_pair(smem + S::OFF_B + stage * S::B_BYTES, &tm_b, bar, kb * 128, tile.n0 + static_cast<int>(rank) * (BN / 2), tile.gb);
-          mbar_arrive_expect_tx(&sf_full[stage], (rows ? S::SFA_BYTES : 0) + S::SFB_BYTES);
-          if (rows) tma_load_3d(sf, &tm_sfa, &sf_full[stage], m0, 2 * kb, tile.ga);
-          tma_load_3d(sf + S::SFA_BYTES, &tm_sfb, &sf_full[stage], tile.n0, 2 * kb, tile.gb);
+          if (elect_one()) {
+            uint8_t* const a = smem + stage * S::A_BYTES;
+            uint8_t* const sf = smem + S::OFF_SF + stage * S::SF_BYTES;
+            const uint32_t bar = map_to_rank(&full[stage], 0);
+            if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+            tma_load_4d_pair(smem + S::OFF_B + stage * S::B_BYTES, &tm_b, bar, kb * 128, n0 / 4 + (BN == 256 ? static_cast<int>(rank) * 32 : 0),
+                             BN == 256 ? 0 : static_cast<int>(rank) * 2, tile.gb);
+            if (rows) {
+              if (inner) {
+                tma_load_4d_pair(a, &tm_a, bar, kb * 128, m0 / 4, 0, tile.ga);
+              } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tma_load_3d_pair(a + c * 32 * 128, &tm_a_edge, bar, kb * 128, m0 + c, tile.ga);
+              }
+              tma_load_3d_pair(sf, &tm_sfa, bar, m0, 2 * kb, tile.ga);
+            }
+            tma_load_3d_pair(sf + S::SFA_BYTES, &tm_sfb, bar, n0, 2 * kb, tile.gb);
+          }
+          __syncwarp();
           ++issued;
           advance();
         }
       }
-      grid_launch_dependents();
-      // no copy is in flight when the CTA leaves
-      for (uint32_t s = 0; s < kStages && s < issued; ++s) {
-        const uint32_t last = (issued - 1 - s) / kStages & 1;
-        mbar_wait(&sf_full[s], last, kDrainNs);
-        if (leader) mbar_wait(&full[s], last, kDrainNs);
+      if (lane == 0) {
+        grid_launch_dependents();
+        // no copy is in flight when the pair leaves
+        if (leader)
+          for (uint32_t s = 0; s < kStages && s < issued; ++s) mbar_wait(&full[s], (issued - 1 - s) / kStages & 1, kDrainNs);
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
-    if (leader && lane == 0) {
+    if (leader) {
       constexpr uint32_t kIdesc = instruction(2 * kRows, BN);
       const uint64_t a0 = make_smem_desc(smem_addr(smem), 16, 1024, kLayoutSwizzle128B);
       const uint64_t b0 = make_smem_desc(smem_addr(smem + S::OFF_B), 16, 1024, kLayoutSwizzle128B);
-      uint32_t tiles = 0, buf = 0;
+      uint32_t tiles = 0;
       bool ok = true;
       while (ok && walk.next(p, tile)) {
         const uint32_t acc = tiles % kAccum;
-        if (*abort_flag || !mbar_wait(&acc_empty[acc], (tiles / kAccum & 1) ^ 1, p.timeout_ns)) {
-          on_timeout();
+        if (!warp_wait(&acc_empty[acc], (tiles / kAccum & 1) ^ 1, p.timeout_ns, abort_flag)) {
+          if (lane == 0) on_timeout();
           break;
         }
-        tc_fence_after();
         const uint32_t d = tmem + acc * BN;
         for (int kb = 0; kb < stages_k; ++kb) {
-          if (!mbar_wait(&ready[stage], phase, p.timeout_ns)) {
-            on_timeout();
+          if (!warp_wait(&ready[stage], phase, p.timeout_ns, abort_flag)) {
+            if (lane == 0) on_timeout();
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t a = a0 + (stage * S::A_BYTES >> 4), b = b0 + (stage * S::B_BYTES >> 4);
-          const uint32_t sfa = tmem + kAccum * BN + buf * S::kSfCols, sfb = sfa + 8;
-          const bool whole = p.K - kb * kStageK >= kStageK;
+          if (elect_one()) {
+            const uint64_t a = a0 + (stage * S::A_BYTES >> 4), b = b0 + (stage * S::B_BYTES >> 4);
+            const uint32_t sfa = tmem + kAccum * BN + stage * S::kSfCols, sfb = sfa + 8;
+            const bool whole = p.K - kb * kStageK >= kStageK;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t id = 2u * (k & 1);
-            if (k < 2 || whole)
-              mma<true>(d, a + 2 * k, b + 2 * k, kIdesc | id << 4 | id << 29, sfa + 4 * (k / 2), sfb + 4 * S::kChunks * (k / 2), (kb | k) != 0);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t id = 2u * (k & 1);
+              if (k < 2 || whole)
+                mma<true>(d, a + 2 * k, b + 2 * k, kIdesc | id << 4 | id << 29, sfa + 4 * (k / 2), sfb + 4 * S::kChunks * (k / 2), (kb | k) != 0);
+            }
+            tc_commit_pair(&empty[stage]);
+            if (kb == stages_k - 1) tc_commit_pair(&acc_full[acc]);
           }
-          tc_commit_pair(&empty[stage]);
-          if constexpr (S::kSfBufs < kStages) tc_commit_pair(&sf_free[buf]);
-          if (++buf == S::kSfBufs) buf = 0;
+          __syncwarp();
           advance();
         }
-        if (ok) tc_commit_pair(&acc_full[acc]);
         ++tiles;
       }
-      tc_commit_pair(&drain[0]);
-      mbar_wait(&drain[0], 0, kDrainNs);
+      // what the elected thread has issued is done before TMEM is handed back
+      if (elect_one()) {
+        tc_commit_pair(&drain[0]);
+        mbar_wait(&drain[0], 0, kDrainNs);
+      }
     }
     __syncwarp();
   } else if (warp == 2) {
-    bool ok = true;
-    while (ok && walk.next(p, tile)) {
-      for (int kb = 0; kb < stages_k; ++kb) {
-        if (!warp_wait(&sf_full[stage], phase, p.timeout_ns, abort_flag)) {
-          if (lane == 0) on_timeout();
-          ok = false;
-          break;
-        }
-        arrange_scales<S::SF_BYTES / 512>(smem_addr(smem + S::OFF_SF + stage * S::SF_BYTES), lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(&sf_ready[stage], 0));
-        advance();
-      }
-    }
-  } else if (warp == 3) {
-    if (leader && lane == 0) {
+    if (leader) {
       const uint64_t sf0 = make_smem_desc(smem_addr(smem + S::OFF_SF), 0, 128, kLayoutNone);
-      uint32_t buf = 0, round = 0;
       bool ok = true;
       while (ok && walk.next(p, tile)) {
         for (int kb = 0; kb < stages_k; ++kb) {
-          if (*abort_flag || !mbar_wait(&full[stage], phase, p.timeout_ns) || !mbar_wait_cluster(&sf_ready[stage], phase, p.timeout_ns) ||
-              (S::kSfBufs < kStages && !mbar_wait(&sf_free[buf], (round & 1) ^ 1, p.timeout_ns))) {
-            on_timeout();
+          // (the stage's TMEM buffer is free: what is in the stage now was loaded after the MMAs that read it)
+          if (!warp_wait(&full[stage], phase, p.timeout_ns, abort_flag)) {
+            if (lane == 0) on_timeout();
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t to = tmem + kAccum * BN + buf * S::kSfCols;
-          const uint64_t from = sf0 + (stage * S::SF_BYTES >> 4);
+          if (elect_one()) {
+            const uint32_t to = tmem + kAccum * BN + stage * S::kSfCols;
+            const uint64_t from = sf0 + (stage * S::SF_BYTES >> 4);
 #pragma unroll
-          for (int c = 0; c < S::SF_BYTES / 512; ++c) tmem_copy_32x128b_warpx4_pair(to + 4 * c, from + 32 * c);
-          tc_commit_pair(&ready[stage]);
-          if (++buf == S::kSfBufs) buf = 0, ++round;
+            for (int c = 0; c < S::SF_BYTES / 512; ++c) tmem_copy_32x128b_warpx4_pair(to + 4 * c, from + 32 * c);
+            tc_commit_pair(&ready[stage]);
+          }
+          __syncwarp();
           advance();
         }
       }
-      tc_commit_pair(&drain[1]);
-      mbar_wait(&drain[1], 0, kDrainNs);
+      if (elect_one()) {
+        tc_commit_pair(&drain[1]);
+        mbar_wait(&drain[1], 0, kDrainNs);
+      }
     }
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     const int quad = warp % 4, half = (warp - 4) / 4;
+    const uint32_t staging = smem_addr(smem + S::OFF_EPI + (warp - 4) * S::EPI_BYTES);
     uint32_t tiles = 0;
     while (walk.next(p, tile)) {
       const uint32_t acc = tiles % kAccum;
@@ -414,37 +411,76 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
       }
       ++tiles;
       tc_fence_after();
-      const int r = static_cast<int>(rank) * kRows + quad * 32 + static_cast<int>(lane);
-      const int row = tile.m0 + r;
-      bool live = r < tile.valid;
+      const int m0 = tile.m0 + static_cast<int>(rank) * kRows;
+      const int valid = tile.valid - static_cast<int>(rank) * kRows;        // of this CTA's rows
+      const int mine = 4 * static_cast<int>(lane) + quad;                    // the row of this lane's accumulators
+      bool live = mine < valid;
       if constexpr (kForm == Form::Contiguous) {
         if (live) {
-          const int expert = row < p.M ? ld_cg_s32(p.m_indices + row) : -1;
+          const int expert = m0 + mine < p.M ? ld_cg_s32(p.m_indices + m0 + mine) : -1;
           if (expert != tile.gb && expert != -1 && tile.n0 == 0 && half == 0) atomicOr(p.status, kBadIndexBit);
           live = expert == tile.gb;
         }
       }
-      const size_t at = (static_cast<size_t>(tile.ga) * p.M + row) * p.N + tile.n0;
+      const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
+      // pieces leave eight rows at a time: this lane's 16 bytes of row 4 (lane / 4 + 8 i) + quad
+      const int unit = static_cast<int>(lane) % 4, first = static_cast<int>(lane) / 4;
+      const size_t d0 = (static_cast<size_t>(tile.ga) * p.M + m0 + 4 * first + quad) * p.N + tile.n0 + 8 * unit;
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
-      constexpr int kPieces = BN / 32;
+      constexpr int kPieces = BN / 64;                                       // of 32 columns, for each of the two halves
 #pragma unroll
-      for (int i = 0; i < (kPieces + 1) / 2; ++i) {
-        const int piece = 2 * i + half;
-        uint32_t v[32];
-        if (piece < kPieces) tmem_load_32x32b_x32(from + 32 * piece, v);
+      for (int i = 0; i < kPieces; ++i) {
+        const int col = (half * kPieces + i) * 32;                           // 8 j of each c: columns 128 x + 8 (col / 32 % 4) + j + 32 c
+        uint32_t v[4][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load_32x32b_x8(from + col / 128 * 128 + col % 128 / 4 + 32 * c, v[c]);
+        uint4 add[4];
+        if constexpr (kHasC) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            add[r] = (live_rows >> (first + 8 * r) & 1) && tile.n0 + col + 8 * unit < p.N
+                         ? ld_cg_v4(p.c + d0 + static_cast<size_t>(32 * r) * p.N + col) : make_uint4(0, 0, 0, 0);
+        }
         tmem_load_wait();
-        if (i == (kPieces + 1) / 2 - 1) {
+        if (i == kPieces - 1) {
           // the accumulator is free
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(&acc_empty[acc], 0));
         }
-        if (live && piece < kPieces) {
+        // 16-byte unit u of staging row r at r * 64 + (u ^ (r / 2 % 4)) * 16
+        auto at = [&](int r, int u) { return staging + r * 64 + ((u ^ (r >> 1 & 3)) << 4); };
+        if constexpr (kHasC) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (tile.n0 + 32 * piece + 16 * h < p.N) store_columns<kHasC>(p, at + 32 * piece + 16 * h, v + 16 * h);
-          }
+          for (int r = 0; r < 4; ++r) st_shared_v4(at(first + 8 * r, unit), add[r].x, add[r].y, add[r].z, add[r].w);
+          __syncwarp();
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          // columns 8 u .. 8 u + 7: j = 2 u and 2 u + 1, c = 0 .. 3 of each
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[e & 3][2 * u + (e >> 2)]);
+          if constexpr (kHasC) {
+            const uint4 cv = ld_shared_v4(at(lane, u));
+            const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x, y;
+              unpack_bf16(cw[e], x, y);
+              f[2 * e] += x, f[2 * e + 1] += y;
+            }
+          }
+          st_shared_v4(at(lane, u), pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint4 w = ld_shared_v4(at(first + 8 * r, unit));
+          if ((live_rows >> (first + 8 * r) & 1) && tile.n0 + col + 8 * unit < p.N)
+            st_global_v4(p.d + d0 + static_cast<size_t>(32 * r) * p.N + col, w.x, w.y, w.z, w.w);
+        }
+        __syncwarp();
       }
     }
   }

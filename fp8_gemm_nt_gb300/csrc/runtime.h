@@ -30,10 +30,10 @@ dg_status record_cuda_error(cudaError_t e);
 // failure.
 bool weight_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool e2m1);
 
-// A tensor map of any kind (dims and box innermost first, strides in bytes of dims 1 on), cached per host thread. False
-// on failure.
+// A tensor map of up to four dims (dims and box innermost first, strides in bytes of dims 1 on; steps: every how many
+// elements of each dim a box takes, all of them if null), cached per host thread. False on failure.
 bool tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
-                const uint32_t* box, CUtensorMapSwizzle swizzle);
+                const uint32_t* box, CUtensorMapSwizzle swizzle, const uint32_t* steps = nullptr);
 
 // `bytes` of the stream's workspace, past the arrival counters at its start (kArrivalCounters of them, zero
 // between launches: a kernel that counts in them leaves them so). Held until the object goes out of scope, which
