@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "debug_state.h"
 #include "dg.h"
@@ -101,8 +102,8 @@ dg_status run_pair(const LaunchContext& ctx, const Operands& o, const Params& p,
                 ta_edge, tb, tsa, tsb, p);
 }
 
-template <int BN, int kStages, bool kHasC>
-dg_status run_split(const LaunchContext& ctx, const Operands& o, Params p, int ways, cudaStream_t stream) {
+template <int BN, int kStages, int kWays>
+dg_status run_split(const LaunchContext& ctx, const Operands& o, Params p, cudaStream_t stream) {
   using S = dg::fp4::SplitShape<BN, kStages>;
   // no more rows of A than there are, in whole swizzle atoms of eight
   const int rows = std::min(kRowBox, 8 * up(std::min(p.M, kRowBox), 8));
@@ -111,10 +112,9 @@ dg_status run_split(const LaunchContext& ctx, const Operands& o, Params p, int w
   if (!codes_map(&ta, o.a, 1, p.M, p.K, rows) || !codes_map(&tb, o.b, 1, p.N, p.K, BN) || !scales_map(&tsa, o.sfa, 1, p.M, p.K, kRowBox) ||
       !scales_map(&tsb, o.sfb, 1, p.N, p.K, 128 * S::kChunks))
     return DG_ERR_CUDA;
-  const long long grid = static_cast<long long>(up(p.M, kRowBox)) * up(p.N, BN) * ways;
+  const long long grid = static_cast<long long>(up(p.M, kRowBox)) * up(p.N, BN) * kWays;
   if (grid > (1ll << 30)) return DG_ERR_UNSUPPORTED;
-  return launch(dg::fp4::fp4_split_kernel<BN, kStages, kHasC>, S::SMEM, static_cast<int>(grid), S::kThreads, ways, stream, ctx.pdl, ta, tb, tsa, tsb, p,
-                ways);
+  return launch(dg::fp4::fp4_split_kernel<BN, kStages, kWays>, S::SMEM, static_cast<int>(grid), S::kThreads, kWays, stream, ctx.pdl, ta, tb, tsa, tsb, p);
 }
 
 // rows: of A, in each group.
@@ -132,7 +132,6 @@ Params params(const LaunchContext& ctx, const void* c, void* d, int M, int N, in
   Params p{};
   p.M = M, p.N = N, p.K = K, p.G = G;
   p.c = static_cast<const __nv_bfloat16*>(c), p.d = static_cast<__nv_bfloat16*>(d);
-  p.wide = !misaligned(d, 32);
   p.status = ctx.status, p.timeout_ns = dg::pipeline_wait_timeout_ns(), p.fault = dg::debug_fault_mode();
   return p;
 }
@@ -143,15 +142,50 @@ __global__ void __launch_bounds__(256) pair_list_kernel(const dg::PairListArgs a
   dg::build_pair_list(a);
 }
 
+// Ways to run a dense product: a CTA pair's tiles in turn, or one tile to a CTA or to a cluster that shares out K.
+struct Way {
+  int bn, ways;     // ways 0: CTA pairs
+};
+constexpr Way kDenseWays[] = {{256, 0}, {128, 0}, {64, 1}, {64, 2}, {64, 4}, {96, 2}, {128, 1}, {128, 2}, {192, 1}};
+
+// Estimated microseconds, from the rates that the kernels were measured at: a stage of 256 K costs an SM 0.19 us or the
+// time of its bytes from L2 (91 GB/s an SM; rows of 128 bytes and 8 of scales) or, all CTAs' together, of B's from HBM
+// (6 TB/s); a launch 3 us, a cluster's sums 0.3 us and 20 KB a microsecond, the last drain of a pair's accumulator 1 us.
+// Its choice against every way on its own, in us (128 x 7168 x 16384: 17.1, others 17.6 to 28; 128 x 256 x 512: 2.7, 2.8
+// to 4.9; 128 x 2048 x 16384: 11.0, 12.7 to 20; 512 x 4096 x 7168: 12.2, 12.7 to 22; 1000 x 4096 x 4096: 11.1, 11.7 to 30).
+double estimate(const Way& w, const Params& p, int sms) {
+  const int stages = up(p.K, dg::fp4::kStageK);
+  const double n = up(p.N, w.bn);
+  if (w.ways == 0) {
+    const double tiles = up(p.M, 256) * n, waves = std::ceil(tiles / std::max(1, sms / 2));
+    const double bytes = (128 + w.bn / 2) * 136.0 + w.bn / 2 * 8, stage = std::max(0.19, bytes / 91e3);
+    return 3.5 + waves * stages * stage + (w.bn == 256 ? waves : 1.0);
+  }
+  const double m_tiles = up(p.M, 128), ctas = m_tiles * n * w.ways;
+  // one wave; of clusters of four, three quarters of 152 SMs and more hold 36
+  if (stages < w.ways || ctas > (w.ways == 4 ? 18 * (sms / 19) : sms / w.ways * w.ways)) return HUGE_VAL;
+  const int rows = std::min(p.M, 128);
+  const double stage = std::max({0.19, (rows + w.bn) * 136.0 / 91e3, ctas / m_tiles * w.bn * 136.0 / 6e6});
+  return 3.0 + up(stages, w.ways) * stage + (w.ways > 1 ? 0.3 + rows * w.bn * 4.0 / 20e3 : 0.0);
+}
+
 template <bool kHasC>
 dg_status dense(const LaunchContext& ctx, const Operands& o, const Params& p, cudaStream_t stream) {
-  const long long pair_tiles = static_cast<long long>(up(p.M, 256)) * up(p.N, 256);
-  if (p.M > 128 && pair_tiles * 4 >= ctx.sms) return run_pair<Form::Dense, 256, 1, 6, kHasC>(ctx, o, p, up(p.M, 256), stream);
-  const int stages = up(p.K, dg::fp4::kStageK);
-  const long long tiles = static_cast<long long>(up(p.M, 128)) * up(p.N, 128);
-  int ways = 1;
-  while (ways < 8 && tiles * ways * 2 <= ctx.sms && 2 * ways <= stages) ways *= 2;
-  return run_split<128, 6, kHasC>(ctx, o, p, ways, stream);
+  Way best = kDenseWays[0];
+  double least = HUGE_VAL;
+  for (const Way& w : kDenseWays)
+    if (const double t = estimate(w, p, ctx.sms); t < least) best = w, least = t;
+  switch (best.bn * 10 + best.ways) {
+    case 1280: return run_pair<Form::Dense, 128, 2, 8, kHasC>(ctx, o, p, up(p.M, 256), stream);
+    case 641: return run_split<64, 6, 1>(ctx, o, p, stream);
+    case 642: return run_split<64, 6, 2>(ctx, o, p, stream);
+    case 644: return run_split<64, 6, 4>(ctx, o, p, stream);
+    case 962: return run_split<96, 6, 2>(ctx, o, p, stream);
+    case 1281: return run_split<128, 6, 1>(ctx, o, p, stream);
+    case 1282: return run_split<128, 6, 2>(ctx, o, p, stream);
+    case 1921: return run_split<192, 5, 1>(ctx, o, p, stream);
+  }
+  return run_pair<Form::Dense, 256, 1, 6, kHasC>(ctx, o, p, up(p.M, 256), stream);
 }
 
 }  // namespace

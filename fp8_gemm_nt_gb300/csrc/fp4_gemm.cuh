@@ -35,7 +35,6 @@ struct Params {
   const int* pair_count;
   const __nv_bfloat16* c;
   __nv_bfloat16* d;
-  int wide;                                // d is 32-byte aligned
   uint32_t a_bytes;                        // split kernel: bytes of A that a stage loads
   uint32_t* status;
   unsigned long long timeout_ns;
@@ -86,34 +85,23 @@ __device__ __forceinline__ void arrange_scales(uint32_t at, uint32_t lane) {
 }
 
 // Sixteen columns of a row of D: v, and C's where there is one, rounded to BF16.
-template <bool kHasC>
 __device__ __forceinline__ void store_columns(const Params& p, size_t at, const uint32_t* bits) {
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(bits[i]);
   uint32_t w[8];
-  if constexpr (kHasC) {
+  if (p.c) {
     const uint4 lo = ld_cg_v4(p.c + at), hi = ld_cg_v4(p.c + at + 8);
     const uint32_t cw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float a, b;
       unpack_bf16(cw[i], a, b);
-      w[i] = pack_bf16(a + v[2 * i], b + v[2 * i + 1]);
+      w[i] = pack_bf16(a + __uint_as_float(bits[2 * i]), b + __uint_as_float(bits[2 * i + 1]));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(__uint_as_float(bits[2 * i]), __uint_as_float(bits[2 * i + 1]));
   }
-  __nv_bfloat16* const d = p.d + at;
-  if (p.wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-                 "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    st_global_v4(d, w[0], w[1], w[2], w[3]);
-    st_global_v4(d + 8, w[4], w[5], w[6], w[7]);
-  }
+  st_global_v4(p.d + at, w[0], w[1], w[2], w[3]);
+  st_global_v4(p.d + at + 8, w[4], w[5], w[6], w[7]);
 }
 
 // ------------------------------------------------------------------------------------
@@ -517,14 +505,14 @@ struct SplitShape {
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
 };
 
-// A cluster's tile: 128 rows x BN columns, CTA r of S taking its r-th share of K's stages. The partial sums meet in
-// shared memory: CTA r adds up, in the order of ranks, and stores columns [r, r + 1) * BN / S.
+// A cluster's tile: 128 rows x BN columns, CTA r taking its r-th share of K's stages. The partial sums meet in
+// shared memory: CTA r adds up, in the order of ranks, and stores columns [r, r + 1) * BN / kWays.
 //   warp 0     TMA      warp 1     copies scales to TMEM and issues the MMAs     warp 2     arranges the scale words
-//   warps 4..  TMEM to D (S = 1) or to the partial sum
-template <int BN, int kStages, bool kHasC>
+//   warps 4..  TMEM to D (kWays = 1) or to the partial sum
+template <int BN, int kStages, int kWays>
 __global__ void __launch_bounds__(256)
     fp4_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                     const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb, const Params p, const int S_) {
+                     const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb, const Params p) {
   using S = SplitShape<BN, kStages>;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -538,10 +526,10 @@ __global__ void __launch_bounds__(256)
   const int warp = threadIdx.x / 32;
   const uint32_t lane = threadIdx.x % 32;
   const int rank = static_cast<int>(cluster_cta_rank());
-  const int m_tiles = up(p.M, kRows), of = blockIdx.x / S_;
+  const int m_tiles = up(p.M, kRows), of = blockIdx.x / kWays;
   const int m0 = of % m_tiles * kRows, n0 = of / m_tiles * BN;
   const int stages_k = up(p.K, kStageK);
-  const int k_begin = static_cast<int>(static_cast<long long>(rank) * stages_k / S_), k_end = static_cast<int>(static_cast<long long>(rank + 1) * stages_k / S_);
+  const int k_begin = static_cast<int>(static_cast<long long>(rank) * stages_k / kWays), k_end = static_cast<int>(static_cast<long long>(rank + 1) * stages_k / kWays);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -579,38 +567,44 @@ __global__ void __launch_bounds__(256)
   };
 
   if (warp == 0) {
-    if (lane == 0 && p.fault != kFaultProducerSilent) {
+    if (p.fault != kFaultProducerSilent) {
       uint32_t issued = 0;
       for (int kb = k_begin; kb < k_end; ++kb) {
-        if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1, p.timeout_ns)) {
-          on_timeout();
+        if (!warp_wait(&empty[stage], phase ^ 1, p.timeout_ns, abort_flag)) {
+          if (lane == 0) on_timeout();
           break;
         }
-        uint8_t* const sf = smem + S::OFF_SF + stage * S::SF_BYTES;
-        mbar_arrive_expect_tx(&full[stage], p.a_bytes + S::B_BYTES + S::SF_BYTES);
-        tma_load_3d(smem + S::OFF_B + stage * S::B_BYTES, &tm_b, &full[stage], kb * 128, n0, 0);
-        tma_load_3d(smem + stage * S::A_BYTES, &tm_a, &full[stage], kb * 128, m0, 0);
-        tma_load_3d(sf + S::SFA_BYTES, &tm_sfb, &full[stage], n0, 2 * kb, 0);
-        tma_load_3d(sf, &tm_sfa, &full[stage], m0, 2 * kb, 0);
+        if (elect_one()) {
+          uint8_t* const sf = smem + S::OFF_SF + stage * S::SF_BYTES;
+          mbar_arrive_expect_tx(&full[stage], p.a_bytes + S::B_BYTES + S::SF_BYTES);
+          tma_load_3d(smem + S::OFF_B + stage * S::B_BYTES, &tm_b, &full[stage], kb * 128, n0, 0);
+          tma_load_3d(smem + stage * S::A_BYTES, &tm_a, &full[stage], kb * 128, m0, 0);
+          tma_load_3d(sf + S::SFA_BYTES, &tm_sfb, &full[stage], n0, 2 * kb, 0);
+          tma_load_3d(sf, &tm_sfa, &full[stage], m0, 2 * kb, 0);
+        }
+        __syncwarp();
         ++issued;
         advance();
       }
-      grid_launch_dependents();
-      for (uint32_t s = 0; s < kStages && s < issued; ++s) mbar_wait(&full[s], (issued - 1 - s) / kStages & 1, kDrainNs);
+      if (lane == 0) {
+        grid_launch_dependents();
+        for (uint32_t s = 0; s < kStages && s < issued; ++s) mbar_wait(&full[s], (issued - 1 - s) / kStages & 1, kDrainNs);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = instruction(kRows, BN);
-      const uint64_t a0 = make_smem_desc(smem_addr(smem), 16, 1024, kLayoutSwizzle128B);
-      const uint64_t b0 = make_smem_desc(smem_addr(smem + S::OFF_B), 16, 1024, kLayoutSwizzle128B);
-      const uint64_t sf0 = make_smem_desc(smem_addr(smem + S::OFF_SF), 0, 128, kLayoutNone);
-      for (int kb = k_begin; kb < k_end; ++kb) {
-        if (*abort_flag || !mbar_wait(&full[stage], phase, p.timeout_ns) || !mbar_wait(&ready[stage], phase, p.timeout_ns)) {
-          on_timeout();
-          break;
-        }
-        tc_fence_after();
+    constexpr uint32_t kIdesc = instruction(kRows, BN);
+    const uint64_t a0 = make_smem_desc(smem_addr(smem), 16, 1024, kLayoutSwizzle128B);
+    const uint64_t b0 = make_smem_desc(smem_addr(smem + S::OFF_B), 16, 1024, kLayoutSwizzle128B);
+    const uint64_t sf0 = make_smem_desc(smem_addr(smem + S::OFF_SF), 0, 128, kLayoutNone);
+    for (int kb = k_begin; kb < k_end; ++kb) {
+      // (the stage's TMEM buffer of scales is free: what is in the stage now was loaded after the MMAs that read it)
+      if (!warp_wait(&full[stage], phase, p.timeout_ns, abort_flag) || !warp_wait(&ready[stage], phase, p.timeout_ns, abort_flag)) {
+        if (lane == 0) on_timeout();
+        break;
+      }
+      tc_fence_after();
+      if (elect_one()) {
         const uint32_t sfa = tmem + S::kAccCols + stage * S::kSfCols, sfb = sfa + 8;
         const uint64_t from = sf0 + (stage * S::SF_BYTES >> 4);
 #pragma unroll
@@ -624,8 +618,11 @@ __global__ void __launch_bounds__(256)
             mma<false>(tmem, a + 2 * k, b + 2 * k, kIdesc | id << 4 | id << 29, sfa + 4 * (k / 2), sfb + 4 * S::kChunks * (k / 2), kb != k_begin || k != 0);
         }
         tc_commit(&empty[stage]);
-        advance();
       }
+      __syncwarp();
+      advance();
+    }
+    if (elect_one()) {
       tc_commit(acc_full);
       mbar_wait(acc_full, 0, kDrainNs);
     }
@@ -659,10 +656,10 @@ __global__ void __launch_bounds__(256)
         tmem_load_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + 32 * piece, v);
         tmem_load_wait();
         if (!live) continue;
-        if (S_ == 1) {
+        if constexpr (kWays == 1) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (n0 + 32 * piece + 16 * h < p.N) store_columns<kHasC>(p, at + 32 * piece + 16 * h, v + 16 * h);
+            if (n0 + 32 * piece + 16 * h < p.N) store_columns(p, at + 32 * piece + 16 * h, v + 16 * h);
           }
         } else {
 #pragma unroll
@@ -673,25 +670,38 @@ __global__ void __launch_bounds__(256)
   }
   __syncwarp();
   tc_fence_before();
-  if (S_ > 1) {
+  if constexpr (kWays > 1) {
     cluster_sync();
-    tc_fence_after();
-    const int width = BN / S_, per = width / 8, rows = min(p.M - m0, kRows);
+    constexpr int kWidth = BN / kWays, kPer = kWidth / 8, kItems = up(kRows * kPer, S::kThreads);
+    static_assert(kWidth % 8 == 0, "columns of a CTA");
+    const int rows = min(p.M - m0, kRows);
     if (*abort_flag == 0) {
-      for (int i = threadIdx.x; i < rows * per; i += S::kThreads) {
-        const int r = i / per, col = rank * width + i % per * 8;
-        if (n0 + col >= p.N) continue;
+      // every load is in flight before the first sum
+      uint4 part[kItems][kWays][2], c[kItems];
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int item = i * S::kThreads + static_cast<int>(threadIdx.x), r = item / kPer, col = rank * kWidth + item % kPer * 8;
+        if (r >= rows || n0 + col >= p.N) continue;
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+          const uint32_t from = map_to_rank(reinterpret_cast<float*>(smem) + r * S::kLd + col, w);
+          part[i][w][0] = ld_shared_cluster_v4(from), part[i][w][1] = ld_shared_cluster_v4(from + 16);
+        }
+        if (p.c) c[i] = ld_cg_v4(p.c + static_cast<size_t>(m0 + r) * p.N + n0 + col);
+      }
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int item = i * S::kThreads + static_cast<int>(threadIdx.x), r = item / kPer, col = rank * kWidth + item % kPer * 8;
+        if (r >= rows || n0 + col >= p.N) continue;
         float v[8] = {};
-        for (int s = 0; s < S_; ++s) {
-          const uint32_t from = map_to_rank(reinterpret_cast<float*>(smem) + r * S::kLd + col, s);
-          const uint4 lo = ld_shared_cluster_v4(from), hi = ld_shared_cluster_v4(from + 16);
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+          const uint4 lo = part[i][w][0], hi = part[i][w][1];
           v[0] += __uint_as_float(lo.x), v[1] += __uint_as_float(lo.y), v[2] += __uint_as_float(lo.z), v[3] += __uint_as_float(lo.w);
           v[4] += __uint_as_float(hi.x), v[5] += __uint_as_float(hi.y), v[6] += __uint_as_float(hi.z), v[7] += __uint_as_float(hi.w);
         }
-        const size_t at = static_cast<size_t>(m0 + r) * p.N + n0 + col;
-        if constexpr (kHasC) {
-          const uint4 c = ld_cg_v4(p.c + at);
-          const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+        if (p.c) {
+          const uint32_t cw[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float x, y;
@@ -699,7 +709,8 @@ __global__ void __launch_bounds__(256)
             v[2 * j] += x, v[2 * j + 1] += y;
           }
         }
-        st_global_v4(p.d + at, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        st_global_v4(p.d + static_cast<size_t>(m0 + r) * p.N + n0 + col, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                     pack_bf16(v[6], v[7]));
       }
     }
     cluster_sync();     // no CTA leaves while another reads its sums
