@@ -7,9 +7,8 @@
 //
 // E2M1 has no NaN and no infinity: a block that holds one gets the scale code 255 (NaN) and codes 0.
 //
-// Bound by HBM. A warp takes 8 rows of 512 columns: every access of x is 512 contiguous bytes, all of them are in
-// flight before the first is used, and the 32 scale words of the tile end up one in each lane, so that they leave
-// in whole 32-byte sectors.
+// Bound by HBM. A warp takes 8 rows of 256 columns: every access of x is 512 contiguous bytes, all of them are in flight
+// before the first is used, and the 16 scale words of the tile leave in whole 32-byte sectors.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,7 +24,7 @@ namespace {
 using dg::LaunchContext;
 
 constexpr int kWarps = 4;                    // tiles per block
-constexpr int kTileRows = 8, kTileCols = 512;
+constexpr int kTileRows = 8, kTileCols = 256;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 struct QuantArgs {
@@ -65,7 +64,10 @@ __device__ __forceinline__ uint32_t pack_e2m1(float a, float b, float c, float d
   return w;
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+// 1 / (1 + exp(-g)), within 2^-19 of itself (the rounded exponent of a small one), which FP4 and BF16 do not see; 0 where
+// exp(-g) overflows.
+__device__ __forceinline__ float sigmoid(float g) { return dg::reciprocal(1.0f + dg::exp2_fast(-dg::kLog2e * g)); }
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
 
 // The columns of 16 bytes of x.
 template <class T>
@@ -90,79 +92,91 @@ __device__ __forceinline__ Tile tile_of(uint32_t tile, uint32_t row_tiles, uint3
   return {static_cast<int>(rest / row_tiles), static_cast<int>(rest % row_tiles) * rows, static_cast<int>(tile % col_tiles) * cols};
 }
 
+// The largest magnitude of 16 bytes, as bits that a block's are compared by: NaN above infinity above the rest.
+__device__ __forceinline__ uint32_t magnitude(const uint4& u, const float (&)[8]) {
+  const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+  return max(m << 16, m & 0xFFFF0000u);
+}
+template <int V>
+__device__ __forceinline__ uint32_t magnitude(const float (&v)[V]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
 // T: type of x. kGate: x has 2 K columns, and y = silu(gate) * up.
 template <class T, bool kGate>
 __global__ void __launch_bounds__(kWarps * 32) quantize_kernel(const QuantArgs a) {
   constexpr int V = kPiece<T>, kChunk = 32 * V, kChunks = kTileCols / kChunk;   // a chunk: one access of the warp
-  constexpr int kBlockLanes = 32 / V, kWordLanes = 128 / V;                     // lanes of a scale, of a word of four
-  static_assert(kChunks * kTileRows == kWordLanes, "a scale word for every lane");
+  constexpr int kBlockLanes = 32 / V;                                           // lanes of a scale
+  __shared__ __align__(8) uint8_t codes_of[kWarps][kTileRows][kTileCols / 32];  // the tile's scale codes
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const uint32_t tile = blockIdx.x * kWarps + threadIdx.x / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const uint32_t tile = blockIdx.x * kWarps + warp;
   if (tile >= a.tiles) return;
   const Tile t = tile_of(tile, a.row_tiles, a.col_tiles, kTileRows, kTileCols);
-  const int valid = rows_of(a.masked_m, t.g, a.M, a.status);
-  const T* const x = static_cast<const T*>(a.x) + t.g * a.ldg;
+  const int valid = rows_of(a.masked_m, t.g, a.M, a.status), rows = valid - t.row0;
+  const T* const x = static_cast<const T*>(a.x) + t.g * a.ldg + t.row0 * a.ldx + t.col0 + lane * V;
+  uint8_t* const q = a.q + ((static_cast<size_t>(t.g) * a.M + t.row0) * a.K + t.col0 + lane * V) / 2;
   uint4 in[kChunks][kTileRows], up[kGate ? kChunks : 1][kGate ? kTileRows : 1];
 #pragma unroll
   for (int r = 0; r < kTileRows; ++r) {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int col = t.col0 + c * kChunk + lane * V;
-      if (t.row0 + r < valid && col < a.K) {
-        const T* at = x + (t.row0 + r) * a.ldx + col;
+      if (r < rows && t.col0 + c * kChunk + lane * V < a.K) {
+        const T* at = x + r * a.ldx + c * kChunk;
         in[c][r] = __ldcg(reinterpret_cast<const uint4*>(at));
         if constexpr (kGate) up[c][r] = __ldcg(reinterpret_cast<const uint4*>(at + a.K));
       }
     }
   }
-  uint32_t mine = 0;
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int col = t.col0 + c * kChunk + lane * V;
+  for (int r = 0; r < kTileRows; ++r) {
+    if (r >= rows) break;
 #pragma unroll
-    for (int r = 0; r < kTileRows; ++r) {
-      const bool live = t.row0 + r < valid && col < a.K;
+    for (int c = 0; c < kChunks; ++c) {
+      const bool live = t.col0 + c * kChunk + lane * V < a.K;
       float v[V];
-      uint32_t top = 0;
-      if (live) {
-        unpack(in[c][r], v);
-        if constexpr (kGate) {
-          float u[V];
-          unpack(up[c][r], u);
+      uint32_t top;
+      unpack(in[c][r], v);
+      if constexpr (kGate) {
+        float u[V];
+        unpack(up[c][r], u);
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[i] = silu(v[i]) * u[i];
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < V; ++i) v[i] = silu(v[i]) * u[i];
       }
+      if constexpr (V == 8 && !kGate)
+        top = magnitude(in[c][r], v);
+      else
+        top = magnitude(v);
+      if (!live) top = 0;
 #pragma unroll
       for (int o = 1; o < kBlockLanes; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
       const int e = code_for(top);
-      if (live) {
-        const float by = dg::ue8m0_inverse(min(e, 254));
-        uint32_t codes = 0;
+      const float by = dg::ue8m0_inverse(min(e, 254));
+      uint32_t codes = 0;
 #pragma unroll
-        for (int i = 0; i < V; i += 4) codes |= pack_e2m1(v[i] * by, v[i + 1] * by, v[i + 2] * by, v[i + 3] * by) << (4 * i);
-        if (e == 255) codes = 0;
-        uint8_t* const to = a.q + ((static_cast<size_t>(t.g) * a.M + t.row0 + r) * a.K + col) / 2;
+      for (int i = 0; i < V; i += 4) codes |= pack_e2m1(v[i] * by, v[i + 1] * by, v[i + 2] * by, v[i + 3] * by) << (4 * i);
+      if (e == 255) codes = 0;
+      if (live) {
+        uint8_t* const to = q + (static_cast<size_t>(r) * a.K + c * kChunk) / 2;
         if constexpr (V == 8)
           *reinterpret_cast<uint32_t*>(to) = codes;
         else
           *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(codes);
       }
-      uint32_t word = static_cast<uint32_t>(e) << (8 * (lane / kBlockLanes % 4));
-#pragma unroll
-      for (int o = kBlockLanes; o < kWordLanes; o <<= 1) word |= __shfl_xor_sync(kAll, word, o);
-      if (lane % kWordLanes == c * kTileRows + r) mine = word;
+      if (lane % kBlockLanes == 0) codes_of[warp][r][c * (kChunk / 32) + lane / kBlockLanes] = static_cast<uint8_t>(e);
     }
   }
-  const int row = t.row0 + lane % kTileRows;
-  const int group = t.col0 / 128 + lane % kWordLanes / kTileRows * (kChunk / 128) + lane / kWordLanes;
+  __syncwarp();
+  // lane l: the word of row l % 8 and the l / 8-th 128 columns, so that words leave in whole sectors
+  const int row = t.row0 + lane % kTileRows, group = lane / kTileRows;
   const bool padding = row >= a.M;
-  if (group < a.K / 128 && row < a.sf_rows && (row < valid || padding))
-    a.sf[(static_cast<size_t>(t.g) * (a.K / 128) + group) * a.sf_rows + row] = padding ? 0 : static_cast<int32_t>(mine);
+  if (group < kTileCols / 128 && t.col0 / 128 + group < a.K / 128 && row < a.sf_rows && (row < valid || padding))
+    a.sf[(static_cast<size_t>(t.g) * (a.K / 128) + t.col0 / 128 + group) * a.sf_rows + row] =
+        padding ? 0 : *reinterpret_cast<const int32_t*>(&codes_of[warp][lane % kTileRows][4 * group]);
 }
 
 struct SwigluGradArgs {
@@ -208,7 +222,7 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_grad_kernel(const SwigluGr
     unpack(wd[r], d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = 1.0f / (1.0f + expf(-gate[i]));
+      const float s = sigmoid(gate[i]);
       const float dgate = d[i] * up[i] * s * (1.0f + gate[i] * (1.0f - s));
       up[i] = d[i] * gate[i] * s;
       gate[i] = dgate;

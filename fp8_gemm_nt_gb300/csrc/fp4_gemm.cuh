@@ -416,12 +416,30 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
       const size_t d0 = (static_cast<size_t>(tile.ga) * p.M + m0 + 4 * first + quad) * p.N + tile.n0 + 8 * unit;
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
       constexpr int kPieces = BN / 64;                                       // of 32 columns, for each of the two halves
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      // one accumulator: all of the warp's share at once, then it is free; two: piece by piece
+      constexpr int kHeld = kAccum == 1 ? kPieces : 1;
+      uint32_t held[kHeld][4][8];
+      auto load_piece = [&](int i, uint32_t (&v)[4][8]) {
         const int col = (half * kPieces + i) * 32;                           // 8 j of each c: columns 128 x + 8 (col / 32 % 4) + j + 32 c
-        uint32_t v[4][8];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_load_32x32b_x8(from + col / 128 * 128 + col % 128 / 4 + 32 * c, v[c]);
+      };
+      auto release = [&]() {
+        tmem_load_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(&acc_empty[acc], 0));
+      };
+      if constexpr (kAccum == 1) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) load_piece(i, held[i]);
+        release();
+      }
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int col = (half * kPieces + i) * 32;
+        uint32_t(&v)[4][8] = held[kAccum == 1 ? i : 0];
+        if constexpr (kAccum > 1) load_piece(i, v);
         uint4 add[4];
         if constexpr (kHasC) {
 #pragma unroll
@@ -429,12 +447,11 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
             add[r] = (live_rows >> (first + 8 * r) & 1) && tile.n0 + col + 8 * unit < p.N
                          ? ld_cg_v4(p.c + d0 + static_cast<size_t>(32 * r) * p.N + col) : make_uint4(0, 0, 0, 0);
         }
-        tmem_load_wait();
-        if (i == kPieces - 1) {
-          // the accumulator is free
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_rank(&acc_empty[acc], 0));
+        if constexpr (kAccum > 1) {
+          if (i == kPieces - 1)
+            release();
+          else
+            tmem_load_wait();
         }
         // 16-byte unit u of staging row r at r * 64 + (u ^ (r / 2 % 4)) * 16
         auto at = [&](int r, int u) { return staging + r * 64 + ((u ^ (r >> 1 & 3)) << 4); };

@@ -1,4 +1,4 @@
-// Scalar helpers of the scale and element formats, shared by the kernels around the GEMMs.
+// Scalar helpers of the scale and element formats and of exponentials, shared by the kernels around the GEMMs.
 #pragma once
 
 #include <cstdint>
@@ -41,5 +41,18 @@ __device__ __forceinline__ void unpack_bf16(uint32_t w, float& a, float& b) {
   a = __uint_as_float(w << 16);
   b = __uint_as_float(w & 0xFFFF0000u);
 }
+
+// 2^v and 1 / v within two units of the last place (results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 }  // namespace dg
