@@ -275,11 +275,11 @@ dg_status quantize(const void* x, const int32_t* masked_m, void* q, int32_t* sf,
   constexpr int kPerRow = kGate ? 2 : 1;
   if (dg_status s = check(x, masked_m, q, sf, desc, kPerRow); s != DG_OK) return s;
   if (desc->M == 0) return DG_OK;
-  LaunchContext ctx;
-  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   // (4 divides the tile's rows, so the padding rows of sf are within the last tile)
   Tiles n;
   if (!n.count(*desc, kTileRows, kTileCols)) return DG_ERR_UNSUPPORTED;
+  LaunchContext ctx;
+  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   const QuantArgs a{x, masked_m, static_cast<uint8_t*>(q), sf, ctx.status, n.all, n.row, n.col, desc->M, desc->K,
                     desc->M + (4 - desc->M % 4) % 4, row_stride(*desc, kPerRow), group_stride(*desc)};
   const unsigned grid = n.blocks();
@@ -306,10 +306,10 @@ dg_status dg_swiglu_backward(const void* x, const void* dy, const int32_t* maske
                              cudaStream_t stream) {
   if (dg_status s = check(x, masked_m, dy, static_cast<const int32_t*>(dx), desc, 2); s != DG_OK) return s;
   if (desc->M == 0) return DG_OK;
-  LaunchContext ctx;
-  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   Tiles n;
   if (!n.count(*desc, kGradRows, kGradCols)) return DG_ERR_UNSUPPORTED;
+  LaunchContext ctx;
+  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   const SwigluGradArgs a{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dx),
                          masked_m, ctx.status, n.all, n.row, n.col, desc->M, desc->K, row_stride(*desc, 2), group_stride(*desc)};
   return dg::launch(swiglu_grad_kernel, n.blocks(), kWarps * 32, 0, stream, ctx.pdl, a);
