@@ -71,6 +71,11 @@ def values(packed, sf):
     return decode_e2m1(unpack_e2m1(packed, K)) * np.repeat(s, BLOCK, -1)
 
 
+def values_of(codes, e):
+    """Values of codes [..., K] and scale codes [..., K/32]."""
+    return decode_e2m1(codes) * np.repeat(decode_ue8m0(e), BLOCK, -1)
+
+
 def swiglu(x):
     gate, up = np.split(np.asarray(x, np.float64), 2, axis=-1)
     return gate / (1 + np.exp(-gate)) * up
