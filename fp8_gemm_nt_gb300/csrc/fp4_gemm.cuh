@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "ue8m0.cuh"
@@ -84,25 +85,64 @@ __device__ __forceinline__ void arrange_scales(uint32_t at, uint32_t lane) {
   for (int c = 0; c < kChunks; ++c) st_shared_v4(at + 512 * c + 16 * lane, w[c][0], w[c][1], w[c][2], w[c][3]);
 }
 
-// Sixteen columns of a row of D: v, and C's where there is one, rounded to BF16.
-__device__ __forceinline__ void store_columns(const Params& p, size_t at, const uint32_t* bits) {
-  uint32_t w[8];
-  if (p.c) {
-    const uint4 lo = ld_cg_v4(p.c + at), hi = ld_cg_v4(p.c + at + 8);
-    const uint32_t cw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float a, b;
-      unpack_bf16(cw[i], a, b);
-      w[i] = pack_bf16(a + __uint_as_float(bits[2 * i]), b + __uint_as_float(bits[2 * i + 1]));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(__uint_as_float(bits[2 * i]), __uint_as_float(bits[2 * i + 1]));
+// A warp's piece of D: 32 rows of 32 columns, a row of the accumulator in each lane, through 2 KB of shared memory, so
+// that its rows (and C's) are read and written in pieces of 64 bytes, eight rows at a time. Row i of the piece is row
+// `kStep` i of D from d0's; lane l reads and writes 16 bytes of rows l / 4 + 8 r.
+template <int kStep>
+struct Piece {
+  const Params& p;
+  uint32_t staging, lane, live;            // live: rows that are written
+  size_t d0;                               // of row lane / 4, at the piece's first column + 8 (lane % 4)
+
+  __device__ __forceinline__ size_t at(int r, int col) const { return d0 + static_cast<size_t>(8 * kStep * r) * p.N + col; }
+  __device__ __forceinline__ bool mine(int r, int col, int n0) const {
+    return (live >> (lane / 4 + 8 * r) & 1) && n0 + col + 8 * static_cast<int>(lane % 4) < p.N;
   }
-  st_global_v4(p.d + at, w[0], w[1], w[2], w[3]);
-  st_global_v4(p.d + at + 8, w[4], w[5], w[6], w[7]);
-}
+  // 16-byte unit u of row r
+  __device__ __forceinline__ uint32_t unit(int r, int u) const { return staging + r * 64 + ((u ^ (r >> 1 & 3)) << 4); }
+
+  // C of the piece at column col of the tile, whose first is n0.
+  __device__ __forceinline__ void load_c(uint4 (&c)[4], int col, int n0) const {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c[r] = mine(r, col, n0) ? ld_cg_v4(p.c + at(r, col)) : make_uint4(0, 0, 0, 0);
+  }
+  // value(i): column i of this lane's row. c: C's share as load_c left it, and then that of the next piece, if there is
+  // one: at column next_col of the tile that `next` belongs to.
+  template <bool kHasC, class Value>
+  __device__ __forceinline__ void store(int col, int n0, uint4 (&c)[4], bool more, const Piece& next, int next_col, int next_n0, Value value) const {
+    const int row = lane, own = lane % 4, first = lane / 4;
+    if constexpr (kHasC) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) st_shared_v4(unit(first + 8 * r, own), c[r].x, c[r].y, c[r].z, c[r].w);
+      __syncwarp();
+      if (more) next.load_c(c, next_col, next_n0);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(value(8 * u + e));
+      if constexpr (kHasC) {
+        const uint4 cv = ld_shared_v4(unit(row, u));
+        const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x, y;
+          unpack_bf16(cw[e], x, y);
+          f[2 * e] += x, f[2 * e + 1] += y;
+        }
+      }
+      st_shared_v4(unit(row, u), pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint4 w = ld_shared_v4(unit(first + 8 * r, own));
+      if (mine(r, col, n0)) st_global_v4(p.d + at(r, col), w.x, w.y, w.z, w.w);
+    }
+    __syncwarp();
+  }
+};
 
 // ------------------------------------------------------------------------------------
 // CTA pairs
@@ -390,15 +430,31 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
   } else if (warp >= 4) {
     const int quad = warp % 4, half = (warp - 4) / 4;
     const uint32_t staging = smem_addr(smem + S::OFF_EPI + (warp - 4) * S::EPI_BYTES);
-    uint32_t tiles = 0;
-    while (walk.next(p, tile)) {
-      const uint32_t acc = tiles % kAccum;
-      if (!warp_wait(&acc_full[acc], tiles / kAccum & 1, p.timeout_ns, abort_flag)) {
-        if (lane == 0) on_timeout();
-        break;
+    constexpr int kPieces = BN / 64;                                         // of 32 columns, for each of the two halves
+    // with C: a tile's arrives while the tile before it is written
+    auto piece_of = [&](const Tile& t, uint32_t live_rows) {
+      return Piece<4>{p, staging, lane, live_rows,
+                      (static_cast<size_t>(t.ga) * p.M + t.m0 + static_cast<int>(rank) * kRows + 4 * (lane / 4) + quad) * p.N + t.n0 + 8 * (lane % 4)};
+    };
+    auto dense_rows = [&](const Tile& t) { return __ballot_sync(0xffffffffu, static_cast<int>(rank) * kRows + 4 * static_cast<int>(lane) + quad < t.valid); };
+    uint4 c[kPieces][4];
+    Tile ahead;
+    bool more = false;
+    if constexpr (kHasC) {
+      static_assert(kForm == Form::Dense, "C: the dense form");
+      more = walk.next(p, ahead);
+      if (more) {
+        const Piece<4> d = piece_of(ahead, dense_rows(ahead));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) d.load_c(c[i], (half * kPieces + i) * 32, ahead.n0);
       }
-      ++tiles;
-      tc_fence_after();
+    }
+    uint32_t tiles = 0;
+    while (kHasC ? more : walk.next(p, tile)) {
+      if constexpr (kHasC) {
+        tile = ahead;
+        more = walk.next(p, ahead);
+      }
       const int m0 = tile.m0 + static_cast<int>(rank) * kRows;
       const int valid = tile.valid - static_cast<int>(rank) * kRows;        // of this CTA's rows
       const int mine = 4 * static_cast<int>(lane) + quad;                    // the row of this lane's accumulators
@@ -411,13 +467,18 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
         }
       }
       const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
-      // pieces leave eight rows at a time: this lane's 16 bytes of row 4 (lane / 4 + 8 i) + quad
-      const int unit = static_cast<int>(lane) % 4, first = static_cast<int>(lane) / 4;
-      const size_t d0 = (static_cast<size_t>(tile.ga) * p.M + m0 + 4 * first + quad) * p.N + tile.n0 + 8 * unit;
+      const Piece<4> d = piece_of(tile, live_rows), later = piece_of(ahead, kHasC && more ? dense_rows(ahead) : 0u);
+      const uint32_t acc = tiles % kAccum;
+      if (!warp_wait(&acc_full[acc], tiles / kAccum & 1, p.timeout_ns, abort_flag)) {
+        if (lane == 0) on_timeout();
+        break;
+      }
+      ++tiles;
+      tc_fence_after();
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
-      constexpr int kPieces = BN / 64;                                       // of 32 columns, for each of the two halves
-      // one accumulator: all of the warp's share at once, then it is free; two: piece by piece
-      constexpr int kHeld = kAccum == 1 ? kPieces : 1;
+      // one accumulator, no C: all of the warp's share at once, then it is free; else piece by piece
+      constexpr bool kAtOnce = kAccum == 1 && !kHasC;
+      constexpr int kHeld = kAtOnce ? kPieces : 1;
       uint32_t held[kHeld][4][8];
       auto load_piece = [&](int i, uint32_t (&v)[4][8]) {
         const int col = (half * kPieces + i) * 32;                           // 8 j of each c: columns 128 x + 8 (col / 32 % 4) + j + 32 c
@@ -430,62 +491,24 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_to_rank(&acc_empty[acc], 0));
       };
-      if constexpr (kAccum == 1) {
+      if constexpr (kAtOnce) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) load_piece(i, held[i]);
+        for (int i = 0; i < kHeld; ++i) load_piece(i, held[i]);
         release();
       }
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int col = (half * kPieces + i) * 32;
-        uint32_t(&v)[4][8] = held[kAccum == 1 ? i : 0];
-        if constexpr (kAccum > 1) load_piece(i, v);
-        uint4 add[4];
-        if constexpr (kHasC) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            add[r] = (live_rows >> (first + 8 * r) & 1) && tile.n0 + col + 8 * unit < p.N
-                         ? ld_cg_v4(p.c + d0 + static_cast<size_t>(32 * r) * p.N + col) : make_uint4(0, 0, 0, 0);
-        }
-        if constexpr (kAccum > 1) {
+        uint32_t(&v)[4][8] = held[kAtOnce ? i : 0];
+        if constexpr (!kAtOnce) {
+          load_piece(i, v);
           if (i == kPieces - 1)
             release();
           else
             tmem_load_wait();
         }
-        // 16-byte unit u of staging row r at r * 64 + (u ^ (r / 2 % 4)) * 16
-        auto at = [&](int r, int u) { return staging + r * 64 + ((u ^ (r >> 1 & 3)) << 4); };
-        if constexpr (kHasC) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) st_shared_v4(at(first + 8 * r, unit), add[r].x, add[r].y, add[r].z, add[r].w);
-          __syncwarp();
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          // columns 8 u .. 8 u + 7: j = 2 u and 2 u + 1, c = 0 .. 3 of each
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[e & 3][2 * u + (e >> 2)]);
-          if constexpr (kHasC) {
-            const uint4 cv = ld_shared_v4(at(lane, u));
-            const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x, y;
-              unpack_bf16(cw[e], x, y);
-              f[2 * e] += x, f[2 * e + 1] += y;
-            }
-          }
-          st_shared_v4(at(lane, u), pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-        }
-        __syncwarp();
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint4 w = ld_shared_v4(at(first + 8 * r, unit));
-          if ((live_rows >> (first + 8 * r) & 1) && tile.n0 + col + 8 * unit < p.N)
-            st_global_v4(p.d + d0 + static_cast<size_t>(32 * r) * p.N + col, w.x, w.y, w.z, w.w);
-        }
-        __syncwarp();
+        // column i of the piece: j = i / 4 of the eight, c = i % 4
+        d.template store<kHasC>(col, tile.n0, c[i], kHasC && more, later, col, ahead.n0, [&](int at) { return v[at & 3][at >> 2]; });
       }
     }
   }
@@ -527,7 +550,7 @@ struct SplitShape {
 //   warp 0     TMA      warp 1     copies scales to TMEM and issues the MMAs     warp 2     arranges the scale words
 //   warps 4..  TMEM to D (kWays = 1) or to the partial sum
 template <int BN, int kStages, int kWays>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 1)
     fp4_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb, const Params p) {
   using S = SplitShape<BN, kStages>;
@@ -664,21 +687,35 @@ __global__ void __launch_bounds__(256)
       if (lane == 0) on_timeout();
     } else if (m0 + quad * 32 < p.M) {
       tc_fence_after();
-      const bool live = m0 + row < p.M;
-      const size_t at = static_cast<size_t>(m0 + row) * p.N + n0;
-      float* const partial = reinterpret_cast<float*>(smem) + row * S::kLd;
+      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+      if constexpr (kWays == 1) {
+        // (the ring is idle)
+        const Piece<1> d{p, smem_addr(smem) + quad * 2048, lane, __ballot_sync(0xffffffffu, m0 + row < p.M),
+                         static_cast<size_t>(m0 + quad * 32 + lane / 4) * p.N + n0 + 8 * (lane % 4)};
+        auto write = [&](auto has_c) {
+          constexpr bool kHasC = decltype(has_c)::value;
+          uint4 c[4] = {};
+          if constexpr (kHasC) d.load_c(c, 0, n0);
 #pragma unroll
-      for (int piece = 0; piece < BN / 32; ++piece) {
-        uint32_t v[32];
-        tmem_load_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + 32 * piece, v);
-        tmem_load_wait();
-        if (!live) continue;
-        if constexpr (kWays == 1) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (n0 + 32 * piece + 16 * h < p.N) store_columns(p, at + 32 * piece + 16 * h, v + 16 * h);
+          for (int piece = 0; piece < BN / 32; ++piece) {
+            uint32_t v[32];
+            tmem_load_32x32b_x32(from + 32 * piece, v);
+            tmem_load_wait();
+            d.template store<kHasC>(32 * piece, n0, c, piece + 1 < BN / 32, d, 32 * piece + 32, n0, [&](int at) { return v[at]; });
           }
-        } else {
+        };
+        if (p.c)
+          write(std::true_type());
+        else
+          write(std::false_type());
+      } else {
+        float* const partial = reinterpret_cast<float*>(smem) + row * S::kLd;
+#pragma unroll
+        for (int piece = 0; piece < BN / 32; ++piece) {
+          uint32_t v[32];
+          tmem_load_32x32b_x32(from + 32 * piece, v);
+          tmem_load_wait();
+          // (rows past the last are zeros, which no one reads)
 #pragma unroll
           for (int i = 0; i < 32; i += 4) st_shared_v4(smem_addr(partial + 32 * piece + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
