@@ -39,6 +39,13 @@ bool apart_map(CUtensorMap* m, const void* base, int G, int rows, int K, int of_
   const uint32_t box[4] = {128, 32, static_cast<uint32_t>(of_four), 1};
   return dg::tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
+// D [G, rows, N] the same way, in boxes of 32 columns of 32 rows four apart.
+bool out_map(CUtensorMap* m, void* base, int G, int rows, int N) {
+  const uint64_t bytes = static_cast<uint64_t>(N) * 2;
+  const uint64_t dims[4] = {static_cast<uint64_t>(N), static_cast<uint64_t>(rows / 4), 4, static_cast<uint64_t>(G)}, strides[3] = {4 * bytes, bytes, bytes * rows};
+  const uint32_t box[4] = {32, 32, 1, 1};
+  return dg::tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
 // All rows, in boxes of every fourth of 128.
 bool every_fourth_map(CUtensorMap* m, const void* base, int G, int rows, int K) {
   const uint64_t bytes = static_cast<uint64_t>(K) / 2;
@@ -87,19 +94,19 @@ dg_status launch(Kernel kernel, int smem, int grid, int threads, int cluster, cu
 // pair_rows: 256-row strips of all groups, or a bound of their number.
 template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
 dg_status run_pair(const LaunchContext& ctx, const Operands& o, const Params& p, long long pair_rows, cudaStream_t stream) {
-  using S = dg::fp4::PairShape<BN, kAccum, kStages>;
+  using S = dg::fp4::PairShape<BN, kAccum, kStages, kHasC>;
   const int ga = kForm == Form::Masked ? p.G : 1, gb = kForm == Form::Dense ? 1 : p.G;
-  CUtensorMap ta, ta_edge, tb, tsa, tsb;
+  CUtensorMap ta, ta_edge, tb, tsa, tsb, td;
   if (!every_fourth_map(&ta_edge, o.a, ga, p.M, p.K) || !apart_map(&tb, o.b, gb, p.N, p.K, BN / 64) || !scales_map(&tsa, o.sfa, ga, p.M, p.K, kRowBox) ||
       !scales_map(&tsb, o.sfb, gb, p.N, p.K, BN))
     return DG_ERR_CUDA;
-  ta = ta_edge;      // (where A has fewer than four rows, none of its tiles is an inner one)
-  if (p.M >= 4 && !apart_map(&ta, o.a, ga, p.M, p.K, 4)) return DG_ERR_CUDA;
+  ta = td = ta_edge;      // (where A has fewer than four rows, none of its tiles is an inner one)
+  if (p.M >= 4 && (!apart_map(&ta, o.a, ga, p.M, p.K, 4) || !out_map(&td, p.d, ga, p.M, p.N))) return DG_ERR_CUDA;
   const long long tiles = pair_rows * up(p.N, BN);
   if (tiles > (1ll << 30)) return DG_ERR_UNSUPPORTED;
   const int clusters = static_cast<int>(std::min<long long>(std::max(1, ctx.sms / 2), tiles));
   return launch(dg::fp4::fp4_pair_kernel<kForm, BN, kAccum, kStages, kHasC>, S::smem(kForm), 2 * clusters, S::kThreads, 2, stream, ctx.pdl, ta,
-                ta_edge, tb, tsa, tsb, p);
+                ta_edge, tb, tsa, tsb, td, p);
 }
 
 template <int BN, int kStages, int kWays>
@@ -176,7 +183,7 @@ dg_status dense(const LaunchContext& ctx, const Operands& o, const Params& p, cu
   for (const Way& w : kDenseWays)
     if (const double t = estimate(w, p, ctx.sms); t < least) best = w, least = t;
   switch (best.bn * 10 + best.ways) {
-    case 1280: return run_pair<Form::Dense, 128, 2, 8, kHasC>(ctx, o, p, up(p.M, 256), stream);
+    case 1280: return run_pair<Form::Dense, 128, 2, kHasC ? 6 : 8, kHasC>(ctx, o, p, up(p.M, 256), stream);
     case 641: return run_split<64, 6, 1>(ctx, o, p, stream);
     case 642: return run_split<64, 6, 2>(ctx, o, p, stream);
     case 644: return run_split<64, 6, 4>(ctx, o, p, stream);
@@ -185,7 +192,7 @@ dg_status dense(const LaunchContext& ctx, const Operands& o, const Params& p, cu
     case 1282: return run_split<128, 6, 2>(ctx, o, p, stream);
     case 1921: return run_split<192, 5, 1>(ctx, o, p, stream);
   }
-  return run_pair<Form::Dense, 256, 1, 6, kHasC>(ctx, o, p, up(p.M, 256), stream);
+  return run_pair<Form::Dense, 256, 1, kHasC ? 5 : 6, kHasC>(ctx, o, p, up(p.M, 256), stream);
 }
 
 }  // namespace

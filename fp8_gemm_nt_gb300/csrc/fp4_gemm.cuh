@@ -85,45 +85,56 @@ __device__ __forceinline__ void arrange_scales(uint32_t at, uint32_t lane) {
   for (int c = 0; c < kChunks; ++c) st_shared_v4(at + 512 * c + 16 * lane, w[c][0], w[c][1], w[c][2], w[c][3]);
 }
 
-// A warp's piece of D: 32 rows of 32 columns, a row of the accumulator in each lane, through 2 KB of shared memory, so
-// that its rows (and C's) are read and written in pieces of 64 bytes, eight rows at a time. Row i of the piece is row
-// `kStep` i of D from d0's; lane l reads and writes 16 bytes of rows l / 4 + 8 r.
-template <int kStep>
-struct Piece {
+// A warp's pieces of D, of 32 rows of 32 columns, a row of the accumulator in each lane. A piece goes through 2 KB of
+// shared memory, from where it leaves by TMA, or, where not all of its rows are written, in runs of 64 bytes, eight rows
+// at a time. C comes the same way, in runs, the copies of two pieces on their way at once. Row i of a piece is row kStep i
+// of D from d0's; lane l reads and writes 16 bytes of rows l / 4 + 8 r.
+constexpr int kPieceBytes = 32 * 64;
+template <int kStep, bool kHasC>
+struct Pieces {
+  static constexpr int kBytes = (kHasC ? 3 : 1) * kPieceBytes;
   const Params& p;
-  uint32_t staging, lane, live;            // live: rows that are written
-  size_t d0;                               // of row lane / 4, at the piece's first column + 8 (lane % 4)
+  uint32_t smem, lane, live;               // live: rows that are written
+  int n0;                                  // first column of the tile
+  size_t d0;                               // of row lane / 4, at column n0 + 8 (lane % 4)
 
   __device__ __forceinline__ size_t at(int r, int col) const { return d0 + static_cast<size_t>(8 * kStep * r) * p.N + col; }
-  __device__ __forceinline__ bool mine(int r, int col, int n0) const {
+  __device__ __forceinline__ bool mine(int r, int col) const {
     return (live >> (lane / 4 + 8 * r) & 1) && n0 + col + 8 * static_cast<int>(lane % 4) < p.N;
   }
-  // 16-byte unit u of row r
-  __device__ __forceinline__ uint32_t unit(int r, int u) const { return staging + r * 64 + ((u ^ (r >> 1 & 3)) << 4); }
-
-  // C of the piece at column col of the tile, whose first is n0.
-  __device__ __forceinline__ void load_c(uint4 (&c)[4], int col, int n0) const {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) c[r] = mine(r, col, n0) ? ld_cg_v4(p.c + at(r, col)) : make_uint4(0, 0, 0, 0);
+  // 16-byte unit u of row r of a buffer (0: D's), in the 64-byte swizzle
+  __device__ __forceinline__ uint32_t unit(int buffer, int r, int u) const {
+    return smem + buffer * kPieceBytes + r * 64 + ((u ^ (r >> 1 & 3)) << 4);
   }
-  // value(i): column i of this lane's row. c: C's share as load_c left it, and then that of the next piece, if there is
-  // one: at column next_col of the tile that `next` belongs to.
-  template <bool kHasC, class Value>
-  __device__ __forceinline__ void store(int col, int n0, uint4 (&c)[4], bool more, const Piece& next, int next_col, int next_n0, Value value) const {
-    const int row = lane, own = lane % 4, first = lane / 4;
+  // Begins to copy C of the i-th piece, at column col of the tile. Every piece is fetched in its turn, at most one ahead of
+  // the piece before the one that is written next.
+  __device__ __forceinline__ void fetch(int i, int col) const {
     if constexpr (kHasC) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) st_shared_v4(unit(first + 8 * r, own), c[r].x, c[r].y, c[r].z, c[r].w);
-      __syncwarp();
-      if (more) next.load_c(c, next_col, next_n0);
+      for (int r = 0; r < 4; ++r)
+        if (mine(r, col)) cp_async_16(unit(1 + (i & 1), lane / 4 + 8 * r, lane % 4), p.c + at(r, col));
+      cp_async_commit();
     }
+  }
+  // Writes the i-th of `count` pieces, at column col. value(j): column j of this lane's row. tma(): sends the piece, if `whole`.
+  template <class Value, class Tma>
+  __device__ __forceinline__ void write(int i, int count, int col, bool whole, Value value, Tma tma) const {
+    const int row = lane, own = lane % 4, first = lane / 4;
+    if (lane == 0) bulk_wait_group_read<0>();      // the last piece has left
+    if constexpr (kHasC) {
+      if (i + 1 < count)
+        cp_async_wait<1>();
+      else
+        cp_async_wait<0>();
+    }
+    __syncwarp();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(value(8 * u + e));
       if constexpr (kHasC) {
-        const uint4 cv = ld_shared_v4(unit(row, u));
+        const uint4 cv = ld_shared_v4(unit(1 + (i & 1), row, u));
         const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -132,15 +143,23 @@ struct Piece {
           f[2 * e] += x, f[2 * e + 1] += y;
         }
       }
-      st_shared_v4(unit(row, u), pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+      st_shared_v4(unit(0, row, u), pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
     }
+    if (whole) fence_proxy_async_smem();
     __syncwarp();
+    if (whole) {
+      if (lane == 0) {
+        tma();
+        bulk_commit_group();
+      }
+    } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint4 w = ld_shared_v4(unit(first + 8 * r, own));
-      if (mine(r, col, n0)) st_global_v4(p.d + at(r, col), w.x, w.y, w.z, w.w);
+      for (int r = 0; r < 4; ++r) {
+        const uint4 w = ld_shared_v4(unit(0, first + 8 * r, own));
+        if (mine(r, col)) st_global_v4(p.d + at(r, col), w.x, w.y, w.z, w.w);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 };
 
@@ -152,14 +171,14 @@ struct Piece {
 // 4 j + c of the tile. TMA loads them in that order, through a map that takes four rows apart ([rows / 4] of every
 // fourth row, then the four); a lane of the accumulator is row 4 lane + quadrant, and its columns 32 c + j, c = 0 .. 3,
 // are columns 4 j + c of D. Rows of A past the last whole four go by a second map, of every fourth row from a given one.
-template <int kBN, int kAccums, int kStages_>
+template <int kBN, int kAccums, int kStages_, bool kHasC>
 struct PairShape {
   static constexpr int BN = kBN, kAccum = kAccums, kStages = kStages_;
   static constexpr int kEpilogueWarps = 8, kThreads = (4 + kEpilogueWarps) * 32;
   static constexpr int kChunks = BN / 128;                          // of 128 scale words of B
   static constexpr int A_BYTES = kRows * 128, B_BYTES = BN / 2 * 128;
   static constexpr int SFA_BYTES = 2 * 512, SFB_BYTES = 2 * kChunks * 512, SF_BYTES = SFA_BYTES + SFB_BYTES;
-  static constexpr int EPI_BYTES = 32 * 64;                         // of a warp: 32 rows of 32 columns
+  static constexpr int EPI_BYTES = Pieces<4, kHasC>::kBytes;        // of a warp
   static constexpr int OFF_B = kStages * A_BYTES, OFF_SF = OFF_B + kStages * B_BYTES, OFF_EPI = OFF_SF + kStages * SF_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + kEpilogueWarps * EPI_BYTES;
   // TMEM: the accumulators, then a buffer of scales for each stage
@@ -232,11 +251,11 @@ struct Walk {
 //   warps 4..  epilogue: 32 columns at a time from TMEM to registers to the warp's staging buffer, from which D's rows
 //              leave in pieces of 64 bytes
 template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
-__global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
+__global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_edge,
                     const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_sfa,
-                    const __grid_constant__ CUtensorMap tm_sfb, const Params p) {
-  using S = PairShape<BN, kAccum, kStages>;
+                    const __grid_constant__ CUtensorMap tm_sfb, const __grid_constant__ CUtensorMap tm_d, const Params p) {
+  using S = PairShape<BN, kAccum, kStages, kHasC>;
   extern __shared__ __align__(1024) uint8_t smem[];   // at a multiple of 1024: nothing static lies before it
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);   // leader: the stage of both CTAs
   uint64_t* const ready = full + kStages;          // leader: its scales are in TMEM
@@ -275,6 +294,7 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
     tma_prefetch_desc(&tm_b);
     tma_prefetch_desc(&tm_sfa);
     tma_prefetch_desc(&tm_sfb);
+    tma_prefetch_desc(&tm_d);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -431,30 +451,8 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
     const int quad = warp % 4, half = (warp - 4) / 4;
     const uint32_t staging = smem_addr(smem + S::OFF_EPI + (warp - 4) * S::EPI_BYTES);
     constexpr int kPieces = BN / 64;                                         // of 32 columns, for each of the two halves
-    // with C: a tile's arrives while the tile before it is written
-    auto piece_of = [&](const Tile& t, uint32_t live_rows) {
-      return Piece<4>{p, staging, lane, live_rows,
-                      (static_cast<size_t>(t.ga) * p.M + t.m0 + static_cast<int>(rank) * kRows + 4 * (lane / 4) + quad) * p.N + t.n0 + 8 * (lane % 4)};
-    };
-    auto dense_rows = [&](const Tile& t) { return __ballot_sync(0xffffffffu, static_cast<int>(rank) * kRows + 4 * static_cast<int>(lane) + quad < t.valid); };
-    uint4 c[kPieces][4];
-    Tile ahead;
-    bool more = false;
-    if constexpr (kHasC) {
-      static_assert(kForm == Form::Dense, "C: the dense form");
-      more = walk.next(p, ahead);
-      if (more) {
-        const Piece<4> d = piece_of(ahead, dense_rows(ahead));
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) d.load_c(c[i], (half * kPieces + i) * 32, ahead.n0);
-      }
-    }
     uint32_t tiles = 0;
-    while (kHasC ? more : walk.next(p, tile)) {
-      if constexpr (kHasC) {
-        tile = ahead;
-        more = walk.next(p, ahead);
-      }
+    while (walk.next(p, tile)) {
       const int m0 = tile.m0 + static_cast<int>(rank) * kRows;
       const int valid = tile.valid - static_cast<int>(rank) * kRows;        // of this CTA's rows
       const int mine = 4 * static_cast<int>(lane) + quad;                    // the row of this lane's accumulators
@@ -467,7 +465,13 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
         }
       }
       const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
-      const Piece<4> d = piece_of(tile, live_rows), later = piece_of(ahead, kHasC && more ? dense_rows(ahead) : 0u);
+      // (rows past the last whole four are in no four of the map)
+      const bool whole = live_rows == 0xffffffffu && m0 + kRows <= (p.M & ~3);
+      const Pieces<4, kHasC> d{p, staging, lane, live_rows, tile.n0,
+                               (static_cast<size_t>(tile.ga) * p.M + m0 + 4 * (lane / 4) + quad) * p.N + tile.n0 + 8 * (lane % 4)};
+      const int col0 = half * kPieces * 32;
+      d.fetch(0, col0);
+      d.fetch(1, col0 + 32);
       const uint32_t acc = tiles % kAccum;
       if (!warp_wait(&acc_full[acc], tiles / kAccum & 1, p.timeout_ns, abort_flag)) {
         if (lane == 0) on_timeout();
@@ -476,12 +480,12 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
       ++tiles;
       tc_fence_after();
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
-      // one accumulator, no C: all of the warp's share at once, then it is free; else piece by piece
-      constexpr bool kAtOnce = kAccum == 1 && !kHasC;
+      // one accumulator: all of the warp's share at once, then it is free; two: piece by piece
+      constexpr bool kAtOnce = kAccum == 1;
       constexpr int kHeld = kAtOnce ? kPieces : 1;
       uint32_t held[kHeld][4][8];
       auto load_piece = [&](int i, uint32_t (&v)[4][8]) {
-        const int col = (half * kPieces + i) * 32;                           // 8 j of each c: columns 128 x + 8 (col / 32 % 4) + j + 32 c
+        const int col = col0 + 32 * i;                                       // 8 j of each c: columns 128 x + 8 (col / 32 % 4) + j + 32 c
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_load_32x32b_x8(from + col / 128 * 128 + col % 128 / 4 + 32 * c, v[c]);
       };
@@ -498,7 +502,7 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
       }
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int col = (half * kPieces + i) * 32;
+        const int col = col0 + 32 * i;
         uint32_t(&v)[4][8] = held[kAtOnce ? i : 0];
         if constexpr (!kAtOnce) {
           load_piece(i, v);
@@ -508,9 +512,13 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages>::kThreads, 1)
             tmem_load_wait();
         }
         // column i of the piece: j = i / 4 of the eight, c = i % 4
-        d.template store<kHasC>(col, tile.n0, c[i], kHasC && more, later, col, ahead.n0, [&](int at) { return v[at & 3][at >> 2]; });
+        d.write(i, kPieces, col, whole, [&](int at) { return v[at & 3][at >> 2]; },
+                [&]() { tma_store_4d(&tm_d, staging, tile.n0 + col, m0 / 4, quad, tile.ga); });
+        if (i + 2 < kPieces) d.fetch(i, col + 64);
       }
     }
+    if constexpr (kHasC) cp_async_wait<0>();
+    if (lane == 0) bulk_wait_group_all();
   }
 
   __syncwarp();
@@ -690,18 +698,18 @@ __global__ void __launch_bounds__(256, 1)
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       if constexpr (kWays == 1) {
         // (the ring is idle)
-        const Piece<1> d{p, smem_addr(smem) + quad * 2048, lane, __ballot_sync(0xffffffffu, m0 + row < p.M),
-                         static_cast<size_t>(m0 + quad * 32 + lane / 4) * p.N + n0 + 8 * (lane % 4)};
         auto write = [&](auto has_c) {
-          constexpr bool kHasC = decltype(has_c)::value;
-          uint4 c[4] = {};
-          if constexpr (kHasC) d.load_c(c, 0, n0);
+          const Pieces<1, decltype(has_c)::value> d{p, smem_addr(smem) + quad * Pieces<1, true>::kBytes, lane, __ballot_sync(0xffffffffu, m0 + row < p.M), n0,
+                                                    static_cast<size_t>(m0 + quad * 32 + lane / 4) * p.N + n0 + 8 * (lane % 4)};
+          d.fetch(0, 0);
+          d.fetch(1, 32);
 #pragma unroll
           for (int piece = 0; piece < BN / 32; ++piece) {
             uint32_t v[32];
             tmem_load_32x32b_x32(from + 32 * piece, v);
             tmem_load_wait();
-            d.template store<kHasC>(32 * piece, n0, c, piece + 1 < BN / 32, d, 32 * piece + 32, n0, [&](int at) { return v[at]; });
+            d.write(piece, BN / 32, 32 * piece, false, [&](int at) { return v[at]; }, []() {});
+            if (piece + 2 < BN / 32) d.fetch(piece, 32 * piece + 64);
           }
         };
         if (p.c)
