@@ -96,9 +96,9 @@ template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
 dg_status run_pair(const LaunchContext& ctx, const Operands& o, const Params& p, long long pair_rows, cudaStream_t stream) {
   using S = dg::fp4::PairShape<BN, kAccum, kStages, kHasC>;
   const int ga = kForm == Form::Masked ? p.G : 1, gb = kForm == Form::Dense ? 1 : p.G;
-  CUtensorMap ta, ta_edge, tb, tsa, tsb, td;
-  if (!every_fourth_map(&ta_edge, o.a, ga, p.M, p.K) || !apart_map(&tb, o.b, gb, p.N, p.K, BN / 64) || !scales_map(&tsa, o.sfa, ga, p.M, p.K, kRowBox) ||
-      !scales_map(&tsb, o.sfb, gb, p.N, p.K, BN))
+  CUtensorMap ta, ta_edge, tb, tb_narrow, tsa, tsb, td;
+  if (!every_fourth_map(&ta_edge, o.a, ga, p.M, p.K) || !apart_map(&tb, o.b, gb, p.N, p.K, 4) || !apart_map(&tb_narrow, o.b, gb, p.N, p.K, 2) || !scales_map(&tsa, o.sfa, ga, p.M, p.K, kRowBox) ||
+      !scales_map(&tsb, o.sfb, gb, p.N, p.K, S::kSfBox))
     return DG_ERR_CUDA;
   ta = td = ta_edge;      // (where A has fewer than four rows, none of its tiles is an inner one)
   if (p.M >= 4 && (!apart_map(&ta, o.a, ga, p.M, p.K, 4) || !out_map(&td, p.d, ga, p.M, p.N))) return DG_ERR_CUDA;
@@ -106,7 +106,7 @@ dg_status run_pair(const LaunchContext& ctx, const Operands& o, const Params& p,
   if (tiles > (1ll << 30)) return DG_ERR_UNSUPPORTED;
   const int clusters = static_cast<int>(std::min<long long>(std::max(1, ctx.sms / 2), tiles));
   return launch(dg::fp4::fp4_pair_kernel<kForm, BN, kAccum, kStages, kHasC>, S::smem(kForm), 2 * clusters, S::kThreads, 2, stream, ctx.pdl, ta,
-                ta_edge, tb, tsa, tsb, td, p);
+                ta_edge, tb, tb_narrow, tsa, tsb, td, p);
 }
 
 template <int BN, int kStages, int kWays>
@@ -149,41 +149,62 @@ __global__ void __launch_bounds__(256) pair_list_kernel(const dg::PairListArgs a
   dg::build_pair_list(a);
 }
 
-// Ways to run a dense product: a CTA pair's tiles in turn, or one tile to a CTA or to a cluster that shares out K.
-struct Way {
-  int bn, ways;     // ways 0: CTA pairs
-};
-constexpr Way kDenseWays[] = {{256, 0}, {128, 0}, {64, 1}, {64, 2}, {64, 4}, {96, 2}, {128, 1}, {128, 2}, {192, 1}};
+// Estimated microseconds of a product by CTA pairs with tiles of bn columns, from what the kernel was measured at: a launch
+// 4.5, then for each tile of a pair a start and a time for each stage of 256 K, no less than its output takes, and no less
+// than its share of B takes from HBM. pair_rows: 256-row strips; sharing: how many of them read the same of B. Widths 256,
+// 384 and 128 in us: 8 experts, 32768 x 4096 x 7168 278, 307, 429; of 8 x 32768 x 4096 x 512 89, 76, 116; masked 32 x 256 x
+// 7168 x 2048 67, 60, 70; 4096 x 24576 x 1536 72, 77, 92; 512 x 4096 x 7168 14.2, 20, 12.2.
+double pair_time(int bn, const Params& p, double pair_rows, double sharing, int sms) {
+  const int stages = up(p.K, dg::fp4::kStageK), clusters = std::max(1, sms / 2);
+  const double tiles = pair_rows * up(p.N, bn), waves = std::ceil(tiles / clusters);
+  const double tile = bn == 256 ? std::max(3.3, 1.4 + 0.3 * stages) : bn == 384 ? 2.6 + 0.47 * stages : std::max(2.0, 1.0 + 0.25 * stages);
+  const double bytes = std::min<double>(tiles, clusters) / sharing * bn * (p.K * 0.53125);
+  return 4.5 + waves * std::max(tile, 1.6 + bytes / 6.2e6);
+}
 
-// Estimated microseconds, from the rates that the kernels were measured at: a stage of 256 K costs an SM 0.19 us or the
-// time of its bytes from L2 (91 GB/s an SM; rows of 128 bytes and 8 of scales) or, all CTAs' together, of B's from HBM
-// (6 TB/s); a launch 3 us, a cluster's sums 0.3 us and 20 KB a microsecond, the last drain of a pair's accumulator 1 us.
-// Its choice against every way on its own, in us (128 x 7168 x 16384: 17.1, others 17.6 to 28; 128 x 256 x 512: 2.7, 2.8
-// to 4.9; 128 x 2048 x 16384: 11.0, 12.7 to 20; 512 x 4096 x 7168: 12.2, 12.7 to 22; 1000 x 4096 x 4096: 11.1, 11.7 to 30).
-double estimate(const Way& w, const Params& p, int sms) {
-  const int stages = up(p.K, dg::fp4::kStageK);
-  const double n = up(p.N, w.bn);
-  if (w.ways == 0) {
-    const double tiles = up(p.M, 256) * n, waves = std::ceil(tiles / std::max(1, sms / 2));
-    const double bytes = (128 + w.bn / 2) * 136.0 + w.bn / 2 * 8, stage = std::max(0.19, bytes / 91e3);
-    return 3.5 + waves * stages * stage + (w.bn == 256 ? waves : 1.0);
-  }
-  const double m_tiles = up(p.M, 128), ctas = m_tiles * n * w.ways;
-  // one wave; of clusters of four, three quarters of 152 SMs and more hold 36
+int pair_width(const Params& p, double pair_rows, double sharing, int sms) {
+  int best = 256;
+  for (int bn : {384, 128})
+    if (pair_time(bn, p, pair_rows, sharing, sms) < pair_time(best, p, pair_rows, sharing, sms)) best = bn;
+  return best;
+}
+
+// By width; stages as many as shared memory and, of the widest, TMEM hold.
+template <Form kForm, bool kHasC>
+dg_status run_pair_width(int bn, const LaunchContext& ctx, const Operands& o, const Params& p, long long pair_rows, cudaStream_t stream) {
+  constexpr bool kFew = kForm == Form::Masked;      // (its counts take a stage's room)
+  if (bn == 384) return run_pair<kForm, 384, 1, 4, kHasC>(ctx, o, p, pair_rows, stream);
+  if (bn == 128) return run_pair<kForm, 128, 2, kHasC ? 6 : kFew ? 7 : 8, kHasC>(ctx, o, p, pair_rows, stream);
+  return run_pair<kForm, 256, 1, kHasC || kFew ? 5 : 6, kHasC>(ctx, o, p, pair_rows, stream);
+}
+
+// Ways to run a dense product other than by CTA pairs: one tile to a CTA or to a cluster that shares out K.
+struct Split {
+  int bn, ways;
+};
+constexpr Split kSplits[] = {{64, 1}, {64, 2}, {64, 4}, {96, 2}, {128, 1}, {128, 2}, {192, 1}};
+
+// Estimated microseconds of one: a stage of 256 K costs an SM 0.19 us or the time of its bytes from L2 (91 GB/s an SM; rows
+// of 128 bytes and 8 of scales) or, all CTAs' together, of B's from HBM (6 TB/s); a launch 3 us, a cluster's sums 0.3 us and
+// 20 KB a microsecond. Its choice against every way on its own, in us (128 x 7168 x 16384: 16.9, others 17.5 to 28; 128 x
+// 256 x 512: 2.7, 2.8 to 4.9; 128 x 2048 x 16384: 11.0, 12.7 to 20).
+double split_time(const Split& w, const Params& p, int sms) {
+  const int stages = up(p.K, dg::fp4::kStageK), rows = std::min(p.M, 128);
+  const double m_tiles = up(p.M, 128), ctas = m_tiles * up(p.N, w.bn) * w.ways;
+  // one wave; of clusters of four, 152 SMs hold 36
   if (stages < w.ways || ctas > (w.ways == 4 ? 18 * (sms / 19) : sms / w.ways * w.ways)) return HUGE_VAL;
-  const int rows = std::min(p.M, 128);
   const double stage = std::max({0.19, (rows + w.bn) * 136.0 / 91e3, ctas / m_tiles * w.bn * 136.0 / 6e6});
   return 3.0 + up(stages, w.ways) * stage + (w.ways > 1 ? 0.3 + rows * w.bn * 4.0 / 20e3 : 0.0);
 }
 
 template <bool kHasC>
 dg_status dense(const LaunchContext& ctx, const Operands& o, const Params& p, cudaStream_t stream) {
-  Way best = kDenseWays[0];
-  double least = HUGE_VAL;
-  for (const Way& w : kDenseWays)
-    if (const double t = estimate(w, p, ctx.sms); t < least) best = w, least = t;
+  const int strips = up(p.M, 256), width = pair_width(p, strips, strips, ctx.sms);
+  double least = pair_time(width, p, strips, strips, ctx.sms);
+  Split best{0, 0};
+  for (const Split& w : kSplits)
+    if (const double t = split_time(w, p, ctx.sms); t < least) best = w, least = t;
   switch (best.bn * 10 + best.ways) {
-    case 1280: return run_pair<Form::Dense, 128, 2, kHasC ? 6 : 8, kHasC>(ctx, o, p, up(p.M, 256), stream);
     case 641: return run_split<64, 6, 1>(ctx, o, p, stream);
     case 642: return run_split<64, 6, 2>(ctx, o, p, stream);
     case 644: return run_split<64, 6, 4>(ctx, o, p, stream);
@@ -192,7 +213,7 @@ dg_status dense(const LaunchContext& ctx, const Operands& o, const Params& p, cu
     case 1282: return run_split<128, 6, 2>(ctx, o, p, stream);
     case 1921: return run_split<192, 5, 1>(ctx, o, p, stream);
   }
-  return run_pair<Form::Dense, 256, 1, kHasC ? 5 : 6, kHasC>(ctx, o, p, up(p.M, 256), stream);
+  return run_pair_width<Form::Dense, kHasC>(width, ctx, o, p, strips, stream);
 }
 
 }  // namespace
@@ -228,7 +249,9 @@ dg_status dg_m_grouped_fp4_gemm_nt_contiguous(const void* a, const int32_t* sfa,
   list.pair_count = static_cast<int*>(scratch), list.pair_list = list.pair_count + 4;
   if (dg_status s = dg::launch(pair_list_kernel, 1, 256, 0, stream, ctx.pdl, list); s != DG_OK) return s;
   p.m_indices = m_indices, p.pair_count = list.pair_count, p.pair_list = list.pair_list;
-  return run_pair<Form::Contiguous, 256, 1, 6, false>(ctx, o, p, blocks, stream);
+  // (strips as they are if every expert's rows fill them; a bound of their number sizes the grid)
+  const double strips = up(M_total, 256);
+  return run_pair_width<Form::Contiguous, false>(pair_width(p, strips, std::max(1.0, strips / G), ctx.sms), ctx, o, p, blocks, stream);
 }
 
 dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, void* d, const int32_t* masked_m,
@@ -242,7 +265,9 @@ dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const int32_t* sfa, con
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   Params p = params(ctx, nullptr, d, max_m, N, K, G);
   p.masked_m = masked_m;
-  return run_pair<Form::Masked, 256, 1, 5, false>(ctx, o, p, static_cast<long long>(G) * up(max_m, 256), stream);
+  // (the counts are on the device: half of the rows, say)
+  const double strips = up(up(max_m, 2), 256);
+  return run_pair_width<Form::Masked, false>(pair_width(p, G * strips, strips, ctx.sms), ctx, o, p, static_cast<long long>(G) * up(max_m, 256), stream);
 }
 
 }  // extern "C"

@@ -183,7 +183,12 @@ struct PairShape {
   static constexpr int OFF_BAR = OFF_EPI + kEpilogueWarps * EPI_BYTES;
   // TMEM: the accumulators, then a buffer of scales for each stage
   static constexpr int kSfCols = 8 + 8 * kChunks;
-  static_assert(BN % 128 == 0 && kAccum * BN + kStages * kSfCols <= 512, "TMEM columns");
+  static_assert(BN % 128 == 0 && BN <= 384 && kAccum * BN + kStages * kSfCols <= 512, "TMEM columns");
+  // B's columns by MMAs of 256, of which a CTA loads 128 rows, and a last one of 128 where BN has it, of which it loads 64
+  static constexpr int kWide = BN / 256;
+  static constexpr bool kNarrow = BN % 256 != 0;
+  // scale words of B: a copy has both words of up to 256 rows
+  static constexpr int kSfBox = BN <= 256 ? BN : 128;
   static constexpr int kBars = 3 * kStages + 2 * kAccum + 2;
   static constexpr int OFF_COUNTS = OFF_BAR + kBars * 8 + 16;
   static constexpr int smem(Form f) { return OFF_COUNTS + (f == Form::Masked ? kCountCache * 4 : 0); }
@@ -253,8 +258,9 @@ struct Walk {
 template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
 __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_edge,
-                    const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_sfa,
-                    const __grid_constant__ CUtensorMap tm_sfb, const __grid_constant__ CUtensorMap tm_d, const Params p) {
+                    const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_b_narrow,
+                    const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfb,
+                    const __grid_constant__ CUtensorMap tm_d, const Params p) {
   using S = PairShape<BN, kAccum, kStages, kHasC>;
   extern __shared__ __align__(1024) uint8_t smem[];   // at a multiple of 1024: nothing static lies before it
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);   // leader: the stage of both CTAs
@@ -345,8 +351,12 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThread
             uint8_t* const sf = smem + S::OFF_SF + stage * S::SF_BYTES;
             const uint32_t bar = map_to_rank(&full[stage], 0);
             if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-            tma_load_4d_pair(smem + S::OFF_B + stage * S::B_BYTES, &tm_b, bar, kb * 128, n0 / 4 + (BN == 256 ? static_cast<int>(rank) * 32 : 0),
-                             BN == 256 ? 0 : static_cast<int>(rank) * 2, tile.gb);
+            uint8_t* const b = smem + S::OFF_B + stage * S::B_BYTES;
+#pragma unroll
+            for (int w = 0; w < S::kWide; ++w)
+              tma_load_4d_pair(b + w * 128 * 128, &tm_b, bar, kb * 128, (n0 + 256 * w) / 4 + 32 * static_cast<int>(rank), 0, tile.gb);
+            if constexpr (S::kNarrow)
+              tma_load_4d_pair(b + S::kWide * 128 * 128, &tm_b_narrow, bar, kb * 128, (n0 + 256 * S::kWide) / 4, 2 * static_cast<int>(rank), tile.gb);
             if (rows) {
               if (inner) {
                 tma_load_4d_pair(a, &tm_a, bar, kb * 128, m0 / 4, 0, tile.ga);
@@ -356,7 +366,9 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThread
               }
               tma_load_3d_pair(sf, &tm_sfa, bar, m0, 2 * kb, tile.ga);
             }
-            tma_load_3d_pair(sf + S::SFA_BYTES, &tm_sfb, bar, n0, 2 * kb, tile.gb);
+#pragma unroll
+            for (int c = 0; c < BN / S::kSfBox; ++c)
+              tma_load_3d_pair(sf + S::SFA_BYTES + c * S::kSfBox * 8, &tm_sfb, bar, n0 + c * S::kSfBox, 2 * kb, tile.gb);
           }
           __syncwarp();
           ++issued;
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThread
     __syncwarp();
   } else if (warp == 1) {
     if (leader) {
-      constexpr uint32_t kIdesc = instruction(2 * kRows, BN);
+      constexpr uint32_t kWideMma = instruction(2 * kRows, 256), kNarrowMma = instruction(2 * kRows, 128);
       const uint64_t a0 = make_smem_desc(smem_addr(smem), 16, 1024, kLayoutSwizzle128B);
       const uint64_t b0 = make_smem_desc(smem_addr(smem + S::OFF_B), 16, 1024, kLayoutSwizzle128B);
       uint32_t tiles = 0;
@@ -398,9 +410,13 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThread
             const bool whole = p.K - kb * kStageK >= kStageK;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t id = 2u * (k & 1);
-              if (k < 2 || whole)
-                mma<true>(d, a + 2 * k, b + 2 * k, kIdesc | id << 4 | id << 29, sfa + 4 * (k / 2), sfb + 4 * S::kChunks * (k / 2), (kb | k) != 0);
+              if (k >= 2 && !whole) break;
+              const uint32_t id = 2u * (k & 1), ids = id << 4 | id << 29, sa = sfa + 4 * (k / 2), sb = sfb + 4 * S::kChunks * (k / 2);
+#pragma unroll
+              for (int w = 0; w < S::kWide; ++w)
+                mma<true>(d + 256 * w, a + 2 * k, b + (w * 128 * 128 >> 4) + 2 * k, kWideMma | ids, sa, sb + 8 * w, (kb | k) != 0);
+              if constexpr (S::kNarrow)
+                mma<true>(d + 256 * S::kWide, a + 2 * k, b + (S::kWide * 128 * 128 >> 4) + 2 * k, kNarrowMma | ids, sa, sb + 8 * S::kWide, (kb | k) != 0);
             }
             tc_commit_pair(&empty[stage]);
             if (kb == stages_k - 1) tc_commit_pair(&acc_full[acc]);
@@ -434,7 +450,12 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThread
             const uint32_t to = tmem + kAccum * BN + stage * S::kSfCols;
             const uint64_t from = sf0 + (stage * S::SF_BYTES >> 4);
 #pragma unroll
-            for (int c = 0; c < S::SF_BYTES / 512; ++c) tmem_copy_32x128b_warpx4_pair(to + 4 * c, from + 32 * c);
+            for (int c = 0; c < S::SF_BYTES / 512; ++c) {
+              // A's two words; then of B, for each copy, the first words of its chunks and the second ones
+              constexpr int kIn = S::kSfBox / 128;
+              const int x = c - 2, word = x / kIn % 2, chunk = x / (2 * kIn) * kIn + x % kIn;
+              tmem_copy_32x128b_warpx4_pair(to + (c < 2 ? 4 * c : 8 + 4 * (word * S::kChunks + chunk)), from + 32 * c);
+            }
             tc_commit_pair(&ready[stage]);
           }
           __syncwarp();
@@ -480,41 +501,32 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThread
       ++tiles;
       tc_fence_after();
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
-      // one accumulator: all of the warp's share at once, then it is free; two: piece by piece
-      constexpr bool kAtOnce = kAccum == 1;
-      constexpr int kHeld = kAtOnce ? kPieces : 1;
-      uint32_t held[kHeld][4][8];
-      auto load_piece = [&](int i, uint32_t (&v)[4][8]) {
-        const int col = col0 + 32 * i;                                       // 8 j of each c: columns 128 x + 8 (col / 32 % 4) + j + 32 c
+      // one accumulator: all of the warp's share at once (of a 384-wide tile half of it), then it is free; two: piece by piece
+      constexpr int kHeld = kAccum > 1 ? 1 : kPieces > 4 ? kPieces / 2 : kPieces;
+      static_assert(kPieces % kHeld == 0, "rounds of pieces");
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_load_32x32b_x8(from + col / 128 * 128 + col % 128 / 4 + 32 * c, v[c]);
-      };
-      auto release = [&]() {
-        tmem_load_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(&acc_empty[acc], 0));
-      };
-      if constexpr (kAtOnce) {
+      for (int begin = 0; begin < kPieces; begin += kHeld) {
+        uint32_t held[kHeld][4][8];
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) load_piece(i, held[i]);
-        release();
-      }
+        for (int i = 0; i < kHeld; ++i) {
+          const int col = col0 + 32 * (begin + i);                             // 8 j of each c: columns 128 x + 8 (col / 32 % 4) + j + 32 c
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int col = col0 + 32 * i;
-        uint32_t(&v)[4][8] = held[kAtOnce ? i : 0];
-        if constexpr (!kAtOnce) {
-          load_piece(i, v);
-          if (i == kPieces - 1)
-            release();
-          else
-            tmem_load_wait();
+          for (int c = 0; c < 4; ++c) tmem_load_32x32b_x8(from + col / 128 * 128 + col % 128 / 4 + 32 * c, held[i][c]);
         }
-        // column i of the piece: j = i / 4 of the eight, c = i % 4
-        d.write(i, kPieces, col, whole, [&](int at) { return v[at & 3][at >> 2]; },
-                [&]() { tma_store_4d(&tm_d, staging, tile.n0 + col, m0 / 4, quad, tile.ga); });
-        if (i + 2 < kPieces) d.fetch(i, col + 64);
+        tmem_load_wait();
+        if (begin + kHeld == kPieces) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(&acc_empty[acc], 0));
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          const int piece = begin + i, col = col0 + 32 * piece;
+          // column n of the piece: j = n / 4 of the eight, c = n % 4
+          d.write(piece, kPieces, col, whole, [&](int n) { return held[i][n & 3][n >> 2]; },
+                  [&]() { tma_store_4d(&tm_d, staging, tile.n0 + col, m0 / 4, quad, tile.ga); });
+          if (piece + 2 < kPieces) d.fetch(piece, col + 64);
+        }
       }
     }
     if constexpr (kHasC) cp_async_wait<0>();
