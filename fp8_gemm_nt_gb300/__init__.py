@@ -677,24 +677,28 @@ def dg_moe_balance_loss_backward(logits, counts, live_rows, dloss, dlogits, base
 # --------------------------------------------------------------------------------------
 
 def _fp4_rows(x, per, dtypes, masked_m):
-    """Device, (groups or None, rows, result columns), pointers of x and masked_m, descriptor."""
+    """Device, leading shape, rows, result columns, pointers of x and masked_m, descriptor."""
     dev = _device(x, "x")
-    shape = tuple(x.shape)
-    _need(len(shape) in (2, 3), "x must be [M, K] or [G, M, K]")
-    _need(x.dtype in dtypes, f"x must have type {' or '.join(str(d).replace('torch.', '') for d in dtypes)}")
-    _need(max(shape) <= _MAX_SIZE, f"x has a size above {_MAX_SIZE}: {shape}")
-    strides = x.stride()
-    _need(strides[-1] == 1 or shape[-1] == 1, "x must have contiguous columns")
-    _need(shape[-1] % (128 * per) == 0, f"x must have a multiple of {128 * per} columns")
-    M, K = shape[-2], shape[-1] // per
+    shape, strides = x.shape, x.stride()
     grouped = len(shape) == 3
+    if not grouped and len(shape) != 2:
+        raise ValueError("x must be [M, K] or [G, M, K]")
+    if x.dtype not in dtypes:
+        raise ValueError(f"x must have type {' or '.join(str(d).replace('torch.', '') for d in dtypes)}")
+    M, C = shape[-2:]
     G = shape[0] if grouped else 1
+    if G > _MAX_SIZE or M > _MAX_SIZE or C > _MAX_SIZE:
+        raise ValueError(f"x has a size above {_MAX_SIZE}: {tuple(shape)}")
+    if strides[-1] != 1:
+        raise ValueError("x must have contiguous columns")
+    if C % (128 * per):
+        raise ValueError(f"x must have a multiple of {128 * per} columns")
     pm = None
     if masked_m is not None:
         _need(grouped, "masked_m needs x with groups, [G, M, K]")
         pm = _arg(masked_m, "masked_m", _I32_ONLY, (G,), dev)
-    desc = _rows_desc(G, M, K, strides[-2] if M > 1 else shape[-1], strides[0] if grouped and G > 1 else 0, _TYPES[x.dtype])
-    return dev, (shape[:1] if grouped else ()), M, K, x.data_ptr(), pm, desc
+    desc = _rows_desc(G, M, C // per, strides[-2] if M > 1 else C, strides[0] if G > 1 else 0, _TYPES[x.dtype])
+    return dev, shape[:1] if grouped else (), M, C // per, x.data_ptr(), pm, desc
 
 
 def _quantize(name, per, dtypes, x, q, sf, masked_m, stream):
@@ -730,8 +734,8 @@ def dg_swiglu_backward(x, dy, dx, masked_m=None, stream=None) -> torch.Tensor:
 
 
 def _sizes(*sizes):
-    for n in sizes:
-        _need(n <= _MAX_SIZE, f"a size is above {_MAX_SIZE}: {n}")
+    if max(sizes) > _MAX_SIZE:
+        raise ValueError(f"a size is above {_MAX_SIZE}: {max(sizes)}")
 
 
 def dg_fp4_gemm_nt(a, sfa, b, sfb, c, d, stream=None) -> torch.Tensor:
@@ -740,7 +744,7 @@ def dg_fp4_gemm_nt(a, sfa, b, sfb, c, d, stream=None) -> torch.Tensor:
     dev = _device(a, "a")
     M, Kh = _two_d(a, "a")
     N = _two_d(b, "b")[0]
-    _sizes(2 * Kh)
+    _sizes(2 * Kh, N)
     pa = _arg(a, "a", _FP4_DTYPES, (M, Kh), dev)
     pb = _arg(b, "b", _FP4_DTYPES, (N, Kh), dev)
     psa = _arg(sfa, "sfa", _I32_ONLY, sf_fp4_shape(M, 2 * Kh), dev)

@@ -69,11 +69,17 @@ struct Operands {
   const int32_t* sfb;
 };
 
-template <class Kernel, class... Args>
-dg_status launch(Kernel kernel, int smem, int grid, int threads, int cluster, cudaStream_t stream, bool pdl, const Args&... args) {
-  // (set per device; a call costs less than a microsecond)
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e != cudaSuccess)
-    return dg::record_cuda_error(e);
+// kKernel's shared memory is set once per device and host thread.
+template <auto kKernel, class... Args>
+dg_status launch(int smem, int grid, int threads, int cluster, cudaStream_t stream, bool pdl, const Args&... args) {
+  static thread_local int set_on = -1;
+  int device = 0;
+  if (cudaError_t e = cudaGetDevice(&device); e != cudaSuccess) return dg::record_cuda_error(e);
+  if (set_on != device) {
+    if (cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e != cudaSuccess)
+      return dg::record_cuda_error(e);
+    set_on = device;
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -87,7 +93,7 @@ dg_status launch(Kernel kernel, int smem, int grid, int threads, int cluster, cu
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kKernel, args...);
   return e == cudaSuccess ? DG_OK : dg::record_cuda_error(e);
 }
 
@@ -105,7 +111,7 @@ dg_status run_pair(const LaunchContext& ctx, const Operands& o, const Params& p,
   const long long tiles = pair_rows * up(p.N, BN);
   if (tiles > (1ll << 30)) return DG_ERR_UNSUPPORTED;
   const int clusters = static_cast<int>(std::min<long long>(std::max(1, ctx.sms / 2), tiles));
-  return launch(dg::fp4::fp4_pair_kernel<kForm, BN, kAccum, kStages, kHasC>, S::smem(kForm), 2 * clusters, S::kThreads, 2, stream, ctx.pdl, ta,
+  return launch<dg::fp4::fp4_pair_kernel<kForm, BN, kAccum, kStages, kHasC>>(S::smem(kForm), 2 * clusters, S::kThreads, 2, stream, ctx.pdl, ta,
                 ta_edge, tb, tb_narrow, tsa, tsb, td, p);
 }
 
@@ -121,7 +127,7 @@ dg_status run_split(const LaunchContext& ctx, const Operands& o, Params p, cudaS
     return DG_ERR_CUDA;
   const long long grid = static_cast<long long>(up(p.M, kRowBox)) * up(p.N, BN) * kWays;
   if (grid > (1ll << 30)) return DG_ERR_UNSUPPORTED;
-  return launch(dg::fp4::fp4_split_kernel<BN, kStages, kWays>, S::SMEM, static_cast<int>(grid), S::kThreads, kWays, stream, ctx.pdl, ta, tb, tsa, tsb, p);
+  return launch<dg::fp4::fp4_split_kernel<BN, kStages, kWays>>(S::SMEM, static_cast<int>(grid), S::kThreads, kWays, stream, ctx.pdl, ta, tb, tsa, tsb, p);
 }
 
 // rows: of A, in each group.
