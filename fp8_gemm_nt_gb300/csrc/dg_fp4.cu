@@ -8,7 +8,6 @@
 #include "debug_state.h"
 #include "dg.h"
 #include "fp4_gemm.cuh"
-#include "pair_list.cuh"
 #include "runtime.h"
 
 namespace {
@@ -149,12 +148,6 @@ Params params(const LaunchContext& ctx, const void* c, void* d, int M, int N, in
   return p;
 }
 
-__global__ void __launch_bounds__(256) pair_list_kernel(const dg::PairListArgs a) {
-  dg::grid_dependency_wait();
-  dg::grid_launch_dependents();
-  dg::build_pair_list(a);
-}
-
 // Estimated microseconds of a product by CTA pairs with tiles of bn columns, from what the kernel was measured at: a launch
 // 4.5, then for each tile of a pair a start and a time for each stage of 256 K, no less than its output takes, and no less
 // than its share of B takes from HBM. pair_rows: 256-row strips; sharing: how many of them read the same of B. Widths 256,
@@ -246,18 +239,10 @@ dg_status dg_m_grouped_fp4_gemm_nt_contiguous(const void* a, const int32_t* sfa,
   LaunchContext ctx;
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   Params p = params(ctx, nullptr, d, M_total, N, K, G);
-  const int blocks = up(M_total, kRowBox);
-  dg::StreamWorkspace ws;
-  void* scratch = nullptr;
-  if (dg_status s = ws.acquire(stream, (4 + 3 * static_cast<size_t>(blocks)) * sizeof(int), &scratch); s != DG_OK) return s;
-  dg::PairListArgs list{};
-  list.m_indices = m_indices, list.num_mb = blocks, list.groups_g = G, list.status = ctx.status;
-  list.pair_count = static_cast<int*>(scratch), list.pair_list = list.pair_count + 4;
-  if (dg_status s = dg::launch(pair_list_kernel, 1, 256, 0, stream, ctx.pdl, list); s != DG_OK) return s;
-  p.m_indices = m_indices, p.pair_count = list.pair_count, p.pair_list = list.pair_list;
+  p.m_indices = m_indices;
   // (strips as they are if every expert's rows fill them; a bound of their number sizes the grid)
   const double strips = up(M_total, 256);
-  return run_pair_width<Form::Contiguous, false>(pair_width(p, strips, std::max(1.0, strips / G), ctx.sms), ctx, o, p, blocks, stream);
+  return run_pair_width<Form::Contiguous, false>(pair_width(p, strips, std::max(1.0, strips / G), ctx.sms), ctx, o, p, up(M_total, kRowBox), stream);
 }
 
 dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, void* d, const int32_t* masked_m,

@@ -32,8 +32,6 @@ struct Params {
   int M, N, K, G;                          // M: rows of A, of each group in the masked form
   const int32_t* m_indices;                // contiguous form
   const int32_t* masked_m;                 // masked form
-  const int* pair_list;                    // contiguous form: first block, expert and own blocks of every pair row
-  const int* pair_count;
   const __nv_bfloat16* c;
   __nv_bfloat16* d;
   uint32_t a_bytes;                        // split kernel: bytes of A that a stage loads
@@ -200,24 +198,51 @@ struct Tile {
   int m0, valid, n0, ga, gb;
 };
 
-// The tiles of cluster `t`, t + step, ...: every role of a CTA walks the same ones.
+// The tiles of cluster `t`, t + step, ...: every role of a CTA, a whole warp each, walks the same ones.
 template <Form kForm, int BN>
 struct Walk {
   int t, step, total, num_n;
   int g = 0, first = 0, tiles = 0;         // masked form: the group that t is in, its first tile and its tiles
+  // contiguous form, of the 32 blocks of 128 rows from `chunk`: a lane's block's expert, and how many of it and the next
+  // are its expert's; the blocks that begin a tile, and how many do before the chunk; the expert before the chunk, and
+  // whether an odd number of blocks of its run are before it
+  int chunk = -32, expert_of = -1, own = 0, before = 0, last = -1, odd = 0;
+  uint32_t begins = 0;
   const int* counts;
 
   __device__ __forceinline__ Walk(const Params& p, const int* counts_) : counts(counts_) {
     t = blockIdx.x / 2;
     step = gridDim.x / 2;
     num_n = up(p.N, BN);
-    total = kForm == Form::Dense ? up(p.M, 2 * kRows) * num_n : kForm == Form::Contiguous ? ld_cg_s32(p.pair_count) * num_n : 0;
+    total = up(p.M, 2 * kRows) * num_n;
     if (kForm == Form::Masked) tiles = tiles_of(p, 0);
   }
   __device__ __forceinline__ int count(const Params& p, int group) const {
     return group < kCountCache ? counts[group] : min(max(ld_cg_s32(p.masked_m + group), 0), p.M);
   }
   __device__ __forceinline__ int tiles_of(const Params& p, int group) const { return up(count(p, group), 2 * kRows) * num_n; }
+  // The expert of a block of 128 rows, by its first row; -1 where it is to be skipped.
+  __device__ __forceinline__ int expert(const Params& p, int block) const {
+    const int e = block < up(p.M, kRows) ? ld_cg_s32(p.m_indices + block * kRows) : -1;
+    if (e < -1 || e >= p.G) atomicOr(p.status, kBadIndexBit);
+    return e < p.G ? e : -1;
+  }
+  // Looks at the next 32 blocks. Two neighbouring blocks of an expert are a tile, counted from the first block of its run.
+  __device__ __forceinline__ void next_chunk(const Params& p) {
+    const int lane = static_cast<int>(lane_id());
+    before += __popc(begins);
+    chunk += 32;
+    expert_of = expert(p, chunk + lane);
+    int prev = __shfl_up_sync(0xffffffffu, expert_of, 1), after = __shfl_down_sync(0xffffffffu, expert_of, 1);
+    if (lane == 0) prev = last;
+    if (lane == 31) after = expert(p, chunk + 32);
+    own = after == expert_of ? 2 : 1;
+    const uint32_t runs = __ballot_sync(0xffffffffu, expert_of >= 0 && expert_of != prev) & (0xffffffffu >> (31 - lane));
+    const int place = runs ? lane - (31 - __clz(runs)) : lane + odd;       // in its run
+    begins = __ballot_sync(0xffffffffu, expert_of >= 0 && place % 2 == 0);
+    last = __shfl_sync(0xffffffffu, expert_of, 31);
+    odd = (__shfl_sync(0xffffffffu, place, 31) + 1) & 1;
+  }
 
   __device__ __forceinline__ bool next(const Params& p, Tile& s) {
     if constexpr (kForm == Form::Masked) {
@@ -230,17 +255,20 @@ struct Walk {
       const int local = t - first, pairs = tiles / num_n;
       s = {local % pairs * 2 * kRows, 0, local / pairs * BN, g, g};
       s.valid = count(p, g) - s.m0;
-    } else {
+    } else if constexpr (kForm == Form::Dense) {
       if (t >= total) return false;
-      const int pair = t / num_n;
-      s = {pair * 2 * kRows, 0, t % num_n * BN, 0, 0};
-      if constexpr (kForm == Form::Contiguous) {
-        s.m0 = ld_cg_s32(p.pair_list + 3 * pair) * kRows;
-        s.gb = ld_cg_s32(p.pair_list + 3 * pair + 1);
-        s.valid = ld_cg_s32(p.pair_list + 3 * pair + 2) * kRows;
-      } else {
-        s.valid = p.M - s.m0;
+      s = {t / num_n * 2 * kRows, 0, t % num_n * BN, 0, 0};
+      s.valid = p.M - s.m0;
+    } else {
+      const int want = t / num_n;
+      while (before + __popc(begins) <= want) {
+        if (chunk + 32 >= up(p.M, kRows)) return false;
+        next_chunk(p);
       }
+      uint32_t left = begins;
+      for (int i = before; i < want; ++i) left &= left - 1;
+      const int at = __ffs(left) - 1;
+      s = {(chunk + at) * kRows, __shfl_sync(0xffffffffu, own, at) * kRows, t % num_n * BN, 0, __shfl_sync(0xffffffffu, expert_of, at)};
     }
     t += step;
     return true;
@@ -475,9 +503,8 @@ __global__ void __launch_bounds__(PairShape<BN, kAccum, kStages, kHasC>::kThread
     uint32_t tiles = 0;
     while (walk.next(p, tile)) {
       const int m0 = tile.m0 + static_cast<int>(rank) * kRows;
-      const int valid = tile.valid - static_cast<int>(rank) * kRows;        // of this CTA's rows
-      const int mine = 4 * static_cast<int>(lane) + quad;                    // the row of this lane's accumulators
-      bool live = mine < valid;
+      const int mine = 4 * static_cast<int>(lane) + quad, r = static_cast<int>(rank) * kRows + mine;   // the row of this lane's accumulators
+      bool live = r < tile.valid;
       if constexpr (kForm == Form::Contiguous) {
         if (live) {
           const int expert = m0 + mine < p.M ? ld_cg_s32(p.m_indices + m0 + mine) : -1;

@@ -41,7 +41,8 @@
  *     uncaptured call of at least the same size on the capturing stream first (allocating
  *     inside a capture works only in cudaStreamCaptureModeRelaxed). Nothing is freed during a
  *     capture, and a workspace used in one is kept until the process exits, so replays stay
- *     valid however many streams come later.
+ *     valid however many streams come later. Graphs captured on one stream share its workspace, with
+ *     each other and with later calls on it: what runs at the same time is captured on streams of its own.
  */
 #ifndef DG_H_
 #define DG_H_
@@ -484,8 +485,7 @@ dg_status dg_fp4_gemm_nt(const void* a, const int32_t* sfa, const void* b, const
 
 /*
  * Contiguous M-grouped FP4 x FP4 GEMM: a uint8 [M_total, K/2] with sfa [K/128, ceil4(M_total)], b uint8 [G, N, K/2]
- * with sfb [G, K/128, ceil4(N)]; d, m_indices and the layout as dg_m_grouped_fp8_gemm_nt_contiguous. Uses the stream's
- * workspace.
+ * with sfb [G, K/128, ceil4(N)]; d, m_indices and the layout as dg_m_grouped_fp8_gemm_nt_contiguous.
  */
 dg_status dg_m_grouped_fp4_gemm_nt_contiguous(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
                                               void* d, const int32_t* m_indices, int M_total, int N, int K, int G,

@@ -244,6 +244,32 @@ def test_contiguous_padding_blocks_and_experts_without_rows(lib):
     check_contiguous(lib, [200, 30], 256, 256, align=256)
 
 
+def test_contiguous_long_runs(lib):
+    # runs that pass the 32 blocks that are looked at together, of odd and even lengths
+    check_contiguous(lib, [128 * 33, 5, 128 * 40 + 3, 128 * 31, 128 * 2], 144, 128)
+
+
+def test_contiguous_blocks_of_every_neighbour(lib):
+    # every order of experts and padding over two neighbouring blocks, in steps of 256 rows and across them
+    rng = np.random.default_rng(20)
+    N, K, G = 400, 256, 3
+    blocks = rng.permutation([e for e in (-1, 0, 1, 2) for _ in range(9)])
+    s = spread(K)
+    a, b = Operand(rng, 128 * len(blocks), K, 127, 127 + s // 2), [Operand(rng, N, K, 127, 127 + s - s // 2) for _ in range(G)]
+    index = np.repeat(blocks, 128).astype(np.int32)
+    index[128 * 5 + 100:128 * 6] = -1                    # padding rows at a block's end
+    db, dsb = stacked(b)
+    d = sentinel_like((len(index), N))
+    before = bf16_bits(d).copy()
+    lib.dg_m_grouped_fp4_gemm_nt_contiguous(dev(a.packed), dev(a.sf), db, dsb, d, dev(index))
+    assert lib.dg_get_device_status() == 0
+    got, av = bf16_bits(d), F.values(a.packed, a.sf)
+    for e in range(G):
+        at = index == e
+        assert (got[at] == rounded(av[at] @ F.values(b[e].packed, b[e].sf).T)).all()
+    assert (got[index < 0] == before[index < 0]).all()
+
+
 def test_contiguous_all_padding(lib):
     d = sentinel_like((256, 64))
     before = d.clone()
