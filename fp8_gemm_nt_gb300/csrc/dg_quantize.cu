@@ -7,8 +7,12 @@
 //
 // E2M1 has no NaN and no infinity: a block that holds one gets the scale code 255 (NaN) and codes 0.
 //
-// Bound by HBM. A warp takes 8 rows of 256 columns: every access of x is 512 contiguous bytes, all of them are in flight
-// before the first is used, and the 16 scale words of the tile leave in whole 32-byte sectors.
+// Bound by HBM where there are many rows: 32768 x 7168 BF16 take 100 us (5.9 TB/s), 32768 x 4096 gated ones 102 (5.9), the
+// gradient of 8192 x 2048 26 (6.5). Fewer are gone before the loads of enough warps overlap: 8192 x 7168 28 us (5.3), 8192 x
+// 2048 gated 16 (4.7). A warp takes a tile of 256 columns: every access of x is 512 contiguous bytes, all of them are in
+// flight before the first is used, and the tile's scale words leave together, by column. The largest magnitude of a block
+// is found among the bits of x, two BF16 values at once (124 us with float maxima, scale words joined by shuffles and 512
+// columns a warp, which left half as many warps room).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,7 +28,12 @@ namespace {
 using dg::LaunchContext;
 
 constexpr int kWarps = 4;                    // tiles per block
-constexpr int kTileRows = 8, kTileCols = 256;
+constexpr int kTileCols = 256;
+// Rows of a tile: 8, whose scale words are whole 32-byte sectors, where that leaves registers for 32 warps an SM (plain BF16
+// rows: 100 us against 111 with 4, at 32768 x 7168), else 4 (FP32 rows: 21.7 us against 26.8, at 4096 x 7168; gated ones: 16.2
+// against 17.9, at 8192 x 2048).
+template <class T, bool kGate>
+constexpr int kRowsOf = kGate || sizeof(T) == 4 ? 4 : 8;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 struct QuantArgs {
@@ -109,7 +118,7 @@ __device__ __forceinline__ uint32_t magnitude(const float (&v)[V]) {
 template <class T, bool kGate>
 __global__ void __launch_bounds__(kWarps * 32) quantize_kernel(const QuantArgs a) {
   constexpr int V = kPiece<T>, kChunk = 32 * V, kChunks = kTileCols / kChunk;   // a chunk: one access of the warp
-  constexpr int kBlockLanes = 32 / V;                                           // lanes of a scale
+  constexpr int kBlockLanes = 32 / V, kTileRows = kRowsOf<T, kGate>;            // lanes of a scale
   __shared__ __align__(8) uint8_t codes_of[kWarps][kTileRows][kTileCols / 32];  // the tile's scale codes
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
@@ -275,17 +284,20 @@ dg_status quantize(const void* x, const int32_t* masked_m, void* q, int32_t* sf,
   constexpr int kPerRow = kGate ? 2 : 1;
   if (dg_status s = check(x, masked_m, q, sf, desc, kPerRow); s != DG_OK) return s;
   if (desc->M == 0) return DG_OK;
-  // (4 divides the tile's rows, so the padding rows of sf are within the last tile)
-  Tiles n;
-  if (!n.count(*desc, kTileRows, kTileCols)) return DG_ERR_UNSUPPORTED;
-  LaunchContext ctx;
-  if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
-  const QuantArgs a{x, masked_m, static_cast<uint8_t*>(q), sf, ctx.status, n.all, n.row, n.col, desc->M, desc->K,
-                    desc->M + (4 - desc->M % 4) % 4, row_stride(*desc, kPerRow), group_stride(*desc)};
-  const unsigned grid = n.blocks();
+  auto run = [&](auto* type) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    // (4 divides the tile's rows, so the padding rows of sf are within the last tile)
+    Tiles n;
+    if (!n.count(*desc, kRowsOf<T, kGate>, kTileCols)) return DG_ERR_UNSUPPORTED;
+    LaunchContext ctx;
+    if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
+    const QuantArgs a{x, masked_m, static_cast<uint8_t*>(q), sf, ctx.status, n.all, n.row, n.col, desc->M, desc->K,
+                      desc->M + (4 - desc->M % 4) % 4, row_stride(*desc, kPerRow), group_stride(*desc)};
+    return dg::launch(quantize_kernel<T, kGate>, n.blocks(), kWarps * 32, 0, stream, ctx.pdl, a);
+  };
   if constexpr (!kGate)
-    if (desc->x_type == DG_F32) return dg::launch(quantize_kernel<float, false>, grid, kWarps * 32, 0, stream, ctx.pdl, a);
-  return dg::launch(quantize_kernel<__nv_bfloat16, kGate>, grid, kWarps * 32, 0, stream, ctx.pdl, a);
+    if (desc->x_type == DG_F32) return run(static_cast<float*>(nullptr));
+  return run(static_cast<__nv_bfloat16*>(nullptr));
 }
 
 }  // namespace
