@@ -4,9 +4,10 @@
 //   f = counts / sum of counts,   P = mean of p over the live rows,   loss = coef E sum f P
 //   dloss/dx_e = coef E / live p_e (f_e - sum_j p_j f_j), with sigmoid scores times 1 - sigmoid(x_e)
 //
-// A warp takes rows in turn, the next row's loads in flight while it works on one, and keeps its sums over rows (or
-// f, the same for every row) in registers. Sums are joined per block, then over the blocks by the last one to finish,
-// in a fixed order; the counts are integers, whose atomics have no order to keep.
+// A warp takes rows in turn and keeps its sums over rows (or f, the same for every row) in registers. Forward, it works on
+// two rows or four side by side while the next ones load; its sums are joined per block, then over the blocks by the last
+// one to finish, in a fixed order; the counts are integers, whose atomics have no order to keep. 65536 rows of 256 FP32
+// logits: 19.4 us, of which 6 are the chain of sums at the end (64 rows take 6 us) and the rest waits for loads (5 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -209,6 +209,23 @@ def test_masked_many_groups(lib):
     check_masked(lib, 1100, 3, 16, 128, rng.integers(0, 4, 1100).tolist())
 
 
+def test_masked_rows_past_32_bits(lib):
+    # D's last group begins past 2^31 elements
+    rng = np.random.default_rng(12)
+    G, max_m, N, K = 4, 45001, 16384, 128
+    a, b = torch.zeros(G, max_m, K // 2, dtype=torch.uint8, device="cuda"), torch.zeros(G, N, K // 2, dtype=torch.uint8, device="cuda")
+    sfa, sfb = (torch.full((G, 1, up), 0x7F7F7F7F, dtype=torch.int32, device="cuda") for up in (45004, N))
+    rows, columns = rng.integers(0, 256, (300, K // 2), dtype=np.uint8), rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    a[3, :300], b[3] = dev(rows), dev(columns)
+    d = torch.full((G, max_m, N), 7.0, dtype=BF16, device="cuda")
+    lib.dg_m_grouped_fp4_gemm_nt_masked(a, sfa, b, sfb, d, dev(np.array([0, 1, 0, 300], np.int32)))
+    assert lib.dg_get_device_status() == 0
+    ones = W.pack_sf(np.full((N, 4), 127, np.uint8))
+    want = F.gemm(rows, ones[:, :300], columns, ones)
+    assert (bf16_bits(d[3, :300]) == rounded(want)).all()
+    assert (d[3, 300:400] == 7).all() and (d[1, 0] == 0).all() and (d[1, 1:100] == 7).all() and (d[2, :100] == 7).all()
+
+
 def check_contiguous(L, sizes, N, K, G=None, seed=0, hole=None, align=128):
     rng = np.random.default_rng(seed)
     G = len(sizes) if G is None else G
