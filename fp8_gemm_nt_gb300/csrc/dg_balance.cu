@@ -8,7 +8,7 @@
 // two rows or four side by side while the next ones load; its sums are joined per block, then over the blocks by the last
 // one to finish, in a fixed order; the counts are integers, whose atomics have no order to keep. A block that is alone (one
 // round of its warps covers the rows) keeps all of it to itself: 64 rows take 3.4 us instead of 6. 65536 rows of 256 FP32
-// logits: 17.5 us, of which some 4 are the chain of sums at the end and the rest waits for loads (5 TB/s).
+// logits: 17.1 us, of which some 4 are the chain of sums at the end; the rest is two thirds of the issue slots.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -71,13 +71,21 @@ __device__ __forceinline__ void scores(const float (&x)[R][P], float (&p)[R][P],
     live[r] = top > -INFINITY;
     const float base = live[r] ? top : 0.0f;      // (subtracted first: rows of the type's lowest value differ by 0)
     if constexpr (kSigmoid) {
-      const bool large = top > 0;
-      const float sign = large ? -kLog2e : kLog2e;
+      if (top > 0) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float e = fminf(exp2_fast(sign * p[r][i]), 3.0e38f), one = reciprocal(1.0f + e);
-        if constexpr (kRest) rest[r][i] = large ? e * one : one;
-        p[r][i] = large ? one : one * exp2_fast((p[r][i] - base) * kLog2e);
+        for (int i = 0; i < P; ++i) {
+          float e = exp2_fast(-kLog2e * p[r][i]);
+          if constexpr (kRest) e = fminf(e, 3.0e38f);
+          p[r][i] = reciprocal(1.0f + e);
+          if constexpr (kRest) rest[r][i] = e * p[r][i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float one = reciprocal(1.0f + exp2_fast(kLog2e * p[r][i]));
+          if constexpr (kRest) rest[r][i] = one;
+          p[r][i] = one * exp2_fast((p[r][i] - base) * kLog2e);
+        }
       }
     } else {
 #pragma unroll
@@ -90,6 +98,14 @@ __device__ __forceinline__ void scores(const float (&x)[R][P], float (&p)[R][P],
   warp_sums(total);
 #pragma unroll
   for (int r = 0; r < R; ++r) by[r] = live[r] ? reciprocal(total[r]) : 0.0f;
+}
+
+// Has the lines of a row brought to L2, by a warp. Forward, for rows that are worked on alone, two ahead: 65536 of 512 FP32
+// logits 34.2 -> 29.3 us (narrower ones, with more loads of their own under way: the same).
+template <class L>
+__device__ __forceinline__ void prefetch_row(const L* row, int lane, int E) {
+  if (lane * 128 < E * static_cast<int>(sizeof(L)))
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(row) + lane * 128));
 }
 
 template <class L>
@@ -125,26 +141,27 @@ __global__ void __launch_bounds__(kWarpsOf<J * kVec> * 32, 1) balance_kernel(con
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
 
-  const long long step = static_cast<long long>(gridDim.x) * kWarps;
-  long long t = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  // (rows and slots are below 2^31, and a few steps more below 2^32)
+  const uint32_t step = gridDim.x * kWarps, T = static_cast<uint32_t>(a.T), slots = static_cast<uint32_t>(a.slots);
+  uint32_t t = blockIdx.x * kWarps + warp;
   constexpr int R = kRowsOf<P>;
   float next[R][P], acc[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) acc[i] = 0;
   // (in place of rows past the last a warp loads its first one again, and does not count it: the loads stay free of
   // branches)
-  const long long own = t;
-  auto row = [&](long long at) { return a.logits + (at < a.T ? at : own) * a.ld; };
-  if (t < a.T) {
+  const uint32_t own = t;
+  auto row = [&](uint32_t at) { return a.logits + (at < T ? at : own) * a.ld; };
+  if (t < T) {
 #pragma unroll
     for (int r = 0; r < R; ++r) At::load(row(t + r * step), lane, a.E, next[r]);
   }
   // the block's share of the slots, while the first rows arrive
   constexpr int kBatch = 4;
-  for (long long s = static_cast<long long>(blockIdx.x) * (kWarps * 32) + threadIdx.x; s < a.slots; s += kBatch * step * 32) {
+  for (uint32_t s = blockIdx.x * (kWarps * 32) + threadIdx.x; s < slots; s += kBatch * step * 32) {
     int id[kBatch];
 #pragma unroll
-    for (int n = 0; n < kBatch; ++n) id[n] = s + n * step * 32 < a.slots ? __ldcg(a.ids + s + n * step * 32) : -1;
+    for (int n = 0; n < kBatch; ++n) id[n] = s + n * step * 32 < slots ? __ldcg(a.ids + s + n * step * 32) : -1;
 #pragma unroll
     for (int n = 0; n < kBatch; ++n) {
       if (id[n] >= 0 && id[n] < a.E)
@@ -154,17 +171,19 @@ __global__ void __launch_bounds__(kWarpsOf<J * kVec> * 32, 1) balance_kernel(con
     }
   }
   int rows = 0;
-  for (; t < a.T; t += R * step) {
+  for (; t < T; t += R * step) {
     float p[R][P], none[R][P], by[R];
     bool live[R];
+    if constexpr (R == 1)
+      if (t + 2 * step < T) prefetch_row(a.logits + (t + 2 * step) * a.ld, lane, a.E);
     scores<kSigmoid, false>(next, p, none, by, live);
-    if (t + R * step < a.T) {
+    if (t + R * step < T) {
 #pragma unroll
       for (int r = 0; r < R; ++r) At::load(row(t + (R + r) * step), lane, a.E, next[r]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (t + r * step >= a.T) break;
+      if (t + r * step >= T) break;
       rows += live[r];
 #pragma unroll
       for (int i = 0; i < P; ++i) acc[i] = fmaf(p[r][i], by[r], acc[i]);
@@ -272,33 +291,46 @@ struct BalanceGradArgs {
   float coef;
 };
 
-// Warps keep f in registers and take rows in turn, as many of them as registers allow, to cover each other's loads. 65536
-// rows of 256 FP32 logits with a base: 38 us, 5.3 TB/s, bound by those loads' latency (152 us with a warp for each row,
-// whose reads of the same few lines of counts wait for one another).
+// Warps keep f in registers and take rows in turn, as many of them as registers allow, to cover each other's loads. The
+// counts are read once by a block: reads of the same few lines of L2 wait for one another (65536 rows of 256 FP32 logits with
+// a base: 33.4 us, 6.0 TB/s, 0.90 of HBM's copy rate; 41.6 with the counts read by each warp, 152 with a warp for each row;
+// 4096 rows: 4.7 us, 13 by each warp).
 template <class L, int J, int kVec, bool kSigmoid, bool kBase>
 __global__ void __launch_bounds__(kGradWarps * 32, kGradBlocks<J * kVec>) balance_grad_kernel(const BalanceGradArgs<L> a) {
   using At = Lane<L, J, kVec>;
   constexpr int P = At::kCount;
+  __shared__ float shares[kMaxExperts], scale;               // the experts' slots; what every gradient is multiplied by
+  __shared__ long long totals[kGradWarps];
   dg::grid_dependency_wait();
   dg::grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const long long step = static_cast<long long>(gridDim.x) * kGradWarps;
   long long t = static_cast<long long>(blockIdx.x) * kGradWarps + threadIdx.x / 32;
-  if (t >= a.T) return;
-  float f[P];
+  if (t < a.T) {
+    prefetch_row(a.logits + t * a.ld, lane, a.E);
+    if constexpr (kBase) prefetch_row(a.base + t * a.E, lane, a.E);
+  }
   long long total = 0;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = At::index(lane, i), c = e < a.E ? max(__ldcg(a.counts + e), 0) : 0;
+  for (int e = threadIdx.x; e < a.E; e += kGradWarps * 32) {
+    const int c = max(__ldcg(a.counts + e), 0);
+    shares[e] = static_cast<float>(c);
     total += c;
-    f[i] = static_cast<float>(c);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-  const float inv = 1.0f / static_cast<float>(total > 1 ? total : 1);
+  if (lane == 0) totals[threadIdx.x / 32] = total;
+  if (threadIdx.x == 0) scale = __ldcg(a.dloss) * (a.coef * static_cast<float>(a.E)) / static_cast<float>(max(__ldcg(a.live_rows), 1));
+  __syncthreads();
+  total = 0;
 #pragma unroll
-  for (int i = 0; i < P; ++i) f[i] *= inv;
-  const float scale = __ldcg(a.dloss) * (a.coef * static_cast<float>(a.E)) / static_cast<float>(max(__ldcg(a.live_rows), 1));
+  for (int w = 0; w < kGradWarps; ++w) total += totals[w];
+  const float inv = 1.0f / static_cast<float>(total > 1 ? total : 1);
+  float f[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int e = At::index(lane, i);
+    f[i] = e < a.E ? shares[e] * inv : 0.0f;
+  }
   for (; t < a.T; t += step) {
     float x[1][P], d[P], p[1][P], rest[1][P], by[1], inner[1] = {0};
     bool live[1];
@@ -337,6 +369,11 @@ bool words(std::initializer_list<const void*> all) {
   return (any & 3u) == 0;
 }
 
+// Whether pieces of 16 bytes leave no more logits to a lane than single ones do: 65536 rows of 64 BF16 logits, sigmoid scores,
+// 13.4 us with single ones, 22.3 with pieces, and their gradient 13.9 and 33.7.
+template <class L>
+bool wide(int E) { return E > 16 * static_cast<int>(16 / sizeof(L)); }
+
 // Blocks that take `rows` rows at a time, `most` at most.
 unsigned blocks_for(int T, int rows, int most) {
   return static_cast<unsigned>(std::max(1, std::min(T / rows + (T % rows != 0), most)));
@@ -362,7 +399,7 @@ dg_status dg_moe_balance_loss(const void* logits, const int32_t* topk_ids, int32
     using L = std::remove_pointer_t<decltype(type)>;
     const BalanceArgs<L> a{static_cast<const L*>(logits), topk_ids, counts, live_rows, prob_mean, loss, static_cast<float*>(scratch),
                            ws.counters(), ctx.status, desc->T, desc->E, desc->T * desc->topk, ld, desc->coef};
-    return with_shape<L>(desc->E, whole_pieces<L>(logits, ld, desc->E), [&](auto j, auto vec) {
+    return with_shape<L>(desc->E, wide<L>(desc->E) && whole_pieces<L>(logits, ld, desc->E), [&](auto j, auto vec) {
       constexpr int kWarps = kWarpsOf<decltype(j)::value * decltype(vec)::value>;
       const size_t smem = static_cast<size_t>(kWarps + 1) * desc->E * sizeof(float);
       auto kernel = desc->scoring == DG_ROUTE_SIGMOID ? balance_kernel<L, decltype(j)::value, decltype(vec)::value, true>
@@ -391,7 +428,7 @@ dg_status dg_moe_balance_loss_backward(const void* logits, const int32_t* counts
     using L = std::remove_pointer_t<decltype(type)>;
     const BalanceGradArgs<L> a{static_cast<const L*>(logits), counts, live_rows, dloss, static_cast<const L*>(base), static_cast<L*>(dlogits),
                                desc->T, desc->E, ld, desc->coef};
-    const bool aligned = whole_pieces<L>(logits, ld, desc->E) && whole_pieces<L>(dlogits, desc->E, desc->E) && whole_pieces<L>(base, desc->E, desc->E);
+    const bool aligned = wide<L>(desc->E) && whole_pieces<L>(logits, ld, desc->E) && whole_pieces<L>(dlogits, desc->E, desc->E) && whole_pieces<L>(base, desc->E, desc->E);
     return with_shape<L>(desc->E, aligned, [&](auto j, auto vec) {
       constexpr int J = decltype(j)::value, kVec = decltype(vec)::value;
       const bool sig = desc->scoring == DG_ROUTE_SIGMOID;
