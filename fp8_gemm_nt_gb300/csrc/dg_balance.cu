@@ -400,14 +400,14 @@ dg_status dg_moe_balance_loss(const void* logits, const int32_t* topk_ids, int32
     const BalanceArgs<L> a{static_cast<const L*>(logits), topk_ids, counts, live_rows, prob_mean, loss, static_cast<float*>(scratch),
                            ws.counters(), ctx.status, desc->T, desc->E, desc->T * desc->topk, ld, desc->coef};
     return with_shape<L>(desc->E, wide<L>(desc->E) && whole_pieces<L>(logits, ld, desc->E), [&](auto j, auto vec) {
-      constexpr int kWarps = kWarpsOf<decltype(j)::value * decltype(vec)::value>;
+      constexpr int P = decltype(j)::value * decltype(vec)::value, kWarps = kWarpsOf<P>;
       const size_t smem = static_cast<size_t>(kWarps + 1) * desc->E * sizeof(float);
       auto kernel = desc->scoring == DG_ROUTE_SIGMOID ? balance_kernel<L, decltype(j)::value, decltype(vec)::value, true>
                                                       : balance_kernel<L, decltype(j)::value, decltype(vec)::value, false>;
       if (smem > 48 * 1024)
         if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)); e != cudaSuccess)
           return dg::record_cuda_error(e);
-      return dg::launch(kernel, blocks_for(desc->T, kWarps * kRowsOf<decltype(j)::value * decltype(vec)::value>, ctx.sms), kWarps * 32, smem, stream, ctx.pdl, a);
+      return dg::launch(kernel, blocks_for(desc->T, kWarps * kRowsOf<P>, ctx.sms), kWarps * 32, smem, stream, ctx.pdl, a);
     });
   };
   return desc->logits_type == DG_BF16 ? run(static_cast<__nv_bfloat16*>(nullptr)) : run(static_cast<float*>(nullptr));
@@ -428,7 +428,8 @@ dg_status dg_moe_balance_loss_backward(const void* logits, const int32_t* counts
     using L = std::remove_pointer_t<decltype(type)>;
     const BalanceGradArgs<L> a{static_cast<const L*>(logits), counts, live_rows, dloss, static_cast<const L*>(base), static_cast<L*>(dlogits),
                                desc->T, desc->E, ld, desc->coef};
-    const bool aligned = wide<L>(desc->E) && whole_pieces<L>(logits, ld, desc->E) && whole_pieces<L>(dlogits, desc->E, desc->E) && whole_pieces<L>(base, desc->E, desc->E);
+    const bool aligned = wide<L>(desc->E) && whole_pieces<L>(logits, ld, desc->E) && whole_pieces<L>(dlogits, desc->E, desc->E) &&
+                         whole_pieces<L>(base, desc->E, desc->E);
     return with_shape<L>(desc->E, aligned, [&](auto j, auto vec) {
       constexpr int J = decltype(j)::value, kVec = decltype(vec)::value;
       const bool sig = desc->scoring == DG_ROUTE_SIGMOID;
