@@ -210,3 +210,36 @@ def test_the_same_bits_twice_and_in_a_graph(lib):
         g.replay()
         s.synchronize()
     check_loss(x, ids, out, "softmax", 1.0)
+
+
+@pytest.mark.parametrize("sms", [1, 2, 7])
+def test_on_few_sms(lib, sms):
+    # a block that is alone with all rows, and blocks that take their rows in many rounds
+    for T, E, dtype, scoring in ((2000, 60, BF16, "sigmoid"), (700, 512, F32, "softmax")):
+        x = make(T, E, dtype, 13)
+        ids = ids_of(x, 6, 13)
+        dx = torch.empty_like(x)
+        try:
+            lib.dg_set_num_sms(sms)
+            got = loss_of(lib, x, ids, scoring, 0.5)
+            lib.dg_moe_balance_loss_backward(x, got[0], got[1], torch.ones(1, device="cuda"), dx, scoring=scoring, coef=0.5)
+        finally:
+            lib.dg_set_num_sms(0)
+        check_loss(x, ids, got, scoring, 0.5)
+        check_gradient(x, got[0].cpu().numpy().astype(np.float64), int(got[1]), 1.0, None, dx, scoring, 0.5)
+
+
+def test_two_streams_at_once(lib):
+    sets = []
+    for seed, T, E in ((14, 4000, 256), (15, 3500, 60)):
+        x = make(T, E, F32, seed)
+        ids = ids_of(x, 4, seed)
+        sets.append((x, ids, loss_of(lib, x, ids, "softmax", 1.0), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(20):
+        for x, ids, alone, s in sets:
+            with torch.cuda.stream(s):
+                runs.append((alone, loss_of(lib, x, ids, "softmax", 1.0)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for alone, got in runs for a, b in zip(alone, got))
