@@ -1,13 +1,14 @@
-// Host side of the FP4 x FP4 GEMMs: checks, tensor maps, choice of kernel and launch. The kernels are in fp4_gemm.cuh.
+// Host side of the FP4 x FP4 GEMMs: checks, tensor maps and launches. The kernels are in fp4_gemm.cuh, the choice between
+// them in fp4_ways.h.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 
 #include "debug_state.h"
 #include "dg.h"
 #include "fp4_gemm.cuh"
+#include "fp4_ways.h"
 #include "runtime.h"
 
 namespace {
@@ -18,6 +19,7 @@ using dg::fp4::Params;
 using dg::fp4::up;
 
 constexpr int kRowBox = dg::fp4::kRows;
+static_assert(dg::fp4::kWayStageK == dg::fp4::kStageK, "the estimates' stage");
 constexpr int kMaxSize = 1 << 30;          // of a row count, N or K
 
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
@@ -148,26 +150,6 @@ Params params(const LaunchContext& ctx, const void* c, void* d, int M, int N, in
   return p;
 }
 
-// Estimated microseconds of a product by CTA pairs with tiles of bn columns, from what the kernel was measured at: a launch
-// 4.5, then for each tile of a pair a start and a time for each stage of 256 K, no less than its output takes, and no less
-// than its share of B takes from HBM. pair_rows: 256-row strips; sharing: how many of them read the same of B. Widths 256,
-// 384 and 128 in us: 8 experts, 32768 x 4096 x 7168 278, 307, 429; of 8 x 32768 x 4096 x 512 89, 76, 116; masked 32 x 256 x
-// 7168 x 2048 67, 60, 70; 4096 x 24576 x 1536 72, 77, 92; 512 x 4096 x 7168 14.2, 20, 12.2.
-double pair_time(int bn, const Params& p, double pair_rows, double sharing, int sms) {
-  const int stages = up(p.K, dg::fp4::kStageK), clusters = std::max(1, sms / 2);
-  const double tiles = pair_rows * up(p.N, bn), waves = std::ceil(tiles / clusters);
-  const double tile = bn == 256 ? std::max(3.3, 1.4 + 0.3 * stages) : bn == 384 ? 2.6 + 0.47 * stages : std::max(2.0, 1.0 + 0.25 * stages);
-  const double bytes = std::min<double>(tiles, clusters) / sharing * bn * (p.K * 0.53125);
-  return 4.5 + waves * std::max(tile, 1.6 + bytes / 6.2e6);
-}
-
-int pair_width(const Params& p, double pair_rows, double sharing, int sms) {
-  int best = 256;
-  for (int bn : {384, 128})
-    if (pair_time(bn, p, pair_rows, sharing, sms) < pair_time(best, p, pair_rows, sharing, sms)) best = bn;
-  return best;
-}
-
 // By width; stages as many as shared memory and, of the widest, TMEM hold.
 template <Form kForm, bool kHasC>
 dg_status run_pair_width(int bn, const LaunchContext& ctx, const Operands& o, const Params& p, long long pair_rows, cudaStream_t stream) {
@@ -177,42 +159,19 @@ dg_status run_pair_width(int bn, const LaunchContext& ctx, const Operands& o, co
   return run_pair<kForm, 256, 1, kHasC || kFew ? 5 : 6, kHasC>(ctx, o, p, pair_rows, stream);
 }
 
-// Ways to run a dense product other than by CTA pairs: one tile to a CTA or to a cluster that shares out K.
-struct Split {
-  int bn, ways;
-};
-constexpr Split kSplits[] = {{64, 1}, {64, 2}, {64, 4}, {96, 2}, {128, 1}, {128, 2}, {192, 1}};
-
-// Estimated microseconds of one: a stage of 256 K costs an SM 0.19 us or the time of its bytes from L2 (91 GB/s an SM; rows
-// of 128 bytes and 8 of scales) or, all CTAs' together, of B's from HBM (6 TB/s); a launch 3 us, a cluster's sums 0.3 us and
-// 20 KB a microsecond. Its choice against every way on its own, in us (128 x 7168 x 16384: 16.9, others 17.5 to 28; 128 x
-// 256 x 512: 2.7, 2.8 to 4.9; 128 x 2048 x 16384: 11.0, 12.7 to 20).
-double split_time(const Split& w, const Params& p, int sms) {
-  const int stages = up(p.K, dg::fp4::kStageK), rows = std::min(p.M, 128);
-  const double m_tiles = up(p.M, 128), ctas = m_tiles * up(p.N, w.bn) * w.ways;
-  // one wave; of clusters of four, 152 SMs hold 36
-  if (stages < w.ways || ctas > (w.ways == 4 ? 18 * (sms / 19) : sms / w.ways * w.ways)) return HUGE_VAL;
-  const double stage = std::max({0.19, (rows + w.bn) * 136.0 / 91e3, ctas / m_tiles * w.bn * 136.0 / 6e6});
-  return 3.0 + up(stages, w.ways) * stage + (w.ways > 1 ? 0.3 + rows * w.bn * 4.0 / 20e3 : 0.0);
-}
-
 template <bool kHasC>
 dg_status dense(const LaunchContext& ctx, const Operands& o, const Params& p, cudaStream_t stream) {
-  const int strips = up(p.M, 256), width = pair_width(p, strips, strips, ctx.sms);
-  double least = pair_time(width, p, strips, strips, ctx.sms);
-  Split best{0, 0};
-  for (const Split& w : kSplits)
-    if (const double t = split_time(w, p, ctx.sms); t < least) best = w, least = t;
-  switch (best.bn * 10 + best.ways) {
+  const dg::fp4::Way way = dg::fp4::dense_way(p.M, p.N, p.K, ctx.sms);
+  if (way.ways == 0) return run_pair_width<Form::Dense, kHasC>(way.bn, ctx, o, p, up(p.M, 256), stream);
+  switch (way.bn * 10 + way.ways) {
     case 641: return run_split<64, 6, 1>(ctx, o, p, stream);
     case 642: return run_split<64, 6, 2>(ctx, o, p, stream);
     case 644: return run_split<64, 6, 4>(ctx, o, p, stream);
     case 962: return run_split<96, 6, 2>(ctx, o, p, stream);
     case 1281: return run_split<128, 6, 1>(ctx, o, p, stream);
     case 1282: return run_split<128, 6, 2>(ctx, o, p, stream);
-    case 1921: return run_split<192, 5, 1>(ctx, o, p, stream);
+    default: return run_split<192, 5, 1>(ctx, o, p, stream);
   }
-  return run_pair_width<Form::Dense, kHasC>(width, ctx, o, p, strips, stream);
 }
 
 }  // namespace
@@ -240,9 +199,8 @@ dg_status dg_m_grouped_fp4_gemm_nt_contiguous(const void* a, const int32_t* sfa,
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   Params p = params(ctx, nullptr, d, M_total, N, K, G);
   p.m_indices = m_indices;
-  // (strips as they are if every expert's rows fill them; a bound of their number sizes the grid)
-  const double strips = up(M_total, 256);
-  return run_pair_width<Form::Contiguous, false>(pair_width(p, strips, std::max(1.0, strips / G), ctx.sms), ctx, o, p, up(M_total, kRowBox), stream);
+  // (a bound of the strips' number sizes the grid)
+  return run_pair_width<Form::Contiguous, false>(dg::fp4::contiguous_width(M_total, N, K, G, ctx.sms), ctx, o, p, up(M_total, kRowBox), stream);
 }
 
 dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, void* d, const int32_t* masked_m,
@@ -256,9 +214,7 @@ dg_status dg_m_grouped_fp4_gemm_nt_masked(const void* a, const int32_t* sfa, con
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   Params p = params(ctx, nullptr, d, max_m, N, K, G);
   p.masked_m = masked_m;
-  // (the counts are on the device: half of the rows, say)
-  const double strips = up(up(max_m, 2), 256);
-  return run_pair_width<Form::Masked, false>(pair_width(p, G * strips, strips, ctx.sms), ctx, o, p, static_cast<long long>(G) * up(max_m, 256), stream);
+  return run_pair_width<Form::Masked, false>(dg::fp4::masked_width(G, max_m, N, K, ctx.sms), ctx, o, p, static_cast<long long>(G) * up(max_m, 256), stream);
 }
 
 }  // extern "C"
