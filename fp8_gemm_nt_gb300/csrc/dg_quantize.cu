@@ -231,9 +231,11 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_grad_kernel(const SwigluGr
     unpack(wd[r], d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = sigmoid(gate[i]);
-      const float dgate = d[i] * up[i] * s * (1.0f + gate[i] * (1.0f - s));
-      up[i] = d[i] * gate[i] * s;
+      // (dy times the gate or up first would pass FP32's range where the gradient does not: 0 times infinity at a gate that
+      // is masked by its type's lowest value)
+      const float s = sigmoid(gate[i]), slope = s * (1.0f + gate[i] * (1.0f - s));
+      const float dgate = d[i] * slope * up[i];
+      up[i] = d[i] * (gate[i] * s);
       gate[i] = dgate;
     }
     __nv_bfloat16* const to = a.dx + (row0 + r) * 2 * a.K + col;
