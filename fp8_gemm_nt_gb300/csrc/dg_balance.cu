@@ -116,7 +116,7 @@ struct BalanceArgs {
   int32_t* live_rows;
   float* prob_mean;
   float* loss;
-  float* partial;       // [blocks][E]
+  float* partial;       // [blocks][E]; this and the next not read by a block that is alone
   int* counters;        // blocks that have finished, live rows, and from kCountsAt on the counts; zero between launches
   uint32_t* status;
   int T, E, slots;
@@ -392,13 +392,10 @@ dg_status dg_moe_balance_loss(const void* logits, const int32_t* topk_ids, int32
   LaunchContext ctx;
   if (dg_status s = dg::launch_context(&ctx); s != DG_OK) return s;
   const size_t ld = row_stride(*desc);
-  dg::StreamWorkspace ws;
-  void* scratch = nullptr;
-  if (dg_status s = ws.acquire(stream, static_cast<size_t>(ctx.sms) * desc->E * sizeof(float), &scratch); s != DG_OK) return s;
   auto run = [&](auto* type) {
     using L = std::remove_pointer_t<decltype(type)>;
-    const BalanceArgs<L> a{static_cast<const L*>(logits), topk_ids, counts, live_rows, prob_mean, loss, static_cast<float*>(scratch),
-                           ws.counters(), ctx.status, desc->T, desc->E, desc->T * desc->topk, ld, desc->coef};
+    BalanceArgs<L> a{static_cast<const L*>(logits), topk_ids, counts, live_rows, prob_mean, loss, nullptr, nullptr, ctx.status,
+                     desc->T, desc->E, desc->T * desc->topk, ld, desc->coef};
     return with_shape<L>(desc->E, wide<L>(desc->E) && whole_pieces<L>(logits, ld, desc->E), [&](auto j, auto vec) {
       constexpr int P = decltype(j)::value * decltype(vec)::value, kWarps = kWarpsOf<P>;
       const size_t smem = static_cast<size_t>(kWarps + 1) * desc->E * sizeof(float);
@@ -407,7 +404,13 @@ dg_status dg_moe_balance_loss(const void* logits, const int32_t* topk_ids, int32
       if (smem > 48 * 1024)
         if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)); e != cudaSuccess)
           return dg::record_cuda_error(e);
-      return dg::launch(kernel, blocks_for(desc->T, kWarps * kRowsOf<P>, ctx.sms), kWarps * 32, smem, stream, ctx.pdl, a);
+      const unsigned blocks = blocks_for(desc->T, kWarps * kRowsOf<P>, ctx.sms);
+      dg::StreamWorkspace ws;      // (what a block alone has no use for: a stream without one can be captured)
+      void* scratch = nullptr;
+      if (blocks > 1)
+        if (dg_status s = ws.acquire(stream, static_cast<size_t>(ctx.sms) * desc->E * sizeof(float), &scratch); s != DG_OK) return s;
+      a.partial = static_cast<float*>(scratch), a.counters = ws.counters();
+      return dg::launch(kernel, blocks, kWarps * 32, smem, stream, ctx.pdl, a);
     });
   };
   return desc->logits_type == DG_BF16 ? run(static_cast<__nv_bfloat16*>(nullptr)) : run(static_cast<float*>(nullptr));

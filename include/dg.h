@@ -452,7 +452,8 @@ typedef struct {
  *   live_rows: int32 [1].      prob_mean : float32 [E].      loss : float32 [1].
  * All four are written (zeros for T = 0). Sums are FP32 in a fixed order: the same inputs give the same bits on the
  * same number of SMs. Limits: E <= 1024, topk <= 32, T * topk < 2^31 (DG_ERR_UNSUPPORTED above); topk > 0, coef finite.
- * Pointers are aligned to their element. Uses the stream's workspace.
+ * Pointers are aligned to their element. Uses the stream's workspace, unless one block covers the rows (up to 128
+ * rows of up to 128 logits, at least 8 of any).
  */
 dg_status dg_moe_balance_loss(const void* logits, const int32_t* topk_ids, int32_t* counts, int32_t* live_rows,
                               float* prob_mean, float* loss, const dg_balance_desc* desc, cudaStream_t stream);
