@@ -398,12 +398,11 @@ dg_status dg_moe_balance_loss(const void* logits, const int32_t* topk_ids, int32
                      desc->T, desc->E, desc->T * desc->topk, ld, desc->coef};
     return with_shape<L>(desc->E, wide<L>(desc->E) && whole_pieces<L>(logits, ld, desc->E), [&](auto j, auto vec) {
       constexpr int P = decltype(j)::value * decltype(vec)::value, kWarps = kWarpsOf<P>;
+      // (a lane's P logits are of 32 P experts at most: 37 KB, less than a kernel has to ask for)
+      static_assert((kWarps + 1) * std::min(32 * P, kMaxExperts) * sizeof(float) <= 40 * 1024, "shared memory");
       const size_t smem = static_cast<size_t>(kWarps + 1) * desc->E * sizeof(float);
       auto kernel = desc->scoring == DG_ROUTE_SIGMOID ? balance_kernel<L, decltype(j)::value, decltype(vec)::value, true>
                                                       : balance_kernel<L, decltype(j)::value, decltype(vec)::value, false>;
-      if (smem > 48 * 1024)
-        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)); e != cudaSuccess)
-          return dg::record_cuda_error(e);
       const unsigned blocks = blocks_for(desc->T, kWarps * kRowsOf<P>, ctx.sms);
       dg::StreamWorkspace ws;      // (what a block alone has no use for: a stream without one can be captured)
       void* scratch = nullptr;
