@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(256, 1)
           uint32_t v[32];
           tmem_load_32x32b_x32(from + 32 * piece, v);
           tmem_load_wait();
-          // (rows past the last are zeros, which no one reads)
+          // (rows past the last are sums of whatever lay in shared memory: no one reads them)
 #pragma unroll
           for (int i = 0; i < 32; i += 4) st_shared_v4(smem_addr(partial + 32 * piece + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
