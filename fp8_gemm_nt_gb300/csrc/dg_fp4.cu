@@ -103,12 +103,19 @@ template <Form kForm, int BN, int kAccum, int kStages, bool kHasC>
 dg_status run_pair(const LaunchContext& ctx, const Operands& o, const Params& p, long long pair_rows, cudaStream_t stream) {
   using S = dg::fp4::PairShape<BN, kAccum, kStages, kHasC>;
   const int ga = kForm == Form::Masked ? p.G : 1, gb = kForm == Form::Dense ? 1 : p.G;
+  // Only maps that a tile goes by: a host thread keeps 32, which a few products use up. Whole blocks of 128 rows of A and D go
+  // by the first and the last of these, A's rows past them by the second.
   CUtensorMap ta, ta_edge, tb, tb_narrow, tsa, tsb, td;
-  if (!every_fourth_map(&ta_edge, o.a, ga, p.M, p.K) || !apart_map(&tb, o.b, gb, p.N, p.K, 4) || !apart_map(&tb_narrow, o.b, gb, p.N, p.K, 2) || !scales_map(&tsa, o.sfa, ga, p.M, p.K, kRowBox) ||
-      !scales_map(&tsb, o.sfb, gb, p.N, p.K, S::kSfBox))
-    return DG_ERR_CUDA;
-  ta = td = ta_edge;      // (where A has fewer than four rows, none of its tiles is an inner one)
-  if (p.M >= 4 && (!apart_map(&ta, o.a, ga, p.M, p.K, 4) || !out_map(&td, p.d, ga, p.M, p.N))) return DG_ERR_CUDA;
+  const bool inner = p.M >= kRowBox, edge = p.M % kRowBox != 0;
+  if (inner && (!apart_map(&ta, o.a, ga, p.M, p.K, 4) || !out_map(&td, p.d, ga, p.M, p.N))) return DG_ERR_CUDA;
+  if (edge && !every_fourth_map(&ta_edge, o.a, ga, p.M, p.K)) return DG_ERR_CUDA;
+  if (!inner) ta = td = ta_edge;
+  if (!edge) ta_edge = ta;
+  if (S::kWide > 0 && !apart_map(&tb, o.b, gb, p.N, p.K, 4)) return DG_ERR_CUDA;
+  if (S::kNarrow && !apart_map(&tb_narrow, o.b, gb, p.N, p.K, 2)) return DG_ERR_CUDA;
+  if (S::kWide == 0) tb = tb_narrow;
+  if (!S::kNarrow) tb_narrow = tb;
+  if (!scales_map(&tsa, o.sfa, ga, p.M, p.K, kRowBox) || !scales_map(&tsb, o.sfb, gb, p.N, p.K, S::kSfBox)) return DG_ERR_CUDA;
   const long long tiles = pair_rows * up(p.N, BN);
   if (tiles > (1ll << 30)) return DG_ERR_UNSUPPORTED;
   const int clusters = static_cast<int>(std::min<long long>(std::max(1, ctx.sms / 2), tiles));
