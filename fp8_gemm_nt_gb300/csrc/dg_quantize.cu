@@ -7,9 +7,9 @@
 //
 // E2M1 has no NaN and no infinity: a block that holds one gets the scale code 255 (NaN) and codes 0.
 //
-// Bound by HBM where there are many rows: 32768 x 7168 BF16 take 100 us (5.9 TB/s), 32768 x 4096 gated ones 102 (5.9), the
+// Bound by HBM where there are many rows: 32768 x 7168 BF16 take 100 us (5.9 TB/s), 32768 x 4096 gated ones 96 (6.3), the
 // gradient of 8192 x 2048 26 (6.5). Fewer are gone before the loads of enough warps overlap: 8192 x 7168 28 us (5.3), 8192 x
-// 2048 gated 16 (4.7). A warp takes a tile of 256 columns: every access of x is 512 contiguous bytes, all of them are in
+// 2048 gated 15 (5.1). A warp takes a tile of 256 columns: every access of x is 512 contiguous bytes, all of them are in
 // flight before the first is used, and the tile's scale words leave together, by column. The largest magnitude of a block
 // is found among the bits of x, two BF16 values at once (124 us with float maxima, scale words joined by shuffles and 512
 // columns a warp, which left half as many warps room).
@@ -73,10 +73,20 @@ __device__ __forceinline__ uint32_t pack_e2m1(float a, float b, float c, float d
   return w;
 }
 
-// 1 / (1 + exp(-g)), within 2^-19 of itself (the rounded exponent of a small one), which FP4 and BF16 do not see; 0 where
-// exp(-g) overflows.
-__device__ __forceinline__ float sigmoid(float g) { return dg::reciprocal(1.0f + dg::exp2_fast(-dg::kLog2e * g)); }
-__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
+// 2^7 / (1 + exp(-g)) of two gates, and 0 where exp(-g) passes 2^133 (g < -92.2, where silu is below FP32's normal numbers):
+// the reciprocal of 1 + exp(-g) itself would be flushed from 2^126 on, gates of -87.5, where silu is not small yet. Off by the
+// exponent's rounding: 2^-18 of itself at the farthest gates, 2^-21 at gates within 10, which FP4 and BF16 do not see.
+// Sums and products of two floats to an instruction: 32768 x 4096 gated rows 96.1 us, by single ones 105.7, and 102.5 without
+// the shift.
+constexpr float kUnshift = 1.0f / 128;
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 sigmoid_shifted(float2 g) {
+  const float2 e = __ffma2_rn(g, both(-dg::kLog2e), both(-7.0f));
+  const float2 d = __fadd2_rn(make_float2(dg::exp2_fast(e.x), dg::exp2_fast(e.y)), both(kUnshift));
+  return make_float2(dg::reciprocal(d.x), dg::reciprocal(d.y));
+}
+// (a BF16 gate times 2^-7 is exact)
+__device__ __forceinline__ float2 silu(float2 g) { return __fmul2_rn(__fmul2_rn(g, both(kUnshift)), sigmoid_shifted(g)); }
 
 // The columns of 16 bytes of x.
 template <class T>
@@ -154,7 +164,10 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_kernel(const QuantArgs a
         float u[V];
         unpack(up[c][r], u);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = silu(v[i]) * u[i];
+        for (int i = 0; i < V; i += 2) {
+          const float2 y = __fmul2_rn(silu(make_float2(v[i], v[i + 1])), make_float2(u[i], u[i + 1]));
+          v[i] = y.x, v[i + 1] = y.y;
+        }
       }
       if constexpr (V == 8 && !kGate)
         top = magnitude(in[c][r], v);
@@ -230,13 +243,15 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_grad_kernel(const SwigluGr
     unpack(wu[r], up);
     unpack(wd[r], d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; i += 2) {
       // (dy times the gate or up first would pass FP32's range where the gradient does not: 0 times infinity at a gate that
       // is masked by its type's lowest value)
-      const float s = sigmoid(gate[i]), slope = s * (1.0f + gate[i] * (1.0f - s));
-      const float dgate = d[i] * slope * up[i];
-      up[i] = d[i] * (gate[i] * s);
-      gate[i] = dgate;
+      const float2 g = make_float2(gate[i], gate[i + 1]), u = make_float2(up[i], up[i + 1]), dy = make_float2(d[i], d[i + 1]);
+      const float2 s = sigmoid_shifted(g), rest = __ffma2_rn(s, both(-kUnshift), both(1.0f));
+      const float2 slope = __fmul2_rn(__fmul2_rn(__ffma2_rn(g, rest, both(1.0f)), both(kUnshift)), s);
+      const float2 dgate = __fmul2_rn(__fmul2_rn(dy, slope), u), dup = __fmul2_rn(dy, __fmul2_rn(__fmul2_rn(g, both(kUnshift)), s));
+      gate[i] = dgate.x, gate[i + 1] = dgate.y;
+      up[i] = dup.x, up[i + 1] = dup.y;
     }
     __nv_bfloat16* const to = a.dx + (row0 + r) * 2 * a.K + col;
     *reinterpret_cast<uint4*>(to) = make_uint4(dg::pack_bf16(gate[0], gate[1]), dg::pack_bf16(gate[2], gate[3]),

@@ -412,7 +412,7 @@ dg_status dg_quantize_fp4(const void* x, const int32_t* masked_m, void* q, int32
 /*
  * SwiGLU and quantisation to FP4, the step between the two products of a feed-forward layer: dg_quantize_fp4 of
  *     y[m, k] = silu(x[m, k]) * x[m, K + k],     silu(v) = v / (1 + exp(-v))
- * computed in FP32.
+ * computed in FP32; silu is 0 where exp(-v) passes 2^133 (v < -92.2: below FP32's normal numbers).
  *   x : BF16 [G, M, 2 K], the K gate columns before the K up columns; K at most 2^29. Everything else as above.
  */
 dg_status dg_swiglu_quantize_fp4(const void* x, const int32_t* masked_m, void* q, int32_t* sf, const dg_rows_desc* desc,

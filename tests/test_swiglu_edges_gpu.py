@@ -1,5 +1,8 @@
-"""The SwiGLU and its gradient where the products around a gate's exponential leave the range of FP32; tolerances as in
-test_quantize_fp4_gpu.py."""
+"""The SwiGLU and its gradient where a gate's exponential, or the products around it, leave the range of FP32.
+
+silu(g) = g / (1 + exp(-g)) is a normal number down to g = -91.9. The exponent of exp(-g) is at most 133 there: it rounds by
+2^-18 (half a unit of [64, 128)), its constant's own rounding (2^-26 of itself) adds under 2^-19, so the exponential is off by
+1.5 * 2^-18 ln 2 < 2^-17.9 relative, the approximations and products by a few 2^-23 more: NEAR = 2^-17 as for other gates."""
 from __future__ import annotations
 
 import numpy as np
@@ -7,7 +10,7 @@ import pytest
 import torch
 
 import oracle.four_bit as F
-from test_quantize_fp4_gpu import BF16, NEAR, buffers, np64
+from test_quantize_fp4_gpu import BF16, NEAR, buffers, check_near, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -24,6 +27,23 @@ def lib():
     return L
 
 
+def far_gates(first):
+    """A row for each four BF16 gates of [first, -40], a block of 32 columns with one gate each, beside `up` of both signs."""
+    gates = torch.cat([torch.arange(first, -64, 0.5), torch.arange(-64, -39.9, 0.25)])
+    gates = gates[:len(gates) // 4 * 4].view(-1, 4)
+    up = torch.randn(len(gates), 128, generator=torch.Generator().manual_seed(1)).clamp_(-3, 3)
+    return torch.cat([gates.repeat_interleave(32, 1), up], 1).to("cuda", BF16)
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 20, 2.0 ** 100])
+def test_small_silu_is_not_zero(lib, scale):
+    x = far_gates(-91.5)
+    x[:, 128:] *= scale
+    q, sf = buffers((), len(x), 128)
+    lib.dg_swiglu_quantize_fp4(x, q, sf)
+    check_near(F.swiglu(np64(x)), q, sf)
+
+
 def check_gradient(x, dy, dx):
     """Within the formula's terms, 2^-17 of each, and the rounding to BF16 (of what is below 2^-126 a step of 2^-133)."""
     x64, dy64 = np64(x), np64(dy)
@@ -32,6 +52,15 @@ def check_gradient(x, dy, dx):
     s = 1 / (1 + np.exp(-gate))
     room = np.concatenate([np.abs(dy64 * up * s) * (1 + np.abs(gate)), np.abs(dy64 * gate * s)], -1) * NEAR
     assert (np.abs(np64(dx) - want) <= room + 2.0 ** -8 * np.abs(want) + 2.0 ** -134).all()
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 60])
+def test_gradient_of_far_gates_is_not_zero(lib, scale):
+    x = far_gates(-91.5)
+    dy = (scale * torch.randn(len(x), 128, generator=torch.Generator().manual_seed(2))).to("cuda", BF16)
+    dx = torch.full_like(x, 77.0)
+    lib.dg_swiglu_backward(x, dy, dx)
+    check_gradient(x, dy, dx)
 
 
 def test_gradient_of_the_lowest_gates(lib):
