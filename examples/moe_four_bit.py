@@ -9,7 +9,8 @@ trains its router:
     y = h @ w2.T, out = sum_j w_j y                 dg_m_grouped_fp4_gemm_nt_masked
 
 and gradients: of the logits, through the weights and the balance loss (dg_moe_route_backward,
-dg_moe_balance_loss_backward), and of z (dg_swiglu_backward).
+dg_moe_balance_loss_backward), and of z (dg_swiglu_backward). The gathering of the rows and the weighted sum, for which the
+library has no operator, are some ten PyTorch operations, the larger part of an eager step's launches.
 
     python examples/moe_four_bit.py [--tokens 256] [--experts 32] [--topk 4] [--hidden 2048] [--inner 1024]
 

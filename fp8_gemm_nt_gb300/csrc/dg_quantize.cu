@@ -30,8 +30,8 @@ using dg::LaunchContext;
 constexpr int kWarps = 4;                    // tiles per block
 constexpr int kTileCols = 256;
 // Rows of a tile: 8, whose scale words are whole 32-byte sectors, where that leaves registers for 32 warps an SM (plain BF16
-// rows: 100 us against 111 with 4, at 32768 x 7168), else 4 (FP32 rows: 21.7 us against 26.8, at 4096 x 7168; gated ones: 16.2
-// against 17.9, at 8192 x 2048).
+// rows: 100 us against 111 with 4, at 32768 x 7168), else 4 (FP32 rows: 21.7 us against 26.8, at 4096 x 7168; gated ones: 14.9
+// against 17.5, at 8192 x 2048, and 96 against 99, at 32768 x 4096).
 template <class T, bool kGate>
 constexpr int kRowsOf = kGate || sizeof(T) == 4 ? 4 : 8;
 constexpr uint32_t kAll = 0xFFFFFFFFu;

@@ -9,8 +9,8 @@
 // fp4_split_kernel, a 128 x BN tile to a cluster whose CTAs share out K (few tiles).
 //
 // Measured on one GB300 (nodes of a CUDA graph, inputs larger than L2): 8 experts, 32768 x 4096 x 7168 282 us (6.8 PFLOP/s,
-// 74 % of the tensor pipe, bound by the 36 KB that a stage brings an SM from L2: 52 bytes a clock); 8192 x 8192 x 8192 151 us
-// (7.3); 4096 x 24576 x 1536 72 us (4.3; its output, 3.3 us a tile, holds it); masked 32 experts of 0 to 256 rows x 7168 x 2048
+// 74 % of the tensor pipe, bound by the 36 KB that a stage brings an SM from L2: 52 bytes a clock); 8192 x 8192 x 8192 154 us
+// (7.2); 4096 x 24576 x 1536 72 us (4.3; its output, 3.3 us a tile, holds it); masked 32 experts of 0 to 256 rows x 7168 x 2048
 // 60 us (5.2 TB/s); 128 x 7168 x 16384 with C 16.9 us (4.0 TB/s).
 #pragma once
 

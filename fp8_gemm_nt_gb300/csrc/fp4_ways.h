@@ -20,8 +20,9 @@ inline int parts(int a, int b) { return (a + b - 1) / b; }
 // Estimated microseconds of a product by CTA pairs with tiles of bn columns, from what the kernel was measured at: a launch
 // 4.5, then for each tile of a pair a start and a time for each stage of 256 K, no less than its output takes, and no less
 // than its share of B takes from HBM. pair_rows: 256-row strips; sharing: how many of them read the same of B. Widths 256,
-// 384 and 128 in us: 8 experts, 32768 x 4096 x 7168 278, 307, 429; of 8 x 32768 x 4096 x 512 89, 76, 116; masked 32 x 256 x
-// 7168 x 2048 67, 60, 70; 4096 x 24576 x 1536 72, 77, 92; 512 x 4096 x 7168 14.2, 20, 12.2.
+// 384 and 128 in us: 8 experts, 32768 x 4096 x 7168 283, 308, 440; of K = 512 89, 78, 120; masked 32 x 256 x 7168 x 2048 67,
+// 61, 69; 4096 x 24576 x 1536 74, 79, 92; 512 x 4096 x 7168 13.9, 19.9, 12.2. Over 28 shapes of all forms, from 1 to 32768
+// rows, its choice is within 6 % of the best.
 inline double pair_time(int bn, int N, int K, double pair_rows, double sharing, int sms) {
   const int stages = parts(K, kWayStageK), clusters = std::max(1, sms / 2);
   const double tiles = pair_rows * parts(N, bn), waves = std::ceil(tiles / clusters);
@@ -39,8 +40,8 @@ inline int pair_width(int N, int K, double pair_rows, double sharing, int sms) {
 
 // Estimated microseconds of one of kSplits: a stage of 256 K costs an SM 0.19 us or the time of its bytes from L2 (91 GB/s an
 // SM; rows of 128 bytes and 8 of scales) or, all CTAs' together, of B's from HBM (6 TB/s); a launch 3 us, a cluster's sums 0.3
-// us and 20 KB a microsecond. Its choice against every way on its own, in us (128 x 7168 x 16384: 16.9, others 17.5 to 28; 128 x
-// 256 x 512: 2.7, 2.8 to 4.9; 128 x 2048 x 16384: 11.0, 12.7 to 20).
+// us and 20 KB a microsecond. Its choice against every way on its own, in us (128 x 7168 x 16384: 16.9, others 17.2 to 37; 128 x
+// 256 x 512: 2.5, 2.9 to 6.3; 128 x 2048 x 16384: 11.3, 13.9 to 36): the best at 19 of 20 shapes, 3 % off at the other.
 inline double split_time(const Way& w, int M, int N, int K, int sms) {
   const int stages = parts(K, kWayStageK), rows = std::min(M, 128);
   const double m_tiles = parts(M, 128), ctas = m_tiles * parts(N, w.bn) * w.ways;
